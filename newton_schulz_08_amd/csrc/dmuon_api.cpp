@@ -23,6 +23,7 @@
 
 #include "../../include/dmuon.h"
 #include "adamw.hpp"
+#include "api_util.hpp"
 #include "clip.hpp"
 #include "common.hpp"
 #include "launch.hpp"
@@ -30,15 +31,6 @@
 namespace dmuon {
 namespace {
 
-thread_local std::string g_last_error;
-
-int fail(int code, const std::string& msg) {
-  g_last_error = msg;
-  return code;
-}
-
-constexpr size_t kAlign = 256;
-size_t align_up(size_t v, size_t a = kAlign) { return (v + a - 1) / a * a; }
 int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
 struct MatPlan {
@@ -281,102 +273,6 @@ Plan make_plan(int count, const int64_t* rows, const int64_t* cols, int dt, bool
   return pl;
 }
 
-// ---------------------------------------------------------------- device checks
-std::mutex g_dev_mu;
-std::map<int, int> g_dev_status;  // device -> status
-
-// The device must be a gfx950, and the stream must not be capturing a graph:
-// every call uploads its descriptors with hipMemcpyAsync from host memory that
-// lives only for the call, which a replayed graph would read after it is gone.
-int check_device(void* hip_stream) {
-  int ndev = 0;
-  if (hipGetDeviceCount(&ndev) != hipSuccess || ndev <= 0) {
-    (void)hipGetLastError();
-    return fail(DMUON_ERR_NO_DEVICE, "no HIP device visible");
-  }
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return fail(DMUON_ERR_HIP, "hipGetDevice failed");
-  {
-    std::lock_guard<std::mutex> lk(g_dev_mu);
-    auto it = g_dev_status.find(dev);
-    if (it == g_dev_status.end()) {
-      hipDeviceProp_t prop;
-      if (hipGetDeviceProperties(&prop, dev) != hipSuccess)
-        return fail(DMUON_ERR_HIP, "hipGetDeviceProperties failed");
-      const int st = (std::strncmp(prop.gcnArchName, "gfx950", 6) == 0) ? DMUON_OK : DMUON_ERR_UNSUPPORTED_ARCH;
-      g_dev_status[dev] = st;
-      if (st != DMUON_OK) return fail(st, std::string("current device is ") + prop.gcnArchName + ", not gfx950");
-    } else if (it->second != DMUON_OK) {
-      return fail(it->second, "current device is not gfx950");
-    }
-  }
-  hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
-  const hipError_t e = hipStreamIsCapturing(static_cast<hipStream_t>(hip_stream), &cs);
-  if (e != hipSuccess) {
-    (void)hipGetLastError();
-    return fail(DMUON_ERR_HIP, std::string("hipStreamIsCapturing: ") + hipGetErrorString(e));
-  }
-  if (cs != hipStreamCaptureStatusNone)
-    return fail(DMUON_ERR_INVALID_ARG,
-                "the stream is capturing a graph; the descriptor upload reads host memory that does not outlive "
-                "the call, so these calls cannot be recorded");
-  return DMUON_OK;
-}
-
-// ---------------------------------------------------------------- profiler
-enum KernelClass { kKPrologue = 0, kKNorm, kKSyrk, kKGemm, kKApply, kKSquare, kKClip, kKAdamw, kKNumClasses };
-const char* kClassNames[kKNumClasses] = {"prologue", "norm_finalize", "syrk", "ns_gemm", "apply_x0",
-                                         "syrk_square", "grad_clip",     "adamw"};
-
-struct ProfRecord {
-  int cls;
-  hipEvent_t start, stop;
-  double flops, bytes;
-};
-
-std::mutex g_prof_mu;
-bool g_prof_on = false;
-std::vector<ProfRecord> g_prof_records;
-std::vector<hipEvent_t> g_event_pool;
-
-hipEvent_t take_event() {
-  if (!g_event_pool.empty()) {
-    hipEvent_t e = g_event_pool.back();
-    g_event_pool.pop_back();
-    return e;
-  }
-  hipEvent_t e = nullptr;
-  if (hipEventCreate(&e) != hipSuccess) return nullptr;
-  return e;
-}
-
-// Runs `launch` on `stream`, bracketed by events when profiling is on.
-template <typename F>
-hipError_t timed(int cls, double flops, double bytes, hipStream_t stream, F&& launch) {
-  bool on;
-  {
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    on = g_prof_on;
-  }
-  if (!on) return launch();
-  hipEvent_t a, b;
-  {
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    a = take_event();
-    b = take_event();
-  }
-  if (!a || !b) return hipErrorOutOfMemory;
-  hipError_t e = hipEventRecord(a, stream);
-  if (e != hipSuccess) return e;
-  e = launch();
-  if (e != hipSuccess) return e;
-  e = hipEventRecord(b, stream);
-  if (e != hipSuccess) return e;
-  std::lock_guard<std::mutex> lk(g_prof_mu);
-  g_prof_records.push_back(ProfRecord{cls, a, b, flops, bytes});
-  return hipSuccess;
-}
-
 // ---------------------------------------------------------------- execution
 struct Call {
   int mode;
@@ -395,8 +291,6 @@ struct Call {
   const float* gcoef = nullptr;   // device, per-segment clipping coefficients (NULL: no clipping)
   const int* clip_seg = nullptr;  // host, per matrix: its clipping segment
 };
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int run(const Plan& pl, const Call& call, void* workspace, hipStream_t stream) {
   char* ws = static_cast<char*>(workspace);
@@ -887,7 +781,7 @@ extern "C" {
 
 int dmuon_ns_workspace_bytes(int count, const int64_t* rows, const int64_t* cols, int dtype,
                              const dmuon_ns_config* ns_config, size_t* bytes_out) {
-  g_last_error.clear();
+  clear_error();
   if (!bytes_out) return fail(DMUON_ERR_INVALID_ARG, "bytes_out is NULL");
   int st = validate_shapes(count, rows, cols, dtype);
   if (st != DMUON_OK) return st;
@@ -899,7 +793,7 @@ int dmuon_ns_workspace_bytes(int count, const int64_t* rows, const int64_t* cols
 
 int dmuon_muon_step_workspace_bytes(int count, const int64_t* rows, const int64_t* cols, int dtype,
                                     const dmuon_ns_config* ns_config, size_t* bytes_out) {
-  g_last_error.clear();
+  clear_error();
   if (!bytes_out) return fail(DMUON_ERR_INVALID_ARG, "bytes_out is NULL");
   int st = validate_shapes(count, rows, cols, dtype);
   if (st != DMUON_OK) return st;
@@ -912,7 +806,7 @@ int dmuon_muon_step_workspace_bytes(int count, const int64_t* rows, const int64_
 int dmuon_ns_batched(int count, const void* const* x_in, void* const* x_out, const int64_t* rows,
                      const int64_t* cols, int dtype, int ns_steps, const dmuon_ns_config* ns_config,
                      void* workspace, size_t workspace_bytes, void* hip_stream) {
-  g_last_error.clear();
+  clear_error();
   int st = validate_shapes(count, rows, cols, dtype);
   if (st != DMUON_OK) return st;
   if (ns_steps < 0 || ns_steps > DMUON_MAX_NS_STEPS)
@@ -1044,7 +938,7 @@ int dmuon_muon_step(int count, void* const* params, const void* const* grads, fl
                     const dmuon_ns_config* ns_config, float mu, int nesterov, float lr, float weight_decay,
                     int lr_scale_mode, const float* lr_scale, float* const* update_out, float* norms_out,
                     void* workspace, size_t workspace_bytes, void* hip_stream) {
-  g_last_error.clear();
+  clear_error();
   Plan pl;
   Call call{};
   bool empty = false;
@@ -1062,7 +956,7 @@ int dmuon_muon_step_noalloc(int count, void* const* params, const void* const* g
                             const dmuon_ns_config* ns_config, float mu, int nesterov, float lr, float weight_decay,
                             int lr_scale_mode, const float* lr_scale, float* const* update_out, float* norms_out,
                             void* hip_stream) {
-  g_last_error.clear();
+  clear_error();
   Plan pl;
   Call call{};
   bool empty = false;
@@ -1082,7 +976,7 @@ int dmuon_muon_step_noalloc(int count, void* const* params, const void* const* g
 }
 
 int dmuon_clip_grad_norm_workspace_bytes(int count, const int64_t* numel, int num_segments, size_t* bytes_out) {
-  g_last_error.clear();
+  clear_error();
   if (!bytes_out) return fail(DMUON_ERR_INVALID_ARG, "bytes_out is NULL");
   int st = validate_clip(count, numel, num_segments);
   if (st != DMUON_OK) return st;
@@ -1093,7 +987,7 @@ int dmuon_clip_grad_norm_workspace_bytes(int count, const int64_t* numel, int nu
 int dmuon_clip_grad_norm(int count, void* const* grads, const int64_t* numel, int dtype, const int* segment,
                          int num_segments, const float* max_norm, float norm_type, float* totals_out,
                          void* workspace, size_t workspace_bytes, void* hip_stream) {
-  g_last_error.clear();
+  clear_error();
   int st = validate_clip(count, numel, num_segments);
   if (st != DMUON_OK) return st;
   if (dtype != kF32 && dtype != kBF16)
@@ -1128,7 +1022,7 @@ std::vector<int64_t> matrix_numel(int count, const int64_t* rows, const int64_t*
 
 int dmuon_muon_step_clip_workspace_bytes(int count, const int64_t* rows, const int64_t* cols, int dtype,
                                          const dmuon_ns_config* ns_config, int num_segments, size_t* bytes_out) {
-  g_last_error.clear();
+  clear_error();
   if (!bytes_out) return fail(DMUON_ERR_INVALID_ARG, "bytes_out is NULL");
   int st = validate_shapes(count, rows, cols, dtype);
   if (st != DMUON_OK) return st;
@@ -1151,7 +1045,7 @@ int dmuon_muon_step_clipped(int count, void* const* params, const void* const* g
                             int lr_scale_mode, const float* lr_scale, float* const* update_out, float* norms_out,
                             const int* segment, int num_segments, const float* max_norm, float norm_type,
                             float* totals_out, void* workspace, size_t workspace_bytes, void* hip_stream) {
-  g_last_error.clear();
+  clear_error();
   Plan pl;
   Call call{};
   bool empty = false;
@@ -1183,7 +1077,7 @@ int dmuon_muon_step_clipped(int count, void* const* params, const void* const* g
 }
 
 int dmuon_adamw_step_workspace_bytes(int count, const int64_t* numel, size_t* bytes_out) {
-  g_last_error.clear();
+  clear_error();
   if (!bytes_out) return fail(DMUON_ERR_INVALID_ARG, "bytes_out is NULL");
   int st = validate_adamw(count, numel);
   if (st != DMUON_OK) return st;
@@ -1195,7 +1089,7 @@ int dmuon_adamw_step(int count, void* const* params, const void* const* grads, f
                      float* const* exp_avg_sq, const int64_t* numel, int dtype, int step, float lr, float beta1,
                      float beta2, float eps, float weight_decay, void* workspace, size_t workspace_bytes,
                      void* hip_stream) {
-  g_last_error.clear();
+  clear_error();
   int st = validate_adamw(count, numel);
   if (st != DMUON_OK) return st;
   if (dtype != kF32 && dtype != kBF16)
@@ -1278,7 +1172,7 @@ int dmuon_adamw_step(int count, void* const* params, const void* const* grads, f
 int dmuon_plan_summary(int count, const int64_t* rows, const int64_t* cols, int dtype,
                        const dmuon_ns_config* ns_config, int ns_steps, int muon_step, char* buf, size_t buf_len,
                        size_t* needed) {
-  g_last_error.clear();
+  clear_error();
   int st = validate_shapes(count, rows, cols, dtype);
   if (st != DMUON_OK) return st;
   if (ns_steps < 0 || ns_steps > DMUON_MAX_NS_STEPS)
@@ -1310,8 +1204,6 @@ const char* dmuon_status_string(int status) {
   }
 }
 
-const char* dmuon_last_error(void) { return g_last_error.c_str(); }
-
 const char* dmuon_backend_info(void) {
   return "dmuon gfx950 | prologue: fused momentum/Nesterov/Frobenius partials, 16x256 tiles (64x64 with an"
          " LDS transpose for tall matrices) | syrk: lower-triangle 256x256 tiles + transposed mirror,"
@@ -1320,52 +1212,6 @@ const char* dmuon_backend_info(void) {
          " add a c2 A^2 + c1 A square launch), bf16 iterate kept as a hi/lo pair, last step writes"
          " p = p (1 - lr wd) - lr s U | fp32 with m' <= 512: 128x128 tiles"
          " | ragged batch: shape-grouped segments, per-XCD balanced tile shares | built " __DATE__;
-}
-
-int dmuon_profile_enable(int on) {
-  std::lock_guard<std::mutex> lk(g_prof_mu);
-  g_prof_on = on != 0;
-  return DMUON_OK;
-}
-
-int dmuon_profile_read(dmuon_kernel_stat* stats, int max_stats, int* n_stats) {
-  g_last_error.clear();
-  if (!n_stats || (max_stats > 0 && !stats)) return fail(DMUON_ERR_INVALID_ARG, "NULL output");
-  std::vector<ProfRecord> recs;
-  {
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    recs.swap(g_prof_records);
-  }
-  dmuon_kernel_stat agg[kKNumClasses];
-  std::memset(agg, 0, sizeof(agg));
-  int status = DMUON_OK;
-  for (const auto& r : recs) {
-    float ms = 0.0f;
-    if (hipEventSynchronize(r.stop) != hipSuccess || hipEventElapsedTime(&ms, r.start, r.stop) != hipSuccess)
-      status = fail(DMUON_ERR_HIP, "event timing failed");
-    agg[r.cls].launches++;
-    agg[r.cls].total_ms += ms;
-    agg[r.cls].flops += r.flops;
-    agg[r.cls].bytes += r.bytes;
-  }
-  {
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    for (const auto& r : recs) {
-      g_event_pool.push_back(r.start);
-      g_event_pool.push_back(r.stop);
-    }
-  }
-  int n = 0;
-  for (int c = 0; c < kKNumClasses; ++c) {
-    if (agg[c].launches == 0) continue;
-    if (n < max_stats) {
-      stats[n] = agg[c];
-      std::snprintf(stats[n].name, sizeof(stats[n].name), "%s", kClassNames[c]);
-    }
-    ++n;
-  }
-  *n_stats = std::min(n, std::max(max_stats, 0));
-  return status;
 }
 
 }  // extern "C"
