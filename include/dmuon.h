@@ -41,7 +41,8 @@
  *   run concurrently only with distinct workspaces and disjoint outputs.
  * - The calls cannot be recorded into a HIP graph: each uploads its
  *   descriptors from host memory that lives only for the call.  A call on a
- *   stream that is capturing returns DMUON_ERR_INVALID_ARG.
+ *   stream that is capturing returns DMUON_ERR_INVALID_ARG.  (The operators
+ *   from dmuon_embedding_forward on upload nothing and can be recorded.)
  * - Argument errors are detected before anything is enqueued; nothing is
  *   modified in that case.  A later DMUON_ERR_HIP means a launch failed and the
  *   outputs are unspecified.
@@ -329,6 +330,203 @@ int dmuon_adamw_step(int count, void* const* params, const void* const* grads, f
                      float* const* exp_avg_sq, const int64_t* numel, int dtype, int step, float lr, float beta1,
                      float beta2, float eps, float weight_decay, void* workspace, size_t workspace_bytes,
                      void* hip_stream);
+
+/* ------------------------------------------------------------------------
+ * Operators that feed the non-matrix parameters of a training step: the
+ * embedding table, the norm gains and the output head, which the training
+ * guide ("第 4 步：创建优化器") leaves to the AdamW group.
+ *
+ * They keep the conventions above, with these additions:
+ * - Every argument travels with the launch, nothing is uploaded: these calls
+ *   may be recorded into a HIP graph (kernel timing is off while a stream
+ *   captures).  Workspaces are then the graph's: two graphs, or a graph and
+ *   eager calls, share one only if they never overlap in time.
+ * - All pointers belong to the current device.
+ * - 16-byte aligned pointers with row lengths that are multiples of 8 take the
+ *   vector path; anything aligned to its element size is accepted.
+ * - bf16 results are rounded once (RNE) from fp32.
+ * ------------------------------------------------------------------------ */
+
+/* Types of token, index and position arrays. */
+#define DMUON_I32 2
+#define DMUON_I64 3
+
+#define DMUON_MAX_TOKENS 4194304    /* tokens or rows per call */
+#define DMUON_MAX_VOCAB 16777216    /* rows of a table, length of a row of logits */
+#define DMUON_MAX_HEAD_DIM 512
+#define DMUON_MAX_HEADS 1024
+#define DMUON_MAX_TEACHER_K 1024    /* teacher entries per row */
+
+/*
+ * Embedding lookup with scaling: out[t, :] = scale * table[tokens[t], :].
+ *
+ * table  : device, vocab x dim, table_dtype, read only.
+ * tokens : device, n entries of token_dtype (DMUON_I32 or DMUON_I64).  A token
+ *          outside [0, vocab) names no row: its output row is zero.
+ * out    : device, n x dim, out_dtype; must not overlap table or tokens.
+ * scale  : finite (sqrt(dim) in models that scale their embeddings).
+ */
+int dmuon_embedding_forward(const void* table, int64_t vocab, int64_t dim, int table_dtype, const void* tokens,
+                            int64_t n, int token_dtype, float scale, void* out, int out_dtype, void* hip_stream);
+
+/*
+ * Sorted order of a batch's tokens, which dmuon_embedding_backward sums along
+ * and dmuon_adamw_rows_step looks rows up in.  With U distinct tokens inside
+ * [0, vocab) and cap = min(n, vocab):
+ *
+ * order[n]         : positions of the batch, sorted by token (stable); positions
+ *                    of tokens outside [0, vocab) come last.
+ * slot[n]          : slot[i] = number of the distinct token of position order[i]
+ *                    (0 .. U - 1, ascending), or -1 outside [0, vocab).
+ * rows[cap]        : the distinct tokens, ascending; -1 from U on.
+ * row_index[vocab] : the inverse: the number of a distinct token, or -1.
+ * count[1]         : U.
+ * All are device int32 and written whole.
+ */
+int dmuon_embedding_plan_workspace_bytes(int64_t n, int64_t vocab, size_t* bytes_out);
+int dmuon_embedding_plan(const void* tokens, int64_t n, int token_dtype, int64_t vocab, int32_t* order, int32_t* slot,
+                         int32_t* rows, int32_t* row_index, int32_t* count, void* workspace, size_t workspace_bytes,
+                         void* hip_stream);
+
+/* Forms of the embedding gradient. */
+#define DMUON_EMBED_DENSE 0   /* grad is vocab x dim, written whole: zero rows for tokens not in the batch */
+#define DMUON_EMBED_ADD 1     /* grad is vocab x dim: the batch's rows are added to, the others left as they are */
+#define DMUON_EMBED_ROWS 2    /* grad is cap x dim: row i belongs to token rows[i]; zero rows from U on */
+
+/*
+ * Gradient of dmuon_embedding_forward with respect to the table:
+ *
+ *   grad[v, :] = scale * sum over t with tokens[t] = v of dout[t, :]
+ *
+ * Sums are fp32, a token's positions in their order in the batch, cut into
+ * pieces at fixed sorted positions: the same inputs give the same bits.
+ *
+ * dout      : device, n x dim, dout_dtype.  Rows of tokens outside [0, vocab)
+ *             are not read.
+ * order, slot, rows, row_index, count : as dmuon_embedding_plan wrote them for
+ *             the same n and vocab.
+ * grad      : device, grad_dtype; with DMUON_EMBED_ADD the sum is fp32 and
+ *             rounded once.
+ */
+int dmuon_embedding_backward_workspace_bytes(int64_t n, int64_t dim, int dout_dtype, size_t* bytes_out);
+int dmuon_embedding_backward(const void* dout, int64_t n, int64_t dim, int dout_dtype, float scale,
+                             const int32_t* order, const int32_t* slot, const int32_t* rows,
+                             const int32_t* row_index, const int32_t* count, int64_t vocab, int form, void* grad,
+                             int grad_dtype, void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
+ * dmuon_adamw_step for one table whose gradient comes as rows.  Row r of the
+ * table has the gradient grad_rows[row_index[r], :], or zero where
+ * row_index[r] is outside [0, n_grad_rows); every element of the table takes
+ * the AdamW update (the moments of rows without a gradient decay as they would
+ * under a zero gradient).  Bitwise the result of dmuon_adamw_step on the dense
+ * gradient, which is never formed.
+ *
+ * param     : device, rows x dim, `dtype`; updated in place.
+ * grad_rows : device, n_grad_rows x dim, `dtype` (the DMUON_EMBED_ROWS form);
+ *             may be NULL when n_grad_rows is 0.
+ * row_index : device, int32[rows].
+ * exp_avg, exp_avg_sq : device, rows x dim float32; updated in place.
+ * Other arguments as in dmuon_adamw_step.
+ */
+int dmuon_adamw_rows_step(void* param, const void* grad_rows, int64_t n_grad_rows, const int32_t* row_index,
+                          float* exp_avg, float* exp_avg_sq, int64_t rows, int64_t dim, int dtype, int step, float lr,
+                          float beta1, float beta2, float eps, float weight_decay, void* hip_stream);
+
+/*
+ * Distillation from a teacher's top logits, loss and gradient in one call.
+ * With q = softmax(teacher / T) over a row's valid teacher entries and z the
+ * student's row:
+ *
+ *   KD     = T^2 sum_j q_j (log q_j - log softmax(z / T)[index_j])
+ *   CE     = -log softmax(z)[label]
+ *   losses = row_weight (kd_weight KD + ce_weight CE)
+ *   dlogits = grad_scale * d losses / dz
+ *
+ * logits    : device, n rows of vocab elements of `dtype`, logits_stride
+ *             elements apart (>= vocab).
+ * teacher_index  : device, n x k, index_dtype.  An entry outside [0, vocab) is
+ *             left out (rows with fewer entries are padded with -1); entries
+ *             that name the same element add up.
+ * teacher_logits : device, n x k float32; any constant per row cancels, so log
+ *             probabilities serve as well.  -inf gives q = 0.
+ * labels    : NULL (then ce_weight must be 0), or device, n entries of
+ *             index_dtype.  A label outside [0, vocab) leaves CE out of its row.
+ * k         : 0 .. DMUON_MAX_TEACHER_K; 0 needs kd_weight = 0.
+ * temperature : T > 0, finite.  kd_weight, ce_weight, grad_scale: finite.
+ * row_weight : NULL (1), or device float32[n].  A row of weight 0 is not read:
+ *             its loss and gradient are 0 whatever it holds.  The same holds
+ *             for a row without a valid teacher entry and without a label.
+ * losses    : device float32[n].
+ * dlogits   : NULL (loss only), or device, n rows of vocab elements of
+ *             `dtype`, dlogits_stride apart.  May equal logits with the same
+ *             stride (in place); must not overlap it otherwise.  Elements
+ *             between the rows are left as they are.
+ * -inf logits are masked elements (probability 0); a row of nothing but -inf
+ * has no distribution and gets NaN.
+ */
+int dmuon_distill_loss_workspace_bytes(int64_t n, int64_t vocab, size_t* bytes_out);
+int dmuon_distill_loss(const void* logits, int64_t n, int64_t vocab, int64_t logits_stride, int dtype,
+                       const void* teacher_index, int index_dtype, const float* teacher_logits, int k,
+                       const void* labels, float temperature, float kd_weight, float ce_weight,
+                       const float* row_weight, float grad_scale, float* losses, void* dlogits,
+                       int64_t dlogits_stride, void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
+ * Shape and types of dmuon_qk_norm_rope_forward and _backward.
+ */
+typedef struct {
+    int64_t tokens;       /* 0 .. DMUON_MAX_TOKENS */
+    int q_heads, k_heads; /* 0 .. DMUON_MAX_HEADS; not both 0 */
+    int head_dim;         /* D, 1 .. DMUON_MAX_HEAD_DIM */
+    int rot_dim;          /* rotated elements of a head: even, 0 .. D; 0 = norm only */
+    int interleaved;      /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1) */
+    int64_t max_pos;      /* rows of the rotation table */
+    float eps;            /* finite, >= 0 */
+    float weight_offset;  /* finite; 1 for gains stored around zero */
+    int dtype;            /* queries, keys, outputs and their gradients */
+    int weight_dtype;     /* gains and their gradients */
+    int pos_dtype;        /* DMUON_I32 or DMUON_I64 */
+} dmuon_qk_shape;
+
+/*
+ * Root-mean-square norm of every query and key head, then the rotation by the
+ * token's position:
+ *
+ *   n = x / sqrt(mean(x^2) + eps) * (weight_offset + w),   out = R(position) n
+ *
+ * q, k       : device; token t's heads are contiguous (heads x D) at element
+ *              t * stride: a packed projection's output is read in place.
+ * q_weight, k_weight : device, D entries of weight_dtype, or NULL for no gain.
+ * positions  : device, tokens entries.  A negative position marks a padding
+ *              token: its outputs are zero and its inputs are not read.  A
+ *              position >= max_pos gives NaN.  NULL when rot_dim is 0.
+ * rope       : device float32, max_pos x rot_dim: a position's rot_dim / 2
+ *              cosines, then its sines.  NULL when rot_dim is 0.
+ * q_out, k_out : device; may equal q and k with the same stride (in place).
+ * Pointers of a tensor with 0 heads are ignored.  The sum of a head's squares
+ * has to be a finite float32.
+ */
+int dmuon_qk_norm_rope_forward(const dmuon_qk_shape* shape, const void* q, int64_t q_stride, const void* k,
+                               int64_t k_stride, const void* q_weight, const void* k_weight, const void* positions,
+                               const float* rope, void* q_out, int64_t q_out_stride, void* k_out,
+                               int64_t k_out_stride, void* hip_stream);
+
+/*
+ * Gradients of dmuon_qk_norm_rope_forward: dq, dk from dq_out, dk_out and the
+ * forward's inputs, and the gains' gradients, summed over tokens and heads in
+ * fp32 in a fixed order.  Padding tokens get zeros and add nothing to the gains.
+ *
+ * dq, dk may equal dq_out, dk_out or q, k with the same stride.
+ * dq_weight, dk_weight : device, D entries of weight_dtype, or NULL.
+ */
+int dmuon_qk_norm_rope_backward_workspace_bytes(const dmuon_qk_shape* shape, size_t* bytes_out);
+int dmuon_qk_norm_rope_backward(const dmuon_qk_shape* shape, const void* dq_out, int64_t dq_out_stride,
+                                const void* dk_out, int64_t dk_out_stride, const void* q, int64_t q_stride,
+                                const void* k, int64_t k_stride, const void* q_weight, const void* k_weight,
+                                const void* positions, const float* rope, void* dq, int64_t dq_stride, void* dk,
+                                int64_t dk_stride, void* dq_weight, void* dk_weight, void* workspace,
+                                size_t workspace_bytes, void* hip_stream);
 
 /*
  * The plan of a call as text: routes (numel < DMUON_MIN_NS_NUMEL goes

@@ -24,4 +24,19 @@ from .api import (  # noqa: F401
     profile_enable,
     profile_read,
 )
+from .ops import (  # noqa: F401
+    EmbeddingPlan,
+    adamw_rows_step_,
+    distill_loss,
+    distill_loss_workspace_bytes,
+    embedding,
+    embedding_grad,
+    embedding_grad_workspace_bytes,
+    embedding_plan,
+    embedding_plan_workspace_bytes,
+    qk_norm_rope,
+    qk_norm_rope_grad,
+    qk_norm_rope_grad_workspace_bytes,
+    rope_table,
+)
 from ._lib import DmuonError, load  # noqa: F401

@@ -35,6 +35,17 @@ DMUON_MAX_NS_TERMS = 3
 DMUON_LR_SCALE_ONE = 0
 DMUON_LR_SCALE_MOONLIGHT = 1
 
+DMUON_I32 = 2
+DMUON_I64 = 3
+DMUON_MAX_TOKENS = 4194304
+DMUON_MAX_VOCAB = 16777216
+DMUON_MAX_HEAD_DIM = 512
+DMUON_MAX_HEADS = 1024
+DMUON_MAX_TEACHER_K = 1024
+DMUON_EMBED_DENSE = 0
+DMUON_EMBED_ADD = 1
+DMUON_EMBED_ROWS = 2
+
 
 class NsConfig(ctypes.Structure):
     """dmuon_ns_config."""
@@ -56,12 +67,32 @@ class KernelStat(ctypes.Structure):
     ]
 
 
+class QkShape(ctypes.Structure):
+    """dmuon_qk_shape."""
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("q_heads", ctypes.c_int),
+        ("k_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+        ("rot_dim", ctypes.c_int),
+        ("interleaved", ctypes.c_int),
+        ("max_pos", ctypes.c_int64),
+        ("eps", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+        ("dtype", ctypes.c_int),
+        ("weight_dtype", ctypes.c_int),
+        ("pos_dtype", ctypes.c_int),
+    ]
+
+
 _P = ctypes.c_void_p
 _PP = ctypes.POINTER(ctypes.c_void_p)
 _I64P = ctypes.POINTER(ctypes.c_int64)
 _SZP = ctypes.POINTER(ctypes.c_size_t)
 _FP = ctypes.POINTER(ctypes.c_float)
 _CFGP = ctypes.POINTER(NsConfig)
+_I, _I64, _F, _SZ = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+_QKP = ctypes.POINTER(QkShape)
 
 # name -> (restype, argtypes); mirrors include/dmuon.h
 SIGNATURES = {
@@ -88,6 +119,19 @@ SIGNATURES = {
     "dmuon_adamw_step": (ctypes.c_int, [ctypes.c_int, _PP, _PP, _PP, _PP, _I64P, ctypes.c_int, ctypes.c_int,
                                         ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_float,
                                         ctypes.c_float, _P, ctypes.c_size_t, _P]),
+    "dmuon_embedding_forward": (_I, [_P, _I64, _I64, _I, _P, _I64, _I, _F, _P, _I, _P]),
+    "dmuon_embedding_plan_workspace_bytes": (_I, [_I64, _I64, _SZP]),
+    "dmuon_embedding_plan": (_I, [_P, _I64, _I, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "dmuon_embedding_backward_workspace_bytes": (_I, [_I64, _I64, _I, _SZP]),
+    "dmuon_embedding_backward": (_I, [_P, _I64, _I64, _I, _F, _P, _P, _P, _P, _P, _I64, _I, _P, _I, _P, _SZ, _P]),
+    "dmuon_adamw_rows_step": (_I, [_P, _P, _I64, _P, _P, _P, _I64, _I64, _I, _I, _F, _F, _F, _F, _F, _P]),
+    "dmuon_distill_loss_workspace_bytes": (_I, [_I64, _I64, _SZP]),
+    "dmuon_distill_loss": (_I, [_P, _I64, _I64, _I64, _I, _P, _I, _P, _I, _P, _F, _F, _F, _P, _F, _P, _P, _I64, _P,
+                                _SZ, _P]),
+    "dmuon_qk_norm_rope_forward": (_I, [_QKP, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _P, _I64, _P]),
+    "dmuon_qk_norm_rope_backward_workspace_bytes": (_I, [_QKP, _SZP]),
+    "dmuon_qk_norm_rope_backward": (_I, [_QKP, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _P,
+                                         _I64, _P, _P, _P, _SZ, _P]),
     "dmuon_plan_summary": (ctypes.c_int, [ctypes.c_int, _I64P, _I64P, ctypes.c_int, _CFGP, ctypes.c_int, ctypes.c_int,
                                           ctypes.c_char_p, ctypes.c_size_t, _SZP]),
     "dmuon_status_string": (ctypes.c_char_p, [ctypes.c_int]),

@@ -21,8 +21,9 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libdmuon.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
-SOURCES = ["kernels_elementwise.hip", "kernels_mfma.hip", "kernels_clip.hip", "kernels_adamw.hip", "api_util.cpp",
-           "dmuon_api.cpp"]
+SOURCES = ["kernels_elementwise.hip", "kernels_mfma.hip", "kernels_clip.hip", "kernels_adamw.hip",
+           "kernels_embedding.hip", "kernels_adamw_rows.hip", "kernels_distill.hip", "kernels_qknorm.hip",
+           "api_util.cpp", "dmuon_api.cpp", "dmuon_ops_api.cpp"]
 ARCH = "gfx950"
 
 COMMON_FLAGS = [
@@ -51,7 +52,7 @@ def _run(cmd, verbose):
         print(out, flush=True)
 
 
-def build(verbose: bool = False, jobs: int = 3) -> str:
+def build(verbose: bool = False, jobs: int = 6) -> str:
     hipcc = _hipcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     objs = []

@@ -1,0 +1,113 @@
+// AdamW step of one table whose gradient comes as rows, on gfx950 (HBM-bound).
+//
+// The gradient of an embedding table is zero outside the rows that the batch
+// names.  Row r of the table has gradient g = grad_rows[row_index[r]], or 0
+// when row_index[r] is outside [0, n_grad_rows); every element then takes the
+// update of the dense step (kernels_adamw.hip, same arithmetic and order, so
+// the result is bitwise that of the dense step on the scattered gradient):
+//
+//   p <- p (1 - lr wd);  m <- beta1 m + (1 - beta1) g;  v <- beta2 v + (1 - beta2) g^2
+//   p <- p - step_size m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+//
+// What is saved is the dense gradient itself: neither its zeros are written
+// by the backward pass, nor read here (2 of 22 bytes per bf16 element, 4 of 28
+// per fp32 element).
+#include <hip/hip_runtime.h>
+
+#include "ops.hpp"
+
+namespace dmuon {
+namespace {
+
+__device__ __forceinline__ void adamw_elem(float& p, float g, float& m, float& v, const AdamArgs& a) {
+  p *= a.decay;
+  m = fmaf(a.beta1, m, a.one_minus_beta1 * g);
+  v = fmaf(a.beta2, v, (a.one_minus_beta2 * g) * g);
+  const float denom = fmaf(sqrtf(v), a.inv_bc2_sqrt, a.eps);
+  p = fmaf(-a.step_size, m / denom, p);
+}
+
+// Gradient row of table row r, or nullptr.
+template <typename T>
+__device__ __forceinline__ const T* grad_row(const AdamRowsArgs& a, int64_t r) {
+  const int64_t i = gmem(a.row_index)[r];
+  return i >= 0 && i < a.n_grad_rows ? static_cast<const T*>(a.g) + i * a.dim : nullptr;
+}
+
+// The table is cut into 4096-element tiles, one block each, as in the dense
+// step.  With dim a multiple of 4 a chunk of four elements lies in one row;
+// `magic` = floor(2^32 / dim) gives that row by a multiplication (the quotient
+// is at most one short for the offsets that occur, below 2^17).
+template <int DT>
+__global__ __launch_bounds__(kAdamThreads) void adamw_rows_kernel(AdamRowsArgs a, int64_t tiles, unsigned magic) {
+  using T = typename OpElem<DT>::T;
+  T* pp = static_cast<T*>(a.p);
+  const int64_t numel = a.rows * a.dim;
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int64_t base = t * kAdamTile;
+    const int64_t r0 = base / a.dim;
+    const unsigned c0 = static_cast<unsigned>(base - r0 * a.dim), dim = static_cast<unsigned>(a.dim);
+    if (a.vec && base + kAdamTile <= numel) {
+      float p[kAdamChunks][4], m[kAdamChunks][4], v[kAdamChunks][4], g[kAdamChunks][4];
+#pragma unroll
+      for (int c = 0; c < kAdamChunks; ++c) {
+        const unsigned o = (c * kAdamThreads + threadIdx.x) * 4;
+        load_n<4>(pp + base + o, p[c]);
+        load_n<4>(a.m + base + o, m[c]);
+        load_n<4>(a.v + base + o, v[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < kAdamChunks; ++c) {
+        const unsigned x = c0 + (c * kAdamThreads + threadIdx.x) * 4;
+        unsigned q = __umulhi(x, magic);
+        unsigned rest = x - q * dim;
+        if (rest >= dim) {
+          rest -= dim;
+          ++q;
+        }
+        const T* gr = grad_row<T>(a, r0 + q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[c][e] = 0.0f;
+        if (gr) load_n<4>(gr + rest, g[c]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int c = 0; c < kAdamChunks; ++c) {
+        const unsigned o = (c * kAdamThreads + threadIdx.x) * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) adamw_elem(p[c][e], g[c][e], m[c][e], v[c][e], a.hp);
+        store_n<4>(pp + base + o, p[c]);
+        store_n<4>(a.m + base + o, m[c]);
+        store_n<4>(a.v + base + o, v[c]);
+      }
+    } else {
+      for (int o = threadIdx.x; o < kAdamTile; o += kAdamThreads) {
+        const int64_t e = base + o;
+        if (e >= numel) break;
+        const int64_t r = e / a.dim;
+        const T* gr = grad_row<T>(a, r);
+        float p = static_cast<float>(gmem(pp)[e]), m = gmem(a.m)[e], v = gmem(a.v)[e];
+        adamw_elem(p, gr ? static_cast<float>(gmem(gr)[e - r * a.dim]) : 0.0f, m, v, a.hp);
+        gmem(pp)[e] = static_cast<T>(p);
+        gmem(a.m)[e] = m;
+        gmem(a.v)[e] = v;
+      }
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_adamw_rows(int dt, const AdamRowsArgs& a, hipStream_t stream) {
+  const int64_t tiles = (a.rows * a.dim + kAdamTile - 1) / kAdamTile;
+  if (tiles == 0) return hipSuccess;
+  const dim3 grid(static_cast<unsigned>(tiles < (int64_t{1} << 22) ? tiles : int64_t{1} << 22));
+  const unsigned magic = static_cast<unsigned>((uint64_t{1} << 32) / static_cast<uint64_t>(a.dim) - (a.dim == 1 ? 1 : 0));
+  if (dt == kBF16)
+    hipLaunchKernelGGL(adamw_rows_kernel<kBF16>, grid, dim3(kAdamThreads), 0, stream, a, tiles, magic);
+  else
+    hipLaunchKernelGGL(adamw_rows_kernel<kF32>, grid, dim3(kAdamThreads), 0, stream, a, tiles, magic);
+  return hipGetLastError();
+}
+
+}  // namespace dmuon

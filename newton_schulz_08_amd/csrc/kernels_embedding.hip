@@ -1,0 +1,572 @@
+// Embedding lookup with scaling, and its gradient by sorted tokens, on gfx950.
+//
+//   out[t, :]    = scale * table[tok[t], :]
+//   dtable[v, :] = scale * sum over t with tok[t] = v of dout[t, :]
+//
+// A token outside [0, vocab) names no row: its output is zero and it gives no
+// gradient.  All of it is bound by HBM: one read of the rows and one write.
+//
+// The gradient needs no atomics.  The plan sorts the tokens stably (an LSD
+// radix sort of (token, position) pairs), so equal tokens lie next to each
+// other in their order of occurrence; the sum of a run of equal tokens is then
+// formed in fp32 in that order, and results are bitwise reproducible.
+#include <hip/hip_runtime.h>
+
+#include "ops.hpp"
+
+namespace dmuon {
+namespace {
+
+__device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
+__device__ __forceinline__ int popc_below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi(static_cast<unsigned>(mask >> 32),
+                                   __builtin_amdgcn_mbcnt_lo(static_cast<unsigned>(mask), 0));
+}
+
+// ---------------------------------------------------------------- lookup
+template <int TDT, int ODT>
+__global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a, int log_tpr) {
+  using T = typename OpElem<TDT>::T;
+  using O = typename OpElem<ODT>::T;
+  constexpr int C = ODT == kBF16 ? 8 : 4;   // elements of a 16-byte store
+  constexpr int U = 2;
+  const int tpr = 1 << log_tpr;
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) << (8 - log_tpr)) + (threadIdx.x >> log_tpr);
+  const int lane = threadIdx.x & (tpr - 1);
+  if (row >= a.n) return;
+  const int64_t tok = load_index(a.tokens, row, a.tok64);
+  const bool known = tok >= 0 && tok < a.vocab;
+  const T* src = static_cast<const T*>(a.table) + (known ? tok : 0) * a.dim;
+  O* dst = static_cast<O*>(a.out) + row * a.dim;
+  if (a.vec) {
+    const int64_t nch = a.dim / C;
+    for (int64_t c0 = lane; c0 < nch; c0 += tpr * U) {
+      float v[U][C];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t c = c0 + u * tpr;
+        if (c < nch && known) {
+          load_n<C>(src + c * C, v[u]);
+#pragma unroll
+          for (int e = 0; e < C; ++e) v[u][e] *= a.scale;
+        } else {
+#pragma unroll
+          for (int e = 0; e < C; ++e) v[u][e] = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t c = c0 + u * tpr;
+        if (c < nch) store_n<C>(dst + c * C, v[u]);
+      }
+    }
+  } else {
+    for (int64_t e = lane; e < a.dim; e += tpr)
+      gmem(dst)[e] = static_cast<O>(known ? static_cast<float>(gmem(src)[e]) * a.scale : 0.0f);
+  }
+}
+
+// ---------------------------------------------------------------- plan
+__device__ __forceinline__ unsigned plan_key(const PlanArgs& a, int i) {
+  const int64_t t = load_index(a.tokens, i, a.tok64);
+  return static_cast<unsigned>(t >= 0 && t < a.vocab ? t : a.vocab);   // unknown tokens sort to the end
+}
+
+// Lanes of the wave with the same digit as this lane (among `valid` lanes).
+__device__ __forceinline__ uint64_t same_digit(unsigned d, int bits, bool valid) {
+  uint64_t peers = __ballot(valid);
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (d >> b) & 1;
+    const uint64_t m = __ballot(one);
+    peers &= one ? m : ~m;
+  }
+  return peers;
+}
+
+// Inclusive scan over the block of one value per thread; total in *sum.
+__device__ __forceinline__ int block_scan(int v, int* wave_tot, int* sum) {
+  const int w = threadIdx.x >> 6;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int t = __shfl_up(v, o, 64);
+    if (lane_id() >= o) v += t;
+  }
+  if (lane_id() == 63) wave_tot[w] = v;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int k = 0; k < kPlanWaves; ++k) {
+    const int t = wave_tot[k];
+    before += k < w ? t : 0;
+    all += t;
+  }
+  __syncthreads();
+  *sum = all;
+  return v + before;
+}
+
+__device__ __forceinline__ void fill_minus_one(int* p, int64_t n, int64_t first, int64_t step) {
+  for (int64_t i = first; i < n; i += step) gmem(p)[i] = -1;
+}
+
+// All of the plan in one block for n <= kPlanSmall: the pairs stay in LDS.
+__global__ __launch_bounds__(kPlanThreads) void plan_small_kernel(PlanArgs a) {
+  __shared__ unsigned key[2][kPlanSmall];
+  __shared__ uint16_t idx[2][kPlanSmall];
+  __shared__ uint16_t cnt[kPlanWaves][kPlanMaxDigits];
+  __shared__ int wave_tot[kPlanWaves];
+  constexpr int kPer = kPlanSmall / kPlanThreads;   // items per thread; a wave owns 64 kPer consecutive ones
+  const int tid = threadIdx.x, w = tid >> 6, lane = lane_id();
+  const int digits = 1 << a.bits;
+  const unsigned mask = digits - 1;
+  fill_minus_one(a.row_index, a.vocab, tid, kPlanThreads);
+  for (int i = tid; i < a.n; i += kPlanThreads) {
+    key[0][i] = plan_key(a, i);
+    idx[0][i] = static_cast<uint16_t>(i);
+  }
+  int cur = 0;
+  for (int pass = 0; pass < a.passes; ++pass, cur ^= 1) {
+    const int shift = pass * a.bits;
+    for (int i = tid; i < kPlanWaves * digits; i += kPlanThreads) cnt[i / digits][i & mask] = 0;
+    __syncthreads();
+    int rank[kPer];
+    unsigned dig[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = (w * kPer + j) * 64 + lane;
+      const bool valid = i < a.n;
+      dig[j] = valid ? (key[cur][i] >> shift) & mask : 0;
+      const uint64_t peers = same_digit(dig[j], a.bits, valid);
+      const int below = popc_below(peers);
+      const int base = valid ? cnt[w][dig[j]] : 0;
+      __builtin_amdgcn_wave_barrier();
+      if (valid && below == 0) cnt[w][dig[j]] = static_cast<uint16_t>(base + __popcll(peers));
+      __builtin_amdgcn_wave_barrier();
+      rank[j] = base + below;
+    }
+    __syncthreads();
+    int total = 0;
+    if (tid < digits)
+      for (int k = 0; k < kPlanWaves; ++k) {
+        const int t = cnt[k][tid];
+        cnt[k][tid] = static_cast<uint16_t>(total);
+        total += t;
+      }
+    int all;
+    const int before = block_scan(total, wave_tot, &all) - total;
+    if (tid < digits)
+      for (int k = 0; k < kPlanWaves; ++k) cnt[k][tid] = static_cast<uint16_t>(cnt[k][tid] + before);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = (w * kPer + j) * 64 + lane;
+      if (i < a.n) {
+        const int pos = cnt[w][dig[j]] + rank[j];
+        key[cur ^ 1][pos] = key[cur][i];
+        idx[cur ^ 1][pos] = idx[cur][i];
+      }
+    }
+    __syncthreads();
+  }
+  // runs of equal tokens
+  const unsigned none = static_cast<unsigned>(a.vocab);
+  uint64_t heads[kPer];
+  int mine = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = (w * kPer + j) * 64 + lane;
+    const bool head = i < a.n && key[cur][i] != none && (i == 0 || key[cur][i - 1] != key[cur][i]);
+    heads[j] = __ballot(head);
+    mine += __popcll(heads[j]);
+  }
+  if (lane == 0) wave_tot[w] = mine;
+  __syncthreads();
+  int base = 0, all = 0;
+  for (int k = 0; k < kPlanWaves; ++k) {
+    base += k < w ? wave_tot[k] : 0;
+    all += wave_tot[k];
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = (w * kPer + j) * 64 + lane;
+    if (i < a.n) {
+      const unsigned kv = key[cur][i];
+      const bool head = (heads[j] >> lane) & 1;
+      const int s = kv == none ? -1 : base + popc_below(heads[j]) + (head ? 0 : -1);
+      gmem(a.order)[i] = idx[cur][i];
+      gmem(a.slot)[i] = s;
+      if (head) {
+        gmem(a.rows)[s] = static_cast<int>(kv);
+        gmem(a.row_index)[kv] = s;
+      }
+    }
+    base += __popcll(heads[j]);
+  }
+  for (int i = all + tid; i < a.cap; i += kPlanThreads) gmem(a.rows)[i] = -1;
+  if (tid == 0) gmem(a.count)[0] = all;
+}
+
+// Digit counts of one block's tokens.
+__global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanArgs a, int pass) {
+  __shared__ int hist[kPlanMaxDigits];
+  const int digits = 1 << a.bits, shift = pass * a.bits;
+  const int tid = threadIdx.x;
+  if (tid < digits) hist[tid] = 0;
+  if (pass == 0) {
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kPlanThreads;
+    fill_minus_one(a.row_index, a.vocab, first, step);
+    fill_minus_one(a.rows, a.cap, first, step);
+  }
+  __syncthreads();
+  const int i0 = blockIdx.x * a.items;
+  const int i1 = min(a.n, i0 + a.items);
+  for (int i = i0 + tid; i < i1; i += kPlanThreads) {
+    const unsigned k = pass == 0 ? plan_key(a, i) : gmem(a.key[(pass + 1) & 1])[i];
+    atomicAdd(&hist[(k >> shift) & (digits - 1)], 1);
+  }
+  __syncthreads();
+  if (tid < digits) gmem(a.counts)[blockIdx.x * digits + tid] = hist[tid];
+}
+
+// Stable scatter of one pass: every wave ranks its own consecutive tokens, the
+// block adds the counts of the waves and blocks before it.
+__global__ __launch_bounds__(kPlanThreads) void plan_scatter_kernel(PlanArgs a, int pass) {
+  __shared__ int cnt[kPlanWaves][kPlanMaxDigits];
+  __shared__ int wave_tot[kPlanWaves];
+  const int tid = threadIdx.x, w = tid >> 6, lane = lane_id();
+  const int digits = 1 << a.bits, shift = pass * a.bits;
+  const unsigned mask = digits - 1;
+  const unsigned* kin = a.key[(pass + 1) & 1];
+  const int* iin = a.idx[(pass + 1) & 1];
+  unsigned* kout = a.key[pass & 1];
+  int* iout = a.idx[pass & 1];
+  const int per_wave = a.items / kPlanWaves;   // a multiple of 64
+  const int64_t w0 = static_cast<int64_t>(blockIdx.x) * a.items + w * per_wave;
+  for (int i = tid; i < kPlanWaves * digits; i += kPlanThreads) cnt[i / digits][i & mask] = 0;
+  __syncthreads();
+  // counts of each wave
+  for (int j = 0; j < per_wave; j += 64) {
+    const int64_t i = w0 + j + lane;
+    const bool valid = i < a.n;
+    const unsigned k = !valid ? 0 : pass == 0 ? plan_key(a, static_cast<int>(i)) : gmem(kin)[i];
+    const unsigned d = (k >> shift) & mask;
+    const uint64_t peers = same_digit(d, a.bits, valid);
+    const int base = valid ? cnt[w][d] : 0;
+    __builtin_amdgcn_wave_barrier();
+    if (valid && popc_below(peers) == 0) cnt[w][d] = base + __popcll(peers);
+    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+  int before = 0, total = 0;
+  if (tid < digits) {
+    for (int b = 0; b < a.blocks; ++b) {
+      const int c = gmem(a.counts)[b * digits + tid];
+      before += b < static_cast<int>(blockIdx.x) ? c : 0;
+      total += c;
+    }
+  }
+  int all;
+  const int first = block_scan(total, wave_tot, &all) - total;
+  if (tid < digits) {
+    int run = first + before;
+    for (int k = 0; k < kPlanWaves; ++k) {
+      const int t = cnt[k][tid];
+      cnt[k][tid] = run;
+      run += t;
+    }
+  }
+  __syncthreads();
+  for (int j = 0; j < per_wave; j += 64) {
+    const int64_t i = w0 + j + lane;
+    const bool valid = i < a.n;
+    const unsigned k = !valid ? 0 : pass == 0 ? plan_key(a, static_cast<int>(i)) : gmem(kin)[i];
+    const unsigned d = (k >> shift) & mask;
+    const uint64_t peers = same_digit(d, a.bits, valid);
+    const int below = popc_below(peers);
+    const int base = valid ? cnt[w][d] : 0;
+    __builtin_amdgcn_wave_barrier();
+    if (valid && below == 0) cnt[w][d] = base + __popcll(peers);
+    __builtin_amdgcn_wave_barrier();
+    if (valid) {
+      const int pos = base + below;
+      gmem(kout)[pos] = k;
+      gmem(iout)[pos] = pass == 0 ? static_cast<int>(i) : gmem(iin)[i];
+    }
+  }
+}
+
+__device__ __forceinline__ bool plan_head(const unsigned* key, int64_t i, unsigned none) {
+  const unsigned k = gmem(key)[i];
+  return k != none && (i == 0 || gmem(key)[i - 1] != k);
+}
+
+// Run heads of one block's sorted tokens: counted, then written.
+__global__ __launch_bounds__(kPlanThreads) void plan_heads_kernel(PlanArgs a) {
+  __shared__ int wave_tot[kPlanWaves];
+  const unsigned* key = a.key[(a.passes + 1) & 1];
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * a.items;
+  int mine = 0;
+  for (int j = threadIdx.x; j < a.items; j += kPlanThreads)
+    if (i0 + j < a.n && plan_head(key, i0 + j, static_cast<unsigned>(a.vocab))) ++mine;
+  int all;
+  block_scan(mine, wave_tot, &all);
+  if (threadIdx.x == 0) gmem(a.heads)[blockIdx.x] = all;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void plan_rows_kernel(PlanArgs a) {
+  __shared__ int wave_tot[kPlanWaves];
+  const unsigned* key = a.key[(a.passes + 1) & 1];
+  const int* idx = a.idx[(a.passes + 1) & 1];
+  const unsigned none = static_cast<unsigned>(a.vocab);
+  const int tid = threadIdx.x;
+  const int h = tid < a.blocks ? gmem(a.heads)[tid] : 0;
+  int before, all;
+  block_scan(tid < static_cast<int>(blockIdx.x) ? h : 0, wave_tot, &before);
+  block_scan(h, wave_tot, &all);
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * a.items;
+  for (int j = 0; j < a.items; j += kPlanThreads) {
+    const int64_t i = i0 + j + tid;
+    const bool head = i < a.n && plan_head(key, i, none);
+    int here;
+    const int s = before + block_scan(head ? 1 : 0, wave_tot, &here) - 1;
+    if (i < a.n) {
+      const unsigned k = gmem(key)[i];
+      gmem(a.order)[i] = gmem(idx)[i];
+      gmem(a.slot)[i] = k == none ? -1 : s;
+      if (head) {
+        gmem(a.rows)[s] = static_cast<int>(k);
+        gmem(a.row_index)[k] = s;
+      }
+    }
+    before += here;
+  }
+  if (blockIdx.x == 0 && tid == 0) gmem(a.count)[0] = all;
+}
+
+// ---------------------------------------------------------------- gradient
+// The sorted positions are cut into chunks of equal length, so that work is
+// even however often a token occurs.  A thread owns one 16-byte column chunk
+// and walks its chunk's positions, adding rows of dout; where the run of a
+// token ends it writes the row.  A run that crosses a chunk's edge leaves fp32
+// sums in `part` (index 2c: the run that began before chunk c; 2c + 1: the one
+// that goes on behind it), which egrad_join_kernel adds up.
+template <int GDT, int C>
+__device__ __forceinline__ void grad_write(const EmbedGradArgs& a, int slot, int64_t col, int cols, float* v) {
+  using G = typename OpElem<GDT>::T;
+  const int64_t row = a.form == kGradRows ? slot : gmem(a.rows)[slot];
+  if (row < 0 || row >= (a.form == kGradRows ? static_cast<int64_t>(a.cap) : a.vocab)) return;
+  G* dst = static_cast<G*>(a.grad) + row * a.dim + col;
+  if (cols == C && a.vec) {
+    float old[C];
+    if (a.form == kGradAdd) load_n<C>(dst, old);
+#pragma unroll
+    for (int e = 0; e < C; ++e) v[e] = a.form == kGradAdd ? fmaf(v[e], a.scale, old[e]) : v[e] * a.scale;
+    store_n<C>(dst, v);
+  } else {
+    for (int e = 0; e < cols; ++e) {
+      const float old = a.form == kGradAdd ? static_cast<float>(gmem(dst)[e]) : 0.0f;
+      gmem(dst)[e] = static_cast<G>(a.form == kGradAdd ? fmaf(v[e], a.scale, old) : v[e] * a.scale);
+    }
+  }
+}
+
+template <int DT, int GDT>
+__global__ __launch_bounds__(kEgThreads) void egrad_kernel(EmbedGradArgs a, int log_tpr, int col_tiles,
+                                                           int64_t sum_blocks) {
+  using T = typename OpElem<DT>::T;
+  using G = typename OpElem<GDT>::T;
+  constexpr int C = DT == kBF16 ? 8 : 4;
+  constexpr int U = 4;
+  const int tid = threadIdx.x;
+  if (static_cast<int64_t>(blockIdx.x) >= sum_blocks) {
+    // rows that no token names: of the table, or behind the last distinct token
+    const int64_t r0 = (blockIdx.x - sum_blocks) * kEgZeroRows;
+    const int64_t rows = a.form == kGradRows ? a.cap : a.vocab;
+    const int used = a.form == kGradRows ? gmem(a.count)[0] : 0;
+    for (int r = 0; r < kEgZeroRows; ++r) {
+      const int64_t row = r0 + r;
+      if (row >= rows) break;
+      if (a.form == kGradRows ? row < used : gmem(a.row_index)[row] >= 0) continue;
+      G* dst = static_cast<G*>(a.grad) + row * a.dim;
+      constexpr int Z = GDT == kBF16 ? 8 : 4;
+      if (a.vec) {
+        const float zero[Z] = {};
+        for (int64_t e = tid * Z; e < a.dim; e += kEgThreads * Z) store_n<Z>(dst + e, zero);
+      } else {
+        for (int64_t e = tid; e < a.dim; e += kEgThreads) gmem(dst)[e] = static_cast<G>(0.0f);
+      }
+    }
+    return;
+  }
+  const int tpr = 1 << log_tpr;
+  const int64_t group = blockIdx.x / col_tiles;
+  const int ct = static_cast<int>(blockIdx.x - group * col_tiles);
+  const int64_t chunk = (group << (8 - log_tpr)) + (tid >> log_tpr);
+  const int64_t col = (static_cast<int64_t>(ct) * tpr + (tid & (tpr - 1))) * C;
+  if (chunk >= a.chunks || col >= a.dim) return;
+  const int cols = static_cast<int>(min<int64_t>(C, a.dim - col));
+  const int64_t p0 = chunk * a.chunk, p1 = min(a.n, p0 + a.chunk);
+  const T* dout = static_cast<const T*>(a.dout) + col;
+  int cur = gmem(a.slot)[p0];
+  if (cur < 0) return;
+  bool began_before = p0 > 0 && gmem(a.slot)[p0 - 1] == cur;
+  const int next = p1 < a.n ? gmem(a.slot)[p1] : -1;
+  float acc[C];
+#pragma unroll
+  for (int e = 0; e < C; ++e) acc[e] = 0.0f;
+  auto flush = [&](bool last) {
+    const bool goes_on = last && next == cur;
+    if (began_before || goes_on) {
+      float* dst = a.part + (2 * chunk + (began_before ? 0 : 1)) * a.dim + col;
+      for (int e = 0; e < cols; ++e) gmem(dst)[e] = acc[e];
+    } else {
+      grad_write<GDT, C>(a, cur, col, cols, acc);
+    }
+    began_before = false;
+#pragma unroll
+    for (int e = 0; e < C; ++e) acc[e] = 0.0f;
+  };
+  for (int64_t p = p0; p < p1; p += U) {
+    int s[U];
+    float v[U][C];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t q = min(p + u, p1 - 1);
+      s[u] = gmem(a.slot)[q];
+      const int t = gmem(a.order)[q];
+      if (p + u >= p1 || static_cast<unsigned>(t) >= a.n) s[u] = -1;
+      const T* src = dout + (s[u] >= 0 ? t : 0) * a.dim;
+      if (s[u] < 0) {
+#pragma unroll
+        for (int e = 0; e < C; ++e) v[u][e] = 0.0f;
+      } else if (cols == C && a.vec) {
+        load_n<C>(src, v[u]);
+      } else {
+        for (int e = 0; e < C; ++e) v[u][e] = e < cols ? static_cast<float>(gmem(src)[e]) : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (s[u] < 0) continue;
+      if (s[u] != cur) {
+        flush(false);
+        cur = s[u];
+      }
+#pragma unroll
+      for (int e = 0; e < C; ++e) acc[e] += v[u][e];
+    }
+  }
+  flush(true);
+}
+
+// Sums of the runs that cross chunk edges.  The block of the chunk in which
+// such a run begins adds its pieces: four waves take every fourth piece, then
+// the four sums are joined in order.
+template <int GDT>
+__global__ __launch_bounds__(kEgThreads) void egrad_join_kernel(EmbedGradArgs a) {
+  __shared__ float red[4][256];
+  const int64_t chunk = blockIdx.x;
+  const int ct = blockIdx.y;
+  const int64_t end = (chunk + 1) * a.chunk;
+  if (end >= a.n) return;
+  const int seg = gmem(a.slot)[end - 1];
+  if (seg < 0 || gmem(a.slot)[end] != seg) return;
+  if (chunk > 0 && gmem(a.slot)[chunk * a.chunk - 1] == seg) return;   // it began earlier: not ours
+  const int lane = lane_id(), w = threadIdx.x >> 6;
+  // pieces: chunks behind this one that begin inside the run
+  int64_t last = chunk + 1;
+  while (true) {
+    const int64_t k = last + lane;
+    const uint64_t in = __ballot(k < a.chunks && gmem(a.slot)[min(k, static_cast<int64_t>(a.chunks) - 1) * a.chunk] == seg);
+    const int m = in == ~0ull ? 64 : __builtin_ctzll(~in);
+    last += m;
+    if (m < 64) break;
+  }
+  const int64_t col = static_cast<int64_t>(ct) * 256 + lane * 4;
+  const int cols = static_cast<int>(max<int64_t>(0, min<int64_t>(4, a.dim - col)));
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int64_t k = chunk + 1 + w; k < last; k += 4)
+    for (int e = 0; e < cols; ++e) acc[e] += gmem(a.part)[2 * k * a.dim + col + e];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) red[w][lane * 4 + e] = acc[e];
+  __syncthreads();
+  if (w == 0 && cols > 0) {
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int e = 0; e < cols; ++e) {
+      v[e] = gmem(a.part)[(2 * chunk + 1) * a.dim + col + e];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[e] += red[k][lane * 4 + e];
+    }
+    grad_write<GDT, 4>(a, seg, col, cols, v);
+  }
+}
+
+int log2_ceil(int64_t v, int most) {
+  int l = 0;
+  while (l < most && (int64_t{1} << l) < v) ++l;
+  return l;
+}
+
+}  // namespace
+
+hipError_t launch_embed(int table_dt, int out_dt, const EmbedArgs& a, hipStream_t stream) {
+  if (a.n == 0) return hipSuccess;
+  const int c = out_dt == kBF16 ? 8 : 4;
+  const int log_tpr = log2_ceil(a.vec ? (a.dim + c - 1) / c : a.dim, 8);
+  const int64_t rpb = 256 >> log_tpr;
+  const dim3 grid(static_cast<unsigned>((a.n + rpb - 1) / rpb));
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, log_tpr); };
+  if (table_dt == kBF16) {
+    if (out_dt == kBF16) go(embed_kernel<kBF16, kBF16>); else go(embed_kernel<kBF16, kF32>);
+  } else {
+    if (out_dt == kBF16) go(embed_kernel<kF32, kBF16>); else go(embed_kernel<kF32, kF32>);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_embed_plan(const PlanArgs& a, hipStream_t stream) {
+  if (a.n <= kPlanSmall) {
+    hipLaunchKernelGGL(plan_small_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
+    return hipGetLastError();
+  }
+  for (int pass = 0; pass < a.passes; ++pass) {
+    hipLaunchKernelGGL(plan_count_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a, pass);
+    hipLaunchKernelGGL(plan_scatter_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a, pass);
+  }
+  hipLaunchKernelGGL(plan_heads_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a);
+  hipLaunchKernelGGL(plan_rows_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_embed_grad(int dout_dt, int grad_dt, const EmbedGradArgs& a, hipStream_t stream) {
+  const int c = dout_dt == kBF16 ? 8 : 4;
+  const int64_t nch = (a.dim + c - 1) / c;
+  const int log_tpr = log2_ceil(nch, 8);
+  const int tpr = 1 << log_tpr;
+  const int col_tiles = static_cast<int>((nch + tpr - 1) / tpr);
+  const int sub = kEgThreads / tpr;
+  const int64_t sum_blocks = (static_cast<int64_t>(a.chunks) + sub - 1) / sub * col_tiles;
+  const int64_t zero_rows = a.form == kGradAdd ? 0 : a.form == kGradRows ? a.cap : a.vocab;
+  const int64_t blocks = sum_blocks + (zero_rows + kEgZeroRows - 1) / kEgZeroRows;
+  if (blocks == 0) return hipSuccess;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kEgThreads), 0, stream, a, log_tpr, col_tiles,
+                       sum_blocks);
+  };
+  if (dout_dt == kBF16) {
+    if (grad_dt == kBF16) go(egrad_kernel<kBF16, kBF16>); else go(egrad_kernel<kBF16, kF32>);
+  } else {
+    if (grad_dt == kBF16) go(egrad_kernel<kF32, kBF16>); else go(egrad_kernel<kF32, kF32>);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.chunks < 2) return e;
+  const dim3 jgrid(static_cast<unsigned>(a.chunks), static_cast<unsigned>((a.dim + 255) / 256));
+  if (grad_dt == kBF16)
+    hipLaunchKernelGGL(egrad_join_kernel<kBF16>, jgrid, dim3(kEgThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL(egrad_join_kernel<kF32>, jgrid, dim3(kEgThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace dmuon
