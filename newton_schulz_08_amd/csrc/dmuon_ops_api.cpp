@@ -201,10 +201,31 @@ int qk_buf(const dmuon_qk_shape& s, const char* name, const void* p, int64_t str
   return DMUON_OK;
 }
 
-// Blocks of the backward pass: each leaves one row of gain sums.
-int qk_grad_blocks(int64_t tokens) { return static_cast<int>(std::min<int64_t>(1024, (tokens + 3) / 4)); }
+// Blocks of the backward pass for one tensor: each leaves one row of gain
+// sums.  At least 32 heads a block, and no more than eight blocks a CU in all.
+int qk_grad_blocks(const dmuon_qk_shape& s, int heads) {
+  const int64_t want = (s.tokens * heads + 31) / 32, all = s.q_heads + s.k_heads;
+  return static_cast<int>(std::min<int64_t>(want, std::max<int64_t>(1, int64_t{2048} * heads / all)));
+}
 
-void fill_qk(const dmuon_qk_shape& s, QkArgs* a) {
+// Pairs that a lane holds: 16 bytes of each half.  By type and shape alone, so
+// that strides and alignment do not change the order of a sum.
+int qk_pairs(const dmuon_qk_shape& s) {
+  return s.dtype == DMUON_BF16 && s.head_dim % 16 == 0 && s.rot_dim % 16 == 0 ? 8 : 4;
+}
+// Those pairs can be loaded at once: whole, aligned runs in every row.
+bool qk_vec(const dmuon_qk_shape& s, std::initializer_list<const Buf*> bufs, std::initializer_list<const void*> gains) {
+  const int pairs = qk_pairs(s);
+  if (s.head_dim % (2 * pairs) || s.rot_dim % (2 * pairs)) return false;
+  const int64_t run = pairs * size_of(s.dtype), gain_run = std::min<int64_t>(16, pairs * size_of(s.weight_dtype));
+  for (const Buf* b : bufs)
+    if (!b->empty() && (!aligned(b->p, run) || (b->rows > 1 && b->pitch % run))) return false;
+  for (const void* w : gains)
+    if (w && !aligned(w, gain_run)) return false;
+  return true;
+}
+
+void fill_qk(const dmuon_qk_shape& s, const float* rope, QkArgs* a) {
   a->n = s.tokens;
   a->heads[0] = s.q_heads;
   a->heads[1] = s.k_heads;
@@ -215,16 +236,8 @@ void fill_qk(const dmuon_qk_shape& s, QkArgs* a) {
   a->eps = s.eps;
   a->offset = s.weight_offset;
   a->pos64 = s.pos_dtype == DMUON_I64;
-}
-// Four elements at a time: whole, aligned units in every row.
-bool qk_vec(const dmuon_qk_shape& s, std::initializer_list<const Buf*> bufs, std::initializer_list<const void*> gains) {
-  if (s.head_dim % 8 || s.rot_dim % 8) return false;
-  const int64_t unit = 4 * size_of(s.dtype);
-  for (const Buf* b : bufs)
-    if (!b->empty() && (!aligned(b->p, unit) || (b->rows > 1 && b->pitch % unit))) return false;
-  for (const void* w : gains)
-    if (w && !aligned(w, 4 * size_of(s.weight_dtype))) return false;
-  return true;
+  a->pairs = qk_pairs(s);
+  a->rope_vec = aligned(rope, 16) && s.rot_dim % 8 == 0;
 }
 
 }  // namespace
@@ -528,7 +541,7 @@ int dmuon_qk_norm_rope_forward(const dmuon_qk_shape* shape, const void* q, int64
     DMUON_TRY(check_device(hip_stream, &capturing));
     if (s.tokens == 0) return DMUON_OK;
     QkArgs a{};
-    fill_qk(s, &a);
+    fill_qk(s, rope, &a);
     a.x[0] = q;
     a.x[1] = k;
     a.x_stride[0] = q_stride;
@@ -553,7 +566,8 @@ int dmuon_qk_norm_rope_backward_workspace_bytes(const dmuon_qk_shape* shape, siz
   return guarded([&]() -> int {
     if (!bytes_out) return invalid("bytes_out is NULL");
     DMUON_TRY(check_qk(shape));
-    *bytes_out = align_up(sizeof(float) * 2 * shape->head_dim * static_cast<size_t>(qk_grad_blocks(shape->tokens)));
+    const size_t blocks = qk_grad_blocks(*shape, shape->q_heads) + qk_grad_blocks(*shape, shape->k_heads);
+    *bytes_out = align_up(sizeof(float) * shape->head_dim * blocks);
     return DMUON_OK;
   });
 }
@@ -591,7 +605,7 @@ int dmuon_qk_norm_rope_backward(const dmuon_qk_shape* shape, const void* dq_out,
     bool capturing = false;
     DMUON_TRY(check_device(hip_stream, &capturing));
     QkArgs a{};
-    fill_qk(s, &a);
+    fill_qk(s, rope, &a);
     a.x[0] = q;
     a.x[1] = k;
     a.x_stride[0] = q_stride;
@@ -610,7 +624,8 @@ int dmuon_qk_norm_rope_backward(const dmuon_qk_shape* shape, const void* dq_out,
     a.dw[1] = dk_weight;
     a.positions = positions;
     a.rope = rope;
-    a.blocks = qk_grad_blocks(s.tokens);
+    a.blocks[0] = qk_grad_blocks(s, s.q_heads);
+    a.blocks[1] = qk_grad_blocks(s, s.k_heads);
     a.part = need ? static_cast<float*>(workspace) : nullptr;
     a.vec = qk_vec(s, {&b[0], &b[1], &b[2], &b[3], &b[4], &b[5]}, {q_weight, k_weight});
     const double elems = static_cast<double>(s.tokens) * (s.q_heads + s.k_heads) * s.head_dim;

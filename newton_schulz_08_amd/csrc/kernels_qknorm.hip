@@ -15,10 +15,14 @@
 // `rot` stay.  A negative position marks a padding token: zeros, and no part
 // in dw.  A position behind the table gives NaN.
 //
-// A lane holds four pairs of one head (a "unit" of eight elements), so both
-// halves of a rotation meet in one lane; the smallest power of two of lanes
-// that covers D holds a head, and a wave works on 64 / that many heads of one
-// token at once.  The cosines and sines are read once per token.
+// A lane holds P pairs of one head, so both halves of a rotation meet in one
+// lane; the smallest power of two of lanes that covers D holds a head.  P = 8
+// makes every access of a bf16 head 16 bytes wide; P = 4 does so for fp32 and
+// serves bf16 heads whose halves are no multiple of 8.  The queries and the
+// keys are worked on by different blocks (one gain, one set of gain sums in
+// registers); a wave takes as many heads of a token at once as it has groups
+// of lanes, or several tokens where a token has fewer heads, and keeps the
+// token's cosines and sines over all of its heads.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -34,11 +38,11 @@ constexpr int kQkWaves = kQkThreads / 64;
 // The query's or the key's entry: a select, where an index would go through memory.
 template <typename V> __device__ __forceinline__ V pick(const V (&v)[2], int which) { return which ? v[1] : v[0]; }
 
-// Elements of pair p; the second is D when there is none.
+// Elements of pair p (the second is >= D when there is none).
 __device__ __forceinline__ void pair_elems(const QkArgs& a, int p, int* e0, int* e1) {
   const int half = a.rot / 2;
   if (a.interleaved || p >= half) {
-    *e0 = 2 * p;   // behind the rotated part both layouts count on: rot + 2 (p - half) = 2 p
+    *e0 = 2 * p;   // behind the rotated part: rot + 2 (p - half) = 2 p
     *e1 = 2 * p + 1;
   } else {
     *e0 = p;
@@ -46,46 +50,53 @@ __device__ __forceinline__ void pair_elems(const QkArgs& a, int p, int* e0, int*
   }
 }
 
-template <int DT, bool VEC>
+// A lane's P pairs (a[i], b[i]), the t-th such run of the head.  VEC: the run
+// is either two runs of P elements half a rotation apart, or 2 P consecutive ones.
+template <int DT, int P, bool VEC>
 __device__ __forceinline__ void load_unit(const QkArgs& q, const typename OpElem<DT>::T* p, int t, float* a, float* b) {
   if constexpr (VEC) {
-    float lo[4], hi[4];
+    float lo[P], hi[P];
     const int half = q.rot / 2;
-    const bool split = !q.interleaved && 4 * t < half;
-    load_n<4>(p + (split ? 4 * t : 8 * t), lo);
-    load_n<4>(p + (split ? half + 4 * t : 8 * t + 4), hi);
+    const bool split = !q.interleaved && P * t < half;
+    load_n<P>(p + (split ? P * t : 2 * P * t), lo);
+    load_n<P>(p + (split ? half + P * t : 2 * P * t + P), hi);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = i < 2 ? lo[2 * i] : hi[2 * i - 4], y = i < 2 ? lo[2 * i + 1] : hi[2 * i - 3];
+    for (int i = 0; i < P; ++i) {
+      const float x = i < P / 2 ? lo[2 * i] : hi[2 * i - P], y = i < P / 2 ? lo[2 * i + 1] : hi[2 * i + 1 - P];
       a[i] = split ? lo[i] : x;
       b[i] = split ? hi[i] : y;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < P; ++i) {
       int e0, e1;
-      pair_elems(q, 4 * t + i, &e0, &e1);
+      pair_elems(q, P * t + i, &e0, &e1);
       a[i] = e0 < q.dim ? static_cast<float>(gmem(p)[e0]) : 0.0f;
       b[i] = e1 < q.dim ? static_cast<float>(gmem(p)[e1]) : 0.0f;
     }
   }
 }
 
-template <int DT, bool VEC>
+template <int DT, int P, bool VEC>
 __device__ __forceinline__ void store_unit(const QkArgs& q, typename OpElem<DT>::T* p, int t, const float* a, const float* b) {
   using T = typename OpElem<DT>::T;
   if constexpr (VEC) {
     const int half = q.rot / 2;
-    const bool split = !q.interleaved && 4 * t < half;
-    const float lo[4] = {a[0], split ? a[1] : b[0], split ? a[2] : a[1], split ? a[3] : b[1]};
-    const float hi[4] = {split ? b[0] : a[2], split ? b[1] : b[2], split ? b[2] : a[3], b[3]};
-    store_n<4>(p + (split ? 4 * t : 8 * t), lo);
-    store_n<4>(p + (split ? half + 4 * t : 8 * t + 4), hi);
+    const bool split = !q.interleaved && P * t < half;
+    float lo[P], hi[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int l = i / 2, h = (P + i) / 2;   // pair that the i-th element of each run belongs to, side by side
+      lo[i] = split ? a[i] : i % 2 ? b[l] : a[l];
+      hi[i] = split ? b[i] : i % 2 ? b[h] : a[h];
+    }
+    store_n<P>(p + (split ? P * t : 2 * P * t), lo);
+    store_n<P>(p + (split ? half + P * t : 2 * P * t + P), hi);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < P; ++i) {
       int e0, e1;
-      pair_elems(q, 4 * t + i, &e0, &e1);
+      pair_elems(q, P * t + i, &e0, &e1);
       if (e0 < q.dim) gmem(p)[e0] = static_cast<T>(a[i]);
       if (e1 < q.dim) gmem(p)[e1] = static_cast<T>(b[i]);
     }
@@ -97,237 +108,305 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
   return v;
 }
 
-// Cosines and sines of a lane's four pairs at the token's position, and how
-// the token is treated: 0 padding, 1 rotated, 2 behind the table.
+// Cosines and sines of a lane's pairs at the token's position, and how the
+// token is treated: 0 padding, 1 rotated, 2 behind the table.
+template <int P, bool VEC>
 __device__ __forceinline__ int token_angles(const QkArgs& a, int64_t token, int t, float* c, float* s) {
-  int64_t pos = 0;
-  if (a.rot > 0) pos = load_index(a.positions, token, a.pos64);
-  const int kind = pos < 0 ? 0 : a.rot > 0 && pos >= a.max_pos ? 2 : 1;
+  if (a.rot == 0) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      c[i] = 1.0f;
+      s[i] = 0.0f;
+    }
+    return 1;
+  }
+  const int64_t pos = load_index(a.positions, token, a.pos64);
+  const int kind = pos < 0 ? 0 : pos >= a.max_pos ? 2 : 1;
   const int half = a.rot / 2;
   const float* row = a.rope + (kind == 1 ? pos : 0) * a.rot;
+  if (VEC && a.rope_vec) {   // a run is turned or not as a whole
+    const bool turn = kind == 1 && P * t < half;
+    if (turn) {
+      load_n<P>(row + P * t, c);
+      load_n<P>(row + half + P * t, s);
+    }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int p = 4 * t + i;
-    const bool turn = kind == 1 && p < half;
-    c[i] = turn ? gmem(row)[p] : 1.0f;
-    s[i] = turn ? gmem(row)[half + p] : 0.0f;
+    for (int i = 0; i < P; ++i) {
+      c[i] = turn ? c[i] : 1.0f;
+      s[i] = turn ? s[i] : 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int p = P * t + i;
+      const bool turn = kind == 1 && p < half;
+      c[i] = turn ? gmem(row)[p] : 1.0f;
+      s[i] = turn ? gmem(row)[half + p] : 0.0f;
+    }
   }
   return kind;
 }
 
-template <int WDT, bool VEC>
+template <int WDT, int P, bool VEC>
 __device__ __forceinline__ void load_gain(const QkArgs& q, int which, int t, float* wa, float* wb) {
   using W = typename OpElem<WDT>::T;
   const W* w = static_cast<const W*>(pick(q.w, which));
   if (!w) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wa[i] = wb[i] = 1.0f;
+    for (int i = 0; i < P; ++i) wa[i] = wb[i] = 1.0f;
     return;
   }
-  load_unit<WDT, VEC>(q, w, t, wa, wb);
+  load_unit<WDT, P, VEC>(q, w, t, wa, wb);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < P; ++i) {
     wa[i] += q.offset;
     wb[i] += q.offset;
   }
 }
 
-template <int DT, int WDT, bool VEC>
-__global__ __launch_bounds__(kQkThreads) void qk_norm_kernel(QkArgs a, int log_lanes, int heads_per_item) {
+// What a wave's lanes do: lane group `head` of `heads_at_once`, token `tok` of
+// the wave's tokens, t-th run of the head.
+struct Place {
+  int which, t, head, tok, heads_at_once, tokens_at_once;
+  int64_t block;   // among the blocks of its tensor
+  bool any;        // the lane has elements
+};
+template <int P>
+__device__ __forceinline__ Place place(const QkArgs& a, int log_lanes, int blocks_q) {
+  Place p;
+  const int lane = threadIdx.x & 63;
+  p.which = static_cast<int>(blockIdx.x) >= blocks_q ? 1 : 0;
+  p.block = static_cast<int64_t>(blockIdx.x) - (p.which ? blocks_q : 0);
+  p.t = lane & ((1 << log_lanes) - 1);
+  p.any = 2 * P * p.t < a.dim;
+  const int group = lane >> log_lanes, log_groups = 6 - log_lanes;
+  const int lh = min(pick(a.log_heads, p.which), log_groups);
+  p.heads_at_once = 1 << lh;
+  p.tokens_at_once = 1 << (log_groups - lh);
+  p.head = group & (p.heads_at_once - 1);
+  p.tok = group >> lh;
+  return p;
+}
+
+// blockIdx.y takes `passes` runs of heads of a token.
+template <int DT, int WDT, int P, bool VEC>
+__global__ __launch_bounds__(kQkThreads) void qk_norm_kernel(QkArgs a, int log_lanes, int blocks_q, int passes) {
   using T = typename OpElem<DT>::T;
-  const int lanes = 1 << log_lanes, lane = threadIdx.x & 63;
-  const int t = lane & (lanes - 1), sub = lane >> log_lanes, per = 64 >> log_lanes;
-  const int64_t token = static_cast<int64_t>(blockIdx.x) * kQkWaves + (threadIdx.x >> 6);
-  if (token >= a.n) return;
-  const bool any = 8 * t < a.dim;
-  float c[4], s[4];
-  const int kind = token_angles(a, token, any ? t : 0, c, s);
-  const int all = a.heads[0] + a.heads[1];
-  const int h0 = static_cast<int>(blockIdx.y) * heads_per_item;
-  const int h1 = min(all, h0 + heads_per_item);
-  for (int hb = h0; hb < h1; hb += per) {
-    const int h = hb + sub;
-    const bool on = any && h < h1;
-    const int which = h >= a.heads[0] ? 1 : 0;
-    const int64_t head = which ? h - a.heads[0] : h;
-    float x[4] = {}, y[4] = {};
-    if (on && kind != 0)
-      load_unit<DT, VEC>(a, static_cast<const T*>(pick(a.x, which)) + token * pick(a.x_stride, which) + head * a.dim, t, x, y);
+  const Place p = place<P>(a, log_lanes, blocks_q);
+  const int heads = pick(a.heads, p.which);
+  const int64_t token = (p.block * kQkWaves + (threadIdx.x >> 6)) * p.tokens_at_once + p.tok;
+  const int h0 = static_cast<int>(blockIdx.y) * passes * p.heads_at_once;
+  if (h0 >= heads || (p.block * kQkWaves + (threadIdx.x >> 6)) * p.tokens_at_once >= a.n) return;
+  const bool here = p.any && token < a.n;
+  float c[P], s[P], wa[P], wb[P];
+  const int kind = token_angles<P, VEC>(a, min(token, a.n - 1), p.any ? p.t : 0, c, s);
+  load_gain<WDT, P, VEC>(a, p.which, p.any ? p.t : 0, wa, wb);
+  const T* src = static_cast<const T*>(pick(a.x, p.which)) + token * pick(a.x_stride, p.which);
+  T* dst = static_cast<T*>(pick(a.out, p.which)) + token * pick(a.out_stride, p.which);
+  for (int k = 0; k < passes; ++k) {
+    const int h = h0 + k * p.heads_at_once + p.head;
+    const bool on = here && h < heads;
+    float x[P] = {}, y[P] = {};
+    if (on && kind != 0) load_unit<DT, P, VEC>(a, src + static_cast<int64_t>(h) * a.dim, p.t, x, y);
     float ss = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ss += x[i] * x[i] + y[i] * y[i];
-    ss = group_sum(ss, lanes);
+    for (int i = 0; i < P; ++i) ss += x[i] * x[i] + y[i] * y[i];
+    ss = group_sum(ss, 1 << log_lanes);
     float r = 1.0f / sqrtf(ss / static_cast<float>(a.dim) + a.eps);
     if (kind == 2) r = NAN;
     if (!on) continue;
-    float wa[4], wb[4];
-    load_gain<WDT, VEC>(a, which, t, wa, wb);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < P; ++i) {
       const float na = x[i] * r * wa[i], nb = y[i] * r * wb[i];
       x[i] = kind == 0 ? 0.0f : na * c[i] - nb * s[i];
       y[i] = kind == 0 ? 0.0f : nb * c[i] + na * s[i];
     }
-    store_unit<DT, VEC>(a, static_cast<T*>(pick(a.out, which)) + token * pick(a.out_stride, which) + head * a.dim, t, x, y);
+    store_unit<DT, P, VEC>(a, dst + static_cast<int64_t>(h) * a.dim, p.t, x, y);
   }
 }
 
-template <int DT, int WDT, bool VEC>
+// The blocks of a tensor stride over its tokens and keep the gain's sums in
+// registers; each leaves one row of sums in `part`.
+template <int DT, int WDT, int P, bool VEC>
 __global__ __launch_bounds__(kQkThreads) void qk_norm_grad_kernel(QkArgs a, int log_lanes) {
   using T = typename OpElem<DT>::T;
-  extern __shared__ float sum[];   // kQkWaves x 2 x dim
-  const int lanes = 1 << log_lanes, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int t = lane & (lanes - 1), sub = lane >> log_lanes, per = 64 >> log_lanes;
-  const bool any = 8 * t < a.dim;
-  const int all = a.heads[0] + a.heads[1];
-  float dwa[2][4] = {}, dwb[2][4] = {};
-  const int64_t waves = static_cast<int64_t>(gridDim.x) * kQkWaves;
-  for (int64_t token = static_cast<int64_t>(blockIdx.x) * kQkWaves + wave; token < a.n; token += waves) {
-    float c[4], s[4];
-    const int kind = token_angles(a, token, any ? t : 0, c, s);
-    for (int hb = 0; hb < all; hb += per) {
-      const int h = hb + sub;
-      const bool on = any && h < all;
-      const int which = h >= a.heads[0] ? 1 : 0;
-      const int64_t head = which ? h - a.heads[0] : h;
-      float x[4] = {}, y[4] = {}, u[4] = {}, v[4] = {};
+  extern __shared__ float sum[];   // kQkWaves x dim
+  const int lanes = 1 << log_lanes, wave = threadIdx.x >> 6;
+  const Place p = place<P>(a, log_lanes, a.blocks[0]);
+  const int heads = pick(a.heads, p.which);
+  float dwa[P] = {}, dwb[P] = {}, wa[P], wb[P];
+  load_gain<WDT, P, VEC>(a, p.which, p.any ? p.t : 0, wa, wb);
+  const float inv_dim = 1.0f / static_cast<float>(a.dim);
+  const int64_t step = static_cast<int64_t>(pick(a.blocks, p.which)) * kQkWaves * p.tokens_at_once;
+  for (int64_t t0 = (p.block * kQkWaves + wave) * p.tokens_at_once; t0 < a.n; t0 += step) {
+    const int64_t token = t0 + p.tok;
+    const bool here = p.any && token < a.n;
+    float c[P], s[P];
+    const int kind = token_angles<P, VEC>(a, min(token, a.n - 1), p.any ? p.t : 0, c, s);
+    const T* src = static_cast<const T*>(pick(a.x, p.which)) + token * pick(a.x_stride, p.which);
+    const T* dsrc = static_cast<const T*>(pick(a.dy, p.which)) + token * pick(a.dy_stride, p.which);
+    T* dst = static_cast<T*>(pick(a.out, p.which)) + token * pick(a.out_stride, p.which);
+    for (int h = p.head; h - p.head < heads; h += p.heads_at_once) {
+      const bool on = here && h < heads;
+      float x[P] = {}, y[P] = {}, u[P] = {}, v[P] = {};
       if (on && kind != 0) {
-        load_unit<DT, VEC>(a, static_cast<const T*>(pick(a.x, which)) + token * pick(a.x_stride, which) + head * a.dim, t, x, y);
-        load_unit<DT, VEC>(a, static_cast<const T*>(pick(a.dy, which)) + token * pick(a.dy_stride, which) + head * a.dim, t, u, v);
+        load_unit<DT, P, VEC>(a, src + static_cast<int64_t>(h) * a.dim, p.t, x, y);
+        load_unit<DT, P, VEC>(a, dsrc + static_cast<int64_t>(h) * a.dim, p.t, u, v);
       }
-      float wa[4] = {}, wb[4] = {};
-      if (on) load_gain<WDT, VEC>(a, which, t, wa, wb);
       float ss = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ss += x[i] * x[i] + y[i] * y[i];
+      for (int i = 0; i < P; ++i) ss += x[i] * x[i] + y[i] * y[i];
       ss = group_sum(ss, lanes);
       float r = 1.0f / sqrtf(ss / static_cast<float>(a.dim) + a.eps);
       r = kind == 2 ? NAN : kind == 0 ? 0.0f : r;
       float dot = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < P; ++i) {
         const float da = u[i] * c[i] + v[i] * s[i], db = v[i] * c[i] - u[i] * s[i];
         x[i] *= r;
         y[i] *= r;
         const float ga = da * x[i], gb = db * y[i];
-        dwa[0][i] += on && !which ? ga : 0.0f;
-        dwb[0][i] += on && !which ? gb : 0.0f;
-        dwa[1][i] += on && which ? ga : 0.0f;
-        dwb[1][i] += on && which ? gb : 0.0f;
+        dwa[i] += on ? ga : 0.0f;
+        dwb[i] += on ? gb : 0.0f;
         dot += ga * wa[i] + gb * wb[i];
         u[i] = da * wa[i];
         v[i] = db * wb[i];
       }
-      dot = group_sum(dot, lanes) / static_cast<float>(a.dim);
+      dot = group_sum(dot, lanes) * inv_dim;
       if (!on) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < P; ++i) {
         u[i] = kind == 0 ? 0.0f : r * (u[i] - x[i] * dot);
         v[i] = kind == 0 ? 0.0f : r * (v[i] - y[i] * dot);
       }
-      store_unit<DT, VEC>(a, static_cast<T*>(pick(a.out, which)) + token * pick(a.out_stride, which) + head * a.dim, t, u, v);
+      store_unit<DT, P, VEC>(a, dst + static_cast<int64_t>(h) * a.dim, p.t, u, v);
     }
   }
   if (!a.part) return;
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      for (int o = 32; o >= lanes; o >>= 1) {
-        dwa[k][i] += __shfl_xor(dwa[k][i], o, 64);
-        dwb[k][i] += __shfl_xor(dwb[k][i], o, 64);
-      }
-      if (sub == 0) {
-        int e0, e1;
-        pair_elems(a, 4 * t + i, &e0, &e1);
-        if (e0 < a.dim) sum[(wave * 2 + k) * a.dim + e0] = dwa[k][i];
-        if (e1 < a.dim) sum[(wave * 2 + k) * a.dim + e1] = dwb[k][i];
-      }
+  for (int i = 0; i < P; ++i) {
+    for (int o = 32; o >= lanes; o >>= 1) {
+      dwa[i] += __shfl_xor(dwa[i], o, 64);
+      dwb[i] += __shfl_xor(dwb[i], o, 64);
     }
+    if ((threadIdx.x & 63) < lanes) {
+      int e0, e1;
+      pair_elems(a, P * p.t + i, &e0, &e1);
+      if (e0 < a.dim) sum[wave * a.dim + e0] = dwa[i];
+      if (e1 < a.dim) sum[wave * a.dim + e1] = dwb[i];
+    }
+  }
   __syncthreads();
-  for (int e = threadIdx.x; e < 2 * a.dim; e += kQkThreads) {
+  for (int e = threadIdx.x; e < a.dim; e += kQkThreads) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kQkWaves; ++w) v += sum[w * 2 * a.dim + e];
-    gmem(a.part)[static_cast<int64_t>(blockIdx.x) * 2 * a.dim + e] = v;
+    for (int w = 0; w < kQkWaves; ++w) v += sum[w * a.dim + e];
+    gmem(a.part)[static_cast<int64_t>(blockIdx.x) * a.dim + e] = v;
   }
 }
 
-// dw = sum of the blocks' parts, in a fixed order.
+// dw = sum of the blocks' rows, in a fixed order: 16 columns a block, every
+// 64th row to one of 64 threads per column, then a tree.
+constexpr int kGainThreads = 1024;
 template <int WDT>
-__global__ __launch_bounds__(kQkThreads) void qk_gain_kernel(QkArgs a) {
+__global__ __launch_bounds__(kGainThreads) void qk_gain_kernel(QkArgs a) {
   using W = typename OpElem<WDT>::T;
-  __shared__ float red[kQkWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int e = blockIdx.x * 64 + lane;
+  __shared__ float red[64][17];
+  const int which = blockIdx.y;
+  W* dw = static_cast<W*>(pick(a.dw, which));
+  if (!dw) return;
+  const int col = threadIdx.x & 15, row = threadIdx.x >> 4, e = blockIdx.x * 16 + col;
+  const float* part = a.part + static_cast<int64_t>(which ? a.blocks[0] : 0) * a.dim;
+  const int rows = pick(a.blocks, which);
   float v = 0.0f;
-  if (e < 2 * a.dim)
-    for (int b = wave; b < a.blocks; b += kQkWaves) v += gmem(a.part)[static_cast<int64_t>(b) * 2 * a.dim + e];
-  red[wave][lane] = v;
-  __syncthreads();
-  if (wave == 0 && e < 2 * a.dim) {
-    float r = 0.0f;
+  if (e < a.dim) {
+    for (int b0 = row; b0 < rows; b0 += 64 * 8) {
+      float w[8];
 #pragma unroll
-    for (int w = 0; w < kQkWaves; ++w) r += red[w][lane];
-    const int which = e >= a.dim ? 1 : 0;
-    W* dw = static_cast<W*>(a.dw[which]);
-    if (dw) gmem(dw)[e - which * a.dim] = static_cast<W>(r);
+      for (int k = 0; k < 8; ++k) w[k] = b0 + 64 * k < rows ? gmem(part)[static_cast<int64_t>(b0 + 64 * k) * a.dim + e] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v += w[k];
+    }
   }
+  red[row][col] = v;
+  __syncthreads();
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    if (row < o) red[row][col] += red[row + o][col];
+    __syncthreads();
+  }
+  if (row == 0 && e < a.dim) gmem(dw)[e] = static_cast<W>(red[0][col]);
 }
 
-int log_lanes_of(int dim) {
+int log2_ceil(int v) {
   int l = 0;
-  while ((8 << l) < dim) ++l;
+  while ((1 << l) < v) ++l;
   return l;
 }
 
-template <typename F> void by_types(int dt, int w_dt, int vec, F&& f) {
-  auto w = [&](auto d) {
-    constexpr int D = decltype(d)::value;
-    if (w_dt == kBF16) {
-      if (vec) f(std::integral_constant<int, D>{}, std::integral_constant<int, kBF16>{}, std::true_type{});
-      else f(std::integral_constant<int, D>{}, std::integral_constant<int, kBF16>{}, std::false_type{});
-    } else {
-      if (vec) f(std::integral_constant<int, D>{}, std::integral_constant<int, kF32>{}, std::true_type{});
-      else f(std::integral_constant<int, D>{}, std::integral_constant<int, kF32>{}, std::false_type{});
-    }
+// f(element type, gain type, pairs per lane, vector path)
+template <typename F> void by_types(int dt, int w_dt, const QkArgs& a, F&& f) {
+  using B = std::integral_constant<int, kBF16>;
+  using S = std::integral_constant<int, kF32>;
+  using P4 = std::integral_constant<int, 4>;
+  using P8 = std::integral_constant<int, 8>;
+  auto v = [&](auto d, auto w, auto p) {
+    if (a.vec) f(d, w, p, std::true_type{});
+    else f(d, w, p, std::false_type{});
   };
-  if (dt == kBF16) w(std::integral_constant<int, kBF16>{});
-  else w(std::integral_constant<int, kF32>{});
+  auto w = [&](auto d, auto p) {
+    if (w_dt == kBF16) v(d, B{}, p);
+    else v(d, S{}, p);
+  };
+  if (dt == kF32) w(S{}, P4{});
+  else if (a.pairs == 8) w(B{}, P8{});
+  else w(B{}, P4{});
 }
 
 }  // namespace
 
-hipError_t launch_qk_norm(int dt, int w_dt, const QkArgs& a, hipStream_t stream) {
-  if (a.n == 0) return hipSuccess;
-  const int ll = log_lanes_of(a.dim), per = 64 >> ll;
-  const int all = a.heads[0] + a.heads[1];
-  // few tokens: one pass of heads per wave; many: up to eight passes share a token's angles
-  const int passes = (all + per - 1) / per;
-  const int item_passes = a.n >= 4096 ? (passes < 8 ? passes : 8) : 1;
-  const int hp = item_passes * per;
-  const dim3 grid(static_cast<unsigned>((a.n + kQkWaves - 1) / kQkWaves), static_cast<unsigned>((all + hp - 1) / hp));
-  by_types(dt, w_dt, a.vec, [&](auto d, auto w, auto v) {
-    hipLaunchKernelGGL((qk_norm_kernel<decltype(d)::value, decltype(w)::value, decltype(v)::value>), grid,
-                       dim3(kQkThreads), 0, stream, a, ll, hp);
+hipError_t launch_qk_norm(int dt, int w_dt, const QkArgs& in, hipStream_t stream) {
+  if (in.n == 0) return hipSuccess;
+  QkArgs a = in;
+  const int pairs = a.pairs;
+  const int ll = log2_ceil((a.dim + 2 * pairs - 1) / (2 * pairs)), groups = 6 - ll;
+  // few tokens: every wave one run of heads; many: up to four share a token's angles
+  int blocks[2], most = 1;
+  const int share = a.n >= 4096 ? 4 : 1;
+  for (int k = 0; k < 2; ++k) {
+    a.log_heads[k] = log2_ceil(a.heads[k]);
+    const int lh = a.log_heads[k] < groups ? a.log_heads[k] : groups;
+    const int64_t tokens = int64_t{kQkWaves} << (groups - lh);
+    blocks[k] = a.heads[k] ? static_cast<int>((a.n + tokens - 1) / tokens) : 0;
+    const int runs = (a.heads[k] + (1 << lh) - 1) >> lh;
+    most = runs > most ? runs : most;
+  }
+  const int passes = most < share ? most : share;
+  const dim3 grid(static_cast<unsigned>(blocks[0] + blocks[1]), static_cast<unsigned>((most + passes - 1) / passes));
+  by_types(dt, w_dt, a, [&](auto d, auto w, auto p, auto v) {
+    hipLaunchKernelGGL((qk_norm_kernel<decltype(d)::value, decltype(w)::value, decltype(p)::value, decltype(v)::value>),
+                       grid, dim3(kQkThreads), 0, stream, a, ll, blocks[0], passes);
   });
   return hipGetLastError();
 }
 
-hipError_t launch_qk_norm_grad(int dt, int w_dt, const QkArgs& a, hipStream_t stream) {
-  const int ll = log_lanes_of(a.dim);
-  if (a.n > 0) {
-    by_types(dt, w_dt, a.vec, [&](auto d, auto w, auto v) {
-      hipLaunchKernelGGL((qk_norm_grad_kernel<decltype(d)::value, decltype(w)::value, decltype(v)::value>),
-                         dim3(a.blocks), dim3(kQkThreads), sizeof(float) * kQkWaves * 2 * a.dim, stream, a, ll);
+hipError_t launch_qk_norm_grad(int dt, int w_dt, const QkArgs& in, hipStream_t stream) {
+  QkArgs a = in;
+  const int pairs = a.pairs;
+  const int ll = log2_ceil((a.dim + 2 * pairs - 1) / (2 * pairs));
+  for (int k = 0; k < 2; ++k) a.log_heads[k] = log2_ceil(a.heads[k]);
+  if (a.blocks[0] + a.blocks[1] > 0) {
+    by_types(dt, w_dt, a, [&](auto d, auto w, auto p, auto v) {
+      hipLaunchKernelGGL((qk_norm_grad_kernel<decltype(d)::value, decltype(w)::value, decltype(p)::value, decltype(v)::value>),
+                         dim3(a.blocks[0] + a.blocks[1]), dim3(kQkThreads), sizeof(float) * kQkWaves * a.dim, stream, a, ll);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (!a.dw[0] && !a.dw[1]) return hipSuccess;
-  const dim3 grid((2 * a.dim + 63) / 64);
-  if (w_dt == kBF16) hipLaunchKernelGGL(qk_gain_kernel<kBF16>, grid, dim3(kQkThreads), 0, stream, a);
-  else hipLaunchKernelGGL(qk_gain_kernel<kF32>, grid, dim3(kQkThreads), 0, stream, a);
+  const dim3 grid((a.dim + 15) / 16, 2);
+  if (w_dt == kBF16) hipLaunchKernelGGL(qk_gain_kernel<kBF16>, grid, dim3(kGainThreads), 0, stream, a);
+  else hipLaunchKernelGGL(qk_gain_kernel<kF32>, grid, dim3(kGainThreads), 0, stream, a);
   return hipGetLastError();
 }
 

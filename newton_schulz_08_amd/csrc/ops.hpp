@@ -122,12 +122,15 @@ struct QkArgs {
   int heads[2];
   const void* positions;
   const float* rope;       // max_pos x rot: cosines, then sines
-  float* part;             // backward: blocks x 2 x head_dim
+  float* part;             // backward: (blocks[0] + blocks[1]) x head_dim
   int64_t n, max_pos;
   int dim, rot, interleaved, pos64;
   float eps, offset;
-  int vec;
-  int blocks;
+  int pairs;               // pairs of a head that a lane holds: 8 or 4, by type and shape alone
+  int vec;                 // ... loaded at once (else one element at a time)
+  int rope_vec;            // the table's rows hold aligned runs of four
+  int blocks[2];           // backward: blocks of each tensor
+  int log_heads[2];        // set by the launch: log2 of the heads, rounded up
 };
 hipError_t launch_qk_norm(int dt, int w_dt, const QkArgs& a, hipStream_t stream);
 hipError_t launch_qk_norm_grad(int dt, int w_dt, const QkArgs& a, hipStream_t stream);

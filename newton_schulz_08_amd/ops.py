@@ -373,8 +373,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tens
     return outs[0], outs[1]
 
 
-def qk_norm_rope_grad_workspace_bytes(tokens: int, head_dim: int) -> int:
-    s = _lib.QkShape(tokens=tokens, q_heads=1, head_dim=head_dim)
+def qk_norm_rope_grad_workspace_bytes(tokens: int, q_heads: int, k_heads: int, head_dim: int) -> int:
+    s = _lib.QkShape(tokens=tokens, q_heads=q_heads, k_heads=k_heads, head_dim=head_dim)
     return _query("dmuon_qk_norm_rope_backward_workspace_bytes", s)
 
 

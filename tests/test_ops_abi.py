@@ -170,7 +170,7 @@ def test_qk_backward(lib):
     accepted(f, dict(QKG, dqw=0, dkw=0, ws=0, bytes=0))                      # no sums, no workspace
     accepted(f, dict(QKG, dqw=0))
     refused(f, QKG, [(dict(shape=qk_shape(**s)), st) for s, st in SHAPES])
-    need = nsa.qk_norm_rope_grad_workspace_bytes(6, 16)
+    need = nsa.qk_norm_rope_grad_workspace_bytes(6, 4, 2, 16)
     refused(f, QKG, [
         (dict(dqo=0), BAD), (dict(dko=0), BAD), (dict(q=0), BAD), (dict(dq=0), BAD), (dict(dk=0), BAD), (dict(ws=0), WS),
         (dict(bytes=need - 1), WS), (dict(ws=addr(10) + 128), WS), (dict(dqw=addr(9)), BAD), (dict(dqw=addr(1)), BAD),
