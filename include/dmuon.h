@@ -499,7 +499,7 @@ typedef struct {
  *              t * stride: a packed projection's output is read in place.
  * q_weight, k_weight : device, D entries of weight_dtype, or NULL for no gain.
  * positions  : device, tokens entries.  A negative position marks a padding
- *              token: its outputs are zero and its inputs are not read.  A
+ *              token: its outputs are zero whatever its inputs hold.  A
  *              position >= max_pos gives NaN.  NULL when rot_dim is 0.
  * rope       : device float32, max_pos x rot_dim: a position's rot_dim / 2
  *              cosines, then its sines.  NULL when rot_dim is 0.

@@ -51,31 +51,53 @@ __device__ __forceinline__ void pair_elems(const QkArgs& a, int p, int* e0, int*
 }
 
 // A lane's P pairs (a[i], b[i]), the t-th such run of the head.  VEC: the run
-// is either two runs of P elements half a rotation apart, or 2 P consecutive ones.
-template <int DT, int P, bool VEC>
-__device__ __forceinline__ void load_unit(const QkArgs& q, const typename OpElem<DT>::T* p, int t, float* a, float* b) {
-  if constexpr (VEC) {
-    float lo[P], hi[P];
+// is either two runs of P elements half a rotation apart, or 2 P consecutive
+// ones; `Raw` keeps it as loaded, so that a load can run ahead of its use.
+template <int DT, int P, bool VEC> struct Raw {
+  using T = typename OpElem<DT>::T;
+  using V = T __attribute__((ext_vector_type(P)));
+  V lo, hi;
+  __device__ __forceinline__ void load(const QkArgs& q, const T* p, int t) {
     const int half = q.rot / 2;
     const bool split = !q.interleaved && P * t < half;
-    load_n<P>(p + (split ? P * t : 2 * P * t), lo);
-    load_n<P>(p + (split ? half + P * t : 2 * P * t + P), hi);
+    lo = *reinterpret_cast<gptr<const V>>(gmem(p + (split ? P * t : 2 * P * t)));
+    hi = *reinterpret_cast<gptr<const V>>(gmem(p + (split ? half + P * t : 2 * P * t + P)));
+  }
+  __device__ __forceinline__ void clear() { lo = hi = V{}; }
+  __device__ __forceinline__ void pairs(const QkArgs& q, int t, float* a, float* b) const {
+    const bool split = !q.interleaved && P * t < q.rot / 2;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const float x = i < P / 2 ? lo[2 * i] : hi[2 * i - P], y = i < P / 2 ? lo[2 * i + 1] : hi[2 * i + 1 - P];
-      a[i] = split ? lo[i] : x;
-      b[i] = split ? hi[i] : y;
+      const T x = i < P / 2 ? lo[2 * i] : hi[2 * i - P], y = i < P / 2 ? lo[2 * i + 1] : hi[2 * i + 1 - P];
+      a[i] = static_cast<float>(split ? lo[i] : x);
+      b[i] = static_cast<float>(split ? hi[i] : y);
     }
-  } else {
+  }
+};
+template <int DT, int P> struct Raw<DT, P, false> {
+  using T = typename OpElem<DT>::T;
+  T x[P], y[P];
+  __device__ __forceinline__ void load(const QkArgs& q, const T* p, int t) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       int e0, e1;
       pair_elems(q, P * t + i, &e0, &e1);
-      a[i] = e0 < q.dim ? static_cast<float>(gmem(p)[e0]) : 0.0f;
-      b[i] = e1 < q.dim ? static_cast<float>(gmem(p)[e1]) : 0.0f;
+      x[i] = e0 < q.dim ? gmem(p)[e0] : static_cast<T>(0.0f);
+      y[i] = e1 < q.dim ? gmem(p)[e1] : static_cast<T>(0.0f);
     }
   }
-}
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < P; ++i) x[i] = y[i] = static_cast<T>(0.0f);
+  }
+  __device__ __forceinline__ void pairs(const QkArgs&, int, float* a, float* b) const {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      a[i] = static_cast<float>(x[i]);
+      b[i] = static_cast<float>(y[i]);
+    }
+  }
+};
 
 template <int DT, int P, bool VEC>
 __device__ __forceinline__ void store_unit(const QkArgs& q, typename OpElem<DT>::T* p, int t, const float* a, const float* b) {
@@ -156,7 +178,24 @@ __device__ __forceinline__ void load_gain(const QkArgs& q, int which, int t, flo
     for (int i = 0; i < P; ++i) wa[i] = wb[i] = 1.0f;
     return;
   }
-  load_unit<WDT, P, VEC>(q, w, t, wa, wb);
+  if constexpr (VEC) {
+    // fp32 gains of eight pairs are wider than one load
+    float lo[P], hi[P];
+    const int half = q.rot / 2;
+    const bool split = !q.interleaved && P * t < half;
+    load_n<P>(w + (split ? P * t : 2 * P * t), lo);
+    load_n<P>(w + (split ? half + P * t : 2 * P * t + P), hi);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const float x = i < P / 2 ? lo[2 * i] : hi[2 * i - P], y = i < P / 2 ? lo[2 * i + 1] : hi[2 * i + 1 - P];
+      wa[i] = split ? lo[i] : x;
+      wb[i] = split ? hi[i] : y;
+    }
+  } else {
+    Raw<WDT, P, false> r;
+    r.load(q, w, t);
+    r.pairs(q, t, wa, wb);
+  }
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     wa[i] += q.offset;
@@ -198,16 +237,22 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_kernel(QkArgs a, int log_l
   const int h0 = static_cast<int>(blockIdx.y) * passes * p.heads_at_once;
   if (h0 >= heads || (p.block * kQkWaves + (threadIdx.x >> 6)) * p.tokens_at_once >= a.n) return;
   const bool here = p.any && token < a.n;
+  const T* src = static_cast<const T*>(pick(a.x, p.which)) + token * pick(a.x_stride, p.which);
+  T* dst = static_cast<T*>(pick(a.out, p.which)) + token * pick(a.out_stride, p.which);
+  // the first heads are on their way while the position leads to its angles
+  Raw<DT, P, VEC> next;
+  next.clear();
+  if (here && h0 + p.head < heads) next.load(a, src + static_cast<int64_t>(h0 + p.head) * a.dim, p.t);
   float c[P], s[P], wa[P], wb[P];
   const int kind = token_angles<P, VEC>(a, min(token, a.n - 1), p.any ? p.t : 0, c, s);
   load_gain<WDT, P, VEC>(a, p.which, p.any ? p.t : 0, wa, wb);
-  const T* src = static_cast<const T*>(pick(a.x, p.which)) + token * pick(a.x_stride, p.which);
-  T* dst = static_cast<T*>(pick(a.out, p.which)) + token * pick(a.out_stride, p.which);
   for (int k = 0; k < passes; ++k) {
     const int h = h0 + k * p.heads_at_once + p.head;
     const bool on = here && h < heads;
-    float x[P] = {}, y[P] = {};
-    if (on && kind != 0) load_unit<DT, P, VEC>(a, src + static_cast<int64_t>(h) * a.dim, p.t, x, y);
+    float x[P], y[P];
+    next.pairs(a, p.t, x, y);
+    if (k + 1 < passes && here && h + p.heads_at_once < heads)
+      next.load(a, src + static_cast<int64_t>(h + p.heads_at_once) * a.dim, p.t);
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < P; ++i) ss += x[i] * x[i] + y[i] * y[i];
@@ -238,24 +283,41 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_grad_kernel(QkArgs a, int 
   load_gain<WDT, P, VEC>(a, p.which, p.any ? p.t : 0, wa, wb);
   const float inv_dim = 1.0f / static_cast<float>(a.dim);
   const int64_t step = static_cast<int64_t>(pick(a.blocks, p.which)) * kQkWaves * p.tokens_at_once;
-  for (int64_t t0 = (p.block * kQkWaves + wave) * p.tokens_at_once; t0 < a.n; t0 += step) {
+  const T* xp = static_cast<const T*>(pick(a.x, p.which));
+  const T* dyp = static_cast<const T*>(pick(a.dy, p.which));
+  T* op = static_cast<T*>(pick(a.out, p.which));
+  const int64_t xs = pick(a.x_stride, p.which), dys = pick(a.dy_stride, p.which), os = pick(a.out_stride, p.which);
+  // one run of heads ahead: its loads cover the angles of its token and the sums of the run before
+  Raw<DT, P, VEC> nx, ny;
+  auto ahead = [&](int64_t token, int h) {
+    nx.clear();
+    ny.clear();
+    if (p.any && token < a.n && h < heads) {
+      nx.load(a, xp + token * xs + static_cast<int64_t>(h) * a.dim, p.t);
+      ny.load(a, dyp + token * dys + static_cast<int64_t>(h) * a.dim, p.t);
+    }
+  };
+  int64_t t0 = (p.block * kQkWaves + wave) * p.tokens_at_once;
+  ahead(t0 + p.tok, p.head);
+  for (; t0 < a.n; t0 += step) {
     const int64_t token = t0 + p.tok;
     const bool here = p.any && token < a.n;
     float c[P], s[P];
     const int kind = token_angles<P, VEC>(a, min(token, a.n - 1), p.any ? p.t : 0, c, s);
-    const T* src = static_cast<const T*>(pick(a.x, p.which)) + token * pick(a.x_stride, p.which);
-    const T* dsrc = static_cast<const T*>(pick(a.dy, p.which)) + token * pick(a.dy_stride, p.which);
-    T* dst = static_cast<T*>(pick(a.out, p.which)) + token * pick(a.out_stride, p.which);
     for (int h = p.head; h - p.head < heads; h += p.heads_at_once) {
       const bool on = here && h < heads;
-      float x[P] = {}, y[P] = {}, u[P] = {}, v[P] = {};
-      if (on && kind != 0) {
-        load_unit<DT, P, VEC>(a, src + static_cast<int64_t>(h) * a.dim, p.t, x, y);
-        load_unit<DT, P, VEC>(a, dsrc + static_cast<int64_t>(h) * a.dim, p.t, u, v);
-      }
+      float x[P], y[P], u[P], v[P];
+      nx.pairs(a, p.t, x, y);
+      ny.pairs(a, p.t, u, v);
+      const int hn = h + p.heads_at_once;
+      if (hn - p.head < heads) ahead(token, hn);
+      else ahead(token + step, p.head);
       float ss = 0.0f;
 #pragma unroll
-      for (int i = 0; i < P; ++i) ss += x[i] * x[i] + y[i] * y[i];
+      for (int i = 0; i < P; ++i) {
+        if (kind == 0) x[i] = y[i] = u[i] = v[i] = 0.0f;   // whatever a padding token holds
+        ss += x[i] * x[i] + y[i] * y[i];
+      }
       ss = group_sum(ss, lanes);
       float r = 1.0f / sqrtf(ss / static_cast<float>(a.dim) + a.eps);
       r = kind == 2 ? NAN : kind == 0 ? 0.0f : r;
@@ -279,7 +341,7 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_grad_kernel(QkArgs a, int 
         u[i] = kind == 0 ? 0.0f : r * (u[i] - x[i] * dot);
         v[i] = kind == 0 ? 0.0f : r * (v[i] - y[i] * dot);
       }
-      store_unit<DT, P, VEC>(a, dst + static_cast<int64_t>(h) * a.dim, p.t, u, v);
+      store_unit<DT, P, VEC>(a, op + token * os + static_cast<int64_t>(h) * a.dim, p.t, u, v);
     }
   }
   if (!a.part) return;
