@@ -57,11 +57,18 @@ template <int DT, int P, bool VEC> struct Raw {
   using T = typename OpElem<DT>::T;
   using V = T __attribute__((ext_vector_type(P)));
   V lo, hi;
-  __device__ __forceinline__ void load(const QkArgs& q, const T* p, int t) {
+  template <bool STREAM> __device__ __forceinline__ void load(const QkArgs& q, const T* p, int t) {
     const int half = q.rot / 2;
     const bool split = !q.interleaved && P * t < half;
-    lo = *reinterpret_cast<gptr<const V>>(gmem(p + (split ? P * t : 2 * P * t)));
-    hi = *reinterpret_cast<gptr<const V>>(gmem(p + (split ? half + P * t : 2 * P * t + P)));
+    const auto pl = reinterpret_cast<gptr<const V>>(gmem(p + (split ? P * t : 2 * P * t)));
+    const auto ph = reinterpret_cast<gptr<const V>>(gmem(p + (split ? half + P * t : 2 * P * t + P)));
+    if constexpr (STREAM) {
+      lo = __builtin_nontemporal_load(pl);
+      hi = __builtin_nontemporal_load(ph);
+    } else {
+      lo = *pl;
+      hi = *ph;
+    }
   }
   __device__ __forceinline__ void clear() { lo = hi = V{}; }
   __device__ __forceinline__ void pairs(const QkArgs& q, int t, float* a, float* b) const {
@@ -77,7 +84,7 @@ template <int DT, int P, bool VEC> struct Raw {
 template <int DT, int P> struct Raw<DT, P, false> {
   using T = typename OpElem<DT>::T;
   T x[P], y[P];
-  __device__ __forceinline__ void load(const QkArgs& q, const T* p, int t) {
+  template <bool STREAM> __device__ __forceinline__ void load(const QkArgs& q, const T* p, int t) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       int e0, e1;
@@ -99,7 +106,7 @@ template <int DT, int P> struct Raw<DT, P, false> {
   }
 };
 
-template <int DT, int P, bool VEC>
+template <int DT, int P, bool VEC, bool STREAM>
 __device__ __forceinline__ void store_unit(const QkArgs& q, typename OpElem<DT>::T* p, int t, const float* a, const float* b) {
   using T = typename OpElem<DT>::T;
   if constexpr (VEC) {
@@ -112,8 +119,8 @@ __device__ __forceinline__ void store_unit(const QkArgs& q, typename OpElem<DT>:
       lo[i] = split ? a[i] : i % 2 ? b[l] : a[l];
       hi[i] = split ? b[i] : i % 2 ? b[h] : a[h];
     }
-    store_n<P>(p + (split ? P * t : 2 * P * t), lo);
-    store_n<P>(p + (split ? half + P * t : 2 * P * t + P), hi);
+    store_n<P, STREAM>(p + (split ? P * t : 2 * P * t), lo);
+    store_n<P, STREAM>(p + (split ? half + P * t : 2 * P * t + P), hi);
   } else {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -193,7 +200,7 @@ __device__ __forceinline__ void load_gain(const QkArgs& q, int which, int t, flo
     }
   } else {
     Raw<WDT, P, false> r;
-    r.load(q, w, t);
+    r.template load<false>(q, w, t);
     r.pairs(q, t, wa, wb);
   }
 #pragma unroll
@@ -228,7 +235,7 @@ __device__ __forceinline__ Place place(const QkArgs& a, int log_lanes, int block
 }
 
 // blockIdx.y takes `passes` runs of heads of a token.
-template <int DT, int WDT, int P, bool VEC>
+template <int DT, int WDT, int P, bool VEC, bool STREAM>
 __global__ __launch_bounds__(kQkThreads) void qk_norm_kernel(QkArgs a, int log_lanes, int blocks_q, int passes) {
   using T = typename OpElem<DT>::T;
   const Place p = place<P>(a, log_lanes, blocks_q);
@@ -242,7 +249,7 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_kernel(QkArgs a, int log_l
   // the first heads are on their way while the position leads to its angles
   Raw<DT, P, VEC> next;
   next.clear();
-  if (here && h0 + p.head < heads) next.load(a, src + static_cast<int64_t>(h0 + p.head) * a.dim, p.t);
+  if (here && h0 + p.head < heads) next.template load<STREAM>(a, src + static_cast<int64_t>(h0 + p.head) * a.dim, p.t);
   float c[P], s[P], wa[P], wb[P];
   const int kind = token_angles<P, VEC>(a, min(token, a.n - 1), p.any ? p.t : 0, c, s);
   load_gain<WDT, P, VEC>(a, p.which, p.any ? p.t : 0, wa, wb);
@@ -252,7 +259,7 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_kernel(QkArgs a, int log_l
     float x[P], y[P];
     next.pairs(a, p.t, x, y);
     if (k + 1 < passes && here && h + p.heads_at_once < heads)
-      next.load(a, src + static_cast<int64_t>(h + p.heads_at_once) * a.dim, p.t);
+      next.template load<STREAM>(a, src + static_cast<int64_t>(h + p.heads_at_once) * a.dim, p.t);
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < P; ++i) ss += x[i] * x[i] + y[i] * y[i];
@@ -266,13 +273,13 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_kernel(QkArgs a, int log_l
       x[i] = kind == 0 ? 0.0f : na * c[i] - nb * s[i];
       y[i] = kind == 0 ? 0.0f : nb * c[i] + na * s[i];
     }
-    store_unit<DT, P, VEC>(a, dst + static_cast<int64_t>(h) * a.dim, p.t, x, y);
+    store_unit<DT, P, VEC, STREAM>(a, dst + static_cast<int64_t>(h) * a.dim, p.t, x, y);
   }
 }
 
 // The blocks of a tensor stride over its tokens and keep the gain's sums in
 // registers; each leaves one row of sums in `part`.
-template <int DT, int WDT, int P, bool VEC>
+template <int DT, int WDT, int P, bool VEC, bool STREAM>
 __global__ __launch_bounds__(kQkThreads) void qk_norm_grad_kernel(QkArgs a, int log_lanes) {
   using T = typename OpElem<DT>::T;
   extern __shared__ float sum[];   // kQkWaves x dim
@@ -293,8 +300,8 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_grad_kernel(QkArgs a, int 
     nx.clear();
     ny.clear();
     if (p.any && token < a.n && h < heads) {
-      nx.load(a, xp + token * xs + static_cast<int64_t>(h) * a.dim, p.t);
-      ny.load(a, dyp + token * dys + static_cast<int64_t>(h) * a.dim, p.t);
+      nx.template load<STREAM>(a, xp + token * xs + static_cast<int64_t>(h) * a.dim, p.t);
+      ny.template load<STREAM>(a, dyp + token * dys + static_cast<int64_t>(h) * a.dim, p.t);
     }
   };
   int64_t t0 = (p.block * kQkWaves + wave) * p.tokens_at_once;
@@ -341,7 +348,7 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_grad_kernel(QkArgs a, int 
         u[i] = kind == 0 ? 0.0f : r * (u[i] - x[i] * dot);
         v[i] = kind == 0 ? 0.0f : r * (v[i] - y[i] * dot);
       }
-      store_unit<DT, P, VEC>(a, op + token * os + static_cast<int64_t>(h) * a.dim, p.t, u, v);
+      store_unit<DT, P, VEC, STREAM>(a, op + token * os + static_cast<int64_t>(h) * a.dim, p.t, u, v);
     }
   }
   if (!a.part) return;
@@ -406,15 +413,24 @@ int log2_ceil(int v) {
   return l;
 }
 
-// f(element type, gain type, pairs per lane, vector path)
-template <typename F> void by_types(int dt, int w_dt, const QkArgs& a, F&& f) {
+// f(element type, gain type, pairs per lane, vector path, streaming accesses).
+// Passes over more than the 256 MB of the memory-side cache leave it alone:
+// non-temporal accesses took the 32768-token bf16 backward pass (1.0 GB) from
+// 228 to 215 us.  Smaller ones find their inputs there, just written by what
+// ran before (8191 fp32 tokens forward, 168 MB: 37 us, 40 non-temporal).  Only
+// where one access of a wave covers whole cache lines, that is for split pairs:
+// interleaved ones (two accesses to each line) went from 248 to 285 us at
+// 16384 tokens of 24 fp32 heads of 256.
+template <typename F> void by_types(int dt, int w_dt, const QkArgs& a, int tensors, F&& f) {
   using B = std::integral_constant<int, kBF16>;
   using S = std::integral_constant<int, kF32>;
   using P4 = std::integral_constant<int, 4>;
   using P8 = std::integral_constant<int, 8>;
+  const double bytes = static_cast<double>(a.n) * (a.heads[0] + a.heads[1]) * a.dim * (dt == kBF16 ? 2 : 4) * tensors;
   auto v = [&](auto d, auto w, auto p) {
-    if (a.vec) f(d, w, p, std::true_type{});
-    else f(d, w, p, std::false_type{});
+    if (a.vec && bytes > 256e6 && !a.interleaved && a.rot == a.dim) f(d, w, p, std::true_type{}, std::true_type{});
+    else if (a.vec) f(d, w, p, std::true_type{}, std::false_type{});
+    else f(d, w, p, std::false_type{}, std::false_type{});
   };
   auto w = [&](auto d, auto p) {
     if (w_dt == kBF16) v(d, B{}, p);
@@ -445,9 +461,10 @@ hipError_t launch_qk_norm(int dt, int w_dt, const QkArgs& in, hipStream_t stream
   }
   const int passes = most < share ? most : share;
   const dim3 grid(static_cast<unsigned>(blocks[0] + blocks[1]), static_cast<unsigned>((most + passes - 1) / passes));
-  by_types(dt, w_dt, a, [&](auto d, auto w, auto p, auto v) {
-    hipLaunchKernelGGL((qk_norm_kernel<decltype(d)::value, decltype(w)::value, decltype(p)::value, decltype(v)::value>),
-                       grid, dim3(kQkThreads), 0, stream, a, ll, blocks[0], passes);
+  by_types(dt, w_dt, a, 2, [&](auto d, auto w, auto p, auto v, auto st) {
+    hipLaunchKernelGGL((qk_norm_kernel<decltype(d)::value, decltype(w)::value, decltype(p)::value, decltype(v)::value,
+                                       decltype(st)::value>), grid,
+                       dim3(kQkThreads), 0, stream, a, ll, blocks[0], passes);
   });
   return hipGetLastError();
 }
@@ -458,8 +475,9 @@ hipError_t launch_qk_norm_grad(int dt, int w_dt, const QkArgs& in, hipStream_t s
   const int ll = log2_ceil((a.dim + 2 * pairs - 1) / (2 * pairs));
   for (int k = 0; k < 2; ++k) a.log_heads[k] = log2_ceil(a.heads[k]);
   if (a.blocks[0] + a.blocks[1] > 0) {
-    by_types(dt, w_dt, a, [&](auto d, auto w, auto p, auto v) {
-      hipLaunchKernelGGL((qk_norm_grad_kernel<decltype(d)::value, decltype(w)::value, decltype(p)::value, decltype(v)::value>),
+    by_types(dt, w_dt, a, 3, [&](auto d, auto w, auto p, auto v, auto st) {
+      hipLaunchKernelGGL((qk_norm_grad_kernel<decltype(d)::value, decltype(w)::value, decltype(p)::value,
+                                              decltype(v)::value, decltype(st)::value>),
                          dim3(a.blocks[0] + a.blocks[1]), dim3(kQkThreads), sizeof(float) * kQkWaves * a.dim, stream, a, ll);
     });
     const hipError_t e = hipGetLastError();

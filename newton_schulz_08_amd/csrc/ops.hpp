@@ -169,23 +169,22 @@ template <int N> __device__ __forceinline__ void load_n(const __bf16* p, float* 
     for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(x[e]);
   }
 }
-template <int N> __device__ __forceinline__ void store_n(float* p, const float* v) {
+// STREAM: non-temporal, for results that do not fit the caches anyway.
+template <bool STREAM, typename V> __device__ __forceinline__ void store_vec(gptr<V> p, V x) {
+  if constexpr (STREAM) __builtin_nontemporal_store(x, p);
+  else *p = x;
+}
+template <int N, bool STREAM = false> __device__ __forceinline__ void store_n(float* p, const float* v) {
 #pragma unroll
   for (int h = 0; h < N / 4; ++h)
-    *reinterpret_cast<gptr<f32v4>>(gmem(p + 4 * h)) = f32v4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+    store_vec<STREAM>(reinterpret_cast<gptr<f32v4>>(gmem(p + 4 * h)), f32v4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]});
 }
-template <int N> __device__ __forceinline__ void store_n(__bf16* p, const float* v) {
-  if constexpr (N == 8) {
-    bf16v8 x;
+template <int N, bool STREAM = false> __device__ __forceinline__ void store_n(__bf16* p, const float* v) {
+  typedef __bf16 V __attribute__((ext_vector_type(N)));
+  V x;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = static_cast<__bf16>(v[e]);
-    *reinterpret_cast<gptr<bf16v8>>(gmem(p)) = x;
-  } else {
-    bf16v4 x;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = static_cast<__bf16>(v[e]);
-    *reinterpret_cast<gptr<bf16v4>>(gmem(p)) = x;
-  }
+  for (int e = 0; e < N; ++e) x[e] = static_cast<__bf16>(v[e]);
+  store_vec<STREAM>(reinterpret_cast<gptr<V>>(gmem(p)), x);
 }
 #endif
 
