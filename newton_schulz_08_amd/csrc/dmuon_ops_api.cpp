@@ -164,10 +164,11 @@ int egrad_chunk(int64_t n, int64_t dim, int dout_dtype) {
 
 // ---------------------------------------------------------------- distillation
 constexpr int64_t kDistillPartBytes = 8 * sizeof(float);
-// Slices per row: enough blocks for the chip, none shorter than 4096 elements.
+// Blocks per row, for a few long rows (at least 8192 elements each); 0: a
+// block takes a whole row, in one launch.
 int distill_slices(int64_t n, int64_t vocab) {
-  const int64_t want = (1024 + n - 1) / std::max<int64_t>(n, 1), most = (vocab + 4095) / 4096;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, 64})));
+  if (n > 128 || vocab <= 65536) return 0;
+  return static_cast<int>(std::min<int64_t>({(1024 + n - 1) / std::max<int64_t>(n, 1), (vocab + 8191) / 8192, 64}));
 }
 
 // ---------------------------------------------------------------- query / key norm
@@ -446,7 +447,7 @@ int dmuon_distill_loss_workspace_bytes(int64_t n, int64_t vocab, size_t* bytes_o
   return guarded([&]() -> int {
     if (!bytes_out) return invalid("bytes_out is NULL");
     DMUON_TRY(check_tokens(n, vocab));
-    *bytes_out = n == 0 ? 0 : align_up(static_cast<size_t>(n * distill_slices(n, vocab) * kDistillPartBytes));
+    *bytes_out = align_up(static_cast<size_t>(n * distill_slices(n, vocab) * kDistillPartBytes));
     return DMUON_OK;
   });
 }
@@ -504,13 +505,11 @@ int dmuon_distill_loss(const void* logits, int64_t n, int64_t vocab, int64_t log
     a.k = k;
     a.idx64 = index_dtype == DMUON_I64;
     a.slices = distill_slices(n, vocab);
-    a.slice_len = ((vocab + a.slices - 1) / a.slices + 7) / 8 * 8;
+    if (a.slices > 0) a.slice_len = ((vocab + a.slices - 1) / a.slices + 7) / 8 * 8;
     a.temperature = temperature;
     a.kd = kd_weight;
     a.ce = ce_weight;
     a.grad_scale = grad_scale;
-    auto rows16 = [&](const void* p, int64_t stride) { return aligned(p, 16) && (n == 1 || stride * es % 16 == 0); };
-    a.vec = rows16(logits, logits_stride) && (!dlogits || rows16(dlogits, dlogits_stride));
     const double elems = static_cast<double>(n) * vocab;
     return launched("distillation loss", kKDistill, (dlogits ? 8.0 : 4.0) * elems, elems * es * (dlogits ? 2.0 : 1.0),
                     hip_stream, capturing,

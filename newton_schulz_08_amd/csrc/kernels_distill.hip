@@ -8,32 +8,44 @@
 //   loss = w (kd KD + ce CE)
 //   dz_i = gs w (kd T (exp(z_i / T - lse_T) - q_i) + ce (exp(z_i - lse_1) - [i = label]))
 //
-// A row is cut into slices.  distill_stats_kernel reads each slice once and
-// leaves its running maximum, its sums of exponentials relative to that maximum
-// and its part of sum_j e_j z_j; distill_grad_kernel joins the slices of its
-// row, writes the loss, and rewrites its slice as the gradient: first the
-// softmax terms of every element, then, behind a barrier, the at most k + 1
-// elements that the teacher or the label name.  HBM-bound: one or two
-// exponentials per element against 2 or 4 bytes each way.
+// HBM-bound: one or two exponentials per element against 2 or 4 bytes each way.
+//
+// Exponentials are taken in base 2 against an integer reference: with
+// s2 = log2(e) / T and M = ceil(max z s2), exp2(z s2 - M) is one fused
+// multiply-add (its only rounding is relative to the small difference) and one
+// v_exp_f32, and moving a sum to another reference multiplies it by an exact
+// power of two.  Where the label's term has another exponent than the
+// teacher's, T = 2 or 4 squares the first exponential (M doubles with it)
+// instead of taking a second one.  A maximum that is not below 2^100 in size
+// (infinite, or a row masked with the type's lowest value) would leave the
+// range of z s2: such rows subtract the maximum first.
 //
 // Sums of exponentials are fp32; the few scalars of a row are joined in fp64,
 // so that the loss is exact to the fp32 sums although it is a difference of
 // terms that grow with the vocabulary.
+//
+// Many rows: a block takes a row, reads it once from HBM for its sums and a
+// second time, now from the memory-side cache, for the gradient.  Few rows:
+// a row is cut into slices over several blocks, one launch for the sums of the
+// slices and one that joins them and writes the gradient.  Either way the
+// softmax terms of all elements are written first and, behind a barrier, the
+// at most k + 1 elements that the teacher or the label name are rewritten.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "ops.hpp"
 
 namespace dmuon {
 namespace {
 
-constexpr int kDsThreads = 256;
-constexpr int kDsWaves = kDsThreads / 64;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLn2 = 0.6931471805599453094;
+constexpr float kFar = 1.2676506e30f;   // 2^100
+constexpr int kHeld = 12;               // vectors kept in registers by a 512-thread row
 
-// Words of a slice's partial result.
-enum { kPmMax = 0, kPmSumT, kPmSum1, kPmDotHi, kPmDotLo, kPmLabel, kPmWords = 8 };
-
-__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// How the exponents of a row's two terms hang together.
+enum DistillMode { kOne = 0, kTwo = 1, kSquare = 2, kFourth = 3 };
 
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
@@ -45,272 +57,502 @@ template <typename F> __device__ __forceinline__ F wave_sum(F v) {
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
   return v;
 }
-__device__ __forceinline__ float block_max(float v, float* red) {
-  v = wave_max(v);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float r = red[0];
-#pragma unroll
-  for (int w = 1; w < kDsWaves; ++w) r = fmaxf(r, red[w]);
-  __syncthreads();
-  return r;
-}
-template <typename F> __device__ __forceinline__ F block_sum(F v, F* red) {
-  v = wave_sum(v);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  F r = red[0];
-#pragma unroll
-  for (int w = 1; w < kDsWaves; ++w) r += red[w];
-  __syncthreads();
-  return r;
-}
 
-// exp((a - b) s) where an empty sum has maximum -inf
-__device__ __forceinline__ float rescale(float a, float b, float s2) {
-  return a == -INFINITY ? 0.0f : exp2_fast((a - b) * s2);
-}
-
-// The teacher's entries of one row: indices (or -1), unnormalised weights
-// e_j = exp((y_j - max) / T) and their sum.
-struct Teacher {
-  int64_t idx[kDistillMaxK];
-  float e[kDistillMaxK];
+// Scalars of a row (or of a slice of one).
+struct Sums {
+  float top = -INFINITY;             // largest logit
+  float st = 0.0f, s1 = 0.0f;        // sums of exponentials, against the references of `top`
+  float ytop = -INFINITY;            // largest teacher logit
+  double ysum = 0.0;                 // sum of e_j = exp((y_j - ytop) / T)
+  double dot = 0.0;                  // sum of e_j z_j
+  double ent = 0.0;                  // sum of e_j (y_j - ytop) / T
 };
-__device__ __forceinline__ void load_teacher(const DistillArgs& a, int64_t row, Teacher& t, float* red, double* dred,
-                                             float* top, double* sum) {
-  float m = -INFINITY;
-  for (int j = threadIdx.x; j < a.k; j += kDsThreads) {
-    const int64_t i = load_index(a.index, row * a.k + j, a.idx64);
-    const float y = gmem(a.teacher)[row * a.k + j];
-    const bool ok = i >= 0 && i < a.vocab;
-    t.idx[j] = ok ? i : -1;
-    t.e[j] = ok ? y : -INFINITY;
-    // a NaN has to reach the sum
-    if (ok) m = fmaxf(m, y);
+
+template <int THREADS> struct Shared {
+  static constexpr int kWaves = THREADS / 64;
+  float top[kWaves], ytop[kWaves], st[kWaves], s1[kWaves];
+  double ysum[kWaves], dot[kWaves], ent[kWaves];
+  int idx[kDistillMaxK + 1];         // elements named by the teacher (label last), or -1
+  float e[kDistillMaxK + 1];
+  float z[kDistillMaxK + 1];
+};
+
+// Exponentials of one row: exponents s2 and, in kTwo, log2(e).
+template <int MODE> struct Expo {
+  float s2, m0, m1, top;
+  bool far;
+  __device__ __forceinline__ static float reference(float top, float s2) {
+    return ceilf(fminf(fmaxf(top, -kFar), kFar) * s2);
   }
-  m = block_max(m, red);
-  double s = 0.0;
-  for (int j = threadIdx.x; j < a.k; j += kDsThreads) {
-    const float e = t.e[j] == -INFINITY ? 0.0f : expf((t.e[j] - m) / a.temperature);
-    t.e[j] = e;
-    s += e;
+  __device__ __forceinline__ void set(float t, float scale) {
+    s2 = scale;
+    top = t;
+    far = !(fabsf(t) < kFar);
+    m0 = reference(t, s2);
+    m1 = MODE == kTwo ? reference(t, kLog2e) : MODE == kSquare ? 2.0f * m0 : 4.0f * m0;
   }
-  *sum = block_sum(s, dred);   // its barriers also publish t
-  *top = m;
+  // FAR: the slow form
+  template <bool FAR> __device__ __forceinline__ void both(float v, float* et, float* e1) const {
+    if constexpr (FAR) {
+      const float d = v - top;
+      *et = __builtin_amdgcn_exp2f(d * s2);
+      if constexpr (MODE != kOne) *e1 = __builtin_amdgcn_exp2f(d * kLog2e);
+    } else {
+      *et = __builtin_amdgcn_exp2f(fmaf(v, s2, -m0));
+      if constexpr (MODE == kTwo) *e1 = __builtin_amdgcn_exp2f(fmaf(v, kLog2e, -m1));
+      if constexpr (MODE == kSquare) *e1 = *et * *et;
+      if constexpr (MODE == kFourth) *e1 = (*et * *et) * (*et * *et);
+    }
+  }
+};
+
+__device__ __forceinline__ float scale_of(const DistillArgs& a) {
+  return a.kd != 0.0f ? kLog2e / a.temperature : kLog2e;
 }
 
-template <int DT, bool DUAL>
-__global__ __launch_bounds__(kDsThreads) void distill_stats_kernel(DistillArgs a) {
-  using T = typename OpElem<DT>::T;
-  constexpr int C = DT == kBF16 ? 8 : 4;
-  constexpr int U = 4;
-  __shared__ Teacher teacher;
-  __shared__ float red[kDsWaves];
-  __shared__ double dred[kDsWaves];
-  const int64_t row = blockIdx.x / a.slices;
-  const int slice = static_cast<int>(blockIdx.x - row * a.slices);
-  if (a.row_weight && gmem(a.row_weight)[row] == 0.0f) return;
-  const T* z = static_cast<const T*>(a.logits) + row * a.stride;
-  const int64_t i0 = slice * a.slice_len, i1 = min(a.vocab, i0 + a.slice_len);
-  const float s2t = kLog2e / a.temperature;
-  const float s2 = a.kd != 0.0f ? s2t : kLog2e;   // the only scale unless DUAL
-  float m = -INFINITY, st = 0.0f, s1 = 0.0f;
-  auto add = [&](const float* v, int count) {
-    float top = m;
-    for (int e = 0; e < count; ++e) top = fmaxf(top, v[e]);
-    if (top > m) {
-      st *= rescale(m, top, s2);
-      if (DUAL) s1 *= rescale(m, top, kLog2e);
-      m = top;
-    }
-    for (int e = 0; e < count; ++e) {
-      // nothing to add for -inf: (-inf) - (-inf) is no number
-      const float d = v[e] == -INFINITY ? -INFINITY : v[e] - m;
-      st += exp2_fast(d * s2);
-      if (DUAL) s1 += exp2_fast(d * kLog2e);
-    }
-  };
-  if (a.vec) {
-    const int64_t whole = i0 + (i1 - i0) / C * C;
-    for (int64_t i = i0 + threadIdx.x * C; i < whole; i += kDsThreads * C * U) {
-      float v[U][C];
+// f(vector of C logits, first element, how many) over elements [from, i1),
+// `from` a multiple of C behind i0.
+template <typename T, int THREADS, int U, typename F>
+__device__ __forceinline__ void sweep(const T* z, int64_t from, int64_t i1, F&& f) {
+  constexpr int C = 16 / sizeof(T);
+  const int64_t whole = from + most<int64_t>(i1 - from, 0) / C * C;
+  int64_t i = from + threadIdx.x * C;
+  for (; i + (U - 1) * THREADS * C < whole; i += U * THREADS * C) {
+    float v[U][C];
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_any<C>(z + i + u * THREADS * C, v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) f(v[u], i + u * THREADS * C, std::integral_constant<int, C>{});
+  }
+  for (; i < whole; i += THREADS * C) {
+    float v[C];
+    load_any<C>(z + i, v);
+    f(v, i, std::integral_constant<int, C>{});
+  }
+  for (i = whole + threadIdx.x; i < i1; i += THREADS) {
+    const float v = static_cast<float>(gmem(z)[i]);
+    f(&v, i, std::integral_constant<int, 1>{});
+  }
+}
+
+// The first R vectors of a thread's share of a row, kept in registers as they
+// were loaded, so that the gradient need not read them again.
+template <typename T, int R> struct Held {
+  static constexpr int C = 16 / sizeof(T);
+  using V = typename Loose<T, C>::V;
+  V raw[R > 0 ? R : 1];
+};
+template <typename T, int THREADS, int R, bool KEPT, typename F>
+__device__ __forceinline__ void sweep_held(const T* z, int64_t i0, int64_t i1, Held<T, R>& held, F&& f) {
+  constexpr int C = 16 / sizeof(T), U = 4;
+  static_assert(R % U == 0, "held vectors come in groups");
+  const int64_t whole = i0 + (i1 - i0) / C * C;
+  const int64_t first = i0 + threadIdx.x * C;
+#pragma unroll
+  for (int r = 0; r < R; r += U) {
+    if constexpr (!KEPT) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t p = i + static_cast<int64_t>(u) * kDsThreads * C;
-        if (p < whole) load_n<C>(z + p, v[u]);
+        const int64_t i = first + (r + u) * THREADS * C;
+        if (i < whole) held.raw[r + u] = *reinterpret_cast<gptr<const typename Held<T, R>::V>>(gmem(z + i));
       }
+    }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i + static_cast<int64_t>(u) * kDsThreads * C < whole) add(v[u], C);
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = first + (r + u) * THREADS * C;
+      if (i < whole) {
+        float v[C];
+#pragma unroll
+        for (int e = 0; e < C; ++e) v[e] = static_cast<float>(held.raw[r + u][e]);
+        f(v, i, std::integral_constant<int, C>{});
+      }
     }
-    for (int64_t i = whole + threadIdx.x; i < i1; i += kDsThreads) {
-      const float v = static_cast<float>(gmem(z)[i]);
-      add(&v, 1);
+  }
+  sweep<T, THREADS, 4>(z, least(whole, i0 + R * THREADS * C), i1, f);
+}
+
+// The sums of [i0, i1) of a row, and of the teacher's entries that lie in it
+// (its own sums are over all entries).  Ends behind a barrier, with the entries
+// in `sh` and everything in `s` of every thread.
+template <int DT, int MODE, int THREADS, int R>
+__device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int64_t i0, int64_t i1,
+                                         Shared<THREADS>& sh, Sums& s, Held<typename OpElem<DT>::T, R>& held) {
+  using T = typename OpElem<DT>::T;
+  constexpr int kPer = (kDistillMaxK + THREADS) / THREADS;
+  const T* z = static_cast<const T*>(a.logits) + row * a.stride;
+  const int tid = threadIdx.x, wave = tid >> 6;
+  // named elements: on their way while the row is swept
+  float y[kPer], zj[kPer];
+  int idx[kPer];
+#pragma unroll
+  for (int p = 0; p < kPer; ++p) {
+    const int j = tid + p * THREADS;
+    idx[p] = -1;
+    y[p] = -INFINITY;
+    zj[p] = 0.0f;
+    if (j < a.k && a.kd != 0.0f) {
+      const int64_t i = load_index(a.index, row * a.k + j, a.idx64);
+      if (i >= 0 && i < a.vocab) {
+        idx[p] = static_cast<int>(i);
+        y[p] = gmem(a.teacher)[row * a.k + j];
+      }
+    } else if (j == a.k && a.labels && a.ce != 0.0f) {
+      const int64_t i = load_index(a.labels, row, a.idx64);
+      if (i >= 0 && i < a.vocab) idx[p] = static_cast<int>(i);
     }
+    if (idx[p] >= i0 && idx[p] < i1) zj[p] = static_cast<float>(gmem(z)[idx[p]]);
+  }
+  const float s2 = scale_of(a);
+  Expo<MODE> x;
+  x.set(-INFINITY, s2);
+  float top = -INFINITY, st = 0.0f, s1 = 0.0f;
+  sweep_held<T, THREADS, R, false>(z, i0, i1, held, [&](const float* v, int64_t, auto count) {
+    constexpr int N = decltype(count)::value;
+    float t = v[0];
+#pragma unroll
+    for (int e = 1; e < N; ++e) t = fmaxf(t, v[e]);
+    if (t > top) {   // rare once a few vectors are in
+      const float old0 = x.m0, old1 = x.m1;
+      top = t;
+      x.set(t, s2);
+      st *= __builtin_amdgcn_exp2f(old0 - x.m0);
+      if constexpr (MODE != kOne) s1 *= __builtin_amdgcn_exp2f(old1 - x.m1);
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      float et, e1;
+      x.template both<false>(v[e], &et, &e1);
+      st += et;
+      if constexpr (MODE != kOne) s1 += e1;
+    }
+  });
+  float ytop = -INFINITY;
+#pragma unroll
+  for (int p = 0; p < kPer; ++p) {
+    const int j = tid + p * THREADS;
+    if (j <= a.k) {
+      sh.idx[j] = idx[p];
+      sh.z[j] = zj[p];
+    }
+    ytop = fmaxf(ytop, y[p]);
+  }
+  {
+    const float m = wave_max(top), n = wave_max(ytop);
+    if ((tid & 63) == 0) {
+      sh.top[wave] = m;
+      sh.ytop[wave] = n;
+    }
+  }
+  __syncthreads();
+  s.top = sh.top[0];
+  s.ytop = sh.ytop[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 64; ++w) {
+    s.top = fmaxf(s.top, sh.top[w]);
+    s.ytop = fmaxf(s.ytop, sh.ytop[w]);
+  }
+  Expo<MODE> all;
+  all.set(s.top, s2);
+  if (all.far) {   // out of the fused form's range: the maximum is subtracted first
+    st = s1 = 0.0f;
+    sweep<T, THREADS, 1>(z, i0, i1, [&](const float* v, int64_t, auto count) {
+#pragma unroll
+      for (int e = 0; e < decltype(count)::value; ++e) {
+        float et, e1;
+        all.template both<true>(v[e], &et, &e1);
+        // nothing but -inf (whose difference is no number) sums to 0, unless a NaN is among it
+        if (s.top == -INFINITY) et = e1 = v[e] == -INFINITY ? 0.0f : v[e];
+        st += et;
+        if constexpr (MODE != kOne) s1 += e1;
+      }
+    });
   } else {
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kDsThreads) {
-      const float v = static_cast<float>(gmem(z)[i]);
-      add(&v, 1);
-    }
+    st *= __builtin_amdgcn_exp2f(x.m0 - all.m0);
+    if constexpr (MODE != kOne) s1 *= __builtin_amdgcn_exp2f(x.m1 - all.m1);
   }
-  const float top = block_max(m, red);
-  st = block_sum(st * rescale(m, top, s2), red);
-  if (DUAL) s1 = block_sum(s1 * rescale(m, top, kLog2e), red);
-  double dot = 0.0;
+  double ysum = 0.0, dot = 0.0, ent = 0.0;
+#pragma unroll
+  for (int p = 0; p < kPer; ++p) {
+    const int j = tid + p * THREADS;
+    float e = 0.0f;
+    if (y[p] != -INFINITY) {
+      const float d = (y[p] - s.ytop) / a.temperature;
+      e = expf(d);
+      ysum += e;
+      if (e != 0.0f) {
+        ent += static_cast<double>(e) * d;
+        if (idx[p] >= i0 && idx[p] < i1) dot += static_cast<double>(e) * zj[p];
+      }
+    }
+    if (j <= a.k) sh.e[j] = e;
+  }
+  st = wave_sum(st);
+  if constexpr (MODE != kOne) s1 = wave_sum(s1);
   if (a.kd != 0.0f) {
-    float ymax;
-    double ysum;
-    load_teacher(a, row, teacher, red, dred, &ymax, &ysum);
-    for (int j = threadIdx.x; j < a.k; j += kDsThreads) {
-      const int64_t i = teacher.idx[j];
-      if (i >= i0 && i < i1 && teacher.e[j] != 0.0f)
-        dot += static_cast<double>(teacher.e[j]) * static_cast<double>(static_cast<float>(gmem(z)[i]));
-    }
-    dot = block_sum(dot, dred);
+    ysum = wave_sum(ysum);
+    dot = wave_sum(dot);
+    ent = wave_sum(ent);
   }
-  if (threadIdx.x == 0) {
-    float* p = a.part + blockIdx.x * static_cast<int64_t>(kPmWords);
-    const int64_t label = a.labels ? load_index(a.labels, row, a.idx64) : -1;
-    p[kPmMax] = top;
-    p[kPmSumT] = st;
-    p[kPmSum1] = DUAL ? s1 : st;
-    const float hi = static_cast<float>(dot);
-    p[kPmDotHi] = hi;
-    p[kPmDotLo] = isfinite(hi) ? static_cast<float>(dot - hi) : 0.0f;
-    p[kPmLabel] = label >= i0 && label < i1 ? static_cast<float>(gmem(z)[label]) : 0.0f;
+  if ((tid & 63) == 0) {
+    sh.st[wave] = st;
+    sh.s1[wave] = s1;
+    sh.ysum[wave] = ysum;
+    sh.dot[wave] = dot;
+    sh.ent[wave] = ent;
+  }
+  __syncthreads();
+  s.st = s.s1 = 0.0f;
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w) {
+    s.st += sh.st[w];
+    s.s1 += MODE != kOne ? sh.s1[w] : sh.st[w];
+    s.ysum += sh.ysum[w];
+    s.dot += sh.dot[w];
+    s.ent += sh.ent[w];
   }
 }
 
-template <int DT, bool DUAL>
-__global__ __launch_bounds__(kDsThreads) void distill_grad_kernel(DistillArgs a) {
-  using T = typename OpElem<DT>::T;
-  constexpr int C = DT == kBF16 ? 8 : 4;
-  __shared__ Teacher teacher;
-  __shared__ float red[kDsWaves];
-  __shared__ double dred[kDsWaves];
-  __shared__ float zsel[kDistillMaxK + 1];
-  const int64_t row = blockIdx.x / a.slices;
-  const int slice = static_cast<int>(blockIdx.x - row * a.slices);
-  const float w = a.row_weight ? gmem(a.row_weight)[row] : 1.0f;
-  const int64_t i0 = slice * a.slice_len, i1 = min(a.vocab, i0 + a.slice_len);
-  const T* z = static_cast<const T*>(a.logits) + row * a.stride;
-  T* dz = a.dlogits ? static_cast<T*>(a.dlogits) + row * a.dstride : nullptr;
-  const int tid = threadIdx.x;
+// log2 of the sum of exponentials, in units of the exponent s2 (or log2(e)).
+template <int MODE> __device__ __forceinline__ double log2_sum(const Expo<MODE>& x, double sum, bool second) {
+  const float s2 = second && MODE != kOne ? kLog2e : x.s2, m = second && MODE != kOne ? x.m1 : x.m0;
+  return (x.far ? static_cast<double>(x.top) * s2 : static_cast<double>(m)) + log2(sum);
+}
 
-  auto zero_row = [&]() {
-    if (slice == 0 && tid == 0) gmem(a.losses)[row] = 0.0f;
-    if (!dz) return;
-    const int64_t whole = a.vec ? i0 + (i1 - i0) / C * C : i0;
-    const float none[C] = {};
-    for (int64_t i = i0 + tid * C; i < whole; i += kDsThreads * C) store_n<C>(dz + i, none);
-    for (int64_t i = whole + tid; i < i1; i += kDsThreads) gmem(dz)[i] = static_cast<T>(0.0f);
-  };
-  if (w == 0.0f) {
-    zero_row();
-    return;
-  }
-  float ymax = -INFINITY;
-  double ysum = 0.0;
-  if (a.kd != 0.0f) load_teacher(a, row, teacher, red, dred, &ymax, &ysum);
-  const bool has_kd = a.kd != 0.0f && !(ysum == 0.0);
-  const int64_t label = a.labels ? load_index(a.labels, row, a.idx64) : -1;
-  const bool has_ce = a.ce != 0.0f && label >= 0 && label < a.vocab;
-  if (!has_kd && !has_ce) {   // neither term has anything to say about this row
-    zero_row();
-    return;
-  }
-  // join the slices of this row
-  float m = -INFINITY, zl = 0.0f;
-  const float* part = a.part + row * a.slices * kPmWords;
-  for (int s = 0; s < a.slices; ++s) m = fmaxf(m, gmem(part)[s * kPmWords + kPmMax]);
-  const float s2t = kLog2e / a.temperature;
-  const float s2 = a.kd != 0.0f ? s2t : kLog2e;
-  double st = 0.0, s1 = 0.0, dot = 0.0;
-  for (int s = 0; s < a.slices; ++s) {
-    const float* p = part + s * kPmWords;
-    const float ms = gmem(p)[kPmMax];
-    st += static_cast<double>(gmem(p)[kPmSumT]) * rescale(ms, m, s2);
-    s1 += static_cast<double>(gmem(p)[kPmSum1]) * rescale(ms, m, DUAL ? kLog2e : s2);
-    dot += static_cast<double>(gmem(p)[kPmDotHi]) + static_cast<double>(gmem(p)[kPmDotLo]);
-    zl += gmem(p)[kPmLabel];
-  }
-  if (slice == 0) {
-    double loss = 0.0;
-    if (has_kd) {
-      const double temp = a.temperature;
-      double h = 0.0;
-      for (int j = tid; j < a.k; j += kDsThreads)
-        if (teacher.e[j] != 0.0f) h += static_cast<double>(teacher.e[j]) * log(static_cast<double>(teacher.e[j]) / ysum);
-      h = block_sum(h, dred) / ysum;
-      loss += a.kd * temp * temp * (h - dot / (ysum * temp) + static_cast<double>(m) / temp + log(st));
-    }
-    if (has_ce) loss += a.ce * (static_cast<double>(m) + log(s1) - static_cast<double>(zl));
-    if (tid == 0) gmem(a.losses)[row] = static_cast<float>(w * loss);
-  }
-  if (!dz) return;
+// The row's loss from its sums; z_label: the label's logit.
+template <int MODE>
+__device__ __forceinline__ float row_loss(const DistillArgs& a, const Sums& s, const Expo<MODE>& x, double st, double s1,
+                                          bool has_kd, bool has_ce, float z_label, float w) {
+  double loss = 0.0;
+  if (has_kd)
+    loss += a.kd * static_cast<double>(a.temperature) * a.temperature *
+            (s.ent / s.ysum - log(s.ysum) + kLn2 * (log2_sum(x, st, false) - s.dot / s.ysum * x.s2));
+  if (has_ce) loss += a.ce * kLn2 * (log2_sum(x, s1, true) - static_cast<double>(z_label) * kLog2e);
+  return static_cast<float>(w * loss);
+}
+
+// Zeros for a row that has nothing to say.
+template <int DT, int THREADS, bool STREAM>
+__device__ __forceinline__ void zero_row(const DistillArgs& a, int64_t row, int64_t i0, int64_t i1) {
+  using T = typename OpElem<DT>::T;
+  constexpr int C = 16 / sizeof(T);
+  if (i0 == 0 && threadIdx.x == 0) gmem(a.losses)[row] = 0.0f;
+  if (!a.dlogits) return;
+  T* dz = static_cast<T*>(a.dlogits) + row * a.dstride;
+  const int64_t whole = i0 + (i1 - i0) / C * C;
+  const float none[C] = {};
+  for (int64_t i = i0 + threadIdx.x * C; i < whole; i += THREADS * C) store_any<C, STREAM>(dz + i, none);
+  for (int64_t i = whole + threadIdx.x; i < i1; i += THREADS) gmem(dz)[i] = static_cast<T>(0.0f);
+}
+
+// The gradient of [i0, i1) of a row.  `sh` holds the named elements' indices,
+// weights and, for those in [i0, i1), logits (dlogits may overwrite them).
+template <int DT, int MODE, int THREADS, bool STREAM, int R>
+__device__ __forceinline__ void row_grad(const DistillArgs& a, int64_t row, int64_t i0, int64_t i1,
+                                         const Shared<THREADS>& sh, const Expo<MODE>& x, double st, double s1,
+                                         double ysum, bool has_kd, bool has_ce, float w,
+                                         Held<typename OpElem<DT>::T, R>& held) {
+  using T = typename OpElem<DT>::T;
+  const T* z = static_cast<const T*>(a.logits) + row * a.stride;
+  T* dz = static_cast<T*>(a.dlogits) + row * a.dstride;
   const float scale = a.grad_scale * w;
   const float kdt = has_kd ? scale * a.kd * a.temperature : 0.0f;
   const float cew = has_ce ? scale * a.ce : 0.0f;
   // one coefficient serves both terms when they share the exponent
-  const float ct = DUAL ? (has_kd ? static_cast<float>(kdt / st) : 0.0f) : static_cast<float>((static_cast<double>(kdt) + cew) / st);
-  const float c1 = DUAL && has_ce ? static_cast<float>(cew / s1) : 0.0f;
-  auto soft = [&](float v) {
-    const float d = v - m;
-    float g = ct == 0.0f ? 0.0f : ct * exp2_fast(d * s2);
-    if (DUAL && c1 != 0.0f) g = fmaf(c1, exp2_fast(d * kLog2e), g);
-    return g;
+  const float ct = MODE == kOne ? static_cast<float>((static_cast<double>(kdt) + cew) / st)
+                   : has_kd     ? static_cast<float>(kdt / st)
+                                : 0.0f;
+  const float c1 = MODE != kOne && has_ce ? static_cast<float>(cew / s1) : 0.0f;
+  auto soft = [&](float v, auto far) {
+    float et, e1;
+    x.template both<decltype(far)::value>(v, &et, &e1);
+    if constexpr (MODE == kOne) return ct * et;
+    else return fmaf(c1, e1, ct * et);
   };
-  // the named elements' logits, before dlogits (which may be logits) is written
-  const int entries = a.k + 1;
-  for (int j = tid; j < entries; j += kDsThreads) {
-    const int64_t i = j < a.k ? (has_kd ? teacher.idx[j] : -1) : (has_ce ? label : -1);
-    zsel[j] = i >= i0 && i < i1 ? static_cast<float>(gmem(z)[i]) : 0.0f;
-  }
-  __syncthreads();
-  const int64_t whole = a.vec ? i0 + (i1 - i0) / C * C : i0;
-  for (int64_t i = i0 + tid * C; i < whole; i += kDsThreads * C) {
-    float v[C];
-    load_n<C>(z + i, v);
+  auto write = [&](auto far) {
+    return [&](const float* v, int64_t i, auto count) {
+      constexpr int N = decltype(count)::value;
+      float g[N];
 #pragma unroll
-    for (int e = 0; e < C; ++e) v[e] = soft(v[e]);
-    store_n<C>(dz + i, v);
-  }
-  for (int64_t i = whole + tid; i < i1; i += kDsThreads) gmem(dz)[i] = static_cast<T>(soft(static_cast<float>(gmem(z)[i])));
+      for (int e = 0; e < N; ++e) g[e] = soft(v[e], decltype(far){});
+      if constexpr (N > 1) store_any<N, STREAM>(dz + i, g);
+      else gmem(dz)[i] = static_cast<T>(g[0]);
+    };
+  };
+  if (x.far) sweep<T, THREADS, 1>(z, i0, i1, write(std::true_type{}));
+  else sweep_held<T, THREADS, R, true>(z, i0, i1, held, write(std::false_type{}));
   __syncthreads();
   // named elements: the first entry that names one collects all that do
-  auto entry = [&](int j) -> int64_t { return j < a.k ? (has_kd ? teacher.idx[j] : -1) : (has_ce ? label : -1); };
-  for (int j = tid; j < entries; j += kDsThreads) {
-    const int64_t i = entry(j);
+  for (int j = threadIdx.x; j <= a.k; j += THREADS) {
+    const int i = sh.idx[j];
     if (i < i0 || i >= i1) continue;
     bool first = true;
-    for (int h = 0; h < j && first; ++h) first = entry(h) != i;
+    for (int h = 0; h < j && first; ++h) first = sh.idx[h] != i;
     if (!first) continue;
     double q = 0.0;
     for (int h = j; h < a.k; ++h)
-      if (entry(h) == i) q += teacher.e[h];
-    const float off = (has_kd ? kdt * static_cast<float>(q / ysum) : 0.0f) + (has_ce && label == i ? cew : 0.0f);
-    gmem(dz)[i] = static_cast<T>(soft(zsel[j]) - off);
+      if (sh.idx[h] == i) q += sh.e[h];
+    const float off = (has_kd ? kdt * static_cast<float>(q / ysum) : 0.0f) + (has_ce && sh.idx[a.k] == i ? cew : 0.0f);
+    const float g = x.far ? soft(sh.z[j], std::true_type{}) : soft(sh.z[j], std::false_type{});
+    gmem(dz)[i] = static_cast<T>(g - off);
   }
+}
+
+__device__ __forceinline__ float weight_of(const DistillArgs& a, int64_t row) {
+  return a.row_weight ? gmem(a.row_weight)[row] : 1.0f;
+}
+
+// One block, one row.
+template <int DT, int MODE, int THREADS, bool STREAM, int R>
+__global__ __launch_bounds__(THREADS, THREADS == 1024 ? 8 : 4) void distill_row_kernel(DistillArgs a) {
+  __shared__ Shared<THREADS> sh;
+  const int64_t row = blockIdx.x;
+  const float w = weight_of(a, row);
+  if (w == 0.0f) {
+    zero_row<DT, THREADS, STREAM>(a, row, 0, a.vocab);
+    return;
+  }
+  Held<typename OpElem<DT>::T, R> held;
+  Sums s;
+  row_sums<DT, MODE, THREADS, R>(a, row, 0, a.vocab, sh, s, held);
+  const bool has_kd = a.kd != 0.0f && !(s.ysum == 0.0), has_ce = sh.idx[a.k] >= 0;
+  if (!has_kd && !has_ce) {
+    zero_row<DT, THREADS, STREAM>(a, row, 0, a.vocab);
+    return;
+  }
+  Expo<MODE> x;
+  x.set(s.top, scale_of(a));
+  if (threadIdx.x == 0) gmem(a.losses)[row] = row_loss(a, s, x, s.st, s.s1, has_kd, has_ce, sh.z[a.k], w);
+  if (a.dlogits)
+    row_grad<DT, MODE, THREADS, STREAM, R>(a, row, 0, a.vocab, sh, x, s.st, s.s1, s.ysum, has_kd, has_ce, w, held);
+}
+
+// Words of a slice's sums.
+enum { kPmMax = 0, kPmSumT, kPmSum1, kPmDotHi, kPmDotLo, kPmLabel, kPmWords = 8 };
+constexpr int kSliceThreads = 256;
+
+template <int DT, int MODE>
+__global__ __launch_bounds__(kSliceThreads) void distill_slice_kernel(DistillArgs a) {
+  __shared__ Shared<kSliceThreads> sh;
+  const int64_t row = blockIdx.x / a.slices;
+  const int slice = static_cast<int>(blockIdx.x - row * a.slices);
+  if (weight_of(a, row) == 0.0f) return;
+  const int64_t i0 = least(a.vocab, slice * a.slice_len), i1 = least(a.vocab, i0 + a.slice_len);
+  Sums s;
+  Held<typename OpElem<DT>::T, 0> none;
+  row_sums<DT, MODE, kSliceThreads, 0>(a, row, i0, i1, sh, s, none);
+  if (threadIdx.x == 0) {
+    float* p = a.part + blockIdx.x * static_cast<int64_t>(kPmWords);
+    p[kPmMax] = s.top;
+    p[kPmSumT] = s.st;
+    p[kPmSum1] = s.s1;
+    const float hi = static_cast<float>(s.dot);
+    p[kPmDotHi] = hi;
+    p[kPmDotLo] = isfinite(hi) ? static_cast<float>(s.dot - hi) : 0.0f;
+    p[kPmLabel] = sh.z[a.k];   // 0 outside this slice
+  }
+}
+
+// Joins a row's slices, writes the loss (first slice) and this slice's gradient.
+template <int DT, int MODE>
+__global__ __launch_bounds__(kSliceThreads) void distill_join_kernel(DistillArgs a) {
+  using T = typename OpElem<DT>::T;
+  __shared__ Shared<kSliceThreads> sh;
+  const int64_t row = a.dlogits ? blockIdx.x / a.slices : blockIdx.x;
+  const int slice = a.dlogits ? static_cast<int>(blockIdx.x - row * a.slices) : 0;
+  const int64_t i0 = least(a.vocab, slice * a.slice_len), i1 = least(a.vocab, i0 + a.slice_len);
+  const float w = weight_of(a, row);
+  if (w == 0.0f) {
+    zero_row<DT, kSliceThreads, false>(a, row, i0, i1);
+    return;
+  }
+  // the teacher's entries again: sums over no elements
+  Sums s;
+  Held<T, 0> none;
+  row_sums<DT, MODE, kSliceThreads, 0>(a, row, 0, 0, sh, s, none);
+  const bool has_kd = a.kd != 0.0f && !(s.ysum == 0.0), has_ce = sh.idx[a.k] >= 0;
+  if (!has_kd && !has_ce) {
+    zero_row<DT, kSliceThreads, false>(a, row, i0, i1);
+    return;
+  }
+  const T* z = static_cast<const T*>(a.logits) + row * a.stride;
+  if (a.dlogits)   // before dlogits (which may be logits) is written
+    for (int j = threadIdx.x; j <= a.k; j += kSliceThreads)
+      if (sh.idx[j] >= i0 && sh.idx[j] < i1) sh.z[j] = static_cast<float>(gmem(z)[sh.idx[j]]);
+  // a lane per slice (at most 64), the same in every wave
+  const int lane = threadIdx.x & 63;
+  const float* p = a.part + (row * a.slices + least(lane, a.slices - 1)) * kPmWords;
+  const bool on = lane < a.slices;
+  const float top = on ? gmem(p)[kPmMax] : -INFINITY;
+  s.top = wave_max(top);
+  Expo<MODE> x, y;
+  x.set(s.top, scale_of(a));
+  y.set(top, x.s2);
+  float ft = 0.0f, f1 = 0.0f;   // a slice of nothing but -inf, or one too far below the maximum
+  if (x.far && (y.far && top != -INFINITY)) {
+    ft = __builtin_amdgcn_exp2f((top - s.top) * x.s2);
+    f1 = __builtin_amdgcn_exp2f((top - s.top) * (MODE == kOne ? x.s2 : kLog2e));
+  } else if (!x.far && !y.far) {
+    ft = __builtin_amdgcn_exp2f(y.m0 - x.m0);
+    f1 = MODE == kOne ? ft : __builtin_amdgcn_exp2f(y.m1 - x.m1);
+  }
+  const double st = wave_sum(on ? static_cast<double>(gmem(p)[kPmSumT]) * ft : 0.0);
+  const double s1 = wave_sum(on ? static_cast<double>(gmem(p)[kPmSum1]) * f1 : 0.0);
+  s.dot = wave_sum(on ? static_cast<double>(gmem(p)[kPmDotHi]) + static_cast<double>(gmem(p)[kPmDotLo]) : 0.0);
+  const float z_label = wave_sum(on ? gmem(p)[kPmLabel] : 0.0f);
+  if (slice == 0 && threadIdx.x == 0) gmem(a.losses)[row] = row_loss(a, s, x, st, s1, has_kd, has_ce, z_label, w);
+  if (!a.dlogits) return;
+  __syncthreads();   // every named logit is read
+  row_grad<DT, MODE, kSliceThreads, false, 0>(a, row, i0, i1, sh, x, st, s1, s.ysum, has_kd, has_ce, w, none);
 }
 
 }  // namespace
 
 hipError_t launch_distill(int dt, const DistillArgs& a, hipStream_t stream) {
   if (a.n == 0) return hipSuccess;
-  const bool dual = a.kd != 0.0f && a.ce != 0.0f && a.temperature != 1.0f;
-  const dim3 grid(static_cast<unsigned>(a.n * a.slices));
-  auto go = [&](auto stats, auto grad) {
-    hipLaunchKernelGGL(stats, grid, dim3(kDsThreads), 0, stream, a);
-    hipLaunchKernelGGL(grad, grid, dim3(kDsThreads), 0, stream, a);
+  const bool two = a.kd != 0.0f && a.ce != 0.0f && a.temperature != 1.0f;
+  const int mode = !two ? kOne : a.temperature == 2.0f ? kSquare : a.temperature == 4.0f ? kFourth : kTwo;
+  const double row_bytes = static_cast<double>(a.vocab) * (dt == kBF16 ? 2 : 4);
+  const bool streams = a.dlogits && row_bytes * a.n * 2 > 256e6;
+  // Threads of a row's block.  Short rows: 256.  Long ones: 512, three blocks to
+  // a CU, while the rows in work fit the 256 MB memory-side cache for their
+  // second reading (50257 bf16: 229 us for 4000 rows, 240 with 256 threads, 273
+  // with 1024); with 1024 and two blocks beyond (128256 fp32: 932 us for 4096
+  // rows, 1211 with 512).  A few rows alone on the chip take 1024 early.
+  const int threads = a.n <= 256 ? (row_bytes > 16384.0 ? 1024 : 256)
+                      : row_bytes <= 65536.0 ? 256 : row_bytes <= 270e3 || !a.dlogits ? 512 : 1024;
+  auto launch = [&](auto d, auto m) {
+    constexpr int D = decltype(d)::value, M = decltype(m)::value;
+    if (a.slices > 0) {
+      const dim3 grid(static_cast<unsigned>(a.n * a.slices));
+      hipLaunchKernelGGL((distill_slice_kernel<D, M>), grid, dim3(kSliceThreads), 0, stream, a);
+      hipLaunchKernelGGL((distill_join_kernel<D, M>), a.dlogits ? grid : dim3(static_cast<unsigned>(a.n)),
+                         dim3(kSliceThreads), 0, stream, a);
+    } else {
+      const dim3 grid(static_cast<unsigned>(a.n));
+      auto rows = [&](auto t, auto st, auto r) {
+        constexpr int N = decltype(t)::value;
+        hipLaunchKernelGGL((distill_row_kernel<D, M, N, decltype(st)::value, decltype(r)::value>), grid, dim3(N), 0,
+                           stream, a);
+      };
+      auto by_stream = [&](auto t, auto r) {
+        if (streams) rows(t, std::true_type{}, r);
+        else rows(t, std::false_type{}, r);
+      };
+      using None = std::integral_constant<int, 0>;
+      if (threads == 1024) by_stream(std::integral_constant<int, 1024>{}, None{});
+      else if (threads == 256) by_stream(std::integral_constant<int, 256>{}, None{});
+      else if (a.dlogits) by_stream(std::integral_constant<int, 512>{}, std::integral_constant<int, kHeld>{});
+      else rows(std::integral_constant<int, 512>{}, std::false_type{}, None{});
+    }
   };
-  if (dt == kBF16) {
-    if (dual) go(distill_stats_kernel<kBF16, true>, distill_grad_kernel<kBF16, true>);
-    else go(distill_stats_kernel<kBF16, false>, distill_grad_kernel<kBF16, false>);
-  } else {
-    if (dual) go(distill_stats_kernel<kF32, true>, distill_grad_kernel<kF32, true>);
-    else go(distill_stats_kernel<kF32, false>, distill_grad_kernel<kF32, false>);
-  }
+  auto by_mode = [&](auto d) {
+    if (mode == kOne) launch(d, std::integral_constant<int, kOne>{});
+    else if (mode == kTwo) launch(d, std::integral_constant<int, kTwo>{});
+    else if (mode == kSquare) launch(d, std::integral_constant<int, kSquare>{});
+    else launch(d, std::integral_constant<int, kFourth>{});
+  };
+  if (dt == kBF16) by_mode(std::integral_constant<int, kBF16>{});
+  else by_mode(std::integral_constant<int, kF32>{});
   return hipGetLastError();
 }
 

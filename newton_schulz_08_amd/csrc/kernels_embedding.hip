@@ -220,7 +220,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanArgs a, in
   }
   __syncthreads();
   const int i0 = blockIdx.x * a.items;
-  const int i1 = min(a.n, i0 + a.items);
+  const int i1 = least(a.n, i0 + a.items);
   for (int i = i0 + tid; i < i1; i += kPlanThreads) {
     const unsigned k = pass == 0 ? plan_key(a, i) : gmem(a.key[(pass + 1) & 1])[i];
     atomicAdd(&hist[(k >> shift) & (digits - 1)], 1);
@@ -405,8 +405,8 @@ __global__ __launch_bounds__(kEgThreads) void egrad_kernel(EmbedGradArgs a, int 
   const int64_t chunk = (group << (8 - log_tpr)) + (tid >> log_tpr);
   const int64_t col = (static_cast<int64_t>(ct) * tpr + (tid & (tpr - 1))) * C;
   if (chunk >= a.chunks || col >= a.dim) return;
-  const int cols = static_cast<int>(min<int64_t>(C, a.dim - col));
-  const int64_t p0 = chunk * a.chunk, p1 = min(a.n, p0 + a.chunk);
+  const int cols = static_cast<int>(least<int64_t>(C, a.dim - col));
+  const int64_t p0 = chunk * a.chunk, p1 = least(a.n, p0 + a.chunk);
   const T* dout = static_cast<const T*>(a.dout) + col;
   int cur = gmem(a.slot)[p0];
   if (cur < 0) return;
@@ -432,7 +432,7 @@ __global__ __launch_bounds__(kEgThreads) void egrad_kernel(EmbedGradArgs a, int 
     float v[U][C];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t q = min(p + u, p1 - 1);
+      const int64_t q = least(p + u, p1 - 1);
       s[u] = gmem(a.slot)[q];
       const int t = gmem(a.order)[q];
       if (p + u >= p1 || static_cast<unsigned>(t) >= a.n) s[u] = -1;
@@ -478,13 +478,13 @@ __global__ __launch_bounds__(kEgThreads) void egrad_join_kernel(EmbedGradArgs a)
   int64_t last = chunk + 1;
   while (true) {
     const int64_t k = last + lane;
-    const uint64_t in = __ballot(k < a.chunks && gmem(a.slot)[min(k, static_cast<int64_t>(a.chunks) - 1) * a.chunk] == seg);
+    const uint64_t in = __ballot(k < a.chunks && gmem(a.slot)[least(k, static_cast<int64_t>(a.chunks) - 1) * a.chunk] == seg);
     const int m = in == ~0ull ? 64 : __builtin_ctzll(~in);
     last += m;
     if (m < 64) break;
   }
   const int64_t col = static_cast<int64_t>(ct) * 256 + lane * 4;
-  const int cols = static_cast<int>(max<int64_t>(0, min<int64_t>(4, a.dim - col)));
+  const int cols = static_cast<int>(most<int64_t>(0, least<int64_t>(4, a.dim - col)));
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int64_t k = chunk + 1 + w; k < last; k += 4)
     for (int e = 0; e < cols; ++e) acc[e] += gmem(a.part)[2 * k * a.dim + col + e];

@@ -226,7 +226,7 @@ __device__ __forceinline__ Place place(const QkArgs& a, int log_lanes, int block
   p.t = lane & ((1 << log_lanes) - 1);
   p.any = 2 * P * p.t < a.dim;
   const int group = lane >> log_lanes, log_groups = 6 - log_lanes;
-  const int lh = min(pick(a.log_heads, p.which), log_groups);
+  const int lh = least(pick(a.log_heads, p.which), log_groups);
   p.heads_at_once = 1 << lh;
   p.tokens_at_once = 1 << (log_groups - lh);
   p.head = group & (p.heads_at_once - 1);
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_kernel(QkArgs a, int log_l
   next.clear();
   if (here && h0 + p.head < heads) next.template load<STREAM>(a, src + static_cast<int64_t>(h0 + p.head) * a.dim, p.t);
   float c[P], s[P], wa[P], wb[P];
-  const int kind = token_angles<P, VEC>(a, min(token, a.n - 1), p.any ? p.t : 0, c, s);
+  const int kind = token_angles<P, VEC>(a, least(token, a.n - 1), p.any ? p.t : 0, c, s);
   load_gain<WDT, P, VEC>(a, p.which, p.any ? p.t : 0, wa, wb);
   for (int k = 0; k < passes; ++k) {
     const int h = h0 + k * p.heads_at_once + p.head;
@@ -310,7 +310,7 @@ __global__ __launch_bounds__(kQkThreads) void qk_norm_grad_kernel(QkArgs a, int 
     const int64_t token = t0 + p.tok;
     const bool here = p.any && token < a.n;
     float c[P], s[P];
-    const int kind = token_angles<P, VEC>(a, min(token, a.n - 1), p.any ? p.t : 0, c, s);
+    const int kind = token_angles<P, VEC>(a, least(token, a.n - 1), p.any ? p.t : 0, c, s);
     for (int h = p.head; h - p.head < heads; h += p.heads_at_once) {
       const bool on = here && h < heads;
       float x[P], y[P], u[P], v[P];

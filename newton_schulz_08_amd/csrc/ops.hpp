@@ -101,13 +101,12 @@ struct DistillArgs {
   const float* row_weight; // nullptr: 1
   float* losses;
   void* dlogits;           // nullptr: loss only
-  float* part;             // n x slices x 8
+  float* part;             // n x slices x 8 (slices > 0)
   int64_t n, vocab, stride, dstride;
   int k, idx64;
-  int slices;
+  int slices;              // 0: a block takes a whole row; else blocks per row
   int64_t slice_len;
   float temperature, kd, ce, grad_scale;
-  int vec;                 // rows start on 16-byte boundaries
 };
 hipError_t launch_distill(int dt, const DistillArgs& a, hipStream_t stream);
 
@@ -136,6 +135,10 @@ hipError_t launch_qk_norm(int dt, int w_dt, const QkArgs& a, hipStream_t stream)
 hipError_t launch_qk_norm_grad(int dt, int w_dt, const QkArgs& a, hipStream_t stream);
 
 #if defined(__HIPCC__)
+// Of integers of one type: `min` and `max` of 64-bit integers may go through floating point.
+template <typename T> __device__ __forceinline__ T least(T a, T b) { return a < b ? a : b; }
+template <typename T> __device__ __forceinline__ T most(T a, T b) { return a > b ? a : b; }
+
 // An index array's entry, int32 or int64.
 __device__ __forceinline__ int64_t load_index(const void* p, int64_t i, int is64) {
   return is64 ? gmem(static_cast<const int64_t*>(p))[i] : static_cast<int64_t>(gmem(static_cast<const int*>(p))[i]);
@@ -148,8 +151,35 @@ template <> struct OpElem<kF32> { using T = float; };
 typedef __bf16 bf16v8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16v4 __attribute__((ext_vector_type(4)));
 
-// N consecutive elements (N = 4 or 8, the address aligned to the whole, fp32
-// to 16 bytes) to and from fp32.
+// N consecutive elements (N = 4 or 8) to and from fp32.  load_n and store_n:
+// the address is aligned to the whole (fp32: to 16 bytes).  load_any and
+// store_any: aligned to one element; gfx950's global accesses take any address,
+// at the price of a second cache line now and then.
+template <typename T, int N> struct Loose {
+  typedef T V __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+};
+template <int N, typename T> __device__ __forceinline__ void load_any(const T* p, float* v) {
+  constexpr int M = 16 / sizeof(T) < N ? 16 / sizeof(T) : N;
+  using V = typename Loose<T, M>::V;
+#pragma unroll
+  for (int h = 0; h < N / M; ++h) {
+    const V x = *reinterpret_cast<gptr<const V>>(gmem(p + M * h));
+#pragma unroll
+    for (int e = 0; e < M; ++e) v[M * h + e] = static_cast<float>(x[e]);
+  }
+}
+template <int N, bool STREAM = false, typename T> __device__ __forceinline__ void store_any(T* p, const float* v) {
+  constexpr int M = 16 / sizeof(T) < N ? 16 / sizeof(T) : N;
+  using V = typename Loose<T, M>::V;
+#pragma unroll
+  for (int h = 0; h < N / M; ++h) {
+    V x;
+#pragma unroll
+    for (int e = 0; e < M; ++e) x[e] = static_cast<T>(v[M * h + e]);
+    if constexpr (STREAM) __builtin_nontemporal_store(x, reinterpret_cast<gptr<V>>(gmem(p + M * h)));
+    else *reinterpret_cast<gptr<V>>(gmem(p + M * h)) = x;
+  }
+}
 template <int N> __device__ __forceinline__ void load_n(const float* p, float* v) {
 #pragma unroll
   for (int h = 0; h < N / 4; ++h) {

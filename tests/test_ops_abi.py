@@ -107,25 +107,27 @@ def test_adamw_rows(lib):
         (dict(m=addr(3) + 2), BAD), (dict(index=addr(3)), BAD)])
 
 
-LOSS = dict(logits=addr(0), n=4, vocab=100, stride=104, dt=1, index=addr(1), idt=3, teacher=addr(2), k=5, labels=addr(3),
-            t=2.0, kd=1.0, ce=0.5, w=addr(4), scale=1.0, losses=addr(5), dz=addr(6), dstride=100, ws=addr(7), bytes=1 << 20,
+LOSS = dict(logits=addr(0), n=4, vocab=80000, stride=80008, dt=1, index=addr(1), idt=3, teacher=addr(2), k=5, labels=addr(3),
+            t=2.0, kd=1.0, ce=0.5, w=addr(4), scale=1.0, losses=addr(5), dz=addr(6), dstride=80000, ws=addr(7), bytes=1 << 20,
             stream=None)
 
 
 def test_distill_loss(lib):
     accepted(lib.dmuon_distill_loss, LOSS)
-    accepted(lib.dmuon_distill_loss, dict(LOSS, dz=addr(0), dstride=104))              # in place
+    accepted(lib.dmuon_distill_loss, dict(LOSS, dz=addr(0), dstride=80008))              # in place
     accepted(lib.dmuon_distill_loss, dict(LOSS, dz=0, dstride=0, labels=0, ce=0.0, w=0))
     accepted(lib.dmuon_distill_loss, dict(LOSS, k=0, kd=0.0, index=0, teacher=0))
     accepted(lib.dmuon_distill_loss, dict(LOSS, n=1, stride=0, dstride=0))
-    need = nsa.distill_loss_workspace_bytes(4, 100)
+    accepted(lib.dmuon_distill_loss, dict(LOSS, vocab=4096, ws=0, bytes=0))   # a block takes the whole row
+    need = nsa.distill_loss_workspace_bytes(4, 80000)
+    assert need > 0
     refused(lib.dmuon_distill_loss, LOSS, [
         (dict(dt=2), TYPE), (dict(idt=0), TYPE), (dict(n=-1), BAD), (dict(vocab=0), BAD), (dict(k=-1), BAD),
         (dict(k=1025), BAD), (dict(t=0.0), BAD), (dict(t=-1.0), BAD), (dict(t=NAN), BAD), (dict(t=INF), BAD),
         (dict(kd=NAN), BAD), (dict(ce=INF), BAD), (dict(scale=NAN), BAD), (dict(k=0), BAD), (dict(labels=0), BAD),
-        (dict(stride=99), BAD), (dict(dstride=99), BAD), (dict(logits=0), BAD), (dict(index=0), BAD),
+        (dict(stride=79999), BAD), (dict(dstride=79999), BAD), (dict(logits=0), BAD), (dict(index=0), BAD),
         (dict(teacher=0), BAD), (dict(losses=0), BAD), (dict(ws=0), WS), (dict(bytes=need - 1), WS),
-        (dict(dz=addr(0)), BAD), (dict(dz=addr(0) + 2, dstride=104), BAD), (dict(losses=addr(4)), BAD),
+        (dict(dz=addr(0)), BAD), (dict(dz=addr(0) + 2, dstride=80008), BAD), (dict(losses=addr(4)), BAD),
         (dict(logits=addr(0) + 1), BAD), (dict(labels=addr(3) + 4), BAD), (dict(ws=addr(7) + 8), WS)])
 
 
