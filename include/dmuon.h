@@ -342,8 +342,8 @@ int dmuon_adamw_step(int count, void* const* params, const void* const* grads, f
  *   captures).  Workspaces are then the graph's: two graphs, or a graph and
  *   eager calls, share one only if they never overlap in time.
  * - All pointers belong to the current device.
- * - 16-byte aligned pointers with row lengths that are multiples of 8 take the
- *   vector path; anything aligned to its element size is accepted.
+ * - Any pointer aligned to its element size is accepted; 16-byte aligned rows are
+ *   the fastest.
  * - bf16 results are rounded once (RNE) from fp32.
  * ------------------------------------------------------------------------ */
 

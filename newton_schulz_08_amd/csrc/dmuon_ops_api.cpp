@@ -157,7 +157,7 @@ int check_tokens(int64_t n, int64_t vocab) {
 int egrad_chunk(int64_t n, int64_t dim, int dout_dtype) {
   const int64_t c = dout_dtype == kBF16 ? 8 : 4;
   const int64_t tiles = ((dim + c - 1) / c + kEgThreads - 1) / kEgThreads;
-  int chunk = 64;
+  int chunk = 32;
   while (chunk > 8 && (n + chunk - 1) / chunk * tiles < 2048) chunk /= 2;
   return chunk;
 }
@@ -273,7 +273,6 @@ int dmuon_embedding_forward(const void* table, int64_t vocab, int64_t dim, int t
     a.dim = dim;
     a.scale = scale;
     a.tok64 = token_dtype == DMUON_I64;
-    a.vec = dim % 8 == 0 && aligned(table, 16) && aligned(out, 16);
     return launched("embedding", kKEmbed, 0.0, static_cast<double>(n) * dim * (ts + os), hip_stream, capturing,
                     [&] { return launch_embed(table_dtype, out_dtype, a, static_cast<hipStream_t>(hip_stream)); });
   });
@@ -386,7 +385,6 @@ int dmuon_embedding_backward(const void* dout, int64_t n, int64_t dim, int dout_
     a.form = form;
     a.chunk = egrad_chunk(n, dim, dout_dtype);
     a.chunks = static_cast<int>((n + a.chunk - 1) / a.chunk);
-    a.vec = dim % 8 == 0 && aligned(dout, 16) && aligned(grad, 16);
     const double out_rows = form == DMUON_EMBED_ADD ? 2.0 * cap : static_cast<double>(grad_rows);
     return launched("embedding gradient", kKEmbedGrad, static_cast<double>(n) * dim,
                     static_cast<double>(dim) * (static_cast<double>(n) * ds + out_rows * gs), hip_stream, capturing,
@@ -423,9 +421,6 @@ int dmuon_adamw_rows_step(void* param, const void* grad_rows, int64_t n_grad_row
     a.rows = rows;
     a.dim = dim;
     a.n_grad_rows = n_grad_rows;
-    const size_t chunk = static_cast<size_t>(4 * es);
-    a.vec = dim % 4 == 0 && aligned(param, chunk) && aligned(grad_rows, chunk) && aligned(exp_avg, 16) &&
-            aligned(exp_avg_sq, 16);
     // the dense step's constants, formed alike
     const double t = static_cast<double>(step);
     a.hp.decay = static_cast<float>(1.0 - static_cast<double>(lr) * static_cast<double>(weight_decay));

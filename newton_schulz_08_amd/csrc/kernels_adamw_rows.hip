@@ -35,40 +35,55 @@ __device__ __forceinline__ const T* grad_row(const AdamRowsArgs& a, int64_t r) {
 }
 
 // The table is cut into 4096-element tiles, one block each, as in the dense
-// step.  With dim a multiple of 4 a chunk of four elements lies in one row;
-// `magic` = floor(2^32 / dim) gives that row by a multiplication (the quotient
-// is at most one short for the offsets that occur, below 2^17).
+// step; a lane takes four consecutive elements of all arrays at a time.
+// `magic` = floor(2^32 / dim) gives their row by a multiplication (the quotient
+// is at most one short for the offsets that occur, below 2^17).  Four elements
+// that lie in two rows look their gradients up one by one.
 template <int DT>
 __global__ __launch_bounds__(kAdamThreads) void adamw_rows_kernel(AdamRowsArgs a, int64_t tiles, unsigned magic) {
   using T = typename OpElem<DT>::T;
   T* pp = static_cast<T*>(a.p);
   const int64_t numel = a.rows * a.dim;
+  const unsigned dim = static_cast<unsigned>(a.dim);
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int64_t base = t * kAdamTile;
     const int64_t r0 = base / a.dim;
-    const unsigned c0 = static_cast<unsigned>(base - r0 * a.dim), dim = static_cast<unsigned>(a.dim);
-    if (a.vec && base + kAdamTile <= numel) {
-      float p[kAdamChunks][4], m[kAdamChunks][4], v[kAdamChunks][4], g[kAdamChunks][4];
+    const unsigned c0 = static_cast<unsigned>(base - r0 * a.dim);
+    auto place = [&](unsigned o, unsigned* col) {   // row behind r0 and column of the tile's element o
+      const unsigned x = c0 + o;
+      unsigned q = __umulhi(x, magic);
+      *col = x - q * dim;
+      if (*col >= dim) {
+        *col -= dim;
+        ++q;
+      }
+      return q;
+    };
+    if (base + kAdamTile <= numel) {
+      float p[kAdamChunks][4], m[kAdamChunks][4], v[kAdamChunks][4], g[kAdamChunks][4] = {};
 #pragma unroll
       for (int c = 0; c < kAdamChunks; ++c) {
         const unsigned o = (c * kAdamThreads + threadIdx.x) * 4;
-        load_n<4>(pp + base + o, p[c]);
-        load_n<4>(a.m + base + o, m[c]);
-        load_n<4>(a.v + base + o, v[c]);
+        load_any<4>(pp + base + o, p[c]);
+        load_any<4>(a.m + base + o, m[c]);
+        load_any<4>(a.v + base + o, v[c]);
       }
 #pragma unroll
       for (int c = 0; c < kAdamChunks; ++c) {
-        const unsigned x = c0 + (c * kAdamThreads + threadIdx.x) * 4;
-        unsigned q = __umulhi(x, magic);
-        unsigned rest = x - q * dim;
-        if (rest >= dim) {
-          rest -= dim;
-          ++q;
-        }
-        const T* gr = grad_row<T>(a, r0 + q);
+        const unsigned o = (c * kAdamThreads + threadIdx.x) * 4;
+        unsigned col;
+        const unsigned q = place(o, &col);
+        if (col + 4 <= dim) {
+          const T* gr = grad_row<T>(a, r0 + q);
+          if (gr) load_any<4>(gr + col, g[c]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) g[c][e] = 0.0f;
-        if (gr) load_n<4>(gr + rest, g[c]);
+          for (int e = 0; e < 4; ++e) {
+            const unsigned qe = place(o + e, &col);
+            const T* gr = grad_row<T>(a, r0 + qe);
+            if (gr) g[c][e] = static_cast<float>(gmem(gr)[col]);
+          }
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -76,9 +91,9 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_rows_kernel(AdamRowsArgs a
         const unsigned o = (c * kAdamThreads + threadIdx.x) * 4;
 #pragma unroll
         for (int e = 0; e < 4; ++e) adamw_elem(p[c][e], g[c][e], m[c][e], v[c][e], a.hp);
-        store_n<4>(pp + base + o, p[c]);
-        store_n<4>(a.m + base + o, m[c]);
-        store_n<4>(a.v + base + o, v[c]);
+        store_any<4>(pp + base + o, p[c]);
+        store_any<4>(a.m + base + o, m[c]);
+        store_any<4>(a.v + base + o, v[c]);
       }
     } else {
       for (int o = threadIdx.x; o < kAdamTile; o += kAdamThreads) {

@@ -24,11 +24,12 @@ __device__ __forceinline__ int popc_below(uint64_t mask) {
 }
 
 // ---------------------------------------------------------------- lookup
+// 2^log_tpr threads take a row, 16 bytes of the output each at a time.
 template <int TDT, int ODT>
 __global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a, int log_tpr) {
   using T = typename OpElem<TDT>::T;
   using O = typename OpElem<ODT>::T;
-  constexpr int C = ODT == kBF16 ? 8 : 4;   // elements of a 16-byte store
+  constexpr int C = ODT == kBF16 ? 8 : 4;
   constexpr int U = 2;
   const int tpr = 1 << log_tpr;
   const int64_t row = (static_cast<int64_t>(blockIdx.x) << (8 - log_tpr)) + (threadIdx.x >> log_tpr);
@@ -38,32 +39,21 @@ __global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a, int log_tpr) {
   const bool known = tok >= 0 && tok < a.vocab;
   const T* src = static_cast<const T*>(a.table) + (known ? tok : 0) * a.dim;
   O* dst = static_cast<O*>(a.out) + row * a.dim;
-  if (a.vec) {
-    const int64_t nch = a.dim / C;
-    for (int64_t c0 = lane; c0 < nch; c0 += tpr * U) {
-      float v[U][C];
+  const int64_t nch = a.dim / C;
+  for (int64_t c0 = lane; c0 < nch; c0 += tpr * U) {
+    float v[U][C] = {};
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t c = c0 + u * tpr;
-        if (c < nch && known) {
-          load_n<C>(src + c * C, v[u]);
+    for (int u = 0; u < U; ++u)
+      if (c0 + u * tpr < nch && known) load_any<C>(src + (c0 + u * tpr) * C, v[u]);
 #pragma unroll
-          for (int e = 0; e < C; ++e) v[u][e] *= a.scale;
-        } else {
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
-          for (int e = 0; e < C; ++e) v[u][e] = 0.0f;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t c = c0 + u * tpr;
-        if (c < nch) store_n<C>(dst + c * C, v[u]);
-      }
+      for (int e = 0; e < C; ++e) v[u][e] *= a.scale;
+      if (c0 + u * tpr < nch) store_any<C>(dst + (c0 + u * tpr) * C, v[u]);
     }
-  } else {
-    for (int64_t e = lane; e < a.dim; e += tpr)
-      gmem(dst)[e] = static_cast<O>(known ? static_cast<float>(gmem(src)[e]) * a.scale : 0.0f);
   }
+  for (int64_t e = nch * C + lane; e < a.dim; e += tpr)
+    gmem(dst)[e] = static_cast<O>(known ? static_cast<float>(gmem(src)[e]) * a.scale : 0.0f);
 }
 
 // ---------------------------------------------------------------- plan
@@ -105,8 +95,11 @@ __device__ __forceinline__ int block_scan(int v, int* wave_tot, int* sum) {
   return v + before;
 }
 
-__device__ __forceinline__ void fill_minus_one(int* p, int64_t n, int64_t first, int64_t step) {
-  for (int64_t i = first; i < n; i += step) gmem(p)[i] = -1;
+// p[0 .. n) = -1 by `threads` threads.
+__device__ __forceinline__ void fill_minus_one(int* p, int64_t n, int64_t thread, int64_t threads) {
+  using V = Loose<int, 4>::V;
+  for (int64_t i = thread; i < n / 4; i += threads) *reinterpret_cast<gptr<V>>(gmem(p + 4 * i)) = V{-1, -1, -1, -1};
+  for (int64_t i = n / 4 * 4 + thread; i < n; i += threads) gmem(p)[i] = -1;
 }
 
 // All of the plan in one block for n <= kPlanSmall: the pairs stay in LDS.
@@ -127,7 +120,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_small_kernel(PlanArgs a) {
   int cur = 0;
   for (int pass = 0; pass < a.passes; ++pass, cur ^= 1) {
     const int shift = pass * a.bits;
-    for (int i = tid; i < kPlanWaves * digits; i += kPlanThreads) cnt[i / digits][i & mask] = 0;
+    for (int i = tid; i < kPlanWaves * digits; i += kPlanThreads) cnt[i >> a.bits][i & mask] = 0;
     __syncthreads();
     int rank[kPer];
     unsigned dig[kPer];
@@ -233,6 +226,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanArgs a, in
 // block adds the counts of the waves and blocks before it.
 __global__ __launch_bounds__(kPlanThreads) void plan_scatter_kernel(PlanArgs a, int pass) {
   __shared__ int cnt[kPlanWaves][kPlanMaxDigits];
+  __shared__ int part[2][kPlanThreads];
   __shared__ int wave_tot[kPlanWaves];
   const int tid = threadIdx.x, w = tid >> 6, lane = lane_id();
   const int digits = 1 << a.bits, shift = pass * a.bits;
@@ -243,7 +237,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_scatter_kernel(PlanArgs a, 
   int* iout = a.idx[pass & 1];
   const int per_wave = a.items / kPlanWaves;   // a multiple of 64
   const int64_t w0 = static_cast<int64_t>(blockIdx.x) * a.items + w * per_wave;
-  for (int i = tid; i < kPlanWaves * digits; i += kPlanThreads) cnt[i / digits][i & mask] = 0;
+  for (int i = tid; i < kPlanWaves * digits; i += kPlanThreads) cnt[i >> a.bits][i & mask] = 0;
   __syncthreads();
   // counts of each wave
   for (int j = 0; j < per_wave; j += 64) {
@@ -258,14 +252,28 @@ __global__ __launch_bounds__(kPlanThreads) void plan_scatter_kernel(PlanArgs a, 
     __builtin_amdgcn_wave_barrier();
   }
   __syncthreads();
+  // tokens of each digit in all blocks and in the ones before: as many threads
+  // per digit as there are, each on every `groups`-th block
+  const int groups = kPlanThreads >> a.bits, digit = tid & (digits - 1), group = tid >> a.bits;
   int before = 0, total = 0;
-  if (tid < digits) {
-    for (int b = 0; b < a.blocks; ++b) {
-      const int c = gmem(a.counts)[b * digits + tid];
-      before += b < static_cast<int>(blockIdx.x) ? c : 0;
-      total += c;
-    }
+#pragma unroll 8
+  for (int b = group; b < a.blocks; b += groups) {
+    const int c = gmem(a.counts)[b * digits + digit];
+    before += b < static_cast<int>(blockIdx.x) ? c : 0;
+    total += c;
   }
+  if (groups > 1) {
+    part[0][tid] = before;
+    part[1][tid] = total;
+    __syncthreads();
+    before = total = 0;
+    if (tid < digits)
+      for (int g = 0; g < groups; ++g) {
+        before += part[0][g * digits + tid];
+        total += part[1][g * digits + tid];
+      }
+  }
+  if (tid >= digits) total = 0;
   int all;
   const int first = block_scan(total, wave_tot, &all) - total;
   if (tid < digits) {
@@ -301,7 +309,7 @@ __device__ __forceinline__ bool plan_head(const unsigned* key, int64_t i, unsign
   return k != none && (i == 0 || gmem(key)[i - 1] != k);
 }
 
-// Run heads of one block's sorted tokens: counted, then written.
+// Run heads of one block's sorted tokens.
 __global__ __launch_bounds__(kPlanThreads) void plan_heads_kernel(PlanArgs a) {
   __shared__ int wave_tot[kPlanWaves];
   const unsigned* key = a.key[(a.passes + 1) & 1];
@@ -314,17 +322,31 @@ __global__ __launch_bounds__(kPlanThreads) void plan_heads_kernel(PlanArgs a) {
   if (threadIdx.x == 0) gmem(a.heads)[blockIdx.x] = all;
 }
 
-__global__ __launch_bounds__(kPlanThreads) void plan_rows_kernel(PlanArgs a) {
+// Numbers the runs.  The heads before a block's tokens come from
+// plan_heads_kernel, or, for batches short enough (kPlanRecount), from reading
+// all of the sorted tokens before them, which costs less than that launch.
+__global__ __launch_bounds__(kPlanThreads) void plan_rows_kernel(PlanArgs a, int recount) {
   __shared__ int wave_tot[kPlanWaves];
   const unsigned* key = a.key[(a.passes + 1) & 1];
   const int* idx = a.idx[(a.passes + 1) & 1];
   const unsigned none = static_cast<unsigned>(a.vocab);
   const int tid = threadIdx.x;
-  const int h = tid < a.blocks ? gmem(a.heads)[tid] : 0;
-  int before, all;
-  block_scan(tid < static_cast<int>(blockIdx.x) ? h : 0, wave_tot, &before);
-  block_scan(h, wave_tot, &all);
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * a.items;
+  int mine = 0, before;
+  if (recount) {
+    // i0 is a multiple of the threads; four tokens and the one before them at a time
+    using V = Loose<unsigned, 4>::V;
+#pragma unroll 4
+    for (int j = tid * 4; j < i0; j += kPlanThreads * 4) {
+      const V k = *reinterpret_cast<gptr<const V>>(gmem(key + j));
+      const unsigned p = gmem(key)[j > 0 ? j - 1 : 0];
+      mine += (k[0] != none && (j == 0 || k[0] != p)) + (k[1] != none && k[1] != k[0]) + (k[2] != none && k[2] != k[1]) +
+              (k[3] != none && k[3] != k[2]);
+    }
+  } else if (tid < static_cast<int>(blockIdx.x)) {
+    mine = gmem(a.heads)[tid];
+  }
+  block_scan(mine, wave_tot, &before);
   for (int j = 0; j < a.items; j += kPlanThreads) {
     const int64_t i = i0 + j + tid;
     const bool head = i < a.n && plan_head(key, i, none);
@@ -341,33 +363,66 @@ __global__ __launch_bounds__(kPlanThreads) void plan_rows_kernel(PlanArgs a) {
     }
     before += here;
   }
-  if (blockIdx.x == 0 && tid == 0) gmem(a.count)[0] = all;
+  if (blockIdx.x == gridDim.x - 1 && tid == 0) gmem(a.count)[0] = before;
 }
 
 // ---------------------------------------------------------------- gradient
 // The sorted positions are cut into chunks of equal length, so that work is
 // even however often a token occurs.  A thread owns one 16-byte column chunk
 // and walks its chunk's positions, adding rows of dout; where the run of a
-// token ends it writes the row.  A run that crosses a chunk's edge leaves fp32
-// sums in `part` (index 2c: the run that began before chunk c; 2c + 1: the one
-// that goes on behind it), which egrad_join_kernel adds up.
+// token ends it writes the row.  A run that crosses a chunk's edge is short when
+// it covers no chunk whole: the chunk in which it begins then walks on to its
+// end, and the next one starts behind it.  A longer run is cut at the edges and
+// leaves fp32 sums in `part` (index 2c: of the run that began before chunk c;
+// 2c + 1: of one that goes on behind it), which egrad_join_kernel adds up.
+struct Edges {
+  int first, last;            // slots of the chunk's first and last position
+  bool inherited, crossing;   // the first run began before, the last one goes on behind
+  bool cut_before, cut_behind;// ... and is cut there
+};
+__device__ __forceinline__ Edges chunk_edges(const EmbedGradArgs& a, int64_t chunk) {
+  const int64_t p0 = chunk * a.chunk, p1 = least(a.n, p0 + a.chunk);
+  const int far_before = p0 >= a.chunk ? gmem(a.slot)[p0 - a.chunk] : -1;
+  const int before = p0 > 0 ? gmem(a.slot)[p0 - 1] : -1;
+  const int behind = p1 < a.n ? gmem(a.slot)[p1] : -1;
+  const int far_behind = p1 + a.chunk <= a.n ? gmem(a.slot)[p1 + a.chunk - 1] : -1;
+  Edges e;
+  e.first = gmem(a.slot)[p0];
+  e.last = gmem(a.slot)[p1 - 1];
+  const bool whole = p1 - p0 == a.chunk && e.first == e.last;   // one run covers this chunk
+  e.inherited = e.first >= 0 && before == e.first;
+  e.crossing = e.last >= 0 && behind == e.last;
+  e.cut_before = e.inherited && (far_before == e.first || whole);
+  e.cut_behind = e.crossing && (whole || far_behind == e.last);
+  return e;
+}
+
+// Writes C columns from `col` of a slot's row, without the first `skip` (which
+// another thread owns); cols < C only where the row is shorter than C.
 template <int GDT, int C>
-__device__ __forceinline__ void grad_write(const EmbedGradArgs& a, int slot, int64_t col, int cols, float* v) {
+__device__ __forceinline__ void grad_write(const EmbedGradArgs& a, int slot, int64_t col, int skip, int cols, float* v) {
   using G = typename OpElem<GDT>::T;
   const int64_t row = a.form == kGradRows ? slot : gmem(a.rows)[slot];
   if (row < 0 || row >= (a.form == kGradRows ? static_cast<int64_t>(a.cap) : a.vocab)) return;
   G* dst = static_cast<G*>(a.grad) + row * a.dim + col;
-  if (cols == C && a.vec) {
-    float old[C];
-    if (a.form == kGradAdd) load_n<C>(dst, old);
+  if (skip == 0 && cols == C) {
+    if (a.form == kGradAdd) {
+      float old[C];
+      load_any<C>(dst, old);
 #pragma unroll
-    for (int e = 0; e < C; ++e) v[e] = a.form == kGradAdd ? fmaf(v[e], a.scale, old[e]) : v[e] * a.scale;
-    store_n<C>(dst, v);
-  } else {
-    for (int e = 0; e < cols; ++e) {
-      const float old = a.form == kGradAdd ? static_cast<float>(gmem(dst)[e]) : 0.0f;
-      gmem(dst)[e] = static_cast<G>(a.form == kGradAdd ? fmaf(v[e], a.scale, old) : v[e] * a.scale);
+      for (int e = 0; e < C; ++e) v[e] = fmaf(v[e], a.scale, old[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < C; ++e) v[e] *= a.scale;
     }
+    store_any<C>(dst, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < C; ++e)
+      if (e >= skip && e < cols) {
+        const float old = a.form == kGradAdd ? static_cast<float>(gmem(dst)[e]) : 0.0f;
+        gmem(dst)[e] = static_cast<G>(a.form == kGradAdd ? fmaf(v[e], a.scale, old) : v[e] * a.scale);
+      }
   }
 }
 
@@ -384,18 +439,16 @@ __global__ __launch_bounds__(kEgThreads) void egrad_kernel(EmbedGradArgs a, int 
     const int64_t r0 = (blockIdx.x - sum_blocks) * kEgZeroRows;
     const int64_t rows = a.form == kGradRows ? a.cap : a.vocab;
     const int used = a.form == kGradRows ? gmem(a.count)[0] : 0;
+    constexpr int Z = GDT == kBF16 ? 8 : 4;
+    const float zero[Z] = {};
     for (int r = 0; r < kEgZeroRows; ++r) {
       const int64_t row = r0 + r;
       if (row >= rows) break;
       if (a.form == kGradRows ? row < used : gmem(a.row_index)[row] >= 0) continue;
       G* dst = static_cast<G*>(a.grad) + row * a.dim;
-      constexpr int Z = GDT == kBF16 ? 8 : 4;
-      if (a.vec) {
-        const float zero[Z] = {};
-        for (int64_t e = tid * Z; e < a.dim; e += kEgThreads * Z) store_n<Z>(dst + e, zero);
-      } else {
-        for (int64_t e = tid; e < a.dim; e += kEgThreads) gmem(dst)[e] = static_cast<G>(0.0f);
-      }
+      const int64_t whole = a.dim / Z * Z;
+      for (int64_t e = tid * Z; e < whole; e += kEgThreads * Z) store_any<Z>(dst + e, zero);
+      for (int64_t e = whole + tid; e < a.dim; e += kEgThreads) gmem(dst)[e] = static_cast<G>(0.0f);
     }
     return;
   }
@@ -403,25 +456,51 @@ __global__ __launch_bounds__(kEgThreads) void egrad_kernel(EmbedGradArgs a, int 
   const int64_t group = blockIdx.x / col_tiles;
   const int ct = static_cast<int>(blockIdx.x - group * col_tiles);
   const int64_t chunk = (group << (8 - log_tpr)) + (tid >> log_tpr);
-  const int64_t col = (static_cast<int64_t>(ct) * tpr + (tid & (tpr - 1))) * C;
-  if (chunk >= a.chunks || col >= a.dim) return;
-  const int cols = static_cast<int>(least<int64_t>(C, a.dim - col));
-  const int64_t p0 = chunk * a.chunk, p1 = least(a.n, p0 + a.chunk);
+  int64_t col = (static_cast<int64_t>(ct) * tpr + (tid & (tpr - 1))) * C;
+  if (chunk >= a.chunks) return;
+  const bool mine = col < a.dim;   // lanes without columns still help to find the runs' ends
+  // the last columns of a row that is no multiple of C: a whole chunk that
+  // reaches back over columns of the thread before, and writes only its own
+  const int cols = static_cast<int>(least<int64_t>(C, a.dim));
+  const int skip = static_cast<int>(most<int64_t>(0, col + cols - a.dim));
+  col -= skip;
+  const Edges edges = chunk_edges(a, chunk);
+  if (edges.first < 0) return;
+  // length of the run of `slot` from position p on, known to be below a chunk
+  auto run = [&](int64_t p, int slot) -> int64_t {
+    if (log_tpr >= 6) {   // the wave works on one chunk: a lane a position (a chunk has at most 64)
+      const int64_t q = p + lane_id();
+      return __popcll(__ballot(lane_id() < a.chunk && q < a.n && gmem(a.slot)[least(q, a.n - 1)] == slot));
+    }
+    int64_t k = 0;
+    while (p + k < a.n && gmem(a.slot)[p + k] == slot) ++k;
+    return k;
+  };
+  int64_t p0 = chunk * a.chunk, p1 = least(a.n, p0 + a.chunk);
+  const int last = edges.last;
+  if (edges.inherited && !edges.cut_before) p0 += run(p0, edges.first);
+  if (edges.crossing && !edges.cut_behind && p0 < p1) p1 += run(p1, last);
+  if (p0 >= p1 || !mine) return;
   const T* dout = static_cast<const T*>(a.dout) + col;
   int cur = gmem(a.slot)[p0];
   if (cur < 0) return;
-  bool began_before = p0 > 0 && gmem(a.slot)[p0 - 1] == cur;
-  const int next = p1 < a.n ? gmem(a.slot)[p1] : -1;
+  bool began_before = edges.cut_before;
   float acc[C];
 #pragma unroll
   for (int e = 0; e < C; ++e) acc[e] = 0.0f;
-  auto flush = [&](bool last) {
-    const bool goes_on = last && next == cur;
+  auto flush = [&](bool at_end) {
+    const bool goes_on = at_end && edges.cut_behind && cur == last;
     if (began_before || goes_on) {
       float* dst = a.part + (2 * chunk + (began_before ? 0 : 1)) * a.dim + col;
-      for (int e = 0; e < cols; ++e) gmem(dst)[e] = acc[e];
+      if (skip == 0 && cols == C) {
+        store_any<C>(dst, acc);
+      } else {
+#pragma unroll
+        for (int e = 0; e < C; ++e)
+          if (e >= skip && e < cols) gmem(dst)[e] = acc[e];
+      }
     } else {
-      grad_write<GDT, C>(a, cur, col, cols, acc);
+      grad_write<GDT, C>(a, cur, col, skip, cols, acc);
     }
     began_before = false;
 #pragma unroll
@@ -429,21 +508,22 @@ __global__ __launch_bounds__(kEgThreads) void egrad_kernel(EmbedGradArgs a, int 
   };
   for (int64_t p = p0; p < p1; p += U) {
     int s[U];
-    float v[U][C];
+    float v[U][C] = {};
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t q = least(p + u, p1 - 1);
       s[u] = gmem(a.slot)[q];
       const int t = gmem(a.order)[q];
       if (p + u >= p1 || static_cast<unsigned>(t) >= a.n) s[u] = -1;
-      const T* src = dout + (s[u] >= 0 ? t : 0) * a.dim;
-      if (s[u] < 0) {
+      if (s[u] >= 0) {
+        const T* src = dout + t * a.dim;
+        if (cols == C) {
+          load_any<C>(src, v[u]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < C; ++e) v[u][e] = 0.0f;
-      } else if (cols == C && a.vec) {
-        load_n<C>(src, v[u]);
-      } else {
-        for (int e = 0; e < C; ++e) v[u][e] = e < cols ? static_cast<float>(gmem(src)[e]) : 0.0f;
+          for (int e = 0; e < C; ++e)
+            if (e < cols) v[u][e] = static_cast<float>(gmem(src)[e]);
+        }
       }
     }
 #pragma unroll
@@ -460,45 +540,76 @@ __global__ __launch_bounds__(kEgThreads) void egrad_kernel(EmbedGradArgs a, int 
   flush(true);
 }
 
-// Sums of the runs that cross chunk edges.  The block of the chunk in which
-// such a run begins adds its pieces: four waves take every fourth piece, then
-// the four sums are joined in order.
+// Sums of the runs that were cut.  A block looks through kJoinChunks chunks for
+// those in which such a run begins, and adds up the run's pieces in its 256
+// columns: four waves take every fourth piece, then the four sums are joined in
+// order.
+constexpr int kJoinChunks = 8;
 template <int GDT>
 __global__ __launch_bounds__(kEgThreads) void egrad_join_kernel(EmbedGradArgs a) {
   __shared__ float red[4][256];
-  const int64_t chunk = blockIdx.x;
-  const int ct = blockIdx.y;
-  const int64_t end = (chunk + 1) * a.chunk;
-  if (end >= a.n) return;
-  const int seg = gmem(a.slot)[end - 1];
-  if (seg < 0 || gmem(a.slot)[end] != seg) return;
-  if (chunk > 0 && gmem(a.slot)[chunk * a.chunk - 1] == seg) return;   // it began earlier: not ours
   const int lane = lane_id(), w = threadIdx.x >> 6;
-  // pieces: chunks behind this one that begin inside the run
-  int64_t last = chunk + 1;
-  while (true) {
-    const int64_t k = last + lane;
-    const uint64_t in = __ballot(k < a.chunks && gmem(a.slot)[least(k, static_cast<int64_t>(a.chunks) - 1) * a.chunk] == seg);
-    const int m = in == ~0ull ? 64 : __builtin_ctzll(~in);
-    last += m;
-    if (m < 64) break;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kJoinChunks;
+  bool owner = false;
+  int owner_slot = -1;
+  if (lane < kJoinChunks && c0 + lane < a.chunks) {
+    const Edges e = chunk_edges(a, c0 + lane);
+    owner = e.cut_behind && !(e.cut_before && e.first == e.last);
+    owner_slot = e.last;
   }
-  const int64_t col = static_cast<int64_t>(ct) * 256 + lane * 4;
-  const int cols = static_cast<int>(most<int64_t>(0, least<int64_t>(4, a.dim - col)));
-  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t k = chunk + 1 + w; k < last; k += 4)
-    for (int e = 0; e < cols; ++e) acc[e] += gmem(a.part)[2 * k * a.dim + col + e];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) red[w][lane * 4 + e] = acc[e];
-  __syncthreads();
-  if (w == 0 && cols > 0) {
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int e = 0; e < cols; ++e) {
-      v[e] = gmem(a.part)[(2 * chunk + 1) * a.dim + col + e];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[e] += red[k][lane * 4 + e];
+  const int64_t col0 = static_cast<int64_t>(blockIdx.y) * 256 + lane * 4;
+  const int cols = static_cast<int>(least<int64_t>(4, a.dim));
+  const int skip = static_cast<int>(least<int64_t>(4, most<int64_t>(0, col0 + cols - a.dim)));
+  const int64_t col = col0 - skip;   // as in egrad_kernel; skip == cols: nothing of the row is left
+  const bool on = col0 < a.dim;
+  for (uint64_t owners = __ballot(owner); owners; owners &= owners - 1) {
+    const int64_t chunk = c0 + __builtin_ctzll(owners);
+    const int seg = __shfl(owner_slot, static_cast<int>(chunk - c0), 64);
+    // pieces: the chunks behind this one that begin inside the run
+    int64_t last = chunk + 1;
+    while (true) {
+      const int64_t k = last + lane;
+      const uint64_t in =
+          __ballot(k < a.chunks && gmem(a.slot)[least(k, static_cast<int64_t>(a.chunks) - 1) * a.chunk] == seg);
+      const int m = in == ~0ull ? 64 : __builtin_ctzll(~in);
+      last += m;
+      if (m < 64) break;
     }
-    grad_write<GDT, 4>(a, seg, col, cols, v);
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto load = [&](int64_t index, float* v) {
+      const float* p = a.part + index * a.dim + col;
+      if (cols == 4) {
+        load_any<4>(p, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = e < cols ? gmem(p)[e] : 0.0f;
+      }
+    };
+    if (on) {
+      for (int64_t k0 = chunk + 1 + w; k0 < last; k0 += 4 * 8) {
+        float v[8][4] = {};
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (k0 + 4 * u < last) load(2 * (k0 + 4 * u), v[u]);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] += v[u][e];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) red[w][lane * 4 + e] = acc[e];
+    __syncthreads();
+    if (w == 0 && on) {
+      float v[4];
+      load(2 * chunk + 1, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[e] += red[k][lane * 4 + e];
+      grad_write<GDT, 4>(a, seg, col, skip, cols, v);
+    }
   }
 }
 
@@ -513,7 +624,7 @@ int log2_ceil(int64_t v, int most) {
 hipError_t launch_embed(int table_dt, int out_dt, const EmbedArgs& a, hipStream_t stream) {
   if (a.n == 0) return hipSuccess;
   const int c = out_dt == kBF16 ? 8 : 4;
-  const int log_tpr = log2_ceil(a.vec ? (a.dim + c - 1) / c : a.dim, 8);
+  const int log_tpr = log2_ceil((a.dim + c - 1) / c, 8);
   const int64_t rpb = 256 >> log_tpr;
   const dim3 grid(static_cast<unsigned>((a.n + rpb - 1) / rpb));
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, log_tpr); };
@@ -534,8 +645,9 @@ hipError_t launch_embed_plan(const PlanArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(plan_count_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a, pass);
     hipLaunchKernelGGL(plan_scatter_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a, pass);
   }
-  hipLaunchKernelGGL(plan_heads_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a);
-  hipLaunchKernelGGL(plan_rows_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a);
+  const int recount = a.n <= kPlanRecount ? 1 : 0;
+  if (!recount) hipLaunchKernelGGL(plan_heads_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a);
+  hipLaunchKernelGGL(plan_rows_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a, recount);
   return hipGetLastError();
 }
 
@@ -561,7 +673,7 @@ hipError_t launch_embed_grad(int dout_dt, int grad_dt, const EmbedGradArgs& a, h
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.chunks < 2) return e;
-  const dim3 jgrid(static_cast<unsigned>(a.chunks), static_cast<unsigned>((a.dim + 255) / 256));
+  const dim3 jgrid(static_cast<unsigned>((a.chunks + kJoinChunks - 1) / kJoinChunks), static_cast<unsigned>((a.dim + 255) / 256));
   if (grad_dt == kBF16)
     hipLaunchKernelGGL(egrad_join_kernel<kBF16>, jgrid, dim3(kEgThreads), 0, stream, a);
   else

@@ -22,7 +22,6 @@ struct EmbedArgs {
   int64_t n, vocab, dim;
   float scale;
   int tok64;   // tokens are int64 (else int32)
-  int vec;     // 16-byte chunks allowed (dim and pointers)
 };
 hipError_t launch_embed(int table_dt, int out_dt, const EmbedArgs& a, hipStream_t stream);
 
@@ -32,6 +31,7 @@ constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanMaxDigits = 512;      // 9 bits a pass
 constexpr int kPlanSmall = 4096;         // tokens sorted by one block in LDS
 constexpr int kPlanMaxBlocks = 128;
+constexpr int kPlanRecount = 32768;
 
 struct PlanArgs {
   const void* tokens;
@@ -74,7 +74,6 @@ struct EmbedGradArgs {
   int form;
   int chunk;            // sorted positions per chunk
   int chunks;
-  int vec;
 };
 hipError_t launch_embed_grad(int dout_dt, int grad_dt, const EmbedGradArgs& a, hipStream_t stream);
 
@@ -86,7 +85,6 @@ struct AdamRowsArgs {
   float* m;
   float* v;
   int64_t rows, dim, n_grad_rows;
-  int vec;
   AdamArgs hp;
 };
 hipError_t launch_adamw_rows(int dt, const AdamRowsArgs& a, hipStream_t stream);
