@@ -57,7 +57,7 @@ hipError_t launch_embed_plan(const PlanArgs& a, hipStream_t stream);
 
 enum EmbedGradForm : int { kGradDense = 0, kGradAdd = 1, kGradRows = 2 };
 constexpr int kEgThreads = 256;
-constexpr int kEgZeroRows = 16;   // rows a zero-filling block looks after
+constexpr int kEgZeroRows = 4;   // rows a zero-filling block looks after
 
 struct EmbedGradArgs {
   const void* dout;
@@ -156,12 +156,16 @@ typedef __bf16 bf16v4 __attribute__((ext_vector_type(4)));
 template <typename T, int N> struct Loose {
   typedef T V __attribute__((ext_vector_type(N), aligned(sizeof(T))));
 };
-template <int N, typename T> __device__ __forceinline__ void load_any(const T* p, float* v) {
+// STREAM: non-temporal, for what does not fit the caches anyway.
+template <int N, bool STREAM = false, typename T> __device__ __forceinline__ void load_any(const T* p, float* v) {
   constexpr int M = 16 / sizeof(T) < N ? 16 / sizeof(T) : N;
   using V = typename Loose<T, M>::V;
 #pragma unroll
   for (int h = 0; h < N / M; ++h) {
-    const V x = *reinterpret_cast<gptr<const V>>(gmem(p + M * h));
+    const auto q = reinterpret_cast<gptr<const V>>(gmem(p + M * h));
+    V x;
+    if constexpr (STREAM) x = __builtin_nontemporal_load(q);
+    else x = *q;
 #pragma unroll
     for (int e = 0; e < M; ++e) v[M * h + e] = static_cast<float>(x[e]);
   }
