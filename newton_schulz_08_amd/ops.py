@@ -23,6 +23,11 @@ from .api import _used_on, alloc_workspace, dtype_code
 _INDEX = {torch.int32: _lib.DMUON_I32, torch.int64: _lib.DMUON_I64}
 _FORMS = {"dense": _lib.DMUON_EMBED_DENSE, "add": _lib.DMUON_EMBED_ADD, "rows": _lib.DMUON_EMBED_ROWS}
 
+# The handle of a device's current stream, without a Stream object (about 2 us)
+# where this build of torch offers it: small calls cost little more than that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 def _index_code(t: torch.Tensor, name: str) -> int:
     try:
@@ -31,54 +36,63 @@ def _index_code(t: torch.Tensor, name: str) -> int:
         raise TypeError(f"{name} must be int32 or int64, got {t.dtype}") from None
 
 
-def _tensor(t, name: str, device: Optional[torch.device] = None, dtype: Optional[torch.dtype] = None,
-            shape=None) -> torch.Tensor:
-    """A contiguous device tensor, of that device, dtype and shape where given."""
+def _tensor(t, name: str, index: int = -1, dtype: Optional[torch.dtype] = None, shape=None) -> int:
+    """Address of a contiguous device tensor, on device `index` and of that
+    dtype and shape where given."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    on = t.get_device() if t.is_cuda else -1
+    if on < 0:
         raise ValueError(f"{name} must be a device tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if index >= 0 and on != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t
+    return t.data_ptr()
 
 
-def _run(name: str, device: torch.device, stream, *args) -> None:
-    """One C call on `device`: the library works on the current device."""
+_fns = {}
+
+
+def _run(name: str, index: int, stream, *args) -> None:
+    """One C call on device `index`: the library works on the current device."""
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(_lib.load(), name)
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
-    fn = getattr(_lib.load(), name)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, stream.cuda_stream)
+        handle = _raw_stream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to cuda:{index}")
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, stream.cuda_stream)
-    check(st, name)
+        handle = stream.cuda_stream
+    if index == torch.cuda.current_device():
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, handle)
+    if st:
+        check(st, name)
 
 
 def _query(name: str, *args) -> int:
     out = ctypes.c_size_t(0)
     check(getattr(_lib.load(), name)(*args, ctypes.byref(out)), name)
-    return int(out.value)
+    return out.value
 
 
-def _workspace(given: Optional[torch.Tensor], need: int, device) -> Tuple[Optional[torch.Tensor], int, int]:
+def _workspace(given: Optional[torch.Tensor], need: int, index: int) -> Tuple[Optional[torch.Tensor], int, int]:
     """(workspace allocated here or None, address, bytes)."""
     if given is not None:
-        if not given.is_cuda or given.device != device or given.dtype != torch.uint8 or not given.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+        if not given.is_cuda or given.get_device() != index or given.dtype != torch.uint8 or not given.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
         return None, given.data_ptr(), given.numel()
     if need == 0:
         return None, 0, 0
-    ws = alloc_workspace(need, device)
+    ws = alloc_workspace(need, torch.device("cuda", index))
     return ws, ws.data_ptr(), ws.numel()
 
 
@@ -89,20 +103,20 @@ def embedding(table: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0,
     """dmuon_embedding_forward: scale * table[tokens], of shape tokens.shape +
     (dim,) and dtype `out_dtype` (default: the table's).  A token outside
     [0, vocab) gives a zero row."""
-    _tensor(table, "table")
+    src = _tensor(table, "table")
     if table.dim() != 2:
         raise ValueError(f"table must be 2-D, got shape {tuple(table.shape)}")
-    dev = table.device
-    _tensor(tokens, "tokens", dev)
+    dev = table.get_device()
+    tok = _tensor(tokens, "tokens", dev)
     vocab, dim = table.shape
-    shape = tokens.shape + (dim,)
     own = out is None
     if own:
-        out = torch.empty(shape, dtype=out_dtype or table.dtype, device=dev)
+        out = table.new_empty((*tokens.shape, dim), dtype=out_dtype or table.dtype)
+        dst = out.data_ptr()
     else:
-        _tensor(out, "out", dev, out_dtype, shape)
-    _run("dmuon_embedding_forward", dev, stream, table.data_ptr(), vocab, dim, dtype_code(table.dtype),
-         tokens.data_ptr(), tokens.numel(), _index_code(tokens, "tokens"), scale, out.data_ptr(), dtype_code(out.dtype))
+        dst = _tensor(out, "out", dev, out_dtype, (*tokens.shape, dim))
+    _run("dmuon_embedding_forward", dev, stream, src, vocab, dim, dtype_code(table.dtype), tok, tokens.numel(),
+         _index_code(tokens, "tokens"), scale, dst, dtype_code(out.dtype))
     if own:
         _used_on(stream, out)
     return out
@@ -113,13 +127,14 @@ class EmbeddingPlan:
     int32 tensors: `order`, `slot` (n), `rows` (min(n, vocab)), `row_index`
     (vocab) and `count` (1)."""
 
-    def __init__(self, n: int, vocab: int, device: torch.device):
-        self.n, self.vocab, self.cap, self.device = n, vocab, min(n, vocab), device
+    def __init__(self, n: int, vocab: int, device):
+        self.n, self.vocab, self.cap = n, vocab, min(n, vocab)
         at, self._at = 0, []
         for size in (n, n, self.cap, vocab, 1):
             self._at.append((at, size))
             at += (size + 63) // 64 * 64   # each on its own 256 bytes
-        self._buf = torch.empty(max(at, 64), dtype=torch.int32, device=device)
+        self._buf = torch.empty(at, dtype=torch.int32, device=device)
+        self.device, self._index = self._buf.device, self._buf.get_device()
         base = self._buf.data_ptr()
         self._ptrs = [base + 4 * a for a, _ in self._at]
 
@@ -142,16 +157,16 @@ def embedding_plan(tokens: torch.Tensor, vocab: int, plan: Optional[EmbeddingPla
                    workspace: Optional[torch.Tensor] = None, stream=None) -> EmbeddingPlan:
     """dmuon_embedding_plan of `tokens` (any shape); with `plan`, into an
     existing plan of the same size."""
-    _tensor(tokens, "tokens")
-    code, n, dev, vocab = _index_code(tokens, "tokens"), tokens.numel(), tokens.device, int(vocab)
+    tok = _tensor(tokens, "tokens")
+    code, n, dev, vocab = _index_code(tokens, "tokens"), tokens.numel(), tokens.get_device(), int(vocab)
     need = embedding_plan_workspace_bytes(n, vocab)   # also the check of n and vocab
     own = plan is None
     if own:
-        plan = EmbeddingPlan(n, vocab, dev)
-    elif (plan.n, plan.vocab, plan.device) != (n, vocab, dev):
-        raise ValueError(f"plan is for {plan.n} tokens of {plan.vocab} on {plan.device}, not {n} of {vocab} on {dev}")
+        plan = EmbeddingPlan(n, vocab, tokens.device)
+    elif (plan.n, plan.vocab, plan._index) != (n, vocab, dev):
+        raise ValueError(f"plan is for {plan.n} tokens of {plan.vocab} on {plan.device}, not {n} of {vocab} on cuda:{dev}")
     ws, ptr, nbytes = _workspace(workspace, need, dev)
-    _run("dmuon_embedding_plan", dev, stream, tokens.data_ptr(), n, code, vocab, *plan._ptrs, ptr, nbytes)
+    _run("dmuon_embedding_plan", dev, stream, tok, n, code, vocab, *plan._ptrs, ptr, nbytes)
     _used_on(stream, ws, plan._buf if own else None)
     return plan
 
@@ -173,8 +188,8 @@ def embedding_grad(plan: EmbeddingPlan, dout: torch.Tensor, scale: float = 1.0, 
     it.  dtype: of the gradient (default: dout's)."""
     if form not in _FORMS:
         raise ValueError(f"form must be 'dense', 'add' or 'rows', got {form!r}")
-    dev = plan.device
-    _tensor(dout, "dout", dev)
+    dev = plan._index
+    src = _tensor(dout, "dout", dev)
     if dout.dim() < 2:
         raise ValueError(f"dout must have the tokens' shape and a last dimension, got {tuple(dout.shape)}")
     dim = dout.shape[-1]
@@ -185,14 +200,15 @@ def embedding_grad(plan: EmbeddingPlan, dout: torch.Tensor, scale: float = 1.0, 
     if own:
         if form == "add":
             raise ValueError("form 'add' needs out")
-        out = torch.empty(shape, dtype=dtype or dout.dtype, device=dev)
+        out = dout.new_empty(shape, dtype=dtype or dout.dtype)
+        dst = out.data_ptr()
     else:
-        _tensor(out, "out", dev, dtype, shape)
+        dst = _tensor(out, "out", dev, dtype, shape)
     code = dtype_code(dout.dtype)
     need = _query("dmuon_embedding_backward_workspace_bytes", plan.n, dim, code)
     ws, ptr, nbytes = _workspace(workspace, need, dev)
-    _run("dmuon_embedding_backward", dev, stream, dout.data_ptr(), plan.n, dim, code, scale, *plan._ptrs, plan.vocab,
-         _FORMS[form], out.data_ptr(), dtype_code(out.dtype), ptr, nbytes)
+    _run("dmuon_embedding_backward", dev, stream, src, plan.n, dim, code, scale, *plan._ptrs, plan.vocab, _FORMS[form],
+         dst, dtype_code(out.dtype), ptr, nbytes)
     _used_on(stream, ws, out if own else None)
     return out
 
@@ -205,20 +221,19 @@ def adamw_rows_step_(param: torch.Tensor, grad_rows: torch.Tensor, row_index: to
     Row r has the gradient grad_rows[row_index[r]], or zero where row_index[r]
     names none: embedding_grad(plan, ..., form="rows") with plan.row_index.
     Defaults as in adamw_step_."""
-    _tensor(param, "param")
+    p = _tensor(param, "param")
     if param.dim() != 2:
         raise ValueError(f"param must be 2-D, got shape {tuple(param.shape)}")
-    dev, (rows, dim) = param.device, param.shape
-    _tensor(grad_rows, "grad_rows", dev, param.dtype)
+    dev, (rows, dim) = param.get_device(), param.shape
+    g = _tensor(grad_rows, "grad_rows", dev, param.dtype)
     if grad_rows.dim() != 2 or grad_rows.shape[1] != dim:
         raise ValueError(f"grad_rows has shape {tuple(grad_rows.shape)}, expected (n, {dim})")
-    _tensor(row_index, "row_index", dev, torch.int32, (rows,))
-    _tensor(exp_avg, "exp_avg", dev, torch.float32, param.shape)
-    _tensor(exp_avg_sq, "exp_avg_sq", dev, torch.float32, param.shape)
+    index = _tensor(row_index, "row_index", dev, torch.int32, (rows,))
+    m = _tensor(exp_avg, "exp_avg", dev, torch.float32, param.shape)
+    v = _tensor(exp_avg_sq, "exp_avg_sq", dev, torch.float32, param.shape)
     b1, b2 = betas
-    _run("dmuon_adamw_rows_step", dev, stream, param.data_ptr(), grad_rows.data_ptr(), grad_rows.shape[0],
-         row_index.data_ptr(), exp_avg.data_ptr(), exp_avg_sq.data_ptr(), rows, dim, dtype_code(param.dtype),
-         int(step), lr, b1, b2, eps, weight_decay)
+    _run("dmuon_adamw_rows_step", dev, stream, p, g, grad_rows.shape[0], index, m, v, rows, dim,
+         dtype_code(param.dtype), int(step), lr, b1, b2, eps, weight_decay)
 
 
 # ---------------------------------------------------------------- distillation loss
@@ -226,18 +241,15 @@ def distill_loss_workspace_bytes(n: int, vocab: int) -> int:
     return _query("dmuon_distill_loss_workspace_bytes", n, vocab)
 
 
-def _rows(t, name: str, device=None, dtype=None, shape=None) -> int:
+def _rows(t, name: str, like: Optional[torch.Tensor] = None) -> int:
     """Stride between the rows of a 2-D device tensor with contiguous rows."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be a 2-D device tensor with contiguous rows")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if like is not None and (t.dtype != like.dtype or t.get_device() != like.get_device() or t.shape != like.shape):
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {like.dtype} "
+                         f"{tuple(like.shape)} on {like.device}")
     return t.stride(0)
 
 
@@ -258,37 +270,38 @@ def distill_loss(logits: torch.Tensor, teacher_index: Optional[torch.Tensor],
     row_weight (n) float32, rows of weight 0 skipped.  dlogits may be logits
     itself: the gradient then takes its place."""
     stride = _rows(logits, "logits")
-    dev, (n, vocab) = logits.device, logits.shape
+    dev, (n, vocab) = logits.get_device(), logits.shape
     if (teacher_index is None) != (teacher_logits is None):
         raise ValueError("teacher_index and teacher_logits come together")
     k, iptr, tptr, code = 0, 0, 0, _lib.DMUON_I64
     if teacher_index is not None:
+        iptr = _tensor(teacher_index, "teacher_index", dev)
         if teacher_index.dim() != 2 or teacher_index.shape[0] != n:
             raise ValueError(f"teacher_index has shape {tuple(teacher_index.shape)}, expected ({n}, k)")
         k, code = teacher_index.shape[1], _index_code(teacher_index, "teacher_index")
-        iptr = _tensor(teacher_index, "teacher_index", dev).data_ptr()
-        tptr = _tensor(teacher_logits, "teacher_logits", dev, torch.float32, teacher_index.shape).data_ptr()
+        tptr = _tensor(teacher_logits, "teacher_logits", dev, torch.float32, teacher_index.shape)
     lptr = 0
     if labels is not None:
-        want = labels.dtype if teacher_index is None else teacher_index.dtype
-        lptr = _tensor(labels, "labels", dev, want, (n,)).data_ptr()
+        lptr = _tensor(labels, "labels", dev, None if teacher_index is None else teacher_index.dtype, (n,))
         code = _index_code(labels, "labels")
-    wptr = 0 if row_weight is None else _tensor(row_weight, "row_weight", dev, torch.float32, (n,)).data_ptr()
-    own_losses, own_grad, dstride = losses is None, grad and dlogits is None, 0
+    wptr = 0 if row_weight is None else _tensor(row_weight, "row_weight", dev, torch.float32, (n,))
+    own_losses, own_grad, dptr, dstride = losses is None, grad and dlogits is None, 0, 0
     if own_losses:
-        losses = torch.empty(n, dtype=torch.float32, device=dev)
+        losses = logits.new_empty((n,), dtype=torch.float32)
     else:
         _tensor(losses, "losses", dev, torch.float32, (n,))
     if not grad:
         dlogits = None
+    elif own_grad:
+        dlogits = logits.new_empty((n, vocab))
+        dptr, dstride = dlogits.data_ptr(), vocab
     else:
-        if own_grad:
-            dlogits = torch.empty((n, vocab), dtype=logits.dtype, device=dev)
-        dstride = _rows(dlogits, "dlogits", dev, logits.dtype, logits.shape)
+        dstride = _rows(dlogits, "dlogits", logits)
+        dptr = dlogits.data_ptr()
     ws, ptr, nbytes = _workspace(workspace, distill_loss_workspace_bytes(n, vocab), dev)
     _run("dmuon_distill_loss", dev, stream, logits.data_ptr(), n, vocab, stride, dtype_code(logits.dtype), iptr, code,
-         tptr, k, lptr, temperature, kd_weight, ce_weight, wptr, grad_scale, losses.data_ptr(),
-         dlogits.data_ptr() if grad else 0, dstride, ptr, nbytes)
+         tptr, k, lptr, temperature, kd_weight, ce_weight, wptr, grad_scale, losses.data_ptr(), dptr, dstride, ptr,
+         nbytes)
     _used_on(stream, ws, losses if own_losses else None, dlogits if own_grad else None)
     return losses, dlogits
 
@@ -302,45 +315,48 @@ def rope_table(max_pos: int, rot_dim: int, theta: float = 10000.0, device=None) 
     return torch.cat([angle.cos(), angle.sin()], 1).float().to(device or "cuda")
 
 
-def _heads(t, name: str, like: Optional[torch.Tensor] = None) -> int:
-    """Stride between the tokens of (tokens, heads, dim), heads contiguous."""
+def _heads(t, name: str, like: Optional[torch.Tensor] = None) -> Tuple[int, int]:
+    """Address of (tokens, heads, dim) with contiguous heads, and the stride
+    between its tokens; of `like`'s type, device and shape if that is given."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 3 or not t.is_cuda:
+    if not t.is_cuda or t.dim() != 3:
         raise ValueError(f"{name} must be a (tokens, heads, head_dim) device tensor")
-    if like is not None and (t.device != like.device or t.dtype != like.dtype):
-        raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
-    n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    if like is not None and (t.dtype != like.dtype or t.get_device() != like.get_device() or t.shape != like.shape):
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {like.dtype} "
+                         f"{tuple(like.shape)} on {like.device}")
+    st, sh, sd = t.stride()
+    _, h, d = t.shape
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{name}'s heads must lie next to each other (strides {t.stride()})")
-    return t.stride(0)
+    return t.data_ptr(), st
 
 
 def _qk_args(q, k, q_weight, k_weight, positions, rope, eps, interleaved, weight_offset):
-    """(dmuon_qk_shape, strides, gains, positions, rope) of a call."""
-    strides = _heads(q, "q"), _heads(k, "k", q)
-    n, qh, d = q.shape
-    if k.shape[0] != n or k.shape[2] != d:
-        raise ValueError(f"q and k have shapes {tuple(q.shape)} and {tuple(k.shape)}")
-    dev = q.device
-    gain = q_weight if q_weight is not None else k_weight
+    """(device index, dmuon_qk_shape, [q, stride, k, stride, gains, positions, rope]) of a call."""
+    args = [*_heads(q, "q"), *_heads(k, "k")]
+    dev, (n, qh, d), (nk, kh, dk) = q.get_device(), q.shape, k.shape
+    if nk != n or dk != d or k.dtype != q.dtype or k.get_device() != dev:
+        raise ValueError(f"q is {q.dtype} {tuple(q.shape)} on {q.device}, k {k.dtype} {tuple(k.shape)} on {k.device}")
+    wdt = None
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _tensor(w, name, dev, gain.dtype, (d,))
-    s = _lib.QkShape(tokens=n, q_heads=qh, k_heads=k.shape[1], head_dim=d, interleaved=1 if interleaved else 0, eps=eps,
-                     weight_offset=weight_offset, dtype=dtype_code(q.dtype),
-                     weight_dtype=dtype_code(q.dtype if gain is None else gain.dtype))
-    pos = table = 0
+        if w is None:
+            args.append(0)
+        else:
+            args.append(_tensor(w, name, dev, wdt, (d,)))
+            wdt = w.dtype
+    max_pos = rot = pos_dtype = pos = table = 0
     if rope is not None:
-        _tensor(rope, "rope", dev, torch.float32)
+        table = _tensor(rope, "rope", dev, torch.float32)
         if rope.dim() != 2:
             raise ValueError(f"rope must be (max_pos, rot_dim), got shape {tuple(rope.shape)}")
-        _tensor(positions, "positions", dev, None, (n,))
-        s.max_pos, s.rot_dim = rope.shape
-        s.pos_dtype = _index_code(positions, "positions")
-        pos, table = positions.data_ptr(), rope.data_ptr()
-    gains = [0 if w is None else w.data_ptr() for w in (q_weight, k_weight)]
-    return s, strides, gains, pos, table
+        pos = _tensor(positions, "positions", dev, None, (n,))
+        max_pos, rot = rope.shape
+        pos_dtype = _index_code(positions, "positions")
+    s = _lib.QkShape(n, qh, kh, d, rot, 1 if interleaved else 0, max_pos, eps, weight_offset, dtype_code(q.dtype),
+                     dtype_code(wdt or q.dtype), pos_dtype)
+    args += [pos, table]
+    return dev, s, args
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor],
@@ -356,20 +372,17 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tens
     be contiguous.  positions (tokens); negative ones mark padding (zeros out).
     rope: rope_table(...), float32 (max_pos, rot_dim); None leaves the rotation
     out.  q_out, k_out may be q and k themselves."""
-    s, strides, gains, pos, table = _qk_args(q, k, q_weight, k_weight, positions, rope, eps, interleaved,
-                                             weight_offset)
-    outs, own, ostr = [], [], []
+    dev, s, args = _qk_args(q, k, q_weight, k_weight, positions, rope, eps, interleaved, weight_offset)
+    outs = []
     for out, x, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-        own.append(out is None)
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        elif out.shape != x.shape:
-            raise ValueError(f"{name} has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
-        ostr.append(_heads(out, name, q))
+            out = x.new_empty(x.shape)
+            args += [out.data_ptr(), x.shape[1] * x.shape[2]]
+            _used_on(stream, out)
+        else:
+            args += _heads(out, name, x)
         outs.append(out)
-    _run("dmuon_qk_norm_rope_forward", q.device, stream, s, q.data_ptr(), strides[0], k.data_ptr(), strides[1], *gains,
-         pos, table, outs[0].data_ptr(), ostr[0], outs[1].data_ptr(), ostr[1])
-    _used_on(stream, *(o for o, mine in zip(outs, own) if mine))
+    _run("dmuon_qk_norm_rope_forward", dev, stream, s, *args)
     return outs[0], outs[1]
 
 
@@ -387,29 +400,29 @@ def qk_norm_rope_grad(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tenso
     gradients of qk_norm_rope's outputs and its inputs; a gain's gradient is
     None where the gain is.  dq, dk may be given, as slices of a packed
     gradient, dq_out, dk_out, or q, k themselves."""
-    s, strides, gains, pos, table = _qk_args(q, k, q_weight, k_weight, positions, rope, eps, interleaved,
-                                             weight_offset)
-    args, outs, own = [], [], []
-    for dy, x, name in ((dq_out, q, "dq_out"), (dk_out, k, "dk_out")):
-        st = _heads(dy, name, q)
-        if dy.shape != x.shape:
-            raise ValueError(f"{name} has shape {tuple(dy.shape)}, expected {tuple(x.shape)}")
-        args += [dy.data_ptr(), st]
-    args += [q.data_ptr(), strides[0], k.data_ptr(), strides[1], *gains, pos, table]
+    dev, s, args = _qk_args(q, k, q_weight, k_weight, positions, rope, eps, interleaved, weight_offset)
+    head = [*_heads(dq_out, "dq_out", q), *_heads(dk_out, "dk_out", k)]
+    outs = []
     for out, x, name in ((dq, q, "dq"), (dk, k, "dk")):
-        own.append(out is None)
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        elif out.shape != x.shape:
-            raise ValueError(f"{name} has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
-        args += [out.data_ptr(), _heads(out, name, q)]
+            out = x.new_empty(x.shape)
+            args += [out.data_ptr(), x.shape[1] * x.shape[2]]
+            _used_on(stream, out)
+        else:
+            args += _heads(out, name, x)
         outs.append(out)
-    dw = [None if w is None else torch.empty_like(w) for w in (q_weight, k_weight)]
     need = 0
-    if q_weight is not None or k_weight is not None:
-        need = _query("dmuon_qk_norm_rope_backward_workspace_bytes", s)
-    ws, ptr, nbytes = _workspace(workspace, need, q.device)
-    _run("dmuon_qk_norm_rope_backward", q.device, stream, s, *args, *(0 if w is None else w.data_ptr() for w in dw),
-         ptr, nbytes)
-    _used_on(stream, ws, *(o for o, mine in zip(outs, own) if mine), *dw)
-    return outs[0], outs[1], dw[0], dw[1]
+    for w in (q_weight, k_weight):
+        if w is None:
+            outs.append(None)
+            args.append(0)
+        else:
+            dw = torch.empty_like(w)
+            outs.append(dw)
+            args.append(dw.data_ptr())
+            _used_on(stream, dw)
+            need = need or _query("dmuon_qk_norm_rope_backward_workspace_bytes", s)
+    ws, ptr, nbytes = _workspace(workspace, need, dev)
+    _run("dmuon_qk_norm_rope_backward", dev, stream, s, *head, *args, ptr, nbytes)
+    _used_on(stream, ws)
+    return tuple(outs)
