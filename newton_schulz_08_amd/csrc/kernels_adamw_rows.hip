@@ -38,7 +38,10 @@ __device__ __forceinline__ const T* grad_row(const AdamRowsArgs& a, int64_t r) {
 // step; a lane takes four consecutive elements of all arrays at a time.
 // `magic` = floor(2^32 / dim) gives their row by a multiplication (the quotient
 // is at most one short for the offsets that occur, below 2^17).  Four elements
-// that lie in two rows look their gradients up one by one.
+// that lie in two rows look their gradients up one by one.  The moments, read
+// and written once a step and by nobody else, pass the caches by (non-temporal:
+// 128256 x 4096 bf16 1975 -> 1880 us, 32000 x 512 fp32 82 -> 66); the parameters,
+// which the next forward pass reads, do not.
 template <int DT>
 __global__ __launch_bounds__(kAdamThreads) void adamw_rows_kernel(AdamRowsArgs a, int64_t tiles, unsigned magic) {
   using T = typename OpElem<DT>::T;
@@ -65,8 +68,8 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_rows_kernel(AdamRowsArgs a
       for (int c = 0; c < kAdamChunks; ++c) {
         const unsigned o = (c * kAdamThreads + threadIdx.x) * 4;
         load_any<4>(pp + base + o, p[c]);
-        load_any<4>(a.m + base + o, m[c]);
-        load_any<4>(a.v + base + o, v[c]);
+        load_any<4, true>(a.m + base + o, m[c]);
+        load_any<4, true>(a.v + base + o, v[c]);
       }
 #pragma unroll
       for (int c = 0; c < kAdamChunks; ++c) {
@@ -92,8 +95,8 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_rows_kernel(AdamRowsArgs a
 #pragma unroll
         for (int e = 0; e < 4; ++e) adamw_elem(p[c][e], g[c][e], m[c][e], v[c][e], a.hp);
         store_any<4>(pp + base + o, p[c]);
-        store_any<4>(a.m + base + o, m[c]);
-        store_any<4>(a.v + base + o, v[c]);
+        store_any<4, true>(a.m + base + o, m[c]);
+        store_any<4, true>(a.v + base + o, v[c]);
       }
     } else {
       for (int o = threadIdx.x; o < kAdamTile; o += kAdamThreads) {

@@ -24,8 +24,10 @@ __device__ __forceinline__ int popc_below(uint64_t mask) {
 }
 
 // ---------------------------------------------------------------- lookup
-// 2^log_tpr threads take a row, 16 bytes of the output each at a time.
-template <int TDT, int ODT>
+// 2^log_tpr threads take a row, 16 bytes of the output each at a time.  STREAM:
+// an output larger than the memory-side cache passes it by, which keeps the
+// table's frequent rows there (65536 x 4096 fp32 to bf16: 187 -> 176 us).
+template <int TDT, int ODT, bool STREAM>
 __global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a, int log_tpr) {
   using T = typename OpElem<TDT>::T;
   using O = typename OpElem<ODT>::T;
@@ -49,7 +51,7 @@ __global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a, int log_tpr) {
     for (int u = 0; u < U; ++u) {
 #pragma unroll
       for (int e = 0; e < C; ++e) v[u][e] *= a.scale;
-      if (c0 + u * tpr < nch) store_any<C>(dst + (c0 + u * tpr) * C, v[u]);
+      if (c0 + u * tpr < nch) store_any<C, STREAM>(dst + (c0 + u * tpr) * C, v[u]);
     }
   }
   for (int64_t e = nch * C + lane; e < a.dim; e += tpr)
@@ -649,11 +651,18 @@ hipError_t launch_embed(int table_dt, int out_dt, const EmbedArgs& a, hipStream_
   const int log_tpr = log2_ceil((a.dim + c - 1) / c, 8);
   const int64_t rpb = 256 >> log_tpr;
   const dim3 grid(static_cast<unsigned>((a.n + rpb - 1) / rpb));
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, log_tpr); };
+  const bool streams = static_cast<double>(a.n) * a.dim * (out_dt == kBF16 ? 2 : 4) > 256e6;
+  auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, log_tpr); };
+  auto go = [&](auto cached, auto streamed) {
+    if (streams) launch(streamed);
+    else launch(cached);
+  };
   if (table_dt == kBF16) {
-    if (out_dt == kBF16) go(embed_kernel<kBF16, kBF16>); else go(embed_kernel<kBF16, kF32>);
+    if (out_dt == kBF16) go(embed_kernel<kBF16, kBF16, false>, embed_kernel<kBF16, kBF16, true>);
+    else go(embed_kernel<kBF16, kF32, false>, embed_kernel<kBF16, kF32, true>);
   } else {
-    if (out_dt == kBF16) go(embed_kernel<kF32, kBF16>); else go(embed_kernel<kF32, kF32>);
+    if (out_dt == kBF16) go(embed_kernel<kF32, kBF16, false>, embed_kernel<kF32, kBF16, true>);
+    else go(embed_kernel<kF32, kF32, false>, embed_kernel<kF32, kF32, true>);
   }
   return hipGetLastError();
 }
