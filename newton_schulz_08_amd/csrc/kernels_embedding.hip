@@ -75,8 +75,8 @@ __device__ __forceinline__ uint64_t same_digit(unsigned d, int bits, bool valid)
   return peers;
 }
 
-// Inclusive scan over the block of one value per thread; total in *sum.
-__device__ __forceinline__ int block_scan(int v, int* wave_tot, int* sum) {
+// Inclusive scan over a block of WAVES waves of one value per thread; total in *sum.
+template <int WAVES> __device__ __forceinline__ int block_scan(int v, int* wave_tot, int* sum) {
   const int w = threadIdx.x >> 6;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -87,7 +87,7 @@ __device__ __forceinline__ int block_scan(int v, int* wave_tot, int* sum) {
   __syncthreads();
   int before = 0, all = 0;
 #pragma unroll
-  for (int k = 0; k < kPlanWaves; ++k) {
+  for (int k = 0; k < WAVES; ++k) {
     const int t = wave_tot[k];
     before += k < w ? t : 0;
     all += t;
@@ -104,60 +104,80 @@ __device__ __forceinline__ void fill_minus_one(int* p, int64_t n, int64_t thread
   for (int64_t i = n / 4 * 4 + thread; i < n; i += threads) gmem(p)[i] = -1;
 }
 
-// All of the plan in one block for n <= kPlanSmall: the pairs stay in LDS.
-__global__ __launch_bounds__(kPlanThreads) void plan_small_kernel(PlanArgs a) {
-  __shared__ unsigned key[2][kPlanSmall];
-  __shared__ uint16_t idx[2][kPlanSmall];
-  __shared__ uint16_t cnt[kPlanWaves][kPlanMaxDigits];
-  __shared__ int wave_tot[kPlanWaves];
-  constexpr int kPer = kPlanSmall / kPlanThreads;   // items per thread; a wave owns 64 kPer consecutive ones
+// All of the plan in one block: up to 64 WAVES PER tokens, whose pairs stay in
+// LDS.  A wave owns 64 PER consecutive ones.
+template <int WAVES, int PER>
+__global__ __launch_bounds__(64 * WAVES) void plan_small_kernel(PlanArgs a) {
+  constexpr int kThreads = 64 * WAVES, kMost = kThreads * PER;
+  constexpr int kDigits = kPlanMaxDigits > kThreads ? kPlanMaxDigits / kThreads : 1;   // consecutive ones per thread
+  __shared__ unsigned key[2][kMost];
+  __shared__ uint16_t idx[2][kMost];
+  __shared__ uint16_t cnt[WAVES][kPlanMaxDigits];
+  __shared__ int wave_tot[WAVES];
   const int tid = threadIdx.x, w = tid >> 6, lane = lane_id();
-  const int digits = 1 << a.bits;
-  const unsigned mask = digits - 1;
-  fill_minus_one(a.row_index, a.vocab, tid, kPlanThreads);
-  for (int i = tid; i < a.n; i += kPlanThreads) {
-    key[0][i] = plan_key(a, i);
+  const unsigned mask = (1u << a.bits) - 1;
+  unsigned mine[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = (w * PER + j) * 64 + lane;
+    mine[j] = i < a.n ? plan_key(a, i) : 0;
+  }
+  fill_minus_one(a.row_index, a.vocab, tid, kThreads);
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = (w * PER + j) * 64 + lane;
+    key[0][i] = mine[j];
     idx[0][i] = static_cast<uint16_t>(i);
   }
   int cur = 0;
   for (int pass = 0; pass < a.passes; ++pass, cur ^= 1) {
     const int shift = pass * a.bits;
-    for (int i = tid; i < kPlanWaves * digits; i += kPlanThreads) cnt[i >> a.bits][i & mask] = 0;
+    for (int i = tid; i < WAVES * kPlanMaxDigits / 2; i += kThreads) reinterpret_cast<unsigned*>(&cnt[0][0])[i] = 0;
     __syncthreads();
-    int rank[kPer];
-    unsigned dig[kPer];
+    int rank[PER];
+    unsigned k[PER];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = (w * kPer + j) * 64 + lane;
+    for (int j = 0; j < PER; ++j) {
+      const int i = (w * PER + j) * 64 + lane;
       const bool valid = i < a.n;
-      dig[j] = valid ? (key[cur][i] >> shift) & mask : 0;
-      const uint64_t peers = same_digit(dig[j], a.bits, valid);
+      k[j] = key[cur][i];
+      if ((w * PER + j) * 64 >= a.n) break;   // nothing left in this wave
+      const unsigned d = (k[j] >> shift) & mask;
+      const uint64_t peers = same_digit(d, a.bits, valid);
       const int below = popc_below(peers);
-      const int base = valid ? cnt[w][dig[j]] : 0;
+      const int base = valid ? cnt[w][d] : 0;
       __builtin_amdgcn_wave_barrier();
-      if (valid && below == 0) cnt[w][dig[j]] = static_cast<uint16_t>(base + __popcll(peers));
+      if (valid && below == 0) cnt[w][d] = static_cast<uint16_t>(base + __popcll(peers));
       __builtin_amdgcn_wave_barrier();
       rank[j] = base + below;
     }
     __syncthreads();
-    int total = 0;
-    if (tid < digits)
-      for (int k = 0; k < kPlanWaves; ++k) {
-        const int t = cnt[k][tid];
-        cnt[k][tid] = static_cast<uint16_t>(total);
-        total += t;
-      }
+    // counts -> first places: over the waves of a digit, over the digits
+    int c[kDigits][WAVES], total = 0;
+#pragma unroll
+    for (int g = 0; g < kDigits; ++g)
+#pragma unroll
+      for (int v = 0; v < WAVES; ++v) c[g][v] = tid * kDigits + g < kPlanMaxDigits ? cnt[v][tid * kDigits + g] : 0;
+#pragma unroll
+    for (int g = 0; g < kDigits; ++g)
+#pragma unroll
+      for (int v = 0; v < WAVES; ++v) total += c[g][v];
     int all;
-    const int before = block_scan(total, wave_tot, &all) - total;
-    if (tid < digits)
-      for (int k = 0; k < kPlanWaves; ++k) cnt[k][tid] = static_cast<uint16_t>(cnt[k][tid] + before);
+    int run = block_scan<WAVES>(total, wave_tot, &all) - total;
+#pragma unroll
+    for (int g = 0; g < kDigits; ++g)
+#pragma unroll
+      for (int v = 0; v < WAVES; ++v) {
+        if (tid * kDigits + g < kPlanMaxDigits) cnt[v][tid * kDigits + g] = static_cast<uint16_t>(run);
+        run += c[g][v];
+      }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = (w * kPer + j) * 64 + lane;
+    for (int j = 0; j < PER; ++j) {
+      const int i = (w * PER + j) * 64 + lane;
       if (i < a.n) {
-        const int pos = cnt[w][dig[j]] + rank[j];
-        key[cur ^ 1][pos] = key[cur][i];
+        const int pos = cnt[w][(k[j] >> shift) & mask] + rank[j];
+        key[cur ^ 1][pos] = k[j];
         idx[cur ^ 1][pos] = idx[cur][i];
       }
     }
@@ -165,25 +185,26 @@ __global__ __launch_bounds__(kPlanThreads) void plan_small_kernel(PlanArgs a) {
   }
   // runs of equal tokens
   const unsigned none = static_cast<unsigned>(a.vocab);
-  uint64_t heads[kPer];
-  int mine = 0;
+  uint64_t heads[PER];
+  int here = 0;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = (w * kPer + j) * 64 + lane;
+  for (int j = 0; j < PER; ++j) {
+    const int i = (w * PER + j) * 64 + lane;
     const bool head = i < a.n && key[cur][i] != none && (i == 0 || key[cur][i - 1] != key[cur][i]);
     heads[j] = __ballot(head);
-    mine += __popcll(heads[j]);
+    here += __popcll(heads[j]);
   }
-  if (lane == 0) wave_tot[w] = mine;
+  if (lane == 0) wave_tot[w] = here;
   __syncthreads();
   int base = 0, all = 0;
-  for (int k = 0; k < kPlanWaves; ++k) {
+#pragma unroll
+  for (int k = 0; k < WAVES; ++k) {
     base += k < w ? wave_tot[k] : 0;
     all += wave_tot[k];
   }
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = (w * kPer + j) * 64 + lane;
+  for (int j = 0; j < PER; ++j) {
+    const int i = (w * PER + j) * 64 + lane;
     if (i < a.n) {
       const unsigned kv = key[cur][i];
       const bool head = (heads[j] >> lane) & 1;
@@ -192,12 +213,12 @@ __global__ __launch_bounds__(kPlanThreads) void plan_small_kernel(PlanArgs a) {
       gmem(a.slot)[i] = s;
       if (head) {
         gmem(a.rows)[s] = static_cast<int>(kv);
-        gmem(a.row_index)[kv] = s;
+        gmem(a.row_index)[kv] = s;   // behind the clearing: barriers lie between
       }
     }
     base += __popcll(heads[j]);
   }
-  for (int i = all + tid; i < a.cap; i += kPlanThreads) gmem(a.rows)[i] = -1;
+  for (int i = all + tid; i < a.cap; i += kThreads) gmem(a.rows)[i] = -1;
   if (tid == 0) gmem(a.count)[0] = all;
 }
 
@@ -294,7 +315,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_scatter_kernel(PlanArgs a, 
       total += part[1][g * digits + tid];
     }
   int all;
-  const int first = block_scan(total, wave_tot, &all) - total;   // its barriers also end the ranking
+  const int first = block_scan<kPlanWaves>(total, wave_tot, &all) - total;   // its barriers also end the ranking
   if (tid < digits) {
     int run = first + before;
     for (int k = 0; k < kPlanWaves; ++k) {
@@ -338,7 +359,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_heads_kernel(PlanArgs a) {
   for (int j = threadIdx.x; j < a.items; j += kPlanThreads)
     if (i0 + j < a.n && plan_head(key, i0 + j, static_cast<unsigned>(a.vocab))) ++mine;
   int all;
-  block_scan(mine, wave_tot, &all);
+  block_scan<kPlanWaves>(mine, wave_tot, &all);
   if (threadIdx.x == 0) gmem(a.heads)[blockIdx.x] = all;
 }
 
@@ -366,12 +387,12 @@ __global__ __launch_bounds__(kPlanThreads) void plan_rows_kernel(PlanArgs a, int
   } else if (tid < static_cast<int>(blockIdx.x)) {
     mine = gmem(a.heads)[tid];
   }
-  block_scan(mine, wave_tot, &before);
+  block_scan<kPlanWaves>(mine, wave_tot, &before);
   for (int j = 0; j < a.items; j += kPlanThreads) {
     const int64_t i = i0 + j + tid;
     const bool head = i < a.n && plan_head(key, i, none);
     int here;
-    const int s = before + block_scan(head ? 1 : 0, wave_tot, &here) - 1;
+    const int s = before + block_scan<kPlanWaves>(head ? 1 : 0, wave_tot, &here) - 1;
     if (i < a.n) {
       const unsigned k = gmem(key)[i];
       gmem(a.order)[i] = gmem(idx)[i];
@@ -669,7 +690,9 @@ hipError_t launch_embed(int table_dt, int out_dt, const EmbedArgs& a, hipStream_
 
 hipError_t launch_embed_plan(const PlanArgs& a, hipStream_t stream) {
   if (a.n <= kPlanSmall) {
-    hipLaunchKernelGGL(plan_small_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
+    // four waves rank up to 1024 tokens, each alone on its SIMD
+    if (a.n <= 1024) hipLaunchKernelGGL((plan_small_kernel<4, 4>), dim3(1), dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((plan_small_kernel<16, 4>), dim3(1), dim3(kPlanThreads), 0, stream, a);
     return hipGetLastError();
   }
   for (int pass = 0; pass < a.passes; ++pass) {

@@ -129,14 +129,16 @@ class EmbeddingPlan:
 
     def __init__(self, n: int, vocab: int, device):
         self.n, self.vocab, self.cap = n, vocab, min(n, vocab)
-        at, self._at = 0, []
-        for size in (n, n, self.cap, vocab, 1):
-            self._at.append((at, size))
-            at += (size + 63) // 64 * 64   # each on its own 256 bytes
-        self._buf = torch.empty(at, dtype=torch.int32, device=device)
+        # each on its own 256 bytes
+        a = n + 63 & ~63
+        b = a + a
+        c = b + (self.cap + 63 & ~63)
+        d = c + (vocab + 63 & ~63)
+        self._at = (0, n), (a, n), (b, self.cap), (c, vocab), (d, 1)
+        self._buf = torch.empty(d + 64, dtype=torch.int32, device=device)
         self.device, self._index = self._buf.device, self._buf.get_device()
-        base = self._buf.data_ptr()
-        self._ptrs = [base + 4 * a for a, _ in self._at]
+        p = self._buf.data_ptr()
+        self._ptrs = p, p + 4 * a, p + 4 * b, p + 4 * c, p + 4 * d
 
     def _view(self, k: int) -> torch.Tensor:
         at, size = self._at[k]
