@@ -505,7 +505,7 @@ typedef struct {
  *              cosines, then its sines.  NULL when rot_dim is 0.
  * q_out, k_out : device; may equal q and k with the same stride (in place).
  * Pointers of a tensor with 0 heads are ignored.  The sum of a head's squares
- * has to be a finite float32.
+ * is formed in float32 and has to be finite (and, when eps is 0, normal).
  */
 int dmuon_qk_norm_rope_forward(const dmuon_qk_shape* shape, const void* q, int64_t q_stride, const void* k,
                                int64_t k_stride, const void* q_weight, const void* k_weight, const void* positions,

@@ -443,6 +443,7 @@ __device__ __forceinline__ Edges chunk_edges(const EmbedGradArgs& a, int64_t chu
 template <int GDT, int C>
 __device__ __forceinline__ void grad_write(const EmbedGradArgs& a, int slot, int64_t col, int skip, int cols, float* v) {
   using G = typename OpElem<GDT>::T;
+  if (slot >= a.cap) return;   // not a slot of this plan
   const int64_t row = a.form == kGradRows ? slot : gmem(a.rows)[slot];
   if (row < 0 || row >= (a.form == kGradRows ? static_cast<int64_t>(a.cap) : a.vocab)) return;
   G* dst = static_cast<G*>(a.grad) + row * a.dim + col;

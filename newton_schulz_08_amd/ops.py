@@ -266,10 +266,11 @@ def distill_loss(logits: torch.Tensor, teacher_index: Optional[torch.Tensor],
     gradient with respect to the logits times `grad_scale` (1 / rows for the
     gradient of a mean); (losses, None) without.
 
-    logits (n, vocab), rows contiguous; teacher_index, teacher_logits (n, k),
-    entries outside the vocabulary left out, or both None for the label's term
-    alone (kd_weight 0); labels (n), those outside the vocabulary ignored;
-    row_weight (n) float32, rows of weight 0 skipped.  dlogits may be logits
+    logits (n, vocab), rows contiguous; teacher_index (n, k) int32 or int64,
+    entries outside the vocabulary left out, and teacher_logits (n, k) float32,
+    or both None for the label's term alone (kd_weight 0); labels (n) of the
+    indices' type, those outside the vocabulary ignored; row_weight (n) float32,
+    rows of weight 0 skipped.  dlogits may be logits
     itself: the gradient then takes its place."""
     stride = _rows(logits, "logits")
     dev, (n, vocab) = logits.get_device(), logits.shape
