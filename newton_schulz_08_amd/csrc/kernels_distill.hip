@@ -44,6 +44,8 @@ constexpr double kLn2 = 0.6931471805599453094;
 constexpr float kFar = 1.2676506e30f;   // 2^100
 constexpr int kHeld = 12;               // vectors kept in registers by a 512-thread row
 
+template <int N> using Int = std::integral_constant<int, N>;
+
 // How the exponents of a row's two terms hang together.
 enum DistillMode { kOne = 0, kTwo = 1, kSquare = 2, kFourth = 3 };
 
@@ -68,13 +70,14 @@ struct Sums {
   double ent = 0.0;                  // sum of e_j (y_j - ytop) / T
 };
 
-template <int THREADS> struct Shared {
-  static constexpr int kWaves = THREADS / 64;
+// PER: named elements per thread, THREADS x PER > k.
+template <int THREADS, int PER> struct Shared {
+  static constexpr int kWaves = THREADS / 64, kNamed = THREADS * PER;
   float top[kWaves], ytop[kWaves], st[kWaves], s1[kWaves];
   double ysum[kWaves], dot[kWaves], ent[kWaves];
-  int idx[kDistillMaxK + 1];         // elements named by the teacher (label last), or -1
-  float e[kDistillMaxK + 1];
-  float z[kDistillMaxK + 1];
+  int idx[kNamed];                   // elements named by the teacher (label last), or -1
+  float e[kNamed];
+  float z[kNamed];
 };
 
 // Exponentials of one row: exponents s2 and, in kTwo, log2(e).
@@ -174,11 +177,11 @@ __device__ __forceinline__ void sweep_held(const T* z, int64_t i0, int64_t i1, H
 // The sums of [i0, i1) of a row, and of the teacher's entries that lie in it
 // (its own sums are over all entries).  Ends behind a barrier, with the entries
 // in `sh` and everything in `s` of every thread.
-template <int DT, int MODE, int THREADS, int R>
+template <int DT, int MODE, int THREADS, int PER, int R>
 __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int64_t i0, int64_t i1,
-                                         Shared<THREADS>& sh, Sums& s, Held<typename OpElem<DT>::T, R>& held) {
+                                         Shared<THREADS, PER>& sh, Sums& s, Held<typename OpElem<DT>::T, R>& held) {
   using T = typename OpElem<DT>::T;
-  constexpr int kPer = (kDistillMaxK + THREADS) / THREADS;
+  constexpr int kPer = PER;
   const T* z = static_cast<const T*>(a.logits) + row * a.stride;
   const int tid = threadIdx.x, wave = tid >> 6;
   // named elements: on their way while the row is swept
@@ -346,9 +349,9 @@ __device__ __forceinline__ void zero_row(const DistillArgs& a, int64_t row, int6
 
 // The gradient of [i0, i1) of a row.  `sh` holds the named elements' indices,
 // weights and, for those in [i0, i1), logits (dlogits may overwrite them).
-template <int DT, int MODE, int THREADS, bool STREAM, int R>
+template <int DT, int MODE, int THREADS, bool STREAM, int PER, int R>
 __device__ __forceinline__ void row_grad(const DistillArgs& a, int64_t row, int64_t i0, int64_t i1,
-                                         const Shared<THREADS>& sh, const Expo<MODE>& x, double st, double s1,
+                                         const Shared<THREADS, PER>& sh, const Expo<MODE>& x, double st, double s1,
                                          double ysum, bool has_kd, bool has_ce, float w,
                                          Held<typename OpElem<DT>::T, R>& held) {
   using T = typename OpElem<DT>::T;
@@ -402,9 +405,9 @@ __device__ __forceinline__ float weight_of(const DistillArgs& a, int64_t row) {
 }
 
 // One block, one row.
-template <int DT, int MODE, int THREADS, bool STREAM, int R>
+template <int DT, int MODE, int THREADS, bool STREAM, int PER, int R>
 __global__ __launch_bounds__(THREADS, THREADS == 1024 ? 8 : 4) void distill_row_kernel(DistillArgs a) {
-  __shared__ Shared<THREADS> sh;
+  __shared__ Shared<THREADS, PER> sh;
   const int64_t row = blockIdx.x;
   const float w = weight_of(a, row);
   if (w == 0.0f) {
@@ -413,7 +416,7 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 ? 8 : 4) void distill_row_
   }
   Held<typename OpElem<DT>::T, R> held;
   Sums s;
-  row_sums<DT, MODE, THREADS, R>(a, row, 0, a.vocab, sh, s, held);
+  row_sums<DT, MODE, THREADS, PER, R>(a, row, 0, a.vocab, sh, s, held);
   const bool has_kd = a.kd != 0.0f && !(s.ysum == 0.0), has_ce = sh.idx[a.k] >= 0;
   if (!has_kd && !has_ce) {
     zero_row<DT, THREADS, STREAM>(a, row, 0, a.vocab);
@@ -423,23 +426,23 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 ? 8 : 4) void distill_row_
   x.set(s.top, scale_of(a));
   if (threadIdx.x == 0) gmem(a.losses)[row] = row_loss(a, s, x, s.st, s.s1, has_kd, has_ce, sh.z[a.k], w);
   if (a.dlogits)
-    row_grad<DT, MODE, THREADS, STREAM, R>(a, row, 0, a.vocab, sh, x, s.st, s.s1, s.ysum, has_kd, has_ce, w, held);
+    row_grad<DT, MODE, THREADS, STREAM, PER, R>(a, row, 0, a.vocab, sh, x, s.st, s.s1, s.ysum, has_kd, has_ce, w, held);
 }
 
 // Words of a slice's sums.
 enum { kPmMax = 0, kPmSumT, kPmSum1, kPmDotHi, kPmDotLo, kPmLabel, kPmWords = 8 };
-constexpr int kSliceThreads = 256;
+constexpr int kSliceThreads = 256, kSlicePer = kDistillMaxK / kSliceThreads + 1;
 
 template <int DT, int MODE>
 __global__ __launch_bounds__(kSliceThreads) void distill_slice_kernel(DistillArgs a) {
-  __shared__ Shared<kSliceThreads> sh;
+  __shared__ Shared<kSliceThreads, kSlicePer> sh;
   const int64_t row = blockIdx.x / a.slices;
   const int slice = static_cast<int>(blockIdx.x - row * a.slices);
   if (weight_of(a, row) == 0.0f) return;
   const int64_t i0 = least(a.vocab, slice * a.slice_len), i1 = least(a.vocab, i0 + a.slice_len);
   Sums s;
   Held<typename OpElem<DT>::T, 0> none;
-  row_sums<DT, MODE, kSliceThreads, 0>(a, row, i0, i1, sh, s, none);
+  row_sums<DT, MODE, kSliceThreads, kSlicePer, 0>(a, row, i0, i1, sh, s, none);
   if (threadIdx.x == 0) {
     float* p = a.part + blockIdx.x * static_cast<int64_t>(kPmWords);
     p[kPmMax] = s.top;
@@ -456,7 +459,7 @@ __global__ __launch_bounds__(kSliceThreads) void distill_slice_kernel(DistillArg
 template <int DT, int MODE>
 __global__ __launch_bounds__(kSliceThreads) void distill_join_kernel(DistillArgs a) {
   using T = typename OpElem<DT>::T;
-  __shared__ Shared<kSliceThreads> sh;
+  __shared__ Shared<kSliceThreads, kSlicePer> sh;
   const int64_t row = a.dlogits ? blockIdx.x / a.slices : blockIdx.x;
   const int slice = a.dlogits ? static_cast<int>(blockIdx.x - row * a.slices) : 0;
   const int64_t i0 = least(a.vocab, slice * a.slice_len), i1 = least(a.vocab, i0 + a.slice_len);
@@ -468,7 +471,7 @@ __global__ __launch_bounds__(kSliceThreads) void distill_join_kernel(DistillArgs
   // the teacher's entries again: sums over no elements
   Sums s;
   Held<T, 0> none;
-  row_sums<DT, MODE, kSliceThreads, 0>(a, row, 0, 0, sh, s, none);
+  row_sums<DT, MODE, kSliceThreads, kSlicePer, 0>(a, row, 0, 0, sh, s, none);
   const bool has_kd = a.kd != 0.0f && !(s.ysum == 0.0), has_ce = sh.idx[a.k] >= 0;
   if (!has_kd && !has_ce) {
     zero_row<DT, kSliceThreads, false>(a, row, i0, i1);
@@ -502,7 +505,7 @@ __global__ __launch_bounds__(kSliceThreads) void distill_join_kernel(DistillArgs
   if (slice == 0 && threadIdx.x == 0) gmem(a.losses)[row] = row_loss(a, s, x, st, s1, has_kd, has_ce, z_label, w);
   if (!a.dlogits) return;
   __syncthreads();   // every named logit is read
-  row_grad<DT, MODE, kSliceThreads, false, 0>(a, row, i0, i1, sh, x, st, s1, s.ysum, has_kd, has_ce, w, none);
+  row_grad<DT, MODE, kSliceThreads, false, kSlicePer, 0>(a, row, i0, i1, sh, x, st, s1, s.ysum, has_kd, has_ce, w, none);
 }
 
 }  // namespace
@@ -513,13 +516,16 @@ hipError_t launch_distill(int dt, const DistillArgs& a, hipStream_t stream) {
   const int mode = !two ? kOne : a.temperature == 2.0f ? kSquare : a.temperature == 4.0f ? kFourth : kTwo;
   const double row_bytes = static_cast<double>(a.vocab) * (dt == kBF16 ? 2 : 4);
   const bool streams = a.dlogits && row_bytes * a.n * 2 > 256e6;
-  // Threads of a row's block.  Short rows: 256.  Long ones: 512, three blocks to
+  // Threads of a row's block.  Rows of up to 12 KB: one wave, which needs no
+  // barriers (8192 rows of 4001 bf16: 40 us, 53 with 256 threads); up to 64 KB:
+  // 256, most of the row in registers (16000 bf16: 111 us, 126 without).  Long
+  // ones: 512, three blocks to
   // a CU, while the rows in work fit the 256 MB memory-side cache for their
   // second reading (50257 bf16: 229 us for 4000 rows, 240 with 256 threads, 273
   // with 1024); with 1024 and two blocks beyond (128256 fp32: 932 us for 4096
   // rows, 1211 with 512).  A few rows alone on the chip take 1024 early.
   const int threads = a.n <= 256 ? (row_bytes > 16384.0 ? 1024 : 256)
-                      : row_bytes <= 65536.0 ? 256 : row_bytes <= 270e3 || !a.dlogits ? 512 : 1024;
+                      : row_bytes <= 12288.0 && a.k < 256 ? 64 : row_bytes <= 65536.0 ? 256 : row_bytes <= 270e3 || !a.dlogits ? 512 : 1024;
   auto launch = [&](auto d, auto m) {
     constexpr int D = decltype(d)::value, M = decltype(m)::value;
     if (a.slices > 0) {
@@ -529,20 +535,25 @@ hipError_t launch_distill(int dt, const DistillArgs& a, hipStream_t stream) {
                          dim3(kSliceThreads), 0, stream, a);
     } else {
       const dim3 grid(static_cast<unsigned>(a.n));
-      auto rows = [&](auto t, auto st, auto r) {
+      auto rows = [&](auto t, auto st, auto per, auto r) {
         constexpr int N = decltype(t)::value;
-        hipLaunchKernelGGL((distill_row_kernel<D, M, N, decltype(st)::value, decltype(r)::value>), grid, dim3(N), 0,
-                           stream, a);
+        hipLaunchKernelGGL((distill_row_kernel<D, M, N, decltype(st)::value, decltype(per)::value, decltype(r)::value>),
+                           grid, dim3(N), 0, stream, a);
       };
-      auto by_stream = [&](auto t, auto r) {
-        if (streams) rows(t, std::true_type{}, r);
-        else rows(t, std::false_type{}, r);
+      auto by_stream = [&](auto t, auto per, auto r) {
+        if (streams) rows(t, std::true_type{}, per, r);
+        else rows(t, std::false_type{}, per, r);
       };
-      using None = std::integral_constant<int, 0>;
-      if (threads == 1024) by_stream(std::integral_constant<int, 1024>{}, None{});
-      else if (threads == 256) by_stream(std::integral_constant<int, 256>{}, None{});
-      else if (a.dlogits) by_stream(std::integral_constant<int, 512>{}, std::integral_constant<int, kHeld>{});
-      else rows(std::integral_constant<int, 512>{}, std::false_type{}, None{});
+      // without a gradient nothing is read again: no vectors held, more rows in flight
+      if (threads == 1024) by_stream(Int<1024>{}, Int<2>{}, Int<0>{});
+      else if (!a.dlogits && threads == 512) rows(Int<512>{}, std::false_type{}, Int<3>{}, Int<0>{});
+      else if (!a.dlogits && threads == 256) rows(Int<256>{}, std::false_type{}, Int<5>{}, Int<0>{});
+      else if (!a.dlogits) rows(Int<64>{}, std::false_type{}, Int<4>{}, Int<0>{});
+      else if (threads == 512) by_stream(Int<512>{}, Int<3>{}, Int<kHeld>{});
+      else if (threads == 256 && row_bytes > 36e3) by_stream(Int<256>{}, Int<5>{}, Int<kHeld>{});
+      else if (threads == 256) by_stream(Int<256>{}, Int<5>{}, Int<8>{});
+      else if (row_bytes > 4096.0) by_stream(Int<64>{}, Int<4>{}, Int<kHeld>{});
+      else by_stream(Int<64>{}, Int<4>{}, Int<4>{});
     }
   };
   auto by_mode = [&](auto d) {
