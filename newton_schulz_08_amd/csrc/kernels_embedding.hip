@@ -363,30 +363,16 @@ __global__ __launch_bounds__(kPlanThreads) void plan_heads_kernel(PlanArgs a) {
   if (threadIdx.x == 0) gmem(a.heads)[blockIdx.x] = all;
 }
 
-// Numbers the runs.  The heads before a block's tokens come from
-// plan_heads_kernel, or, for batches short enough (kPlanRecount), from reading
-// all of the sorted tokens before them, which costs less than that launch.
-__global__ __launch_bounds__(kPlanThreads) void plan_rows_kernel(PlanArgs a, int recount) {
+// Numbers the runs, behind the heads of the blocks before.
+__global__ __launch_bounds__(kPlanThreads) void plan_rows_kernel(PlanArgs a) {
   __shared__ int wave_tot[kPlanWaves];
   const unsigned* key = a.key[(a.passes + 1) & 1];
   const int* idx = a.idx[(a.passes + 1) & 1];
   const unsigned none = static_cast<unsigned>(a.vocab);
   const int tid = threadIdx.x;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * a.items;
-  int mine = 0, before;
-  if (recount) {
-    // i0 is a multiple of the threads; four tokens and the one before them at a time
-    using V = Loose<unsigned, 4>::V;
-#pragma unroll 4
-    for (int j = tid * 4; j < i0; j += kPlanThreads * 4) {
-      const V k = *reinterpret_cast<gptr<const V>>(gmem(key + j));
-      const unsigned p = gmem(key)[j > 0 ? j - 1 : 0];
-      mine += (k[0] != none && (j == 0 || k[0] != p)) + (k[1] != none && k[1] != k[0]) + (k[2] != none && k[2] != k[1]) +
-              (k[3] != none && k[3] != k[2]);
-    }
-  } else if (tid < static_cast<int>(blockIdx.x)) {
-    mine = gmem(a.heads)[tid];
-  }
+  const int mine = tid < static_cast<int>(blockIdx.x) ? gmem(a.heads)[tid] : 0;
+  int before;
   block_scan<kPlanWaves>(mine, wave_tot, &before);
   for (int j = 0; j < a.items; j += kPlanThreads) {
     const int64_t i = i0 + j + tid;
@@ -700,9 +686,8 @@ hipError_t launch_embed_plan(const PlanArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(plan_count_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a, pass);
     hipLaunchKernelGGL(plan_scatter_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a, pass);
   }
-  const int recount = a.n <= kPlanRecount ? 1 : 0;
-  if (!recount) hipLaunchKernelGGL(plan_heads_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a);
-  hipLaunchKernelGGL(plan_rows_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a, recount);
+  hipLaunchKernelGGL(plan_heads_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a);
+  hipLaunchKernelGGL(plan_rows_kernel, dim3(a.blocks), dim3(kPlanThreads), 0, stream, a);
   return hipGetLastError();
 }
 

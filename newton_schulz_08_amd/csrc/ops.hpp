@@ -31,7 +31,6 @@ constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanMaxDigits = 512;      // 9 bits a pass
 constexpr int kPlanSmall = 4096;         // tokens sorted by one block in LDS
 constexpr int kPlanMaxBlocks = 128;
-constexpr int kPlanRecount = 32768;
 
 struct PlanArgs {
   const void* tokens;
