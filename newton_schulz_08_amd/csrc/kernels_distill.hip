@@ -42,7 +42,11 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kLn2 = 0.6931471805599453094;
 constexpr float kFar = 1.2676506e30f;   // 2^100
-constexpr int kHeld = 12;               // vectors kept in registers by a 512-thread row
+// Vectors of a long row's thread that are kept between the two passes, in
+// registers and behind them in LDS (128256 bf16, 31 vectors: 892 us for 8192
+// rows with none, 854 with 12 + 0, 811 with 12 + 3, 817 with 12 + 6; 790 were
+// the second pass to read nothing).
+constexpr int kHeld = 12, kStash = 3;
 
 template <int N> using Int = std::integral_constant<int, N>;
 
@@ -125,61 +129,85 @@ __device__ __forceinline__ void sweep(const T* z, int64_t from, int64_t i1, F&& 
 #pragma unroll
     for (int u = 0; u < U; ++u) load_any<C>(z + i + u * THREADS * C, v[u]);
 #pragma unroll
-    for (int u = 0; u < U; ++u) f(v[u], i + u * THREADS * C, std::integral_constant<int, C>{});
+    for (int u = 0; u < U; ++u) f(v[u], i + u * THREADS * C, Int<C>{});
   }
-  for (; i < whole; i += THREADS * C) {
-    float v[C];
-    load_any<C>(z + i, v);
-    f(v, i, std::integral_constant<int, C>{});
+  if (i < whole) {   // the last group, as far as it goes: its loads go out together as well
+    float v[U][C];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u * THREADS * C < whole) load_any<C>(z + i + u * THREADS * C, v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u * THREADS * C < whole) f(v[u], i + u * THREADS * C, Int<C>{});
   }
   for (i = whole + threadIdx.x; i < i1; i += THREADS) {
     const float v = static_cast<float>(gmem(z)[i]);
-    f(&v, i, std::integral_constant<int, 1>{});
+    f(&v, i, Int<1>{});
   }
 }
 
-// The first R vectors of a thread's share of a row, kept in registers as they
-// were loaded, so that the gradient need not read them again.
-template <typename T, int R> struct Held {
+// The first vectors of a thread's share of a row, kept as they were loaded, so
+// that the gradient need not read them again: R in registers, L in LDS.
+template <typename T, int THREADS, int R, int L> struct Held {
   static constexpr int C = 16 / sizeof(T);
   using V = typename Loose<T, C>::V;
   V raw[R > 0 ? R : 1];
+  uint4* stash = nullptr;   // L x THREADS
 };
-template <typename T, int THREADS, int R, bool KEPT, typename F>
-__device__ __forceinline__ void sweep_held(const T* z, int64_t i0, int64_t i1, Held<T, R>& held, F&& f) {
-  constexpr int C = 16 / sizeof(T), U = 4;
-  static_assert(R % U == 0, "held vectors come in groups");
+// As sweep; KEPT: the held vectors are there from an earlier sweep.
+template <bool KEPT, typename T, int THREADS, int R, int L, typename F>
+__device__ __forceinline__ void sweep_held(const T* z, int64_t i0, int64_t i1, Held<T, THREADS, R, L>& held, F&& f) {
+  using H = Held<T, THREADS, R, L>;
+  constexpr int C = H::C;
   const int64_t whole = i0 + (i1 - i0) / C * C;
   const int64_t first = i0 + threadIdx.x * C;
+  auto at = [&](int r) { return first + r * THREADS * C; };
+  auto fetch = [&](int r) { return *reinterpret_cast<gptr<const typename H::V>>(gmem(z + at(r))); };
+  auto use = [&](const typename H::V& x, int r) {
+    float v[C];
+#pragma unroll
+    for (int e = 0; e < C; ++e) v[e] = static_cast<float>(x[e]);
+    f(v, at(r), Int<C>{});
+  };
+  constexpr int U = 4;
+  static_assert(R % U == 0, "registers are filled in groups");
 #pragma unroll
   for (int r = 0; r < R; r += U) {
-    if constexpr (!KEPT) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t i = first + (r + u) * THREADS * C;
-        if (i < whole) held.raw[r + u] = *reinterpret_cast<gptr<const typename Held<T, R>::V>>(gmem(z + i));
-      }
-    }
+    for (int u = 0; u < U; ++u)
+      if (!KEPT && at(r + u) < whole) held.raw[r + u] = fetch(r + u);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t i = first + (r + u) * THREADS * C;
-      if (i < whole) {
-        float v[C];
-#pragma unroll
-        for (int e = 0; e < C; ++e) v[e] = static_cast<float>(held.raw[r + u][e]);
-        f(v, i, std::integral_constant<int, C>{});
-      }
-    }
+    for (int u = 0; u < U; ++u)
+      if (at(r + u) < whole) use(held.raw[r + u], r + u);
   }
-  sweep<T, THREADS, 4>(z, least(whole, i0 + R * THREADS * C), i1, f);
+  if constexpr (L > 0) {
+    union Word {
+      typename H::V v;
+      uint4 w;
+    } x[L];
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+      if (at(R + l) < whole) {
+        if constexpr (KEPT) x[l].w = held.stash[l * THREADS + threadIdx.x];
+        else x[l].v = fetch(R + l);
+      }
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+      if (at(R + l) < whole) {
+        if constexpr (!KEPT) held.stash[l * THREADS + threadIdx.x] = x[l].w;   // this thread's own place
+        use(x[l].v, R + l);
+      }
+  }
+  sweep<T, THREADS, U>(z, least(whole, i0 + (R + L) * THREADS * C), i1, f);
 }
 
 // The sums of [i0, i1) of a row, and of the teacher's entries that lie in it
 // (its own sums are over all entries).  Ends behind a barrier, with the entries
 // in `sh` and everything in `s` of every thread.
-template <int DT, int MODE, int THREADS, int PER, int R>
+template <int DT, int MODE, int THREADS, int PER, int R, int L>
 __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int64_t i0, int64_t i1,
-                                         Shared<THREADS, PER>& sh, Sums& s, Held<typename OpElem<DT>::T, R>& held) {
+                                         Shared<THREADS, PER>& sh, Sums& s,
+                                         Held<typename OpElem<DT>::T, THREADS, R, L>& held) {
   using T = typename OpElem<DT>::T;
   constexpr int kPer = PER;
   const T* z = static_cast<const T*>(a.logits) + row * a.stride;
@@ -209,7 +237,7 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
   Expo<MODE> x;
   x.set(-INFINITY, s2);
   float top = -INFINITY, st = 0.0f, s1 = 0.0f;
-  sweep_held<T, THREADS, R, false>(z, i0, i1, held, [&](const float* v, int64_t, auto count) {
+  sweep_held<false>(z, i0, i1, held, [&](const float* v, int64_t, auto count) {
     constexpr int N = decltype(count)::value;
     float t = v[0];
 #pragma unroll
@@ -349,11 +377,11 @@ __device__ __forceinline__ void zero_row(const DistillArgs& a, int64_t row, int6
 
 // The gradient of [i0, i1) of a row.  `sh` holds the named elements' indices,
 // weights and, for those in [i0, i1), logits (dlogits may overwrite them).
-template <int DT, int MODE, int THREADS, bool STREAM, int PER, int R>
+template <int DT, int MODE, int THREADS, bool STREAM, int PER, int R, int L>
 __device__ __forceinline__ void row_grad(const DistillArgs& a, int64_t row, int64_t i0, int64_t i1,
                                          const Shared<THREADS, PER>& sh, const Expo<MODE>& x, double st, double s1,
                                          double ysum, bool has_kd, bool has_ce, float w,
-                                         Held<typename OpElem<DT>::T, R>& held) {
+                                         Held<typename OpElem<DT>::T, THREADS, R, L>& held) {
   using T = typename OpElem<DT>::T;
   const T* z = static_cast<const T*>(a.logits) + row * a.stride;
   T* dz = static_cast<T*>(a.dlogits) + row * a.dstride;
@@ -382,7 +410,7 @@ __device__ __forceinline__ void row_grad(const DistillArgs& a, int64_t row, int6
     };
   };
   if (x.far) sweep<T, THREADS, 1>(z, i0, i1, write(std::true_type{}));
-  else sweep_held<T, THREADS, R, true>(z, i0, i1, held, write(std::false_type{}));
+  else sweep_held<true>(z, i0, i1, held, write(std::false_type{}));
   __syncthreads();
   // named elements: the first entry that names one collects all that do
   for (int j = threadIdx.x; j <= a.k; j += THREADS) {
@@ -414,9 +442,12 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 ? 8 : 4) void distill_row_
     zero_row<DT, THREADS, STREAM>(a, row, 0, a.vocab);
     return;
   }
-  Held<typename OpElem<DT>::T, R> held;
+  constexpr int L = THREADS == 512 && R > 0 ? kStash : 0;
+  __shared__ uint4 stash[L > 0 ? L * THREADS : 1];
+  Held<typename OpElem<DT>::T, THREADS, R, L> held;
+  held.stash = stash;
   Sums s;
-  row_sums<DT, MODE, THREADS, PER, R>(a, row, 0, a.vocab, sh, s, held);
+  row_sums<DT, MODE, THREADS, PER>(a, row, 0, a.vocab, sh, s, held);
   const bool has_kd = a.kd != 0.0f && !(s.ysum == 0.0), has_ce = sh.idx[a.k] >= 0;
   if (!has_kd && !has_ce) {
     zero_row<DT, THREADS, STREAM>(a, row, 0, a.vocab);
@@ -426,7 +457,7 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 ? 8 : 4) void distill_row_
   x.set(s.top, scale_of(a));
   if (threadIdx.x == 0) gmem(a.losses)[row] = row_loss(a, s, x, s.st, s.s1, has_kd, has_ce, sh.z[a.k], w);
   if (a.dlogits)
-    row_grad<DT, MODE, THREADS, STREAM, PER, R>(a, row, 0, a.vocab, sh, x, s.st, s.s1, s.ysum, has_kd, has_ce, w, held);
+    row_grad<DT, MODE, THREADS, STREAM, PER>(a, row, 0, a.vocab, sh, x, s.st, s.s1, s.ysum, has_kd, has_ce, w, held);
 }
 
 // Words of a slice's sums.
@@ -441,8 +472,8 @@ __global__ __launch_bounds__(kSliceThreads) void distill_slice_kernel(DistillArg
   if (weight_of(a, row) == 0.0f) return;
   const int64_t i0 = least(a.vocab, slice * a.slice_len), i1 = least(a.vocab, i0 + a.slice_len);
   Sums s;
-  Held<typename OpElem<DT>::T, 0> none;
-  row_sums<DT, MODE, kSliceThreads, kSlicePer, 0>(a, row, i0, i1, sh, s, none);
+  Held<typename OpElem<DT>::T, kSliceThreads, 0, 0> none;
+  row_sums<DT, MODE, kSliceThreads, kSlicePer>(a, row, i0, i1, sh, s, none);
   if (threadIdx.x == 0) {
     float* p = a.part + blockIdx.x * static_cast<int64_t>(kPmWords);
     p[kPmMax] = s.top;
@@ -470,8 +501,8 @@ __global__ __launch_bounds__(kSliceThreads) void distill_join_kernel(DistillArgs
   }
   // the teacher's entries again: sums over no elements
   Sums s;
-  Held<T, 0> none;
-  row_sums<DT, MODE, kSliceThreads, kSlicePer, 0>(a, row, 0, 0, sh, s, none);
+  Held<T, kSliceThreads, 0, 0> none;
+  row_sums<DT, MODE, kSliceThreads, kSlicePer>(a, row, 0, 0, sh, s, none);
   const bool has_kd = a.kd != 0.0f && !(s.ysum == 0.0), has_ce = sh.idx[a.k] >= 0;
   if (!has_kd && !has_ce) {
     zero_row<DT, kSliceThreads, false>(a, row, i0, i1);
@@ -505,7 +536,7 @@ __global__ __launch_bounds__(kSliceThreads) void distill_join_kernel(DistillArgs
   if (slice == 0 && threadIdx.x == 0) gmem(a.losses)[row] = row_loss(a, s, x, st, s1, has_kd, has_ce, z_label, w);
   if (!a.dlogits) return;
   __syncthreads();   // every named logit is read
-  row_grad<DT, MODE, kSliceThreads, false, kSlicePer, 0>(a, row, i0, i1, sh, x, st, s1, s.ysum, has_kd, has_ce, w, none);
+  row_grad<DT, MODE, kSliceThreads, false, kSlicePer>(a, row, i0, i1, sh, x, st, s1, s.ysum, has_kd, has_ce, w, none);
 }
 
 }  // namespace
