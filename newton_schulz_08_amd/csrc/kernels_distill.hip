@@ -434,7 +434,7 @@ __device__ __forceinline__ float weight_of(const DistillArgs& a, int64_t row) {
 
 // One block, one row.
 template <int DT, int MODE, int THREADS, bool STREAM, int PER, int R>
-__global__ __launch_bounds__(THREADS, THREADS == 1024 ? 8 : 4) void distill_row_kernel(DistillArgs a) {
+__global__ __launch_bounds__(THREADS, 4) void distill_row_kernel(DistillArgs a) {
   __shared__ Shared<THREADS, PER> sh;
   const int64_t row = blockIdx.x;
   const float w = weight_of(a, row);
@@ -549,14 +549,13 @@ hipError_t launch_distill(int dt, const DistillArgs& a, hipStream_t stream) {
   const bool streams = a.dlogits && row_bytes * a.n * 2 > 256e6;
   // Threads of a row's block.  Rows of up to 12 KB: one wave, which needs no
   // barriers (8192 rows of 4001 bf16: 40 us, 53 with 256 threads); up to 64 KB:
-  // 256, most of the row in registers (16000 bf16: 111 us, 126 without).  Long
-  // ones: 512, three blocks to
-  // a CU, while the rows in work fit the 256 MB memory-side cache for their
-  // second reading (50257 bf16: 229 us for 4000 rows, 240 with 256 threads, 273
-  // with 1024); with 1024 and two blocks beyond (128256 fp32: 932 us for 4096
-  // rows, 1211 with 512).  A few rows alone on the chip take 1024 early.
-  const int threads = a.n <= 256 ? (row_bytes > 16384.0 ? 1024 : 256)
-                      : row_bytes <= 12288.0 && a.k < 256 ? 64 : row_bytes <= 65536.0 ? 256 : row_bytes <= 270e3 || !a.dlogits ? 512 : 1024;
+  // 256, most of the row in registers (16000 bf16: 111 us, 126 without); longer
+  // ones: 512 and two blocks to a CU, so that the rows in work stay in the 256 MB
+  // memory-side cache for their second reading (50257 bf16: 209 us for 4000 rows,
+  // 240 with 256 threads; 128256 fp32: 911 us for 4096 rows, 925 with 1024).  Few
+  // rows alone on the chip take 1024 early.
+  const int threads = a.n <= 128 ? (row_bytes > 16384.0 ? 1024 : 256)
+                      : row_bytes <= 12288.0 && a.k < 256 ? 64 : row_bytes <= 65536.0 ? 256 : 512;
   auto launch = [&](auto d, auto m) {
     constexpr int D = decltype(d)::value, M = decltype(m)::value;
     if (a.slices > 0) {
@@ -576,7 +575,7 @@ hipError_t launch_distill(int dt, const DistillArgs& a, hipStream_t stream) {
         else rows(t, std::false_type{}, per, r);
       };
       // without a gradient nothing is read again: no vectors held, more rows in flight
-      if (threads == 1024) by_stream(Int<1024>{}, Int<2>{}, Int<0>{});
+      if (threads == 1024) rows(Int<1024>{}, std::false_type{}, Int<2>{}, Int<0>{});
       else if (!a.dlogits && threads == 512) rows(Int<512>{}, std::false_type{}, Int<3>{}, Int<0>{});
       else if (!a.dlogits && threads == 256) rows(Int<256>{}, std::false_type{}, Int<5>{}, Int<0>{});
       else if (!a.dlogits) rows(Int<64>{}, std::false_type{}, Int<4>{}, Int<0>{});
