@@ -345,6 +345,9 @@ int dmuon_adamw_step(int count, void* const* params, const void* const* grads, f
  * - Any pointer aligned to its element size is accepted; 16-byte aligned rows are
  *   the fastest.
  * - bf16 results are rounded once (RNE) from fp32.
+ * - The same inputs in the same shapes give the same bits, whatever their
+ *   addresses and strides.  The order of a sum may follow the shape of the call
+ *   (the number of rows or tokens in it), never what other rows hold.
  * ------------------------------------------------------------------------ */
 
 /* Types of token, index and position arrays. */
