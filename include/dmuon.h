@@ -456,7 +456,7 @@ int dmuon_adamw_rows_step(void* param, const void* grad_rows, int64_t n_grad_row
  * labels    : NULL (then ce_weight must be 0), or device, n entries of
  *             index_dtype.  A label outside [0, vocab) leaves CE out of its row.
  * k         : 0 .. DMUON_MAX_TEACHER_K; 0 needs kd_weight = 0.
- * temperature : T > 0, finite.  kd_weight, ce_weight, grad_scale: finite.
+ * temperature : T in [1e-6, 1e6].  kd_weight, ce_weight, grad_scale: finite.
  * row_weight : NULL (1), or device float32[n].  A row of weight 0 is not read:
  *             its loss and gradient are 0 whatever it holds.  The same holds
  *             for a row without a valid teacher entry and without a label.

@@ -162,6 +162,55 @@ def test_masked_and_extreme_logits():
         assert torch.isnan(losses[3:]).all() and torch.isnan(dz[3:]).any(1).all()
 
 
+@pytest.mark.parametrize("temperature", [0.01, 4.0, 100.0])
+def test_far_temperatures(temperature):
+    z, idx, y, lab, w = make(9, 3001, 8, torch.float32, 13)
+    check(z, idx, y, lab, w, float(np.float32(temperature)), 1.0, 0.5, 1.0)
+
+
+@pytest.mark.parametrize("temperature", [1e-6, 1e6])
+@pytest.mark.parametrize("vocab", [500, 9000, 70000])
+def test_limits_of_the_temperature_with_masked_logits(temperature, vocab):
+    """At the smallest temperature all of the weight is on the largest logit, at
+    the largest it is spread evenly over the elements that are not masked."""
+    rng = np.random.default_rng(14)
+    z = torch.from_numpy(rng.standard_normal((3, vocab)).astype(np.float32)).cuda()
+    z[:, 5:vocab // 2] = -float("inf")
+    z[:, 3] = 40.0
+    idx = torch.tensor([[3, 4], [3, vocab - 1], [3, 0]], device="cuda")
+    y = torch.tensor([[0.0, -float("inf")]] * 3, device="cuda")     # the teacher names element 3 alone
+    losses, dz = nsa.distill_loss(z, idx, y, temperature=temperature, kd_weight=1.0 / temperature)
+    assert torch.isfinite(losses).all() and torch.isfinite(dz).all() and not dz[:, 5:vocab // 2].any()
+    kept = vocab - (vocab // 2 - 5)
+    p = torch.zeros_like(z) if temperature < 1 else torch.where(torch.isinf(z), 0.0, 1.0 / kept)
+    q = torch.zeros_like(z)
+    q[:, 3] = 1.0
+    if temperature < 1:
+        p = q
+    # the spread 45 / 1e6 moves a probability by that share of it
+    torch.testing.assert_close(dz, p - q, rtol=2e-4, atol=1e-6)
+
+
+def test_every_named_element_of_a_large_batch():
+    """Beyond the memory-side cache: each named element is rewritten behind the
+    sweep that wrote its neighbours."""
+    n, vocab, k = 2600, 70000, 40
+    torch.manual_seed(15)
+    z = torch.randn(n, vocab, device="cuda", dtype=torch.bfloat16)
+    idx = torch.stack([torch.randperm(vocab, device="cuda")[:k] for _ in range(n)])
+    y, lab = torch.randn(n, k, device="cuda"), torch.randint(0, vocab, (n,), device="cuda")
+    _, dz = nsa.distill_loss(z, idx, y, lab, temperature=1.0, ce_weight=0.5)
+    p = torch.stack([z[r].double().log_softmax(0).exp() for r in range(n)])
+    want = 1.5 * p
+    named = torch.zeros(n, vocab, dtype=torch.bool, device="cuda")
+    want.scatter_add_(1, idx, -y.double().softmax(1))
+    want.scatter_add_(1, lab[:, None], torch.full((n, 1), -0.5, dtype=torch.float64, device="cuda"))
+    named.scatter_(1, idx, True).scatter_(1, lab[:, None], True)
+    # sums of 70000 positive terms, 140 additions to a thread: 5e-5 covers 800 fp32 units
+    err, bound = (dz.double() - want).abs(), (half_step(torch.bfloat16) + 5e-5) * want.abs() + 5e-5 * 1.5 * p + 1e-7
+    assert bool((err[named] <= bound[named]).all()) and bool((err <= bound).all())
+
+
 def test_skipped_rows_are_not_read():
     z = torch.full((4, 5000), float("nan"), device="cuda")
     z[3] = 1.0

@@ -123,7 +123,7 @@ def test_distill_loss(lib):
     assert need > 0
     refused(lib.dmuon_distill_loss, LOSS, [
         (dict(dt=2), TYPE), (dict(idt=0), TYPE), (dict(n=-1), BAD), (dict(vocab=0), BAD), (dict(k=-1), BAD),
-        (dict(k=1025), BAD), (dict(t=0.0), BAD), (dict(t=-1.0), BAD), (dict(t=NAN), BAD), (dict(t=INF), BAD),
+        (dict(k=1025), BAD), (dict(t=0.0), BAD), (dict(t=-1.0), BAD), (dict(t=NAN), BAD), (dict(t=INF), BAD), (dict(t=9e-7), BAD), (dict(t=1.1e6), BAD),
         (dict(kd=NAN), BAD), (dict(ce=INF), BAD), (dict(scale=NAN), BAD), (dict(k=0), BAD), (dict(labels=0), BAD),
         (dict(stride=79999), BAD), (dict(dstride=79999), BAD), (dict(logits=0), BAD), (dict(index=0), BAD),
         (dict(teacher=0), BAD), (dict(losses=0), BAD), (dict(ws=0), WS), (dict(bytes=need - 1), WS),
