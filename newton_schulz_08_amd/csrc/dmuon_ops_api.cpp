@@ -70,7 +70,9 @@ bool disjoint(const Buf& a, const Buf& b) {
                                              : (pitch - (a.begin() - b.begin()) % pitch) % pitch;
   return d >= static_cast<uintptr_t>(a.width) && d + static_cast<uintptr_t>(b.width) <= pitch;
 }
-bool same(const Buf& a, const Buf& b) { return a.p == b.p && a.pitch == b.pitch && a.rows == b.rows && a.width == b.width; }
+bool same(const Buf& a, const Buf& b) {
+  return a.p == b.p && a.rows == b.rows && a.width == b.width && (a.rows == 1 || a.pitch == b.pitch);
+}
 
 // Pointers set and aligned, written buffers apart from all others.  A written
 // buffer may coincide with a read one of the listed in-place pairs.

@@ -212,7 +212,8 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
   constexpr int kPer = PER;
   const T* z = static_cast<const T*>(a.logits) + row * a.stride;
   const int tid = threadIdx.x, wave = tid >> 6;
-  // named elements: on their way while the row is swept
+  // named elements: their indices are on their way while the row is swept, their
+  // logits while its maximum is found
   float y[kPer], zj[kPer];
   int idx[kPer];
 #pragma unroll
@@ -220,7 +221,6 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
     const int j = tid + p * THREADS;
     idx[p] = -1;
     y[p] = -INFINITY;
-    zj[p] = 0.0f;
     if (j < a.k && a.kd != 0.0f) {
       const int64_t i = load_index(a.index, row * a.k + j, a.idx64);
       if (i >= 0 && i < a.vocab) {
@@ -231,7 +231,6 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
       const int64_t i = load_index(a.labels, row, a.idx64);
       if (i >= 0 && i < a.vocab) idx[p] = static_cast<int>(i);
     }
-    if (idx[p] >= i0 && idx[p] < i1) zj[p] = static_cast<float>(gmem(z)[idx[p]]);
   }
   const float s2 = scale_of(a);
   Expo<MODE> x;
@@ -260,11 +259,7 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
   float ytop = -INFINITY;
 #pragma unroll
   for (int p = 0; p < kPer; ++p) {
-    const int j = tid + p * THREADS;
-    if (j <= a.k) {
-      sh.idx[j] = idx[p];
-      sh.z[j] = zj[p];
-    }
+    zj[p] = idx[p] >= i0 && idx[p] < i1 ? static_cast<float>(gmem(z)[idx[p]]) : 0.0f;
     ytop = fmaxf(ytop, y[p]);
   }
   {
@@ -315,7 +310,11 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
         if (idx[p] >= i0 && idx[p] < i1) dot += static_cast<double>(e) * zj[p];
       }
     }
-    if (j <= a.k) sh.e[j] = e;
+    if (j <= a.k) {
+      sh.idx[j] = idx[p];
+      sh.z[j] = zj[p];
+      sh.e[j] = e;
+    }
   }
   st = wave_sum(st);
   if constexpr (MODE != kOne) s1 = wave_sum(s1);

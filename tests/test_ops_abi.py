@@ -154,6 +154,7 @@ def test_qk_forward(lib):
     f = lib.dmuon_qk_norm_rope_forward
     accepted(f, QK)
     accepted(f, dict(QK, qo=QK["q"], qos=128, ko=QK["k"], kos=128))          # in place, one packed buffer
+    accepted(f, dict(QK, shape=qk_shape(tokens=1), qo=QK["q"], qos=64, ko=QK["k"], kos=32))   # one token has no stride
     accepted(f, dict(QK, qw=0, kw=0))
     accepted(f, dict(QK, shape=qk_shape(rot_dim=0), pos=0, rope=0))
     accepted(f, dict(QK, shape=qk_shape(k_heads=0), k=0, ks=0, ko=0, kos=0))
