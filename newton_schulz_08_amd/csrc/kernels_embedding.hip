@@ -538,26 +538,40 @@ __global__ __launch_bounds__(kEgThreads) void egrad_kernel(EmbedGradArgs a, int 
 #pragma unroll
     for (int e = 0; e < C; ++e) acc[e] = 0.0f;
   };
-  for (int64_t p = p0; p < p1; p += U) {
-    int s[U];
-    float v[U][C] = {};
+  using V = typename Loose<T, C>::V;
+  // slots and positions are read one step ahead of the rows they lead to
+  // (65536 x 4096 bf16 rows: 274 us with neither, 254 with bf16 kept as loaded, 236 with both)
+  int sn[U], tn[U];
+  auto ahead = [&](int64_t p) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t q = least(p + u, p1 - 1);
-      s[u] = gmem(a.slot)[q];
-      const int t = gmem(a.order)[q];
+      sn[u] = gmem(a.slot)[q];
+      tn[u] = gmem(a.order)[q];
+    }
+  };
+  ahead(p0);
+  for (int64_t p = p0; p < p1; p += U) {
+    int s[U];
+    V raw[U];   // bf16 is converted where it is added: 57 registers instead of 76, eight waves a SIMD
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      s[u] = sn[u];
+      const int t = tn[u];
       if (p + u >= p1 || static_cast<unsigned>(t) >= a.n) s[u] = -1;
       if (s[u] >= 0) {
         const T* src = dout + t * a.dim;
         if (cols == C) {
-          load_any<C, STREAM>(src, v[u]);
+          const auto r = reinterpret_cast<gptr<const V>>(gmem(src));
+          if constexpr (STREAM) raw[u] = __builtin_nontemporal_load(r);
+          else raw[u] = *r;
         } else {
 #pragma unroll
-          for (int e = 0; e < C; ++e)
-            if (e < cols) v[u][e] = static_cast<float>(gmem(src)[e]);
+          for (int e = 0; e < C; ++e) raw[u][e] = e < cols ? gmem(src)[e] : static_cast<T>(0.0f);
         }
       }
     }
+    ahead(least(p + U, p1 - 1));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (s[u] < 0) continue;
@@ -566,7 +580,7 @@ __global__ __launch_bounds__(kEgThreads) void egrad_kernel(EmbedGradArgs a, int 
         cur = s[u];
       }
 #pragma unroll
-      for (int e = 0; e < C; ++e) acc[e] += v[u][e];
+      for (int e = 0; e < C; ++e) acc[e] += static_cast<float>(raw[u][e]);
     }
   }
   flush(true);
