@@ -9,6 +9,9 @@
 //   dz_i = gs w (kd T (exp(z_i / T - lse_T) - q_i) + ce (exp(z_i - lse_1) - [i = label]))
 //
 // HBM-bound: one or two exponentials per element against 2 or 4 bytes each way.
+// Measured: 8192 x 128256 bf16 with labels at T = 2, a tenth of the rows masked,
+// 812 us (4.0 GB that it cannot do without, 4.9 TB/s); the loss alone of as many
+// unmasked rows 354 us (5.9 TB/s).
 //
 // Exponentials are taken in base 2 against an integer reference: with
 // s2 = log2(e) / T and M = ceil(max z s2), exp2(z s2 - M) is one fused
