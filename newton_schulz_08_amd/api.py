@@ -383,22 +383,37 @@ def adamw_step_(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], e
 class AdamWStep:
     """AdamW state for a fixed list of non-matrix parameters: float32 moments
     (zeros), the step counter and a reusable workspace.  Each call runs one
-    dmuon_adamw_step on the gradients given at construction."""
+    dmuon_adamw_step on the gradients given at construction.
 
-    def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], lr: float = 1e-3,
+    The gradient of a 2-D table may be a pair (grad_rows, row_index) instead,
+    as embedding_grad(..., form="rows") and its plan hold them: such a table
+    takes the same update through dmuon_adamw_rows_step."""
+
+    def __init__(self, params: Sequence[torch.Tensor], grads: Sequence, lr: float = 1e-3,
                  betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01):
         self.params, self.grads = list(params), list(grads)
         self.exp_avg = [torch.zeros(p.shape, dtype=torch.float32, device=p.device) for p in self.params]
         self.exp_avg_sq = [torch.zeros(p.shape, dtype=torch.float32, device=p.device) for p in self.params]
         self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
         self.step = 0
+        if len(self.grads) != len(self.params):
+            raise ValueError("params and grads must have the same length")
+        self._rows = [i for i, g in enumerate(self.grads) if isinstance(g, tuple)]
+        if any(len(self.grads[i]) != 2 for i in self._rows):
+            raise ValueError("a row gradient is a pair (grad_rows, row_index)")
+        self._dense = [i for i in range(len(self.params)) if i not in self._rows]
         dev = self.params[0].device if self.params else None
-        self.workspace = alloc_workspace(adamw_step_workspace_bytes([p.numel() for p in self.params]), dev)
+        self.workspace = alloc_workspace(adamw_step_workspace_bytes([self.params[i].numel() for i in self._dense]), dev)
 
     def __call__(self, stream=None) -> None:
         self.step += 1
-        adamw_step_(self.params, self.grads, self.exp_avg, self.exp_avg_sq, self.step, self.lr, self.betas,
-                    self.eps, self.weight_decay, self.workspace, stream)
+        adamw_step_(*([t[i] for i in self._dense] for t in (self.params, self.grads, self.exp_avg, self.exp_avg_sq)),
+                    self.step, self.lr, self.betas, self.eps, self.weight_decay, self.workspace, stream)
+        if self._rows:
+            from .ops import adamw_rows_step_   # which builds on this module
+            for i in self._rows:
+                adamw_rows_step_(self.params[i], *self.grads[i], self.exp_avg[i], self.exp_avg_sq[i], self.step, self.lr,
+                                 self.betas, self.eps, self.weight_decay, stream)
         _used_on(stream, self.workspace, *self.exp_avg, *self.exp_avg_sq)
 
 

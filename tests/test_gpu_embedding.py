@@ -203,6 +203,30 @@ def test_adamw_rows_unaligned_and_indices_outside():
     assert torch.equal(p, q) and torch.equal(m, k) and torch.equal(v, w)
 
 
+def test_optimizer_takes_row_gradients_beside_dense_ones():
+    rng = np.random.default_rng(9)
+    tok = dev(rng.integers(0, 60, 90), torch.int64)
+    dout = dev(rng.standard_normal((90, 32)), torch.float32)
+    plan = nsa.embedding_plan(tok, 60)
+    rows, dense = nsa.embedding_grad(plan, dout, form="rows"), nsa.embedding_grad(plan, dout)
+    table, gain, g = (dev(rng.standard_normal(s), torch.float32) for s in ((60, 32), 32, 32))
+    a, b = [table.clone(), gain.clone()], [table.clone(), gain.clone()]
+    one = nsa.AdamWStep(a, [(rows, plan.row_index), g], lr=1e-2)
+    two = nsa.AdamWStep(b, [dense, g], lr=1e-2)
+    for _ in range(3):
+        one()
+        two()
+    assert one.step == 3 and all(torch.equal(x, y) for x, y in zip(a + one.exp_avg + one.exp_avg_sq, b + two.exp_avg + two.exp_avg_sq))
+    alone = nsa.AdamWStep([table], [(rows, plan.row_index)], lr=1e-2)
+    for _ in range(3):
+        alone()
+    assert torch.equal(table, a[0])
+    with pytest.raises(ValueError):
+        nsa.AdamWStep([table], [(rows,)])
+    with pytest.raises(ValueError):
+        nsa.AdamWStep([table], [])
+
+
 # ---------------------------------------------------------------- streams and graphs
 def test_graph_replays_see_new_tokens():
     rng = np.random.default_rng(6)

@@ -130,7 +130,7 @@ def test_training_step():
     scattered = torch.zeros_like(p["table"])
     scattered[plan.rows[used].long()] = rows[used]
     state = [torch.zeros_like(p["table"]) for _ in range(4)]
-    table_dense = p["table"].clone()
+    table_dense, before_table = p["table"].clone(), p["table"].clone()
     nsa.adamw_rows_step_(p["table"], rows, plan.row_index, state[0], state[1], 1)
     nsa.adamw_step_([table_dense], [scattered], [state[2]], [state[3]], 1)
     assert torch.equal(p["table"], table_dense) and torch.equal(state[0], state[2]) and torch.equal(state[1], state[3])
@@ -138,6 +138,8 @@ def test_training_step():
     mats = ["qkv", "o"]
     nsa.muon_step([p[k] for k in mats], [g[k] for k in mats], [torch.zeros_like(p[k]) for k in mats], lr=0.02)
     rest = [k for k in names if k not in mats]
-    nsa.AdamWStep([p[k] for k in rest], [g[k] for k in rest])()
+    table = before_table.clone()
+    nsa.AdamWStep([p[k] for k in rest] + [table], [g[k] for k in rest] + [(rows, plan.row_index)])()
+    assert torch.equal(table, p["table"])   # the optimizer's own way to the row step
     for k in names:
         assert torch.isfinite(p[k]).all() and not torch.equal(p[k], before[k])
