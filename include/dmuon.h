@@ -465,8 +465,10 @@ int dmuon_adamw_rows_step(void* param, const void* grad_rows, int64_t n_grad_row
  *             `dtype`, dlogits_stride apart.  May equal logits with the same
  *             stride (in place); must not overlap it otherwise.  Elements
  *             between the rows are left as they are.
- * -inf logits are masked elements (probability 0); a row of nothing but -inf
- * has no distribution and gets NaN.
+ * -inf logits are masked elements (probability 0), and so are finite ones as
+ * far below the row's largest as masks lie.  Only differences within a row count,
+ * wherever it lies: one that holds a single value throughout is an even
+ * distribution.  A row of nothing but -inf has no distribution and gets NaN.
  */
 int dmuon_distill_loss_workspace_bytes(int64_t n, int64_t vocab, size_t* bytes_out);
 int dmuon_distill_loss(const void* logits, int64_t n, int64_t vocab, int64_t logits_stride, int dtype,

@@ -459,7 +459,7 @@ int dmuon_distill_loss(const void* logits, int64_t n, int64_t vocab, int64_t log
     DMUON_TRY(check_index(index_dtype, "index_dtype"));
     DMUON_TRY(check_tokens(n, vocab));
     DMUON_TRY(check_range(k, 0, DMUON_MAX_TEACHER_K, "k"));
-    // the kernels form z log2(e) / T for |z| up to 2^100 in fp32
+    // log2(e) / T is then a normal float, and its product with a logit at most overflows to infinity
     if (!(temperature >= 1e-6f && temperature <= 1e6f)) return invalid("temperature must lie in [1e-6, 1e6]");
     if (!std::isfinite(kd_weight) || !std::isfinite(ce_weight) || !std::isfinite(grad_scale))
       return invalid("kd_weight, ce_weight and grad_scale must be finite");

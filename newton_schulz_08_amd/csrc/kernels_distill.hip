@@ -19,13 +19,16 @@
 // v_exp_f32, and moving a sum to another reference multiplies it by an exact
 // power of two.  Where the label's term has another exponent than the
 // teacher's, T = 2 or 4 squares the first exponential (M doubles with it)
-// instead of taking a second one.  A maximum that is not below 2^100 in size
-// (infinite, or a row masked with the type's lowest value) would leave the
-// range of z s2: such rows subtract the maximum first.
+// instead of taking a second one.  M is the ceiling of a rounded product, which
+// below 2^22 is within 1/4 of the exact one; further out the difference would
+// overflow the exponential.  So M stops at -+ 2^22: elements further down than
+// that (finite masks) come out as 0, and a row whose maximum lies beyond it on
+// either side subtracts the maximum first.
 //
-// Sums of exponentials are fp32; the few scalars of a row are joined in fp64,
-// so that the loss is exact to the fp32 sums although it is a difference of
-// terms that grow with the vocabulary.
+// Sums of exponentials are fp32; the few scalars of a row are joined in fp64
+// and counted from the row's maximum, so that the loss is exact to the fp32 sums
+// although it is a difference of terms that grow with the vocabulary and with
+// the logits.
 //
 // Many rows: a block takes a row, reads it once from HBM for its sums and a
 // second time, now from the memory-side cache, for the gradient.  Few rows:
@@ -44,7 +47,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kLn2 = 0.6931471805599453094;
-constexpr float kFar = 1.2676506e30f;   // 2^100
+constexpr float kFar = 4194304.0f;   // 2^22, of z s2
 // Vectors of a long row's thread that are kept between the two passes, in
 // registers and behind them in LDS (128256 bf16, 31 vectors: 892 us for 8192
 // rows with none, 854 with 12 + 0, 811 with 12 + 3, 817 with 12 + 6; 790 were
@@ -73,7 +76,8 @@ struct Sums {
   float st = 0.0f, s1 = 0.0f;        // sums of exponentials, against the references of `top`
   float ytop = -INFINITY;            // largest teacher logit
   double ysum = 0.0;                 // sum of e_j = exp((y_j - ytop) / T)
-  double dot = 0.0;                  // sum of e_j z_j
+  double dot = 0.0;                  // sum of e_j (z_j - origin(top)), over the entries in the slice
+  float part = 0.0f;                 // sum of their e_j (what it scales adds up without cancelling)
   double ent = 0.0;                  // sum of e_j (y_j - ytop) / T
 };
 
@@ -81,25 +85,39 @@ struct Sums {
 template <int THREADS, int PER> struct Shared {
   static constexpr int kWaves = THREADS / 64, kNamed = THREADS * PER;
   float top[kWaves], ytop[kWaves], st[kWaves], s1[kWaves];
+  float part[kWaves];
   double ysum[kWaves], dot[kWaves], ent[kWaves];
   int idx[kNamed];                   // elements named by the teacher (label last), or -1
   float e[kNamed];
   float z[kNamed];
 };
 
+// What logits are counted from: the largest one, if that is a number to subtract.
+__device__ __forceinline__ float origin(float top) { return isfinite(top) ? top : 0.0f; }
+
 // Exponentials of one row: exponents s2 and, in kTwo, log2(e).
 template <int MODE> struct Expo {
   float s2, m0, m1, top;
-  bool far;
+  bool far;   // the maximum is beyond the fused form, in one exponent or the other
   __device__ __forceinline__ static float reference(float top, float s2) {
-    return ceilf(fminf(fmaxf(top, -kFar), kFar) * s2);
+    return ceilf(fminf(fmaxf(top * s2, -kFar), kFar));
   }
   __device__ __forceinline__ void set(float t, float scale) {
     s2 = scale;
     top = t;
-    far = !(fabsf(t) < kFar);
+    far = !(fabsf(t) * (MODE == kOne ? s2 : fmaxf(s2, kLog2e)) < kFar);
     m0 = reference(t, s2);
     m1 = MODE == kTwo ? reference(t, kLog2e) : MODE == kSquare ? 2.0f * m0 : 4.0f * m0;
+  }
+  // What the sums' exponentials are relative to, in units of the exponent s2
+  // (`second`: the label's), exactly: products of two floats fit a double.
+  __device__ __forceinline__ double zero(bool second) const {
+    const bool one = second && MODE != kOne;
+    return far ? static_cast<double>(top) * (one ? kLog2e : s2) : static_cast<double>(one ? m1 : m0);
+  }
+  // ... and behind the maximum
+  __device__ __forceinline__ double behind(bool second) const {
+    return far ? 0.0 : zero(second) - static_cast<double>(top) * (second && MODE != kOne ? kLog2e : s2);
   }
   // FAR: the slow form
   template <bool FAR> __device__ __forceinline__ void both(float v, float* et, float* e1) const {
@@ -299,6 +317,8 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
     st *= __builtin_amdgcn_exp2f(x.m0 - all.m0);
     if constexpr (MODE != kOne) s1 *= __builtin_amdgcn_exp2f(x.m1 - all.m1);
   }
+  const double from = origin(s.top);
+  float part = 0.0f;
   double ysum = 0.0, dot = 0.0, ent = 0.0;
 #pragma unroll
   for (int p = 0; p < kPer; ++p) {
@@ -310,7 +330,10 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
       ysum += e;
       if (e != 0.0f) {
         ent += static_cast<double>(e) * d;
-        if (idx[p] >= i0 && idx[p] < i1) dot += static_cast<double>(e) * zj[p];
+        if (idx[p] >= i0 && idx[p] < i1) {
+          dot += e * (zj[p] - from);
+          part += e;
+        }
       }
     }
     if (j <= a.k) {
@@ -324,6 +347,7 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
   if (a.kd != 0.0f) {
     ysum = wave_sum(ysum);
     dot = wave_sum(dot);
+    part = wave_sum(part);
     ent = wave_sum(ent);
   }
   if ((tid & 63) == 0) {
@@ -331,6 +355,7 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
     sh.s1[wave] = s1;
     sh.ysum[wave] = ysum;
     sh.dot[wave] = dot;
+    sh.part[wave] = part;
     sh.ent[wave] = ent;
   }
   __syncthreads();
@@ -341,25 +366,23 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
     s.s1 += MODE != kOne ? sh.s1[w] : sh.st[w];
     s.ysum += sh.ysum[w];
     s.dot += sh.dot[w];
+    s.part += sh.part[w];
     s.ent += sh.ent[w];
   }
 }
 
-// log2 of the sum of exponentials, in units of the exponent s2 (or log2(e)).
-template <int MODE> __device__ __forceinline__ double log2_sum(const Expo<MODE>& x, double sum, bool second) {
-  const float s2 = second && MODE != kOne ? kLog2e : x.s2, m = second && MODE != kOne ? x.m1 : x.m0;
-  return (x.far ? static_cast<double>(x.top) * s2 : static_cast<double>(m)) + log2(sum);
-}
-
-// The row's loss from its sums; z_label: the label's logit.
+// The row's loss from its sums; s.dot over all entries, z_label the label's
+// logit.  Log-sums and logits are both taken from the row's maximum: their
+// difference then keeps its digits however far the row lies from zero.
 template <int MODE>
 __device__ __forceinline__ float row_loss(const DistillArgs& a, const Sums& s, const Expo<MODE>& x, double st, double s1,
                                           bool has_kd, bool has_ce, float z_label, float w) {
   double loss = 0.0;
   if (has_kd)
     loss += a.kd * static_cast<double>(a.temperature) * a.temperature *
-            (s.ent / s.ysum - log(s.ysum) + kLn2 * (log2_sum(x, st, false) - s.dot / s.ysum * x.s2));
-  if (has_ce) loss += a.ce * kLn2 * (log2_sum(x, s1, true) - static_cast<double>(z_label) * kLog2e);
+            (s.ent / s.ysum - log(s.ysum) + kLn2 * (x.behind(false) + log2(st) - s.dot / s.ysum * x.s2));
+  if (has_ce)
+    loss += a.ce * kLn2 * (x.behind(true) + log2(s1) - (static_cast<double>(z_label) - origin(s.top)) * kLog2e);
   return static_cast<float>(w * loss);
 }
 
@@ -463,7 +486,7 @@ __global__ __launch_bounds__(THREADS, 4) void distill_row_kernel(DistillArgs a) 
 }
 
 // Words of a slice's sums.
-enum { kPmMax = 0, kPmSumT, kPmSum1, kPmDotHi, kPmDotLo, kPmLabel, kPmWords = 8 };
+enum { kPmMax = 0, kPmSumT, kPmSum1, kPmDotHi, kPmDotLo, kPmPart, kPmLabel, kPmWords = 8 };
 constexpr int kSliceThreads = 256, kSlicePer = kDistillMaxK / kSliceThreads + 1;
 
 template <int DT, int MODE>
@@ -484,6 +507,7 @@ __global__ __launch_bounds__(kSliceThreads) void distill_slice_kernel(DistillArg
     const float hi = static_cast<float>(s.dot);
     p[kPmDotHi] = hi;
     p[kPmDotLo] = isfinite(hi) ? static_cast<float>(s.dot - hi) : 0.0f;
+    p[kPmPart] = s.part;
     p[kPmLabel] = sh.z[a.k];   // 0 outside this slice
   }
 }
@@ -523,17 +547,17 @@ __global__ __launch_bounds__(kSliceThreads) void distill_join_kernel(DistillArgs
   Expo<MODE> x, y;
   x.set(s.top, scale_of(a));
   y.set(top, x.s2);
-  float ft = 0.0f, f1 = 0.0f;   // a slice of nothing but -inf, or one too far below the maximum
-  if (x.far && (y.far && top != -INFINITY)) {
-    ft = __builtin_amdgcn_exp2f((top - s.top) * x.s2);
-    f1 = __builtin_amdgcn_exp2f((top - s.top) * (MODE == kOne ? x.s2 : kLog2e));
-  } else if (!x.far && !y.far) {
-    ft = __builtin_amdgcn_exp2f(y.m0 - x.m0);
-    f1 = MODE == kOne ? ft : __builtin_amdgcn_exp2f(y.m1 - x.m1);
+  // from a slice's references to the row's; either may be in either form
+  float ft = 0.0f, f1 = 0.0f;   // a slice of nothing but -inf
+  if (top != -INFINITY) {
+    ft = __builtin_amdgcn_exp2f(static_cast<float>(y.zero(false) - x.zero(false)));
+    f1 = MODE == kOne ? ft : __builtin_amdgcn_exp2f(static_cast<float>(y.zero(true) - x.zero(true)));
   }
   const double st = wave_sum(on ? static_cast<double>(gmem(p)[kPmSumT]) * ft : 0.0);
   const double s1 = wave_sum(on ? static_cast<double>(gmem(p)[kPmSum1]) * f1 : 0.0);
-  s.dot = wave_sum(on ? static_cast<double>(gmem(p)[kPmDotHi]) + static_cast<double>(gmem(p)[kPmDotLo]) : 0.0);
+  s.dot = wave_sum(on ? static_cast<double>(gmem(p)[kPmDotHi]) + static_cast<double>(gmem(p)[kPmDotLo]) +
+                            gmem(p)[kPmPart] * (static_cast<double>(origin(top)) - origin(s.top))   // to the row's origin
+                      : 0.0);
   const float z_label = wave_sum(on ? gmem(p)[kPmLabel] : 0.0f);
   if (slice == 0 && threadIdx.x == 0) gmem(a.losses)[row] = row_loss(a, s, x, st, s1, has_kd, has_ce, z_label, w);
   if (!a.dlogits) return;
