@@ -435,6 +435,11 @@ int dmuon_embedding_backward(const void* dout, int64_t n, int64_t dim, int dout_
 int dmuon_adamw_rows_step(void* param, const void* grad_rows, int64_t n_grad_rows, const int32_t* row_index,
                           float* exp_avg, float* exp_avg_sq, int64_t rows, int64_t dim, int dtype, int step, float lr,
                           float beta1, float beta2, float eps, float weight_decay, void* hip_stream);
+/* The argument checks of that step alone, without a device: for a caller that
+ * has several steps to take, all or none. */
+int dmuon_adamw_rows_check(const void* param, const void* grad_rows, int64_t n_grad_rows, const int32_t* row_index,
+                           const float* exp_avg, const float* exp_avg_sq, int64_t rows, int64_t dim, int dtype,
+                           int step, float lr, float beta1, float beta2, float eps, float weight_decay);
 
 /*
  * Distillation from a teacher's top logits, loss and gradient in one call.

@@ -125,6 +125,7 @@ SIGNATURES = {
     "dmuon_embedding_backward_workspace_bytes": (_I, [_I64, _I64, _I, _SZP]),
     "dmuon_embedding_backward": (_I, [_P, _I64, _I64, _I, _F, _P, _P, _P, _P, _P, _I64, _I, _P, _I, _P, _SZ, _P]),
     "dmuon_adamw_rows_step": (_I, [_P, _P, _I64, _P, _P, _P, _I64, _I64, _I, _I, _F, _F, _F, _F, _F, _P]),
+    "dmuon_adamw_rows_check": (_I, [_P, _P, _I64, _P, _P, _P, _I64, _I64, _I, _I, _F, _F, _F, _F, _F]),
     "dmuon_distill_loss_workspace_bytes": (_I, [_I64, _I64, _SZP]),
     "dmuon_distill_loss": (_I, [_P, _I64, _I64, _I64, _I, _P, _I, _P, _I, _P, _F, _F, _F, _P, _F, _P, _P, _I64, _P,
                                 _SZ, _P]),

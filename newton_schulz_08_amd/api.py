@@ -380,6 +380,15 @@ def adamw_step_(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], e
     _used_on(stream, workspace if own_ws else None)
 
 
+def _is_rows(grad) -> bool:
+    """Whether a gradient is given as (grad_rows, row_index)."""
+    if not isinstance(grad, tuple):
+        return False
+    if len(grad) != 2:
+        raise ValueError("a row gradient is a pair (grad_rows, row_index)")
+    return True
+
+
 class AdamWStep:
     """AdamW state for a fixed list of non-matrix parameters: float32 moments
     (zeros), the step counter and a reusable workspace.  Each call runs one
@@ -387,7 +396,8 @@ class AdamWStep:
 
     The gradient of a 2-D table may be a pair (grad_rows, row_index) instead,
     as embedding_grad(..., form="rows") and its plan hold them: such a table
-    takes the same update through dmuon_adamw_rows_step."""
+    takes the same update through dmuon_adamw_rows_step.  A call that refuses
+    an argument changes nothing: no parameter, no moment, not the step counter."""
 
     def __init__(self, params: Sequence[torch.Tensor], grads: Sequence, lr: float = 1e-3,
                  betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01):
@@ -398,22 +408,29 @@ class AdamWStep:
         self.step = 0
         if len(self.grads) != len(self.params):
             raise ValueError("params and grads must have the same length")
-        self._rows = [i for i, g in enumerate(self.grads) if isinstance(g, tuple)]
-        if any(len(self.grads[i]) != 2 for i in self._rows):
-            raise ValueError("a row gradient is a pair (grad_rows, row_index)")
-        self._dense = [i for i in range(len(self.params)) if i not in self._rows]
         dev = self.params[0].device if self.params else None
-        self.workspace = alloc_workspace(adamw_step_workspace_bytes([self.params[i].numel() for i in self._dense]), dev)
+        self.workspace = alloc_workspace(
+            adamw_step_workspace_bytes([p.numel() for p, g in zip(self.params, self.grads) if not _is_rows(g)]), dev)
 
     def __call__(self, stream=None) -> None:
-        self.step += 1
-        adamw_step_(*([t[i] for i in self._dense] for t in (self.params, self.grads, self.exp_avg, self.exp_avg_sq)),
-                    self.step, self.lr, self.betas, self.eps, self.weight_decay, self.workspace, stream)
-        if self._rows:
-            from .ops import adamw_rows_step_   # which builds on this module
-            for i in self._rows:
-                adamw_rows_step_(self.params[i], *self.grads[i], self.exp_avg[i], self.exp_avg_sq[i], self.step, self.lr,
-                                 self.betas, self.eps, self.weight_decay, stream)
+        if not (len(self.params) == len(self.grads) == len(self.exp_avg) == len(self.exp_avg_sq)):
+            raise ValueError("params, grads, exp_avg and exp_avg_sq must have the same length")
+        dense, tables, step = ([], [], [], []), [], self.step + 1
+        for state in zip(self.params, self.grads, self.exp_avg, self.exp_avg_sq):
+            if _is_rows(state[1]):
+                tables.append(state)
+            else:
+                for column, t in zip(dense, state):
+                    column.append(t)
+        row_steps = []
+        if tables:   # all of them checked before the first step is taken
+            from .ops import adamw_rows_prepared   # which builds on this module
+            row_steps = [adamw_rows_prepared(stream, p, *g, m, v, step, self.lr, self.betas, self.eps, self.weight_decay)
+                         for p, g, m, v in tables]
+        adamw_step_(*dense, step, self.lr, self.betas, self.eps, self.weight_decay, self.workspace, stream)
+        for take in row_steps:
+            take()
+        self.step = step
         _used_on(stream, self.workspace, *self.exp_avg, *self.exp_avg_sq)
 
 

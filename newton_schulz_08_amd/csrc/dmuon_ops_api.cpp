@@ -164,6 +164,26 @@ int egrad_chunk(int64_t n, int64_t dim, int dout_dtype) {
   return chunk;
 }
 
+// ---------------------------------------------------------------- AdamW rows
+int check_adamw_rows(const void* param, const void* grad_rows, int64_t n_grad_rows, const int32_t* row_index,
+                     const float* exp_avg, const float* exp_avg_sq, int64_t rows, int64_t dim, int dtype, int step,
+                     float lr, float beta1, float beta2, float eps, float weight_decay) {
+  DMUON_TRY(check_float(dtype, "dtype"));
+  DMUON_TRY(check_range(rows, 1, DMUON_MAX_VOCAB, "rows"));
+  DMUON_TRY(check_range(dim, 1, DMUON_MAX_DIM, "dim"));
+  DMUON_TRY(check_range(n_grad_rows, 0, DMUON_MAX_TOKENS, "n_grad_rows"));
+  if (step < 1) return invalid("step counts from 1");
+  if (!std::isfinite(lr) || !std::isfinite(weight_decay) || !std::isfinite(eps) || eps < 0.0f)
+    return invalid("lr and weight_decay must be finite, eps finite and >= 0");
+  if (!(beta1 >= 0.0f && beta1 < 1.0f) || !(beta2 >= 0.0f && beta2 < 1.0f)) return invalid("betas must lie in [0, 1)");
+  const int64_t es = size_of(dtype), numel = rows * dim;
+  const Buf bufs[] = {flat("param", param, numel * es, es, true), flat("exp_avg", exp_avg, numel * 4, 4, true),
+                      flat("exp_avg_sq", exp_avg_sq, numel * 4, 4, true),
+                      flat("grad_rows", grad_rows, n_grad_rows * dim * es, es, false),
+                      flat("row_index", row_index, rows * 4, 4, false)};
+  return check_bufs(bufs, 5);
+}
+
 // ---------------------------------------------------------------- distillation
 constexpr int64_t kDistillPartBytes = 8 * sizeof(float);
 // Blocks per row, for a few long rows (at least 8192 elements each); 0: a
@@ -394,24 +414,22 @@ int dmuon_embedding_backward(const void* dout, int64_t n, int64_t dim, int dout_
   });
 }
 
+int dmuon_adamw_rows_check(const void* param, const void* grad_rows, int64_t n_grad_rows, const int32_t* row_index,
+                           const float* exp_avg, const float* exp_avg_sq, int64_t rows, int64_t dim, int dtype,
+                           int step, float lr, float beta1, float beta2, float eps, float weight_decay) {
+  return guarded([&]() -> int {
+    return check_adamw_rows(param, grad_rows, n_grad_rows, row_index, exp_avg, exp_avg_sq, rows, dim, dtype, step, lr,
+                            beta1, beta2, eps, weight_decay);
+  });
+}
+
 int dmuon_adamw_rows_step(void* param, const void* grad_rows, int64_t n_grad_rows, const int32_t* row_index,
                           float* exp_avg, float* exp_avg_sq, int64_t rows, int64_t dim, int dtype, int step, float lr,
                           float beta1, float beta2, float eps, float weight_decay, void* hip_stream) {
   return guarded([&]() -> int {
-    DMUON_TRY(check_float(dtype, "dtype"));
-    DMUON_TRY(check_range(rows, 1, DMUON_MAX_VOCAB, "rows"));
-    DMUON_TRY(check_range(dim, 1, DMUON_MAX_DIM, "dim"));
-    DMUON_TRY(check_range(n_grad_rows, 0, DMUON_MAX_TOKENS, "n_grad_rows"));
-    if (step < 1) return invalid("step counts from 1");
-    if (!std::isfinite(lr) || !std::isfinite(weight_decay) || !std::isfinite(eps) || eps < 0.0f)
-      return invalid("lr and weight_decay must be finite, eps finite and >= 0");
-    if (!(beta1 >= 0.0f && beta1 < 1.0f) || !(beta2 >= 0.0f && beta2 < 1.0f)) return invalid("betas must lie in [0, 1)");
+    DMUON_TRY(check_adamw_rows(param, grad_rows, n_grad_rows, row_index, exp_avg, exp_avg_sq, rows, dim, dtype, step, lr,
+                               beta1, beta2, eps, weight_decay));
     const int64_t es = size_of(dtype), numel = rows * dim;
-    const Buf bufs[] = {flat("param", param, numel * es, es, true), flat("exp_avg", exp_avg, numel * 4, 4, true),
-                        flat("exp_avg_sq", exp_avg_sq, numel * 4, 4, true),
-                        flat("grad_rows", grad_rows, n_grad_rows * dim * es, es, false),
-                        flat("row_index", row_index, rows * 4, 4, false)};
-    DMUON_TRY(check_bufs(bufs, 5));
     bool capturing = false;
     DMUON_TRY(check_device(hip_stream, &capturing));
     AdamRowsArgs a{};

@@ -216,13 +216,8 @@ def embedding_grad(plan: EmbeddingPlan, dout: torch.Tensor, scale: float = 1.0, 
 
 
 # ---------------------------------------------------------------- AdamW, gradient as rows
-def adamw_rows_step_(param: torch.Tensor, grad_rows: torch.Tensor, row_index: torch.Tensor, exp_avg: torch.Tensor,
-                     exp_avg_sq: torch.Tensor, step: int, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
-                     weight_decay: float = 0.01, stream=None) -> None:
-    """dmuon_adamw_rows_step: one AdamW step of a (rows, dim) table in place.
-    Row r has the gradient grad_rows[row_index[r]], or zero where row_index[r]
-    names none: embedding_grad(plan, ..., form="rows") with plan.row_index.
-    Defaults as in adamw_step_."""
+def _adamw_rows_args(param, grad_rows, row_index, exp_avg, exp_avg_sq, step, lr, betas, eps, weight_decay):
+    """(device index, arguments of dmuon_adamw_rows_step up to the stream)."""
     p = _tensor(param, "param")
     if param.dim() != 2:
         raise ValueError(f"param must be 2-D, got shape {tuple(param.shape)}")
@@ -234,8 +229,29 @@ def adamw_rows_step_(param: torch.Tensor, grad_rows: torch.Tensor, row_index: to
     m = _tensor(exp_avg, "exp_avg", dev, torch.float32, param.shape)
     v = _tensor(exp_avg_sq, "exp_avg_sq", dev, torch.float32, param.shape)
     b1, b2 = betas
-    _run("dmuon_adamw_rows_step", dev, stream, p, g, grad_rows.shape[0], index, m, v, rows, dim,
-         dtype_code(param.dtype), int(step), lr, b1, b2, eps, weight_decay)
+    return dev, (p, g, grad_rows.shape[0], index, m, v, rows, dim, dtype_code(param.dtype), int(step), lr, b1, b2, eps,
+                 weight_decay)
+
+
+def adamw_rows_step_(param: torch.Tensor, grad_rows: torch.Tensor, row_index: torch.Tensor, exp_avg: torch.Tensor,
+                     exp_avg_sq: torch.Tensor, step: int, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                     weight_decay: float = 0.01, stream=None) -> None:
+    """dmuon_adamw_rows_step: one AdamW step of a (rows, dim) table in place.
+    Row r has the gradient grad_rows[row_index[r]], or zero where row_index[r]
+    names none: embedding_grad(plan, ..., form="rows") with plan.row_index.
+    Defaults as in adamw_step_."""
+    dev, args = _adamw_rows_args(param, grad_rows, row_index, exp_avg, exp_avg_sq, step, lr, betas, eps, weight_decay)
+    _run("dmuon_adamw_rows_step", dev, stream, *args)
+
+
+def adamw_rows_prepared(stream, *args):
+    """The same step, checked now and taken by the call that is returned:
+    several tables can be turned down before the first is changed."""
+    dev, args = _adamw_rows_args(*args)
+    check(_lib.load().dmuon_adamw_rows_check(*args), "dmuon_adamw_rows_step")
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to cuda:{dev}")
+    return lambda: _run("dmuon_adamw_rows_step", dev, stream, *args)
 
 
 # ---------------------------------------------------------------- distillation loss
