@@ -510,7 +510,8 @@ typedef struct {
  * q_weight, k_weight : device, D entries of weight_dtype, or NULL for no gain.
  * positions  : device, tokens entries.  A negative position marks a padding
  *              token: its outputs are zero whatever its inputs hold.  A
- *              position >= max_pos gives NaN.  NULL when rot_dim is 0.
+ *              position >= max_pos gives NaN.  When rot_dim is 0 only the sign
+ *              counts, and NULL means that no token is padding.
  * rope       : device float32, max_pos x rot_dim: a position's rot_dim / 2
  *              cosines, then its sines.  NULL when rot_dim is 0.
  * q_out, k_out : device; may equal q and k with the same stride (in place).

@@ -540,6 +540,7 @@ int dmuon_qk_norm_rope_forward(const dmuon_qk_shape* shape, const void* q, int64
   return guarded([&]() -> int {
     DMUON_TRY(check_qk(shape));
     const dmuon_qk_shape& s = *shape;
+    if (positions) DMUON_TRY(check_index(s.pos_dtype, "pos_dtype"));
     const int64_t ws = size_of(s.weight_dtype), ps = size_of(s.pos_dtype);
     Buf b[8];
     DMUON_TRY(qk_buf(s, "q", q, q_stride, s.q_heads, false, &b[0]));
@@ -548,7 +549,7 @@ int dmuon_qk_norm_rope_forward(const dmuon_qk_shape* shape, const void* q, int64
     DMUON_TRY(qk_buf(s, "k_out", k_out, k_out_stride, s.k_heads, true, &b[3]));
     b[4] = flat("q_weight", q_weight, q_weight ? s.head_dim * ws : 0, ws, false);
     b[5] = flat("k_weight", k_weight, k_weight ? s.head_dim * ws : 0, ws, false);
-    b[6] = flat("positions", positions, s.rot_dim ? s.tokens * ps : 0, ps, false);
+    b[6] = flat("positions", positions, s.rot_dim || positions ? s.tokens * ps : 0, ps, false);
     b[7] = flat("rope", rope, s.rot_dim && s.tokens ? s.max_pos * s.rot_dim * 4 : 0, 4, false);
     const int in_place[2][2] = {{0, 2}, {1, 3}};
     DMUON_TRY(check_bufs(b, 8, in_place, 2));
@@ -596,6 +597,7 @@ int dmuon_qk_norm_rope_backward(const dmuon_qk_shape* shape, const void* dq_out,
   return guarded([&]() -> int {
     DMUON_TRY(check_qk(shape));
     const dmuon_qk_shape& s = *shape;
+    if (positions) DMUON_TRY(check_index(s.pos_dtype, "pos_dtype"));
     size_t need = 0;
     DMUON_TRY(dmuon_qk_norm_rope_backward_workspace_bytes(shape, &need));
     if (!dq_weight && !dk_weight) need = 0;   // no sums over tokens are asked for
@@ -610,7 +612,7 @@ int dmuon_qk_norm_rope_backward(const dmuon_qk_shape* shape, const void* dq_out,
     DMUON_TRY(qk_buf(s, "dk", dk, dk_stride, s.k_heads, true, &b[5]));
     b[6] = flat("q_weight", q_weight, q_weight ? s.head_dim * ws : 0, ws, false);
     b[7] = flat("k_weight", k_weight, k_weight ? s.head_dim * ws : 0, ws, false);
-    b[8] = flat("positions", positions, s.rot_dim ? s.tokens * ps : 0, ps, false);
+    b[8] = flat("positions", positions, s.rot_dim || positions ? s.tokens * ps : 0, ps, false);
     b[9] = flat("rope", rope, s.rot_dim && s.tokens ? s.max_pos * s.rot_dim * 4 : 0, 4, false);
     b[10] = flat("dq_weight", dq_weight, dq_weight ? s.head_dim * ws : 0, ws, true);
     b[11] = flat("dk_weight", dk_weight, dk_weight ? s.head_dim * ws : 0, ws, true);

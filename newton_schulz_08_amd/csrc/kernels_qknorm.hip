@@ -149,7 +149,7 @@ __device__ __forceinline__ int token_angles(const QkArgs& a, int64_t token, int 
       c[i] = 1.0f;
       s[i] = 0.0f;
     }
-    return 1;
+    return a.positions && load_index(a.positions, token, a.pos64) < 0 ? 0 : 1;
   }
   const int64_t pos = load_index(a.positions, token, a.pos64);
   const int kind = pos < 0 ? 0 : pos >= a.max_pos ? 2 : 1;

@@ -369,8 +369,9 @@ def _qk_args(q, k, q_weight, k_weight, positions, rope, eps, interleaved, weight
         table = _tensor(rope, "rope", dev, torch.float32)
         if rope.dim() != 2:
             raise ValueError(f"rope must be (max_pos, rot_dim), got shape {tuple(rope.shape)}")
-        pos = _tensor(positions, "positions", dev, None, (n,))
         max_pos, rot = rope.shape
+    if positions is not None or rot:
+        pos = _tensor(positions, "positions", dev, None, (n,))
         pos_dtype = _index_code(positions, "positions")
     s = _lib.QkShape(n, qh, kh, d, rot, 1 if interleaved else 0, max_pos, eps, weight_offset, dtype_code(q.dtype),
                      dtype_code(wdt or q.dtype), pos_dtype)
@@ -390,7 +391,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tens
     q and k may be slices of a packed projection: only a token's heads have to
     be contiguous.  positions (tokens); negative ones mark padding (zeros out).
     rope: rope_table(...), float32 (max_pos, rot_dim); None leaves the rotation
-    out.  q_out, k_out may be q and k themselves."""
+    out, and positions are then needed only for padding.  q_out, k_out may be q and k themselves."""
     dev, s, args = _qk_args(q, k, q_weight, k_weight, positions, rope, eps, interleaved, weight_offset)
     outs = []
     for out, x, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
