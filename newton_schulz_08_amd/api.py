@@ -6,6 +6,7 @@ entry points in include/dmuon.h.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import List, Optional, Sequence
 
@@ -140,12 +141,35 @@ def _stream_handle(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _alloc(stream, make, *args, **kw) -> torch.Tensor:
+    """make(*args, **kw) for a result that a call on `stream` writes.  A block of
+    the current stream's pool may be one that a freed tensor's last kernels on
+    that stream still use, and `stream` does not wait for those: the block
+    comes from `stream`'s own pool, whose work lies in order.  The caller goes on
+    with it on the current stream, which is recorded for its release."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _alloc_workspace(stream, nbytes: int, device) -> torch.Tensor:
+    """A workspace for one call on `stream`, from that stream's pool: it can be
+    dropped as soon as the call is enqueued."""
+    if stream is None:
+        return alloc_workspace(nbytes, device)
+    with torch.cuda.stream(stream):
+        return alloc_workspace(nbytes, device)
+
+
 def _used_on(stream, *tensors) -> None:
-    """Buffers allocated here come from the caching allocator's pool of the
-    current stream.  When the kernels that use them run on another stream,
-    record that stream, or the block could be handed to a new allocation on
-    the current stream as soon as this function drops its reference, while
-    the kernels still read and write it."""
+    """Buffers that an object keeps come from the pool of the stream that was
+    current when it was made.  When the kernels that use them run on another
+    stream, record that stream, or the block could be handed to a new
+    allocation as soon as the object drops it, while the kernels still read and
+    write it."""
     if stream is None:
         return
     for t in tensors:
@@ -163,9 +187,8 @@ def ns_batched(xs: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]
     dt = xs[0].dtype
     for i, x in enumerate(xs):
         _check_matrix(x, f"xs[{i}]", dt)
-    own_outs = outs is None
-    if own_outs:
-        outs = [torch.empty_like(x) for x in xs]
+    if outs is None:
+        outs = [_alloc(stream, torch.empty_like, x) for x in xs]
     for i, (o, x) in enumerate(zip(outs, xs)):
         _check_matrix(o, f"outs[{i}]", dt)
         if o.shape != x.shape:
@@ -173,15 +196,13 @@ def ns_batched(xs: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]
     shapes = [tuple(x.shape) for x in xs]
     cfg = ns_config(ns_coeffs, ns_backend, int(ns_steps))
     need = ns_workspace_bytes(shapes, dt, ns_coeffs, ns_backend)
-    own_ws = workspace is None
-    if own_ws:
-        workspace = alloc_workspace(need, xs[0].device)
+    if workspace is None:
+        workspace = _alloc_workspace(stream, need, xs[0].device)
     rows, cols = _shape_arrays(shapes)
     check(_lib.load().dmuon_ns_batched(len(xs), _ptrs(xs), _ptrs(outs), rows, cols, dtype_code(dt), int(ns_steps),
                                        _cfg_ptr(cfg), ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
                                        ctypes.c_void_p(_stream_handle(stream))),
           "dmuon_ns_batched")
-    _used_on(stream, workspace if own_ws else None, *(outs if own_outs else ()))
     return list(outs)
 
 
@@ -289,7 +310,8 @@ class MuonStep:
 def muon_step(params, grads, momentum, **kw) -> None:
     """dmuon_muon_step over lists of tensors (one-shot form of MuonStep)."""
     stream = kw.pop("stream", None)
-    MuonStep(params, grads, momentum, **kw)(stream)
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):   # whose pool the workspace is from
+        MuonStep(params, grads, momentum, **kw)(stream)
 
 
 def clip_grad_norm_workspace_bytes(numels: Sequence[int], num_segments: int = 1) -> int:
@@ -322,17 +344,15 @@ def clip_grad_norm_(grads: Sequence[torch.Tensor], max_norm, segments: Optional[
     numel = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
     segarr = (ctypes.c_int * n)(*seg)
     mn = (ctypes.c_float * nseg)(*max_norms)
-    totals = torch.empty(nseg, dtype=torch.float32, device=grads[0].device)
+    totals = _alloc(stream, torch.empty, nseg, dtype=torch.float32, device=grads[0].device)
     need = clip_grad_norm_workspace_bytes([g.numel() for g in grads], nseg)
-    own_ws = workspace is None
-    if own_ws:
-        workspace = alloc_workspace(need, grads[0].device)
+    if workspace is None:
+        workspace = _alloc_workspace(stream, need, grads[0].device)
     check(_lib.load().dmuon_clip_grad_norm(n, _ptrs(grads), numel, dtype_code(dt), segarr, nseg, mn,
                                            ctypes.c_float(norm_type), ctypes.c_void_p(totals.data_ptr()),
                                            ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
                                            ctypes.c_void_p(_stream_handle(stream))),
           "dmuon_clip_grad_norm")
-    _used_on(stream, totals, workspace if own_ws else None)
     return totals
 
 
@@ -366,9 +386,8 @@ def adamw_step_(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], e
                 raise ValueError(f"{name}[{i}] has {t.numel()} elements, params[{i}] has {params[i].numel()}")
     numels = [p.numel() for p in params]
     numel = (ctypes.c_int64 * n)(*numels)
-    own_ws = workspace is None
-    if own_ws:
-        workspace = alloc_workspace(adamw_step_workspace_bytes(numels), params[0].device)
+    if workspace is None:
+        workspace = _alloc_workspace(stream, adamw_step_workspace_bytes(numels), params[0].device)
     b1, b2 = betas
     check(_lib.load().dmuon_adamw_step(n, _ptrs(params), _ptrs(grads), _ptrs(exp_avg), _ptrs(exp_avg_sq), numel,
                                        dtype_code(dt), int(step), ctypes.c_float(lr), ctypes.c_float(b1),
@@ -376,8 +395,6 @@ def adamw_step_(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], e
                                        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
                                        ctypes.c_void_p(_stream_handle(stream))),
           "dmuon_adamw_step")
-    # AdamWStep passes its own workspace and keeps it
-    _used_on(stream, workspace if own_ws else None)
 
 
 def _is_rows(grad) -> bool:

@@ -6,8 +6,13 @@ Like api.py this only marshals arguments; the work runs in libdmuon.so
 (include/dmuon.h, from dmuon_embedding_forward on).  Results are allocated
 unless given.  All tensors of a call lie on one device, which need not be the
 current one; `stream` is a stream of that device (default: its current one).
-Calls can be recorded into a graph; give a call on another stream than the
-current one its own workspace and outputs if they outlive it.
+A call on another stream than the current one does not wait for it: the caller
+orders the two around the call's inputs and results, as for any kernel.  What
+the call allocates comes from that stream's own pool and may be dropped at any
+time.  Calls can be recorded into a graph.
+
+The results do not take part in autograd, whatever the inputs require: a
+gradient goes through the call that this module has for it.
 """
 from __future__ import annotations
 
@@ -18,7 +23,7 @@ import torch
 
 from . import _lib
 from ._lib import check
-from .api import _used_on, alloc_workspace, dtype_code
+from .api import _alloc, _alloc_workspace, _used_on, dtype_code
 
 _INDEX = {torch.int32: _lib.DMUON_I32, torch.int64: _lib.DMUON_I64}
 _FORMS = {"dense": _lib.DMUON_EMBED_DENSE, "add": _lib.DMUON_EMBED_ADD, "rows": _lib.DMUON_EMBED_ROWS}
@@ -84,7 +89,7 @@ def _query(name: str, *args) -> int:
     return out.value
 
 
-def _workspace(given: Optional[torch.Tensor], need: int, index: int) -> Tuple[Optional[torch.Tensor], int, int]:
+def _workspace(given: Optional[torch.Tensor], need: int, index: int, stream) -> Tuple[Optional[torch.Tensor], int, int]:
     """(workspace allocated here or None, address, bytes)."""
     if given is not None:
         if not given.is_cuda or given.get_device() != index or given.dtype != torch.uint8 or not given.is_contiguous():
@@ -92,7 +97,7 @@ def _workspace(given: Optional[torch.Tensor], need: int, index: int) -> Tuple[Op
         return None, given.data_ptr(), given.numel()
     if need == 0:
         return None, 0, 0
-    ws = alloc_workspace(need, torch.device("cuda", index))
+    ws = _alloc_workspace(stream, need, torch.device("cuda", index))
     return ws, ws.data_ptr(), ws.numel()
 
 
@@ -109,16 +114,13 @@ def embedding(table: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0,
     dev = table.get_device()
     tok = _tensor(tokens, "tokens", dev)
     vocab, dim = table.shape
-    own = out is None
-    if own:
-        out = table.new_empty((*tokens.shape, dim), dtype=out_dtype or table.dtype)
+    if out is None:
+        out = _alloc(stream, table.new_empty, (*tokens.shape, dim), dtype=out_dtype or table.dtype)
         dst = out.data_ptr()
     else:
         dst = _tensor(out, "out", dev, out_dtype, (*tokens.shape, dim))
     _run("dmuon_embedding_forward", dev, stream, src, vocab, dim, dtype_code(table.dtype), tok, tokens.numel(),
          _index_code(tokens, "tokens"), scale, dst, dtype_code(out.dtype))
-    if own:
-        _used_on(stream, out)
     return out
 
 
@@ -127,7 +129,7 @@ class EmbeddingPlan:
     int32 tensors: `order`, `slot` (n), `rows` (min(n, vocab)), `row_index`
     (vocab) and `count` (1)."""
 
-    def __init__(self, n: int, vocab: int, device):
+    def __init__(self, n: int, vocab: int, device, stream=None):
         self.n, self.vocab, self.cap = n, vocab, min(n, vocab)
         # each on its own 256 bytes
         a = n + 63 & ~63
@@ -135,7 +137,7 @@ class EmbeddingPlan:
         c = b + (self.cap + 63 & ~63)
         d = c + (vocab + 63 & ~63)
         self._at = (0, n), (a, n), (b, self.cap), (c, vocab), (d, 1)
-        self._buf = torch.empty(d + 64, dtype=torch.int32, device=device)
+        self._buf = _alloc(stream, torch.empty, d + 64, dtype=torch.int32, device=device)
         self.device, self._index = self._buf.device, self._buf.get_device()
         p = self._buf.data_ptr()
         self._ptrs = p, p + 4 * a, p + 4 * b, p + 4 * c, p + 4 * d
@@ -162,14 +164,13 @@ def embedding_plan(tokens: torch.Tensor, vocab: int, plan: Optional[EmbeddingPla
     tok = _tensor(tokens, "tokens")
     code, n, dev, vocab = _index_code(tokens, "tokens"), tokens.numel(), tokens.get_device(), int(vocab)
     need = embedding_plan_workspace_bytes(n, vocab)   # also the check of n and vocab
-    own = plan is None
-    if own:
-        plan = EmbeddingPlan(n, vocab, tokens.device)
+    if plan is None:
+        plan = EmbeddingPlan(n, vocab, tokens.device, stream)
     elif (plan.n, plan.vocab, plan._index) != (n, vocab, dev):
         raise ValueError(f"plan is for {plan.n} tokens of {plan.vocab} on {plan.device}, not {n} of {vocab} on cuda:{dev}")
-    ws, ptr, nbytes = _workspace(workspace, need, dev)
+    _ws, ptr, nbytes = _workspace(workspace, need, dev, stream)
     _run("dmuon_embedding_plan", dev, stream, tok, n, code, vocab, *plan._ptrs, ptr, nbytes)
-    _used_on(stream, ws, plan._buf if own else None)
+    _used_on(stream, plan._buf)
     return plan
 
 
@@ -198,20 +199,19 @@ def embedding_grad(plan: EmbeddingPlan, dout: torch.Tensor, scale: float = 1.0, 
     if dim == 0 or dout.numel() // dim != plan.n:
         raise ValueError(f"dout has shape {tuple(dout.shape)}, the plan {plan.n} tokens")
     shape = (plan.cap if form == "rows" else plan.vocab, dim)
-    own = out is None
-    if own:
+    if out is None:
         if form == "add":
             raise ValueError("form 'add' needs out")
-        out = dout.new_empty(shape, dtype=dtype or dout.dtype)
+        out = _alloc(stream, dout.new_empty, shape, dtype=dtype or dout.dtype)
         dst = out.data_ptr()
     else:
         dst = _tensor(out, "out", dev, dtype, shape)
     code = dtype_code(dout.dtype)
     need = _query("dmuon_embedding_backward_workspace_bytes", plan.n, dim, code)
-    ws, ptr, nbytes = _workspace(workspace, need, dev)
+    _ws, ptr, nbytes = _workspace(workspace, need, dev, stream)
     _run("dmuon_embedding_backward", dev, stream, src, plan.n, dim, code, scale, *plan._ptrs, plan.vocab, _FORMS[form],
          dst, dtype_code(out.dtype), ptr, nbytes)
-    _used_on(stream, ws, out if own else None)
+    _used_on(stream, plan._buf)
     return out
 
 
@@ -304,24 +304,23 @@ def distill_loss(logits: torch.Tensor, teacher_index: Optional[torch.Tensor],
         lptr = _tensor(labels, "labels", dev, None if teacher_index is None else teacher_index.dtype, (n,))
         code = _index_code(labels, "labels")
     wptr = 0 if row_weight is None else _tensor(row_weight, "row_weight", dev, torch.float32, (n,))
-    own_losses, own_grad, dptr, dstride = losses is None, grad and dlogits is None, 0, 0
-    if own_losses:
-        losses = logits.new_empty((n,), dtype=torch.float32)
+    dptr = dstride = 0
+    if losses is None:
+        losses = _alloc(stream, logits.new_empty, (n,), dtype=torch.float32)
     else:
         _tensor(losses, "losses", dev, torch.float32, (n,))
     if not grad:
         dlogits = None
-    elif own_grad:
-        dlogits = logits.new_empty((n, vocab))
+    elif dlogits is None:
+        dlogits = _alloc(stream, logits.new_empty, (n, vocab))
         dptr, dstride = dlogits.data_ptr(), vocab
     else:
         dstride = _rows(dlogits, "dlogits", logits)
         dptr = dlogits.data_ptr()
-    ws, ptr, nbytes = _workspace(workspace, distill_loss_workspace_bytes(n, vocab), dev)
+    _ws, ptr, nbytes = _workspace(workspace, distill_loss_workspace_bytes(n, vocab), dev, stream)
     _run("dmuon_distill_loss", dev, stream, logits.data_ptr(), n, vocab, stride, dtype_code(logits.dtype), iptr, code,
          tptr, k, lptr, temperature, kd_weight, ce_weight, wptr, grad_scale, losses.data_ptr(), dptr, dstride, ptr,
          nbytes)
-    _used_on(stream, ws, losses if own_losses else None, dlogits if own_grad else None)
     return losses, dlogits
 
 
@@ -396,9 +395,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tens
     outs = []
     for out, x, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
         if out is None:
-            out = x.new_empty(x.shape)
+            out = _alloc(stream, x.new_empty, x.shape)
             args += [out.data_ptr(), x.shape[1] * x.shape[2]]
-            _used_on(stream, out)
         else:
             args += _heads(out, name, x)
         outs.append(out)
@@ -425,9 +423,8 @@ def qk_norm_rope_grad(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tenso
     outs = []
     for out, x, name in ((dq, q, "dq"), (dk, k, "dk")):
         if out is None:
-            out = x.new_empty(x.shape)
+            out = _alloc(stream, x.new_empty, x.shape)
             args += [out.data_ptr(), x.shape[1] * x.shape[2]]
-            _used_on(stream, out)
         else:
             args += _heads(out, name, x)
         outs.append(out)
@@ -437,12 +434,10 @@ def qk_norm_rope_grad(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tenso
             outs.append(None)
             args.append(0)
         else:
-            dw = torch.empty_like(w)
+            dw = _alloc(stream, torch.empty_like, w)
             outs.append(dw)
             args.append(dw.data_ptr())
-            _used_on(stream, dw)
             need = need or _query("dmuon_qk_norm_rope_backward_workspace_bytes", s)
-    ws, ptr, nbytes = _workspace(workspace, need, dev)
+    _ws, ptr, nbytes = _workspace(workspace, need, dev, stream)
     _run("dmuon_qk_norm_rope_backward", dev, stream, s, *head, *args, ptr, nbytes)
-    _used_on(stream, ws)
     return tuple(outs)
