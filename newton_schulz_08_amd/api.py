@@ -129,7 +129,7 @@ def muon_step_clip_workspace_bytes(shapes: Sequence[Sequence[int]], dtype: torch
 
 def alloc_workspace(nbytes: int, device=None) -> torch.Tensor:
     """A uint8 device buffer of at least nbytes, 256-byte aligned."""
-    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device or "cuda")
+    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device="cuda" if device is None else device)
     if ws.data_ptr() % 256:
         raise RuntimeError("allocator returned a workspace that is not 256-byte aligned")
     return ws

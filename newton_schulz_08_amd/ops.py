@@ -327,10 +327,13 @@ def distill_loss(logits: torch.Tensor, teacher_index: Optional[torch.Tensor],
 # ---------------------------------------------------------------- query / key norm
 def rope_table(max_pos: int, rot_dim: int, theta: float = 10000.0, device=None) -> torch.Tensor:
     """Rotation table for qk_norm_rope: float32 (max_pos, rot_dim), the cosines
-    of position * theta^(-2 i / rot_dim), then the sines; angles in float64."""
+    of position * theta^(-2 i / rot_dim), then the sines; angles in float64.
+    rot_dim is even; device: the current GPU by default."""
+    if rot_dim < 0 or rot_dim % 2:
+        raise ValueError(f"rot_dim must be even and >= 0, got {rot_dim}")
     freq = theta ** (-torch.arange(rot_dim // 2, dtype=torch.float64) * 2 / rot_dim)
     angle = torch.arange(max_pos, dtype=torch.float64)[:, None] * freq
-    return torch.cat([angle.cos(), angle.sin()], 1).float().to(device or "cuda")
+    return torch.cat([angle.cos(), angle.sin()], 1).float().to("cuda" if device is None else device)
 
 
 def _heads(t, name: str, like: Optional[torch.Tensor] = None) -> Tuple[int, int]:
