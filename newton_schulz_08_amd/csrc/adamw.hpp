@@ -2,6 +2,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "common.hpp"
@@ -34,6 +35,32 @@ struct AdamArgs {
   float inv_bc2_sqrt;  // 1 / sqrt(1 - beta2^t)
   float eps;
 };
+
+// Bias corrections and the decay factor in double, each rounded once.
+inline AdamArgs adam_args(int step, float lr, float beta1, float beta2, float eps, float weight_decay) {
+  const double t = static_cast<double>(step);
+  AdamArgs a{};
+  a.decay = static_cast<float>(1.0 - static_cast<double>(lr) * static_cast<double>(weight_decay));
+  a.beta1 = beta1;
+  a.one_minus_beta1 = static_cast<float>(1.0 - static_cast<double>(beta1));
+  a.beta2 = beta2;
+  a.one_minus_beta2 = static_cast<float>(1.0 - static_cast<double>(beta2));
+  a.step_size = static_cast<float>(static_cast<double>(lr) / (1.0 - pow(static_cast<double>(beta1), t)));
+  a.inv_bc2_sqrt = static_cast<float>(1.0 / sqrt(1.0 - pow(static_cast<double>(beta2), t)));
+  a.eps = eps;
+  return a;
+}
+
+#if defined(__HIPCC__)
+// One element's step, shared by the dense step and the step on row gradients.
+__device__ __forceinline__ void adamw_elem(float& p, float g, float& m, float& v, const AdamArgs& a) {
+  p *= a.decay;
+  m = fmaf(a.beta1, m, a.one_minus_beta1 * g);
+  v = fmaf(a.beta2, v, (a.one_minus_beta2 * g) * g);
+  const float denom = fmaf(sqrtf(v), a.inv_bc2_sqrt, a.eps);
+  p = fmaf(-a.step_size, m / denom, p);
+}
+#endif
 
 hipError_t launch_adamw(int dt, const AdamDesc* descs, const int* tile_prefix, int n, int total_tiles,
                         const AdamArgs& args, int grid, hipStream_t stream);

@@ -1142,17 +1142,7 @@ int dmuon_adamw_step(int count, void* const* params, const void* const* grads, f
     // read p, g, m, v; write p, m, v
     bytes += static_cast<double>(numel[i]) * (3.0 * eb + 16.0);
   }
-  // bias corrections and the decay factor in double, each rounded once
-  const double t = static_cast<double>(step);
-  AdamArgs a{};
-  a.decay = static_cast<float>(1.0 - static_cast<double>(lr) * static_cast<double>(weight_decay));
-  a.beta1 = beta1;
-  a.one_minus_beta1 = static_cast<float>(1.0 - static_cast<double>(beta1));
-  a.beta2 = beta2;
-  a.one_minus_beta2 = static_cast<float>(1.0 - static_cast<double>(beta2));
-  a.step_size = static_cast<float>(static_cast<double>(lr) / (1.0 - std::pow(static_cast<double>(beta1), t)));
-  a.inv_bc2_sqrt = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(static_cast<double>(beta2), t)));
-  a.eps = eps;
+  const AdamArgs a = adam_args(step, lr, beta1, beta2, eps, weight_decay);
   AdamDesc* d_descs = reinterpret_cast<AdamDesc*>(ws + ap.off_descs);
   int* d_prefix = reinterpret_cast<int*>(ws + ap.off_prefix);
   if (hipMemcpyAsync(d_descs, descs.data(), sizeof(AdamDesc) * count, hipMemcpyHostToDevice, stream) != hipSuccess ||

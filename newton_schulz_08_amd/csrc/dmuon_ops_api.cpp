@@ -441,16 +441,7 @@ int dmuon_adamw_rows_step(void* param, const void* grad_rows, int64_t n_grad_row
     a.rows = rows;
     a.dim = dim;
     a.n_grad_rows = n_grad_rows;
-    // the dense step's constants, formed alike
-    const double t = static_cast<double>(step);
-    a.hp.decay = static_cast<float>(1.0 - static_cast<double>(lr) * static_cast<double>(weight_decay));
-    a.hp.beta1 = beta1;
-    a.hp.one_minus_beta1 = static_cast<float>(1.0 - static_cast<double>(beta1));
-    a.hp.beta2 = beta2;
-    a.hp.one_minus_beta2 = static_cast<float>(1.0 - static_cast<double>(beta2));
-    a.hp.step_size = static_cast<float>(static_cast<double>(lr) / (1.0 - std::pow(static_cast<double>(beta1), t)));
-    a.hp.inv_bc2_sqrt = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(static_cast<double>(beta2), t)));
-    a.hp.eps = eps;
+    a.hp = adam_args(step, lr, beta1, beta2, eps, weight_decay);
     const double bytes = static_cast<double>(numel) * (2.0 * es + 16.0) +
                          static_cast<double>(std::min(n_grad_rows, rows)) * dim * es;
     return launched("AdamW rows", kKAdamwRows, 0.0, bytes, hip_stream, capturing,

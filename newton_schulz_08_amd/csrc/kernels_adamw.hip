@@ -41,14 +41,6 @@ __device__ __forceinline__ int find_tensor(const int* __restrict__ prefix, int n
   return lo;
 }
 
-__device__ __forceinline__ void adamw_elem(float& p, float g, float& m, float& v, const AdamArgs& a) {
-  p *= a.decay;
-  m = fmaf(a.beta1, m, a.one_minus_beta1 * g);
-  v = fmaf(a.beta2, v, (a.one_minus_beta2 * g) * g);
-  const float denom = fmaf(sqrtf(v), a.inv_bc2_sqrt, a.eps);
-  p = fmaf(-a.step_size, m / denom, p);
-}
-
 template <int DT>
 __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(const AdamDesc* __restrict__ descs,
                                                             const int* __restrict__ prefix, int n, int total_tiles,

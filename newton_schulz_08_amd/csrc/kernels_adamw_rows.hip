@@ -3,8 +3,8 @@
 // The gradient of an embedding table is zero outside the rows that the batch
 // names.  Row r of the table has gradient g = grad_rows[row_index[r]], or 0
 // when row_index[r] is outside [0, n_grad_rows); every element then takes the
-// update of the dense step (kernels_adamw.hip, same arithmetic and order, so
-// the result is bitwise that of the dense step on the scattered gradient):
+// update of the dense step (adamw_elem of adamw.hpp, so the result is bitwise
+// that of the dense step on the scattered gradient):
 //
 //   p <- p (1 - lr wd);  m <- beta1 m + (1 - beta1) g;  v <- beta2 v + (1 - beta2) g^2
 //   p <- p - step_size m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
@@ -18,14 +18,6 @@
 
 namespace dmuon {
 namespace {
-
-__device__ __forceinline__ void adamw_elem(float& p, float g, float& m, float& v, const AdamArgs& a) {
-  p *= a.decay;
-  m = fmaf(a.beta1, m, a.one_minus_beta1 * g);
-  v = fmaf(a.beta2, v, (a.one_minus_beta2 * g) * g);
-  const float denom = fmaf(sqrtf(v), a.inv_bc2_sqrt, a.eps);
-  p = fmaf(-a.step_size, m / denom, p);
-}
 
 // Gradient row of table row r, or nullptr.
 template <typename T>
