@@ -255,7 +255,7 @@ void fill_qk(const dmuon_qk_shape& s, const float* rope, QkArgs* a) {
   a->dim = s.head_dim;
   a->rot = s.rot_dim;
   a->interleaved = s.interleaved ? 1 : 0;
-  a->max_pos = s.max_pos;
+  a->max_pos = s.rot_dim ? s.max_pos : INT64_MAX;   // no table, none to be behind
   a->eps = s.eps;
   a->offset = s.weight_offset;
   a->pos64 = s.pos_dtype == DMUON_I64;

@@ -143,13 +143,13 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
 // token is treated: 0 padding, 1 rotated, 2 behind the table.
 template <int P, bool VEC>
 __device__ __forceinline__ int token_angles(const QkArgs& a, int64_t token, int t, float* c, float* s) {
-  if (a.rot == 0) {
+  if (!a.positions) {   // no rotation and no padding; without a rotation alone, every run below stays as it is
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       c[i] = 1.0f;
       s[i] = 0.0f;
     }
-    return a.positions && load_index(a.positions, token, a.pos64) < 0 ? 0 : 1;
+    return 1;
   }
   const int64_t pos = load_index(a.positions, token, a.pos64);
   const int kind = pos < 0 ? 0 : pos >= a.max_pos ? 2 : 1;

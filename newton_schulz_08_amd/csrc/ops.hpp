@@ -116,7 +116,7 @@ struct QkArgs {
   void* dw[2];             // backward: gradients of the gains, or nullptr
   int64_t x_stride[2], dy_stride[2], out_stride[2];   // elements between tokens
   int heads[2];
-  const void* positions;
+  const void* positions;   // nullptr: rot is 0 and no token is padding
   const float* rope;       // max_pos x rot: cosines, then sines
   float* part;             // backward: (blocks[0] + blocks[1]) x head_dim
   int64_t n, max_pos;
