@@ -23,7 +23,7 @@ import torch
 
 from . import _lib
 from ._lib import check
-from .api import _alloc, _alloc_workspace, _used_on, dtype_code
+from .api import _alloc, _alloc_workspace, _used_on, alloc_workspace, dtype_code
 
 _INDEX = {torch.int32: _lib.DMUON_I32, torch.int64: _lib.DMUON_I64}
 _FORMS = {"dense": _lib.DMUON_EMBED_DENSE, "add": _lib.DMUON_EMBED_ADD, "rows": _lib.DMUON_EMBED_ROWS}
@@ -97,7 +97,8 @@ def _workspace(given: Optional[torch.Tensor], need: int, index: int, stream) -> 
         return None, given.data_ptr(), given.numel()
     if need == 0:
         return None, 0, 0
-    ws = _alloc_workspace(stream, need, torch.device("cuda", index))
+    device = torch.device("cuda", index)
+    ws = alloc_workspace(need, device) if stream is None else _alloc_workspace(stream, need, device)
     return ws, ws.data_ptr(), ws.numel()
 
 
@@ -115,7 +116,8 @@ def embedding(table: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0,
     tok = _tensor(tokens, "tokens", dev)
     vocab, dim = table.shape
     if out is None:
-        out = _alloc(stream, table.new_empty, (*tokens.shape, dim), dtype=out_dtype or table.dtype)
+        new, shape, dt = table.new_empty, (*tokens.shape, dim), out_dtype or table.dtype
+        out = new(shape, dtype=dt) if stream is None else _alloc(stream, new, shape, dtype=dt)
         dst = out.data_ptr()
     else:
         dst = _tensor(out, "out", dev, out_dtype, (*tokens.shape, dim))
@@ -170,7 +172,8 @@ def embedding_plan(tokens: torch.Tensor, vocab: int, plan: Optional[EmbeddingPla
         raise ValueError(f"plan is for {plan.n} tokens of {plan.vocab} on {plan.device}, not {n} of {vocab} on cuda:{dev}")
     _ws, ptr, nbytes = _workspace(workspace, need, dev, stream)
     _run("dmuon_embedding_plan", dev, stream, tok, n, code, vocab, *plan._ptrs, ptr, nbytes)
-    _used_on(stream, plan._buf)
+    if stream is not None:
+        _used_on(stream, plan._buf)
     return plan
 
 
@@ -202,7 +205,8 @@ def embedding_grad(plan: EmbeddingPlan, dout: torch.Tensor, scale: float = 1.0, 
     if out is None:
         if form == "add":
             raise ValueError("form 'add' needs out")
-        out = _alloc(stream, dout.new_empty, shape, dtype=dtype or dout.dtype)
+        new, dt = dout.new_empty, dtype or dout.dtype
+        out = new(shape, dtype=dt) if stream is None else _alloc(stream, new, shape, dtype=dt)
         dst = out.data_ptr()
     else:
         dst = _tensor(out, "out", dev, dtype, shape)
@@ -211,7 +215,8 @@ def embedding_grad(plan: EmbeddingPlan, dout: torch.Tensor, scale: float = 1.0, 
     _ws, ptr, nbytes = _workspace(workspace, need, dev, stream)
     _run("dmuon_embedding_backward", dev, stream, src, plan.n, dim, code, scale, *plan._ptrs, plan.vocab, _FORMS[form],
          dst, dtype_code(out.dtype), ptr, nbytes)
-    _used_on(stream, plan._buf)
+    if stream is not None:
+        _used_on(stream, plan._buf)
     return out
 
 
@@ -306,13 +311,15 @@ def distill_loss(logits: torch.Tensor, teacher_index: Optional[torch.Tensor],
     wptr = 0 if row_weight is None else _tensor(row_weight, "row_weight", dev, torch.float32, (n,))
     dptr = dstride = 0
     if losses is None:
-        losses = _alloc(stream, logits.new_empty, (n,), dtype=torch.float32)
+        new = logits.new_empty
+        losses = new((n,), dtype=torch.float32) if stream is None else _alloc(stream, new, (n,), dtype=torch.float32)
     else:
         _tensor(losses, "losses", dev, torch.float32, (n,))
     if not grad:
         dlogits = None
     elif dlogits is None:
-        dlogits = _alloc(stream, logits.new_empty, (n, vocab))
+        new = logits.new_empty
+        dlogits = new((n, vocab)) if stream is None else _alloc(stream, new, (n, vocab))
         dptr, dstride = dlogits.data_ptr(), vocab
     else:
         dstride = _rows(dlogits, "dlogits", logits)
@@ -398,7 +405,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tens
     outs = []
     for out, x, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
         if out is None:
-            out = _alloc(stream, x.new_empty, x.shape)
+            out = x.new_empty(x.shape) if stream is None else _alloc(stream, x.new_empty, x.shape)
             args += [out.data_ptr(), x.shape[1] * x.shape[2]]
         else:
             args += _heads(out, name, x)
@@ -426,7 +433,7 @@ def qk_norm_rope_grad(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tenso
     outs = []
     for out, x, name in ((dq, q, "dq"), (dk, k, "dk")):
         if out is None:
-            out = _alloc(stream, x.new_empty, x.shape)
+            out = x.new_empty(x.shape) if stream is None else _alloc(stream, x.new_empty, x.shape)
             args += [out.data_ptr(), x.shape[1] * x.shape[2]]
         else:
             args += _heads(out, name, x)
@@ -437,7 +444,7 @@ def qk_norm_rope_grad(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tenso
             outs.append(None)
             args.append(0)
         else:
-            dw = _alloc(stream, torch.empty_like, w)
+            dw = torch.empty_like(w) if stream is None else _alloc(stream, torch.empty_like, w)
             outs.append(dw)
             args.append(dw.data_ptr())
             need = need or _query("dmuon_qk_norm_rope_backward_workspace_bytes", s)
