@@ -224,8 +224,8 @@ __device__ __forceinline__ void sweep_held(const T* z, int64_t i0, int64_t i1, H
 
 // The sums of [i0, i1) of a row, and of the teacher's entries that lie in it
 // (its own sums are over all entries).  Ends behind a barrier, with the entries
-// in `sh` and everything in `s` of every thread.
-template <int DT, int MODE, int THREADS, int PER, int R, int L>
+// in `sh` and everything in `s` of every thread; s.part only with PART.
+template <int DT, int MODE, int THREADS, int PER, bool PART, int R, int L>
 __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int64_t i0, int64_t i1,
                                          Shared<THREADS, PER>& sh, Sums& s,
                                          Held<typename OpElem<DT>::T, THREADS, R, L>& held) {
@@ -332,7 +332,7 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
         ent += static_cast<double>(e) * d;
         if (idx[p] >= i0 && idx[p] < i1) {
           dot += e * (zj[p] - from);
-          part += e;
+          if constexpr (PART) part += e;
         }
       }
     }
@@ -347,7 +347,7 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
   if (a.kd != 0.0f) {
     ysum = wave_sum(ysum);
     dot = wave_sum(dot);
-    part = wave_sum(part);
+    if constexpr (PART) part = wave_sum(part);
     ent = wave_sum(ent);
   }
   if ((tid & 63) == 0) {
@@ -355,7 +355,7 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
     sh.s1[wave] = s1;
     sh.ysum[wave] = ysum;
     sh.dot[wave] = dot;
-    sh.part[wave] = part;
+    if constexpr (PART) sh.part[wave] = part;
     sh.ent[wave] = ent;
   }
   __syncthreads();
@@ -366,7 +366,7 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
     s.s1 += MODE != kOne ? sh.s1[w] : sh.st[w];
     s.ysum += sh.ysum[w];
     s.dot += sh.dot[w];
-    s.part += sh.part[w];
+    if constexpr (PART) s.part += sh.part[w];
     s.ent += sh.ent[w];
   }
 }
@@ -472,7 +472,7 @@ __global__ __launch_bounds__(THREADS, 4) void distill_row_kernel(DistillArgs a) 
   Held<typename OpElem<DT>::T, THREADS, R, L> held;
   held.stash = stash;
   Sums s;
-  row_sums<DT, MODE, THREADS, PER>(a, row, 0, a.vocab, sh, s, held);
+  row_sums<DT, MODE, THREADS, PER, false>(a, row, 0, a.vocab, sh, s, held);
   const bool has_kd = a.kd != 0.0f && !(s.ysum == 0.0), has_ce = sh.idx[a.k] >= 0;
   if (!has_kd && !has_ce) {
     zero_row<DT, THREADS, STREAM>(a, row, 0, a.vocab);
@@ -498,7 +498,7 @@ __global__ __launch_bounds__(kSliceThreads) void distill_slice_kernel(DistillArg
   const int64_t i0 = least(a.vocab, slice * a.slice_len), i1 = least(a.vocab, i0 + a.slice_len);
   Sums s;
   Held<typename OpElem<DT>::T, kSliceThreads, 0, 0> none;
-  row_sums<DT, MODE, kSliceThreads, kSlicePer>(a, row, i0, i1, sh, s, none);
+  row_sums<DT, MODE, kSliceThreads, kSlicePer, true>(a, row, i0, i1, sh, s, none);
   if (threadIdx.x == 0) {
     float* p = a.part + blockIdx.x * static_cast<int64_t>(kPmWords);
     p[kPmMax] = s.top;
@@ -528,7 +528,7 @@ __global__ __launch_bounds__(kSliceThreads) void distill_join_kernel(DistillArgs
   // the teacher's entries again: sums over no elements
   Sums s;
   Held<T, kSliceThreads, 0, 0> none;
-  row_sums<DT, MODE, kSliceThreads, kSlicePer>(a, row, 0, 0, sh, s, none);
+  row_sums<DT, MODE, kSliceThreads, kSlicePer, false>(a, row, 0, 0, sh, s, none);
   const bool has_kd = a.kd != 0.0f && !(s.ysum == 0.0), has_ce = sh.idx[a.k] >= 0;
   if (!has_kd && !has_ce) {
     zero_row<DT, kSliceThreads, false>(a, row, i0, i1);
