@@ -347,7 +347,9 @@ int dmuon_adamw_step(int count, void* const* params, const void* const* grads, f
  * - bf16 results are rounded once (RNE) from fp32.
  * - The same inputs in the same shapes give the same bits, whatever their
  *   addresses and strides.  The order of a sum may follow the shape of the call
- *   (the number of rows or tokens in it), never what other rows hold.
+ *   (the number of rows or tokens in it), never what other rows hold; but in
+ *   dmuon_embedding_backward it follows the batch's tokens, whose sorted order
+ *   decides where a long run of one token is cut.
  * ------------------------------------------------------------------------ */
 
 /* Types of token, index and position arrays. */
@@ -463,8 +465,9 @@ int dmuon_adamw_rows_check(const void* param, const void* grad_rows, int64_t n_g
  * k         : 0 .. DMUON_MAX_TEACHER_K; 0 needs kd_weight = 0.
  * temperature : T in [1e-6, 1e6].  kd_weight, ce_weight, grad_scale: finite.
  * row_weight : NULL (1), or device float32[n].  A row of weight 0 is not read:
- *             its loss and gradient are 0 whatever it holds.  The same holds
- *             for a row without a valid teacher entry and without a label.
+ *             its loss and gradient are 0 whatever it holds.  A row without a
+ *             valid teacher entry and without a label is read, but to no effect:
+ *             both are 0 whatever it holds, too.
  * losses    : device float32[n].
  * dlogits   : NULL (loss only), or device, n rows of vocab elements of
  *             `dtype`, dlogits_stride apart.  May equal logits with the same

@@ -10,8 +10,8 @@
 //
 // HBM-bound: one or two exponentials per element against 2 or 4 bytes each way.
 // Measured: 8192 x 128256 bf16 with labels at T = 2, a tenth of the rows masked,
-// 812 us (4.0 GB that it cannot do without, 4.9 TB/s); the loss alone of as many
-// unmasked rows 354 us (5.9 TB/s).
+// 811 us a call (4.0 GB that it cannot do without, 4.9 TB/s); the loss alone of
+// as many unmasked rows 353 us (5.9 TB/s).
 //
 // Exponentials are taken in base 2 against an integer reference: with
 // s2 = log2(e) / T and M = ceil(max z s2), exp2(z s2 - M) is one fused
@@ -233,8 +233,9 @@ __device__ __forceinline__ void row_sums(const DistillArgs& a, int64_t row, int6
   constexpr int kPer = PER;
   const T* z = static_cast<const T*>(a.logits) + row * a.stride;
   const int tid = threadIdx.x, wave = tid >> 6;
-  // named elements: their indices are on their way while the row is swept, their
-  // logits while its maximum is found
+  // named elements: the indices are waited for (whether they lie in the row
+  // decides what is loaded); the teacher's logits travel while the row is swept,
+  // the student's while its maximum is found
   float y[kPer], zj[kPer];
   int idx[kPer];
 #pragma unroll

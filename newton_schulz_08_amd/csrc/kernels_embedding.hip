@@ -8,13 +8,16 @@
 //
 // The gradient needs no atomics.  The plan sorts the tokens stably (an LSD
 // radix sort of (token, position) pairs), so equal tokens lie next to each
-// other in their order of occurrence; the sum of a run of equal tokens is then
-// formed in fp32 in that order, and results are bitwise reproducible.
+// other in their order of occurrence.  The sum of a run of equal tokens is then
+// formed in fp32 in that order, a long run's in pieces cut at fixed sorted
+// positions and added up afterwards: the same batch gives the same bits.
 //
 // Measured: lookup of 65536 x 4096, fp32 to bf16, 175 us (0.86 GB that it cannot
 // do without, 4.9 TB/s).  Gradient with its plan, 65536 x 4096 bf16 to one row
-// per distinct token, 232 us (1.06 GB, 4.6 TB/s), of which the sort takes 35 us;
-// 16384 x 2048 fp32 to a dense 32000-row gradient 107 us (0.40 GB), the sums 62.
+// per distinct token, 252 us over three batches in turn (1.06 GB, 4.2 TB/s; 231
+// for one batch again and again, part of which the memory-side cache then
+// holds), of which the sort takes 34 us; 16384 x 2048 fp32 to a dense 32000-row
+// gradient 111 us (0.40 GB; 93 again and again), the sums 61.
 #include <hip/hip_runtime.h>
 
 #include "ops.hpp"

@@ -108,7 +108,8 @@ def embedding(table: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0,
               stream=None) -> torch.Tensor:
     """dmuon_embedding_forward: scale * table[tokens], of shape tokens.shape +
     (dim,) and dtype `out_dtype` (default: the table's).  A token outside
-    [0, vocab) gives a zero row."""
+    [0, vocab) gives a zero row.  Outside autograd: its gradient is
+    embedding_grad."""
     src = _tensor(table, "table")
     if table.dim() != 2:
         raise ValueError(f"table must be 2-D, got shape {tuple(table.shape)}")
@@ -291,8 +292,9 @@ def distill_loss(logits: torch.Tensor, teacher_index: Optional[torch.Tensor],
     entries outside the vocabulary left out, and teacher_logits (n, k) float32,
     or both None for the label's term alone (kd_weight 0); labels (n) of the
     indices' type, those outside the vocabulary ignored; row_weight (n) float32,
-    rows of weight 0 skipped.  dlogits may be logits
-    itself: the gradient then takes its place."""
+    rows of weight 0 skipped.  dlogits may be logits itself: the gradient then
+    takes its place.  Outside autograd: the losses do not lead back to the
+    logits, the gradient is returned beside them."""
     stride = _rows(logits, "logits")
     dev, (n, vocab) = logits.get_device(), logits.shape
     if (teacher_index is None) != (teacher_logits is None):
@@ -400,7 +402,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tens
     q and k may be slices of a packed projection: only a token's heads have to
     be contiguous.  positions (tokens); negative ones mark padding (zeros out).
     rope: rope_table(...), float32 (max_pos, rot_dim); None leaves the rotation
-    out, and positions are then needed only for padding.  q_out, k_out may be q and k themselves."""
+    out, and positions are then needed only for padding.  Outside autograd: the
+    gradients are qk_norm_rope_grad's.  q_out, k_out may be q and k themselves."""
     dev, s, args = _qk_args(q, k, q_weight, k_weight, positions, rope, eps, interleaved, weight_offset)
     outs = []
     for out, x, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
