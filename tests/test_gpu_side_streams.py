@@ -129,3 +129,40 @@ def test_a_plan_outlives_the_call_that_reads_it():
     junk = torch.zeros(size, dtype=torch.int32, device="cuda")
     torch.cuda.synchronize()
     assert torch.equal(got, want) and not junk.any()
+
+
+def test_calls_on_a_forked_stream_are_recorded():
+    """A graph whose capture forks to a second stream: what is allocated there
+    belongs to the graph, and replays follow their inputs."""
+    g = torch.Generator("cuda").manual_seed(3)
+    table = torch.randn(500, 256, generator=g, device="cuda")
+    tok = torch.randint(0, 500, (9000,), generator=g, device="cuda")
+    z = torch.randn(4, 70000, generator=g, device="cuda")
+    idx, y = torch.randint(0, 70000, (4, 5), generator=g, device="cuda"), torch.randn(4, 5, generator=g, device="cuda")
+
+    def both(stream):
+        x = nsa.embedding(table, tok, stream=stream)
+        grad = nsa.embedding_grad(nsa.embedding_plan(tok, 500, stream=stream), x, stream=stream)
+        return (x, grad, *nsa.distill_loss(z, idx, y, stream=stream))
+
+    both(None)
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        outs = both(side)
+        torch.cuda.current_stream().wait_stream(side)
+        total = outs[2] + 1.0
+    for _ in range(4):
+        table.normal_()
+        z.normal_()
+        tok.random_(-3, 520)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = both(None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)) and torch.equal(total, want[2] + 1.0)
+        del want
+        junk = [torch.full_like(o, 5.0) for o in outs]   # eager work between the replays
+        torch.cuda.synchronize()
+        del junk
