@@ -14,7 +14,7 @@
 //
 // Measured: lookup of 65536 x 4096, fp32 to bf16, 175 us (0.86 GB that it cannot
 // do without, 4.9 TB/s).  Gradient with its plan, 65536 x 4096 bf16 to one row
-// per distinct token, 252 us over three batches in turn (1.06 GB, 4.2 TB/s; 231
+// per distinct token, 252-256 us over three batches in turn (1.06 GB, 4.2 TB/s; 231
 // for one batch again and again, part of which the memory-side cache then
 // holds), of which the sort takes 34 us; 16384 x 2048 fp32 to a dense 32000-row
 // gradient 111 us (0.40 GB; 93 again and again), the sums 61.
