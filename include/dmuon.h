@@ -543,6 +543,56 @@ int dmuon_qk_norm_rope_backward(const dmuon_qk_shape* shape, const void* dq_out,
                                 size_t workspace_bytes, void* hip_stream);
 
 /*
+ * Shape and types of dmuon_block_norm_forward and _backward.
+ */
+typedef struct {
+    int64_t rows;         /* 0 .. DMUON_MAX_TOKENS */
+    int64_t dim;          /* 1 .. DMUON_MAX_DIM */
+    int post_norm;        /* 1: the block's output is normed before it is added */
+    float eps;            /* finite, >= 0 */
+    float residual_scale; /* s, finite */
+    float weight_offset;  /* finite; 1 for gains stored around zero (not for the gate) */
+    int dtype;            /* the residual stream and its gradients */
+    int branch_dtype;     /* the block's output, the normed stream and their gradients */
+    int weight_dtype;     /* gains, gate and their gradients */
+} dmuon_block_norm_shape;
+
+/*
+ * What lies between two blocks: the norm of a block's output h, its gate and
+ * scale, the residual sum, and the norm in front of the next block:
+ *
+ *   b     = h / sqrt(mean(h^2) + eps) * (weight_offset + post)    or b = h
+ *   x_out = x + s * gate * b
+ *   y     = x_out / sqrt(mean(x_out^2) + eps) * (weight_offset + pre)
+ *
+ * y reads x_out as it is stored.  pre, post, gate: device, dim entries of
+ * weight_dtype, or NULL for a factor of 1; post is NULL without post_norm.
+ * Row r of a tensor begins at element r * stride.  x_out may equal x, and y
+ * may equal h, with the same stride.  The sums of a row's squares are formed in
+ * float32 and have to be finite (and, when eps is 0, normal).
+ */
+int dmuon_block_norm_forward(const dmuon_block_norm_shape* shape, const void* x, int64_t x_stride, const void* h,
+                             int64_t h_stride, const void* pre, const void* post, const void* gate, void* x_out,
+                             int64_t x_out_stride, void* y, int64_t y_stride, void* hip_stream);
+
+/*
+ * Gradients of dmuon_block_norm_forward: dx and dh from dx_out, dy, the stream
+ * behind the block and the block's output; the gains' and the gate's
+ * gradients, summed over rows in fp32 in a fixed order.
+ *
+ * dx_out     : device, gradient of x_out by its other readers, or NULL for none.
+ * dx         : device; may equal dx_out with the same stride.
+ * dpre, dpost, dgate : device, dim entries of weight_dtype, or NULL.  dpost is
+ *              NULL without post_norm.
+ */
+int dmuon_block_norm_backward_workspace_bytes(const dmuon_block_norm_shape* shape, size_t* bytes_out);
+int dmuon_block_norm_backward(const dmuon_block_norm_shape* shape, const void* dx_out, int64_t dx_out_stride,
+                              const void* dy, int64_t dy_stride, const void* x_out, int64_t x_out_stride,
+                              const void* h, int64_t h_stride, const void* pre, const void* post, const void* gate,
+                              void* dx, int64_t dx_stride, void* dh, int64_t dh_stride, void* dpre, void* dpost,
+                              void* dgate, void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
  * The plan of a call as text: routes (numel < DMUON_MIN_NS_NUMEL goes
  * elementwise when muon_step is nonzero), shape groups with their transposed
  * count, tiles and K slices, launches per Newton-Schulz step, algorithmic

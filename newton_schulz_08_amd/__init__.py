@@ -39,4 +39,9 @@ from .ops import (  # noqa: F401
     qk_norm_rope_grad_workspace_bytes,
     rope_table,
 )
+from .block import (  # noqa: F401
+    block_norm,
+    block_norm_grad,
+    block_norm_grad_workspace_bytes,
+)
 from ._lib import DmuonError, load  # noqa: F401

@@ -85,6 +85,21 @@ class QkShape(ctypes.Structure):
     ]
 
 
+class BlockNormShape(ctypes.Structure):
+    """dmuon_block_norm_shape."""
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("dim", ctypes.c_int64),
+        ("post_norm", ctypes.c_int),
+        ("eps", ctypes.c_float),
+        ("residual_scale", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+        ("dtype", ctypes.c_int),
+        ("branch_dtype", ctypes.c_int),
+        ("weight_dtype", ctypes.c_int),
+    ]
+
+
 _P = ctypes.c_void_p
 _PP = ctypes.POINTER(ctypes.c_void_p)
 _I64P = ctypes.POINTER(ctypes.c_int64)
@@ -93,6 +108,7 @@ _FP = ctypes.POINTER(ctypes.c_float)
 _CFGP = ctypes.POINTER(NsConfig)
 _I, _I64, _F, _SZ = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _QKP = ctypes.POINTER(QkShape)
+_BNP = ctypes.POINTER(BlockNormShape)
 
 # name -> (restype, argtypes); mirrors include/dmuon.h
 SIGNATURES = {
@@ -133,6 +149,10 @@ SIGNATURES = {
     "dmuon_qk_norm_rope_backward_workspace_bytes": (_I, [_QKP, _SZP]),
     "dmuon_qk_norm_rope_backward": (_I, [_QKP, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _P,
                                          _I64, _P, _P, _P, _SZ, _P]),
+    "dmuon_block_norm_forward": (_I, [_BNP, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P]),
+    "dmuon_block_norm_backward_workspace_bytes": (_I, [_BNP, _SZP]),
+    "dmuon_block_norm_backward": (_I, [_BNP, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P,
+                                       _P, _P, _P, _SZ, _P]),
     "dmuon_plan_summary": (ctypes.c_int, [ctypes.c_int, _I64P, _I64P, ctypes.c_int, _CFGP, ctypes.c_int, ctypes.c_int,
                                           ctypes.c_char_p, ctypes.c_size_t, _SZP]),
     "dmuon_status_string": (ctypes.c_char_p, [ctypes.c_int]),

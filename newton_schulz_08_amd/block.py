@@ -1,0 +1,96 @@
+"""Python binding of the operators between a decoder block's projections: norms
+around the block.
+
+Everything that ops.py says of its calls (allocation, devices, streams, graphs,
+autograd) holds here too.
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from . import _lib
+from .api import _alloc, dtype_code
+from .ops import _query, _rows, _run, _tensor, _workspace
+
+
+def _row(t, name: str, like: Optional[torch.Tensor] = None) -> Tuple[int, int]:
+    """(address, row stride) of a 2-D device tensor with contiguous rows."""
+    stride = _rows(t, name, like)
+    return t.data_ptr(), stride
+
+
+def _out(out, name: str, like: torch.Tensor, stream) -> Tuple[torch.Tensor, int, int]:
+    """(tensor, address, row stride) of a result like the 2-D `like`, given or allocated here."""
+    if out is None:
+        new = like.new_empty
+        out = new(like.shape) if stream is None else _alloc(stream, new, like.shape)
+        return out, out.data_ptr(), like.shape[1]
+    return out, *_row(out, name, like)
+
+
+# ---------------------------------------------------------------- norms around a block
+def _bn_args(x, h, pre_weight, post_weight, gate, eps, residual_scale, weight_offset, post_norm):
+    """(device index, dmuon_block_norm_shape, [x, stride, h, stride], [gains and gate])."""
+    head = [*_row(x, "x"), *_row(h, "h")]
+    dev, (n, dim) = x.get_device(), x.shape
+    if h.shape != x.shape or h.get_device() != dev:
+        raise ValueError(f"h is {tuple(h.shape)} on {h.device}, x {tuple(x.shape)} on {x.device}")
+    weights, wdt = [], None
+    for w, name in ((pre_weight, "pre_weight"), (post_weight, "post_weight"), (gate, "gate")):
+        if w is None:
+            weights.append(0)
+        else:
+            weights.append(_tensor(w, name, dev, wdt, (dim,)))
+            wdt = w.dtype
+    s = _lib.BlockNormShape(n, dim, 1 if post_norm else 0, eps, residual_scale, weight_offset, dtype_code(x.dtype),
+                            dtype_code(h.dtype), dtype_code(wdt or h.dtype))
+    return dev, s, head, weights
+
+
+def block_norm(x: torch.Tensor, h: torch.Tensor, pre_weight: Optional[torch.Tensor] = None,
+               post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
+               residual_scale: float = 1.0, weight_offset: float = 0.0, post_norm: bool = False,
+               x_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+               stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """dmuon_block_norm_forward: (x_out, y), the residual stream behind a block
+    and its norm in front of the next one.
+
+    x (rows, dim): the stream; h (rows, dim): the block's output, normed first
+    with `post_norm`, times its gain, `gate` (dim) and residual_scale, then
+    added.  y has h's type.  Gains count as weight_offset + weight; None is a
+    factor of 1.  x_out may be x, y may be h.  Outside autograd: the gradients
+    are block_norm_grad's."""
+    dev, s, head, weights = _bn_args(x, h, pre_weight, post_weight, gate, eps, residual_scale, weight_offset, post_norm)
+    x_out, *xo = _out(x_out, "x_out", x, stream)
+    y, *yo = _out(y, "y", h, stream)
+    _run("dmuon_block_norm_forward", dev, stream, s, *head, *weights, *xo, *yo)
+    return x_out, y
+
+
+def block_norm_grad_workspace_bytes(rows: int, dim: int) -> int:
+    return _query("dmuon_block_norm_backward_workspace_bytes", _lib.BlockNormShape(rows=rows, dim=dim))
+
+
+def block_norm_grad(dx_out: Optional[torch.Tensor], dy: torch.Tensor, x_out: torch.Tensor, h: torch.Tensor,
+                    pre_weight: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
+                    gate: Optional[torch.Tensor] = None, *, eps: float = 1e-6, residual_scale: float = 1.0,
+                    weight_offset: float = 0.0, post_norm: bool = False, dx: Optional[torch.Tensor] = None,
+                    dh: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """dmuon_block_norm_backward: (dx, dh, dpre_weight, dpost_weight, dgate)
+    from the gradients of block_norm's results (dx_out None: the stream has no
+    other reader) and its x_out and h; a weight's gradient is None where the
+    weight is.  dx may be dx_out."""
+    dev, s, head, weights = _bn_args(x_out, h, pre_weight, post_weight, gate, eps, residual_scale, weight_offset,
+                                     post_norm)
+    grads = [*((0, 0) if dx_out is None else _row(dx_out, "dx_out", x_out)), *_row(dy, "dy", h)]
+    dx, *dxo = _out(dx, "dx", x_out, stream)
+    dh, *dho = _out(dh, "dh", h, stream)
+    dws = [None if w is None else torch.empty_like(w) if stream is None else _alloc(stream, torch.empty_like, w)
+           for w in (pre_weight, post_weight, gate)]
+    need = _query("dmuon_block_norm_backward_workspace_bytes", s) if any(weights) else 0
+    _ws, ptr, nbytes = _workspace(workspace, need, dev, stream)
+    _run("dmuon_block_norm_backward", dev, stream, s, *grads, *head, *weights, *dxo, *dho,
+         *[0 if w is None else w.data_ptr() for w in dws], ptr, nbytes)
+    return (dx, dh, *dws)

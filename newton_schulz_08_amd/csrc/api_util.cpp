@@ -21,7 +21,8 @@ std::map<int, int> g_dev_status;  // device -> status
 
 const char* kClassNames[kKNumClasses] = {
     "prologue", "norm_finalize", "syrk", "ns_gemm", "apply_x0", "syrk_square", "grad_clip", "adamw",
-    "adamw_rows", "embedding", "embedding_plan", "embedding_grad", "distill_loss", "qk_norm_rope", "qk_norm_rope_grad"};
+    "adamw_rows", "embedding", "embedding_plan", "embedding_grad", "distill_loss", "qk_norm_rope", "qk_norm_rope_grad",
+    "block_norm", "block_norm_grad", "attention", "attention_grad", "gated_ffn", "gated_ffn_grad"};
 
 struct ProfRecord {
   int cls;

@@ -26,7 +26,8 @@ int check_device(void* hip_stream, bool* capturing = nullptr);
 // Kernel families of dmuon_profile_read.
 enum KernelClass {
   kKPrologue = 0, kKNorm, kKSyrk, kKGemm, kKApply, kKSquare, kKClip, kKAdamw,
-  kKAdamwRows, kKEmbed, kKEmbedPlan, kKEmbedGrad, kKDistill, kKQkNorm, kKQkNormGrad, kKNumClasses
+  kKAdamwRows, kKEmbed, kKEmbedPlan, kKEmbedGrad, kKDistill, kKQkNorm, kKQkNormGrad,
+  kKBlockNorm, kKBlockNormGrad, kKAttention, kKAttentionGrad, kKFfn, kKFfnGrad, kKNumClasses
 };
 
 struct ProfMark { hipEvent_t start = nullptr, stop = nullptr; };
