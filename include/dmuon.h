@@ -593,6 +593,68 @@ int dmuon_block_norm_backward(const dmuon_block_norm_shape* shape, const void* d
                               void* dgate, void* workspace, size_t workspace_bytes, void* hip_stream);
 
 /*
+ * Shape and types of dmuon_attention_forward and _backward.
+ */
+#define DMUON_MAX_ATTENTION_DIM 256
+typedef struct {
+    int64_t q_tokens;     /* 0 .. DMUON_MAX_TOKENS; times q_heads / k_heads at most 2^30 */
+    int64_t k_tokens;     /* 0 .. DMUON_MAX_TOKENS */
+    int64_t sequences;    /* 1 .. DMUON_MAX_TOKENS */
+    int q_heads, k_heads; /* 1 .. DMUON_MAX_HEADS; q_heads a multiple of k_heads */
+    int head_dim;         /* D, 1 .. DMUON_MAX_ATTENTION_DIM */
+    int causal;           /* 1: a query sees no key behind it */
+    int window;           /* with causal: the keys a query sees at most; 0 = no limit */
+    float scale;          /* of q . k; finite, > 0 */
+    int dtype;            /* queries, keys, values, outputs and their gradients */
+} dmuon_attention_shape;
+
+/*
+ * Attention over packed sequences:
+ *
+ *   out = softmax(scale q . k over the visible keys) v,
+ *   lse = log of the sum of exp(scale q . k) over them.
+ *
+ * Sequence b has the queries q_offsets[b] .. q_offsets[b + 1] - 1 and the keys
+ * k_offsets[b] .. k_offsets[b + 1] - 1.  Query i of its lq sees key j of its lk
+ * when, with causal, j <= i + lk - lq, and, with a window too,
+ * j > i + lk - lq - window: the last query stands at the last key, so one call
+ * serves whole sequences and single new tokens behind a cache.  A query that
+ * sees no key has out 0 and lse -infinity.  Query head h reads key head
+ * h / (q_heads / k_heads).
+ *
+ * q, k, v, out : device; token t's heads are contiguous (heads x D) at element
+ *              t * stride: a packed projection's output is read in place.
+ * q_offsets, k_offsets : device int32, sequences + 1 entries that do not
+ *              decrease, from 0 to at most the tokens.  Both NULL for one
+ *              sequence of all tokens.  Rows of out and lse behind the last
+ *              sequence are left as they were.
+ * lse        : device float32, q_heads x q_tokens.
+ * workspace  : as queried; 0 unless few tiles of queries meet many keys.
+ * Scores, their maximum and sum are float32; for DMUON_BF16 the probabilities
+ * are rounded to bf16 in front of their product with v.  Numbers that no query
+ * of a sequence may see are not kept from it: an infinity or NaN in a key or
+ * value can reach any query of its sequence, but no other sequence.
+ */
+int dmuon_attention_workspace_bytes(const dmuon_attention_shape* shape, size_t* bytes_out);
+int dmuon_attention_forward(const dmuon_attention_shape* shape, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride, const int32_t* q_offsets,
+                            const int32_t* k_offsets, void* out, int64_t out_stride, float* lse, void* workspace,
+                            size_t workspace_bytes, void* hip_stream);
+
+/*
+ * Gradients of dmuon_attention_forward: dq, dk, dv from dout, the forward's
+ * inputs and its out and lse.  The probabilities are formed again from lse; a
+ * key head's gradients are summed over the query heads that share it, in fp32,
+ * in a fixed order.  Rows behind the last sequence are left as they were.
+ */
+int dmuon_attention_backward_workspace_bytes(const dmuon_attention_shape* shape, size_t* bytes_out);
+int dmuon_attention_backward(const dmuon_attention_shape* shape, const void* dout, int64_t dout_stride, const void* q,
+                             int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             const void* out, int64_t out_stride, const float* lse, const int32_t* q_offsets,
+                             const int32_t* k_offsets, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride,
+                             void* dv, int64_t dv_stride, void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
  * The plan of a call as text: routes (numel < DMUON_MIN_NS_NUMEL goes
  * elementwise when muon_step is nonzero), shape groups with their transposed
  * count, tiles and K slices, launches per Newton-Schulz step, algorithmic

@@ -40,6 +40,10 @@ from .ops import (  # noqa: F401
     rope_table,
 )
 from .block import (  # noqa: F401
+    attention,
+    attention_grad,
+    attention_grad_workspace_bytes,
+    attention_workspace_bytes,
     block_norm,
     block_norm_grad,
     block_norm_grad_workspace_bytes,

@@ -42,6 +42,7 @@ DMUON_MAX_VOCAB = 16777216
 DMUON_MAX_HEAD_DIM = 512
 DMUON_MAX_HEADS = 1024
 DMUON_MAX_TEACHER_K = 1024
+DMUON_MAX_ATTENTION_DIM = 256
 DMUON_EMBED_DENSE = 0
 DMUON_EMBED_ADD = 1
 DMUON_EMBED_ROWS = 2
@@ -100,6 +101,22 @@ class BlockNormShape(ctypes.Structure):
     ]
 
 
+class AttentionShape(ctypes.Structure):
+    """dmuon_attention_shape."""
+    _fields_ = [
+        ("q_tokens", ctypes.c_int64),
+        ("k_tokens", ctypes.c_int64),
+        ("sequences", ctypes.c_int64),
+        ("q_heads", ctypes.c_int),
+        ("k_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+        ("causal", ctypes.c_int),
+        ("window", ctypes.c_int),
+        ("scale", ctypes.c_float),
+        ("dtype", ctypes.c_int),
+    ]
+
+
 _P = ctypes.c_void_p
 _PP = ctypes.POINTER(ctypes.c_void_p)
 _I64P = ctypes.POINTER(ctypes.c_int64)
@@ -109,6 +126,7 @@ _CFGP = ctypes.POINTER(NsConfig)
 _I, _I64, _F, _SZ = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _QKP = ctypes.POINTER(QkShape)
 _BNP = ctypes.POINTER(BlockNormShape)
+_ATP = ctypes.POINTER(AttentionShape)
 
 # name -> (restype, argtypes); mirrors include/dmuon.h
 SIGNATURES = {
@@ -153,6 +171,11 @@ SIGNATURES = {
     "dmuon_block_norm_backward_workspace_bytes": (_I, [_BNP, _SZP]),
     "dmuon_block_norm_backward": (_I, [_BNP, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P,
                                        _P, _P, _P, _SZ, _P]),
+    "dmuon_attention_workspace_bytes": (_I, [_ATP, _SZP]),
+    "dmuon_attention_forward": (_I, [_ATP, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "dmuon_attention_backward_workspace_bytes": (_I, [_ATP, _SZP]),
+    "dmuon_attention_backward": (_I, [_ATP, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P,
+                                      _I64, _P, _I64, _P, _SZ, _P]),
     "dmuon_plan_summary": (ctypes.c_int, [ctypes.c_int, _I64P, _I64P, ctypes.c_int, _CFGP, ctypes.c_int, ctypes.c_int,
                                           ctypes.c_char_p, ctypes.c_size_t, _SZP]),
     "dmuon_status_string": (ctypes.c_char_p, [ctypes.c_int]),

@@ -1,5 +1,5 @@
 """Python binding of the operators between a decoder block's projections: norms
-around the block.
+around the block, attention over packed sequences.
 
 Everything that ops.py says of its calls (allocation, devices, streams, graphs,
 autograd) holds here too.
@@ -12,7 +12,7 @@ import torch
 
 from . import _lib
 from .api import _alloc, dtype_code
-from .ops import _query, _rows, _run, _tensor, _workspace
+from .ops import _heads, _query, _rows, _run, _tensor, _workspace
 
 
 def _row(t, name: str, like: Optional[torch.Tensor] = None) -> Tuple[int, int]:
@@ -94,3 +94,93 @@ def block_norm_grad(dx_out: Optional[torch.Tensor], dy: torch.Tensor, x_out: tor
     _run("dmuon_block_norm_backward", dev, stream, s, *grads, *head, *weights, *dxo, *dho,
          *[0 if w is None else w.data_ptr() for w in dws], ptr, nbytes)
     return (dx, dh, *dws)
+
+
+# ---------------------------------------------------------------- attention
+def _packed(out, name: str, like: torch.Tensor, stream) -> Tuple[torch.Tensor, int, int]:
+    """(tensor, address, token stride) of a result like `like` (tokens, heads, dim), given or allocated here."""
+    if out is None:
+        new = like.new_empty
+        out = new(like.shape) if stream is None else _alloc(stream, new, like.shape)
+        return out, out.data_ptr(), like.shape[1] * like.shape[2]
+    return out, *_heads(out, name, like)
+
+
+def _attn_args(q, k, v, q_offsets, k_offsets, causal, window, scale):
+    """(device index, dmuon_attention_shape, [q, stride, k, stride, v, stride], [offsets])."""
+    head = [*_heads(q, "q"), *_heads(k, "k"), *_heads(v, "v", k)]
+    dev, (n, qh, d), (nk, kh, dk) = q.get_device(), q.shape, k.shape
+    if dk != d or k.dtype != q.dtype or k.get_device() != dev:
+        raise ValueError(f"q is {q.dtype} {tuple(q.shape)} on {q.device}, k {k.dtype} {tuple(k.shape)} on {k.device}")
+    if (q_offsets is None) != (k_offsets is None):
+        raise ValueError("q_offsets and k_offsets come together")
+    sequences, offs = 1, [0, 0]
+    if q_offsets is not None:
+        offs = [_tensor(q_offsets, "q_offsets", dev, torch.int32),
+                _tensor(k_offsets, "k_offsets", dev, torch.int32, q_offsets.shape)]
+        if q_offsets.dim() != 1 or q_offsets.shape[0] < 2:
+            raise ValueError(f"q_offsets must hold one entry more than there are sequences, got shape {tuple(q_offsets.shape)}")
+        sequences = q_offsets.shape[0] - 1
+    s = _lib.AttentionShape(n, nk, sequences, qh, kh, d, 1 if causal else 0, window, d ** -0.5 if scale is None else scale,
+                            dtype_code(q.dtype))
+    return dev, s, head, offs
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Optional[torch.Tensor] = None,
+              k_offsets: Optional[torch.Tensor] = None, *, causal: bool = True, window: int = 0,
+              scale: Optional[float] = None, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """dmuon_attention_forward: (out, lse) of packed sequences.
+
+    q (tokens, q_heads, head_dim); k, v (keys, k_heads, head_dim), k_heads a
+    divisor of q_heads; all may be slices of a packed projection: only a token's
+    heads have to be contiguous.  q_offsets, k_offsets: int32 (sequences + 1),
+    where each sequence begins and the last ends; None for one sequence.  A
+    sequence's last query stands at its last key: with more keys than queries
+    the first ones are a cache.  causal, window: which keys a query sees.
+    scale: head_dim ** -0.5 by default.  lse: float32 (q_heads, tokens).
+    Rows behind the last sequence are left as they were (unset, where the
+    results are allocated here).  Outside autograd: the gradients are
+    attention_grad's."""
+    dev, s, head, offs = _attn_args(q, k, v, q_offsets, k_offsets, causal, window, scale)
+    out, *o = _packed(out, "out", q, stream)
+    if lse is None:
+        new, shape = q.new_empty, (q.shape[1], q.shape[0])
+        lse = new(shape, dtype=torch.float32) if stream is None else _alloc(stream, new, shape, dtype=torch.float32)
+        at = lse.data_ptr()
+    else:
+        at = _tensor(lse, "lse", dev, torch.float32, (q.shape[1], q.shape[0]))
+    _ws, ptr, nbytes = _workspace(workspace, _query("dmuon_attention_workspace_bytes", s), dev, stream)
+    _run("dmuon_attention_forward", dev, stream, s, *head, *offs, *o, at, ptr, nbytes)
+    return out, lse
+
+
+def attention_workspace_bytes(q_tokens: int, k_tokens: int, q_heads: int, k_heads: int, head_dim: int,
+                              sequences: int = 1) -> int:
+    return _query("dmuon_attention_workspace_bytes",
+                  _lib.AttentionShape(q_tokens, k_tokens, sequences, q_heads, k_heads, head_dim, scale=1.0))
+
+
+def attention_grad(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                   lse: torch.Tensor, q_offsets: Optional[torch.Tensor] = None,
+                   k_offsets: Optional[torch.Tensor] = None, *, causal: bool = True, window: int = 0,
+                   scale: Optional[float] = None, dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                   dv: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """dmuon_attention_backward: (dq, dk, dv) from the gradient of attention's
+    out, its inputs, and its out and lse.  dq, dk, dv may be given, as slices of
+    a packed gradient.  Rows behind the last sequence are left as they were."""
+    dev, s, head, offs = _attn_args(q, k, v, q_offsets, k_offsets, causal, window, scale)
+    first, back = _heads(dout, "dout", q), _heads(out, "out", q)
+    at = _tensor(lse, "lse", dev, torch.float32, (q.shape[1], q.shape[0]))
+    dq, *dqo = _packed(dq, "dq", q, stream)
+    dk, *dko = _packed(dk, "dk", k, stream)
+    dv, *dvo = _packed(dv, "dv", v, stream)
+    _ws, ptr, nbytes = _workspace(workspace, _query("dmuon_attention_backward_workspace_bytes", s), dev, stream)
+    _run("dmuon_attention_backward", dev, stream, s, *first, *head, *back, at, *offs, *dqo, *dko, *dvo, ptr, nbytes)
+    return dq, dk, dv
+
+
+def attention_grad_workspace_bytes(q_tokens: int, q_heads: int) -> int:
+    return _query("dmuon_attention_backward_workspace_bytes",
+                  _lib.AttentionShape(q_tokens, 0, 1, q_heads, q_heads, 1, scale=1.0))

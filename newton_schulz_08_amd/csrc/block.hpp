@@ -36,4 +36,39 @@ constexpr int kBnMaxFused = 8192;   // widest row whose column sums stay in regi
 // Rows that a block of the backward pass works on at once.
 inline int bn_rows_at_once(int64_t dim) { return dim <= 1024 ? 4 : 1; }
 
+// ---------------------------------------------------------------- attention over packed sequences
+constexpr int kAttnMaxDim = 256;
+constexpr int kAttnTile = 128;       // rows of a block: queries x the heads that share a key head, or keys
+struct AttnArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* out;         // backward: the forward's result
+  const void* dout;        // backward
+  const int* q_off;        // sequences + 1, or nullptr: one sequence of all tokens
+  const int* k_off;
+  void* o;                 // forward: out
+  float* lse;              // forward: written; backward: read
+  void* dq;
+  void* dk;
+  void* dv;
+  float* delta;            // backward: q_heads x q_tokens, dout . out of every row
+  float* part;             // forward in slices: per slice, tile and row the sum, then maximum and weight
+  int64_t qs, ks, vs, os, dos, dqs, dks, dvs;   // elements between tokens
+  int q_tokens, k_tokens, sequences;
+  int q_heads, k_heads, group, dim;   // group: query heads of a key head
+  unsigned group_inv;                 // ceil(2^32 / group), for rows / group
+  int causal, window;
+  float scale;
+  int vec;                 // every run of 16 bytes of a head is aligned
+  int slots;               // tiles' places over all sequences, of queries or of keys
+  int slices;              // forward: parts of a tile's keys
+};
+hipError_t launch_attention(int dt, const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attention_grad(int dt, const AttnArgs& a, int k_slots, hipStream_t stream);
+// Places for tiles of kAttnTile rows: sequence i's begin at floor(first row / tile) + i.
+inline int64_t attn_slots(int64_t rows, int64_t sequences) { return rows / kAttnTile + sequences; }
+// Head sizes that have kernels; a smaller head is padded with zeros.
+inline int attn_padded(int dim) { return dim <= 64 ? 64 : dim <= 96 ? 96 : dim <= 128 ? 128 : dim <= 192 ? 192 : 256; }
+
 }  // namespace dmuon

@@ -72,6 +72,79 @@ void fill_bn(const dmuon_block_norm_shape& s, const void* pre, const void* post,
   a->w[2] = gate;
 }
 
+// ---------------------------------------------------------------- attention
+int check_attn(const dmuon_attention_shape* s) {
+  if (!s) return invalid("shape is NULL");
+  DMUON_TRY(check_float(s->dtype, "dtype"));
+  DMUON_TRY(check_range(s->q_tokens, 0, DMUON_MAX_TOKENS, "q_tokens"));
+  DMUON_TRY(check_range(s->k_tokens, 0, DMUON_MAX_TOKENS, "k_tokens"));
+  DMUON_TRY(check_range(s->sequences, 1, DMUON_MAX_TOKENS, "sequences"));
+  DMUON_TRY(check_range(s->q_heads, 1, DMUON_MAX_HEADS, "q_heads"));
+  DMUON_TRY(check_range(s->k_heads, 1, DMUON_MAX_HEADS, "k_heads"));
+  if (s->q_heads % s->k_heads) return invalid("q_heads must be a multiple of k_heads");
+  DMUON_TRY(check_range(s->head_dim, 1, DMUON_MAX_ATTENTION_DIM, "head_dim"));
+  DMUON_TRY(check_range(s->window, 0, int64_t{1} << 30, "window"));
+  if (s->window && !s->causal) return invalid("a window needs causal");
+  if (!(std::isfinite(s->scale) && s->scale > 0.0f)) return invalid("scale must be finite and > 0");
+  return check_range(s->q_tokens * (s->q_heads / s->k_heads), 0, int64_t{1} << 30, "q_tokens * q_heads / k_heads");
+}
+
+// Blocks of a launch stay below the limit of its grid.
+int64_t attn_q_slots(const dmuon_attention_shape& s) {
+  return attn_slots(s.q_tokens * (s.q_heads / s.k_heads), s.sequences);
+}
+int check_attn_grid(const dmuon_attention_shape& s) {
+  const int64_t slots = std::max(attn_q_slots(s), attn_slots(s.k_tokens, s.sequences));
+  return check_range(slots * s.k_heads, 0, int64_t{1} << 24, "tiles (tokens / 128 + sequences, times k_heads)");
+}
+
+// Parts of a tile's keys: where the tiles alone leave CUs idle and the
+// sequences have keys to share out, at least 512 a part.
+int attn_slices(const dmuon_attention_shape& s) {
+  const int64_t tiles = attn_q_slots(s) * s.k_heads, keys = s.k_tokens / s.sequences;
+  if (tiles >= 256 || keys < 1024) return 1;
+  return static_cast<int>(std::min<int64_t>({1024 / tiles, keys / 512, 64}));
+}
+int64_t attn_part_bytes(const dmuon_attention_shape& s) {
+  const int64_t slices = attn_slices(s);
+  if (slices <= 1) return 0;
+  return attn_q_slots(s) * s.k_heads * slices * kAttnTile * (attn_padded(s.head_dim) + 2) * int64_t{4};
+}
+
+int head_buf(const dmuon_attention_shape& s, const char* name, const void* p, int64_t tokens, int64_t heads,
+             int64_t stride, bool written, Buf* out) {
+  return row_buf(name, p, tokens, heads * s.head_dim, stride, s.dtype, written, out);
+}
+
+// Every 16-byte run of every head lies at a multiple of 16 bytes.
+bool attn_vec(const dmuon_attention_shape& s, std::initializer_list<const Buf*> bufs) {
+  if (s.head_dim * size_of(s.dtype) % 16) return false;
+  for (const Buf* b : bufs)
+    if (!b->empty() && (!aligned(b->p, 16) || (b->rows > 1 && b->pitch % 16))) return false;
+  return true;
+}
+
+int check_offsets(const int32_t* q, const int32_t* k, int64_t sequences) {
+  if (!q != !k) return invalid("q_offsets and k_offsets come together");
+  if (!q && sequences != 1) return invalid("several sequences need offsets");
+  return DMUON_OK;
+}
+
+void fill_attn(const dmuon_attention_shape& s, AttnArgs* a) {
+  a->q_tokens = static_cast<int>(s.q_tokens);
+  a->k_tokens = static_cast<int>(s.k_tokens);
+  a->sequences = static_cast<int>(s.sequences);
+  a->q_heads = s.q_heads;
+  a->k_heads = s.k_heads;
+  a->group = s.q_heads / s.k_heads;
+  a->group_inv = static_cast<unsigned>(((uint64_t{1} << 32) + a->group - 1) / a->group);
+  a->dim = s.head_dim;
+  a->causal = s.causal ? 1 : 0;
+  a->window = s.window;
+  a->scale = s.scale;
+  a->slots = static_cast<int>(attn_q_slots(s));
+}
+
 }  // namespace
 }  // namespace dmuon
 
@@ -185,6 +258,135 @@ int dmuon_block_norm_backward(const dmuon_block_norm_shape* shape, const void* d
                     capturing, [&] {
                       return launch_block_norm_grad(s.dtype, s.branch_dtype, a, static_cast<hipStream_t>(hip_stream));
                     });
+  });
+}
+
+int dmuon_attention_workspace_bytes(const dmuon_attention_shape* shape, size_t* bytes_out) {
+  return guarded([&]() -> int {
+    if (!bytes_out) return invalid("bytes_out is NULL");
+    DMUON_TRY(check_attn(shape));
+    *bytes_out = align_up(static_cast<size_t>(attn_part_bytes(*shape)));
+    return DMUON_OK;
+  });
+}
+
+int dmuon_attention_forward(const dmuon_attention_shape* shape, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride, const int32_t* q_offsets,
+                            const int32_t* k_offsets, void* out, int64_t out_stride, float* lse, void* workspace,
+                            size_t workspace_bytes, void* hip_stream) {
+  return guarded([&]() -> int {
+    DMUON_TRY(check_attn(shape));
+    const dmuon_attention_shape& s = *shape;
+    DMUON_TRY(check_attn_grid(s));
+    DMUON_TRY(check_offsets(q_offsets, k_offsets, s.sequences));
+    const int64_t part = attn_part_bytes(s);
+    DMUON_TRY(check_workspace(workspace, workspace_bytes, align_up(static_cast<size_t>(part))));
+    Buf b[8];
+    DMUON_TRY(head_buf(s, "q", q, s.q_tokens, s.q_heads, q_stride, false, &b[0]));
+    DMUON_TRY(head_buf(s, "k", k, s.k_tokens, s.k_heads, k_stride, false, &b[1]));
+    DMUON_TRY(head_buf(s, "v", v, s.k_tokens, s.k_heads, v_stride, false, &b[2]));
+    DMUON_TRY(head_buf(s, "out", out, s.q_tokens, s.q_heads, out_stride, true, &b[3]));
+    b[4] = flat("lse", lse, s.q_tokens * s.q_heads * 4, 4, true);
+    b[5] = flat("q_offsets", q_offsets, q_offsets ? (s.sequences + 1) * 4 : 0, 4, false);
+    b[6] = flat("k_offsets", k_offsets, k_offsets ? (s.sequences + 1) * 4 : 0, 4, false);
+    b[7] = flat("workspace", workspace, part, 1, true);
+    DMUON_TRY(check_bufs(b, 8));
+    bool capturing = false;
+    DMUON_TRY(check_device(hip_stream, &capturing));
+    if (s.q_tokens == 0) return DMUON_OK;
+    AttnArgs a{};
+    fill_attn(s, &a);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.o = out;
+    a.lse = lse;
+    a.q_off = q_offsets;
+    a.k_off = k_offsets;
+    a.qs = q_stride;
+    a.ks = k_stride;
+    a.vs = v_stride;
+    a.os = out_stride;
+    a.part = static_cast<float*>(workspace);
+    a.slices = attn_slices(s);
+    a.vec = attn_vec(s, {&b[0], &b[1], &b[2], &b[3]});
+    const double qe = static_cast<double>(s.q_tokens) * s.q_heads * s.head_dim;
+    const double ke = static_cast<double>(s.k_tokens) * s.k_heads * s.head_dim;
+    // every query of an average sequence with every key
+    return launched("attention", kKAttention, 4.0 * qe * (static_cast<double>(s.k_tokens) / s.sequences),
+                    2.0 * (qe + ke) * size_of(s.dtype), hip_stream, capturing,
+                    [&] { return launch_attention(s.dtype, a, static_cast<hipStream_t>(hip_stream)); });
+  });
+}
+
+int dmuon_attention_backward_workspace_bytes(const dmuon_attention_shape* shape, size_t* bytes_out) {
+  return guarded([&]() -> int {
+    if (!bytes_out) return invalid("bytes_out is NULL");
+    DMUON_TRY(check_attn(shape));
+    *bytes_out = align_up(sizeof(float) * shape->q_tokens * shape->q_heads);
+    return DMUON_OK;
+  });
+}
+
+int dmuon_attention_backward(const dmuon_attention_shape* shape, const void* dout, int64_t dout_stride, const void* q,
+                             int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             const void* out, int64_t out_stride, const float* lse, const int32_t* q_offsets,
+                             const int32_t* k_offsets, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride,
+                             void* dv, int64_t dv_stride, void* workspace, size_t workspace_bytes, void* hip_stream) {
+  return guarded([&]() -> int {
+    DMUON_TRY(check_attn(shape));
+    const dmuon_attention_shape& s = *shape;
+    DMUON_TRY(check_attn_grid(s));
+    DMUON_TRY(check_offsets(q_offsets, k_offsets, s.sequences));
+    const size_t need = align_up(sizeof(float) * s.q_tokens * s.q_heads);
+    DMUON_TRY(check_workspace(workspace, workspace_bytes, need));
+    Buf b[12];
+    DMUON_TRY(head_buf(s, "dout", dout, s.q_tokens, s.q_heads, dout_stride, false, &b[0]));
+    DMUON_TRY(head_buf(s, "q", q, s.q_tokens, s.q_heads, q_stride, false, &b[1]));
+    DMUON_TRY(head_buf(s, "k", k, s.k_tokens, s.k_heads, k_stride, false, &b[2]));
+    DMUON_TRY(head_buf(s, "v", v, s.k_tokens, s.k_heads, v_stride, false, &b[3]));
+    DMUON_TRY(head_buf(s, "out", out, s.q_tokens, s.q_heads, out_stride, false, &b[4]));
+    DMUON_TRY(head_buf(s, "dq", dq, s.q_tokens, s.q_heads, dq_stride, true, &b[5]));
+    DMUON_TRY(head_buf(s, "dk", dk, s.k_tokens, s.k_heads, dk_stride, true, &b[6]));
+    DMUON_TRY(head_buf(s, "dv", dv, s.k_tokens, s.k_heads, dv_stride, true, &b[7]));
+    b[8] = flat("lse", lse, s.q_tokens * s.q_heads * 4, 4, false);
+    b[9] = flat("q_offsets", q_offsets, q_offsets ? (s.sequences + 1) * 4 : 0, 4, false);
+    b[10] = flat("k_offsets", k_offsets, k_offsets ? (s.sequences + 1) * 4 : 0, 4, false);
+    b[11] = flat("workspace", workspace, static_cast<int64_t>(need), 1, true);
+    DMUON_TRY(check_bufs(b, 12));
+    bool capturing = false;
+    DMUON_TRY(check_device(hip_stream, &capturing));
+    if (s.q_tokens == 0 && s.k_tokens == 0) return DMUON_OK;
+    AttnArgs a{};
+    fill_attn(s, &a);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.out = out;
+    a.dout = dout;
+    a.lse = const_cast<float*>(lse);
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.q_off = q_offsets;
+    a.k_off = k_offsets;
+    a.qs = q_stride;
+    a.ks = k_stride;
+    a.vs = v_stride;
+    a.os = out_stride;
+    a.dos = dout_stride;
+    a.dqs = dq_stride;
+    a.dks = dk_stride;
+    a.dvs = dv_stride;
+    a.delta = static_cast<float*>(workspace);
+    a.slices = 1;
+    a.vec = attn_vec(s, {&b[0], &b[1], &b[2], &b[3], &b[4], &b[5], &b[6], &b[7]});
+    const int k_slots = static_cast<int>(attn_slots(s.k_tokens, s.sequences));
+    const double qe = static_cast<double>(s.q_tokens) * s.q_heads * s.head_dim;
+    const double ke = static_cast<double>(s.k_tokens) * s.k_heads * s.head_dim;
+    return launched("attention gradient", kKAttentionGrad, 10.0 * qe * (static_cast<double>(s.k_tokens) / s.sequences),
+                    4.0 * (qe + ke) * size_of(s.dtype), hip_stream, capturing,
+                    [&] { return launch_attention_grad(s.dtype, a, k_slots, static_cast<hipStream_t>(hip_stream)); });
   });
 }
 

@@ -1,0 +1,241 @@
+// Attention over packed sequences, forward, on gfx950 (MFMA-bound for long
+// sequences, HBM-bound for single queries).
+//
+// Of a sequence with lq queries and lk keys, query i sees key j when
+// j <= i + lk - lq (causal) and j > i + lk - lq - window (with a window).  With
+// s = scale q . k, one pass over the keys keeps the maximum m and the sum l of
+// exp(s - m) of every row:
+//
+//   out = sum exp(s - m) v / l,    lse = m + log l
+//
+// A row without visible keys has out 0 and lse -infinity.
+//
+// The rows of a tile are a key head's (query, query head) pairs, so the heads
+// that share keys read them once, and a single query still fills rows.  Each
+// wave keeps 32 rows: S^T = K Q^T puts a row's scores into one pair of lanes,
+// maximum and sum need one exchange, and P^T is the next product's operand
+// where it lies (attention.hpp).  K and V tiles go straight to LDS, one tile
+// ahead.  Exponentials are base 2 with log2(e) folded into the scale.
+//
+// Few tiles (single queries): a tile's keys are cut into slices, each leaving its
+// unnormed sum, maximum and weight; a second launch joins them.
+#include <hip/hip_runtime.h>
+
+#include "attention.hpp"
+
+namespace dmuon {
+namespace attn {
+namespace {
+
+constexpr float kNone = -INFINITY;
+
+// Unnormed sums of a slice: rows x DP, then maximum and weight of each row.
+__host__ __device__ constexpr int64_t slice_floats(int dp) { return static_cast<int64_t>(kAttnTile) * (dp + 2); }
+
+template <int DT, int DP> __global__ __launch_bounds__(kThreads) void attention_kernel(AttnArgs a) {
+  using S = Shape<DT, DP>;
+  using T = typename S::T;
+  constexpr int kKeys = S::kPitch <= 512 ? 64 : 32;          // of a tile
+  constexpr int kKb = kKeys / 32;
+  constexpr int kTileBytes = kKeys * S::kPitch;
+  __shared__ __attribute__((aligned(16))) char lds[4 * kTileBytes];   // K, V; twice
+
+  // heads vary fastest: the blocks of one XCD share few heads' keys.  The last
+  // tiles of a causal sequence have the most keys: they start first.
+  const int head = blockIdx.x % a.k_heads, rest = blockIdx.x / a.k_heads;
+  const int slot = a.slots - 1 - rest % a.slots, slice = rest / a.slots;
+  const Place p = place(a, slot, false);
+  if (!p.any) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int shift = p.lk - p.lq;
+  const int last = (p.rows < p.row0 + kAttnTile ? p.rows : p.row0 + kAttnTile) - 1;
+
+  // keys that any row of the tile sees, whole tiles of them, this slice's share
+  int end = p.lk, begin = 0;
+  if (a.causal) end = min(end, query_of(a, last) + shift + 1);
+  if (a.window) begin = max(0, query_of(a, p.row0) + shift - a.window + 1) / kKeys * kKeys;
+  int tiles = end > begin ? (end - begin + kKeys - 1) / kKeys : 0;
+  if (a.slices > 1) {
+    const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * slice / a.slices);
+    const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (slice + 1) / a.slices);
+    begin += t0 * kKeys;
+    tiles = t1 - t0;
+  }
+
+  // this lane's row
+  const int row = p.row0 + wave * 32 + (lane & 31);
+  const bool any = row < p.rows;
+  const int qi = query_of(a, any ? row : last), g = (any ? row : last) - qi * a.group;
+  const int64_t token = p.q0 + qi;
+  const int qh = head * a.group + g;
+  const T* qrow = static_cast<const T*>(a.q) + token * a.qs + static_cast<int64_t>(qh) * a.dim;
+  const int hi = a.causal ? min(qi + shift, p.lk - 1) : p.lk - 1, lo = a.window ? qi + shift - a.window + 1 : 0;
+  // this wave's rows
+  const int w0 = p.row0 + wave * 32;
+  const bool wave_any = w0 < p.rows;
+  const int wlo = query_of(a, min(w0, last)), whi = query_of(a, min(w0 + 31, last));
+
+  Frag<DT> qf[S::kSteps];
+#pragma unroll
+  for (int s = 0; s < S::kSteps; ++s) qf[s] = frag_global<DT>(qrow, any, s, a.dim, a.vec);
+
+  const T* kbase = static_cast<const T*>(a.k) + p.k0 * a.ks + static_cast<int64_t>(head) * a.dim;
+  const T* vbase = static_cast<const T*>(a.v) + p.k0 * a.vs + static_cast<int64_t>(head) * a.dim;
+  auto fetch = [&](int tile) {
+    char* to = lds + (tile & 1) * 2 * kTileBytes;
+    const int key0 = begin + tile * kKeys, most_ = p.lk - 1;
+    fill_tile<DT, DP, kKeys>(to, a.dim, a.vec, [&](int r) { return kbase + static_cast<int64_t>(min(key0 + r, most_)) * a.ks; });
+    fill_tile<DT, DP, kKeys>(to + kTileBytes, a.dim, a.vec,
+                             [&](int r) { return vbase + static_cast<int64_t>(min(key0 + r, most_)) * a.vs; });
+  };
+
+  f32x16 o[S::kBlocks];
+#pragma unroll
+  for (int b = 0; b < S::kBlocks; ++b) o[b] = f32x16{};
+  float m = kNone, l = 0.0f;   // l: this lane's half of the row
+  const float c = a.scale * kLog2e;
+
+  if (tiles > 0) {
+    if (a.vec && a.dim < DP) {
+      clear_tiles(lds, 4 * kTileBytes);
+      __syncthreads();
+    }
+    fetch(0);
+    tiles_landed();
+  }
+  for (int tile = 0; tile < tiles; ++tile) {
+    if (tile + 1 < tiles) fetch(tile + 1);
+    const char* kt = lds + (tile & 1) * 2 * kTileBytes;
+    const char* vt = kt + kTileBytes;
+    const int key0 = begin + tile * kKeys;
+    const bool see = wave_any && (!a.causal || key0 <= whi + shift) && (!a.window || key0 + kKeys > wlo + shift - a.window + 1);
+    if (see) {
+      f32x16 s[kKb];
+#pragma unroll
+      for (int kb = 0; kb < kKb; ++kb) {
+        s[kb] = f32x16{};
+#pragma unroll
+        for (int st = 0; st < S::kSteps; ++st) s[kb] = mma(frag_rows<DT, DP>(kt, 32 * kb, st), qf[st], s[kb]);
+      }
+      const bool mask = key0 + kKeys > p.lk || (a.causal && key0 + kKeys - 1 > wlo + shift) ||
+                        (a.window && key0 < whi + shift - a.window + 1);
+      if (mask) {
+#pragma unroll
+        for (int kb = 0; kb < kKb; ++kb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int key = key0 + 32 * kb + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
+            if (key > hi || key < lo) s[kb][i] = kNone;
+          }
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int kb = 0; kb < kKb; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
+      top = fmaxf(top, other_half(top)) * c;
+      const float mn = fmaxf(m, top);
+      const float ms = mn == kNone ? 0.0f : mn;   // nothing visible so far: exp2(-inf - 0) = 0
+      if (__any(mn > m)) {
+        const float by = __builtin_amdgcn_exp2f(m - ms);
+        l *= by;
+#pragma unroll
+        for (int b = 0; b < S::kBlocks; ++b) o[b] *= by;
+      }
+      m = mn;
+      Frag<DT> pf[kKb][2];
+#pragma unroll
+      for (int kb = 0; kb < kKb; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float e = __builtin_amdgcn_exp2f(fmaf(s[kb][i], c, -ms));
+          l += e;
+          pf[kb][i >> 3].set(i & 7, e);
+        }
+#pragma unroll
+      for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+        for (int kb = 0; kb < kKb; ++kb)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) o[b] = mma(frag_cols<DT, DP>(vt, 32 * kb + 16 * h, b), pf[kb][h], o[b]);
+    }
+    tiles_landed();
+  }
+
+  l += other_half(l);
+  if (a.slices > 1) {
+    if (!any) return;
+    float* part = a.part + (static_cast<int64_t>(blockIdx.x)) * slice_floats(DP);
+    const int r = wave * 32 + (lane & 31);
+    store_row<kF32, DP>(part + static_cast<int64_t>(r) * DP, o, 1.0f, DP, 1);
+    if (lane < 32) {
+      gmem(part)[static_cast<int64_t>(kAttnTile) * DP + 2 * r] = m;
+      gmem(part)[static_cast<int64_t>(kAttnTile) * DP + 2 * r + 1] = l;
+    }
+    return;
+  }
+  if (!any) return;
+  store_row<DT, DP>(static_cast<T*>(a.o) + token * a.os + static_cast<int64_t>(qh) * a.dim, o, l > 0.0f ? 1.0f / l : l, a.dim,
+                    a.vec);
+  if (lane < 32) gmem(a.lse)[static_cast<int64_t>(qh) * a.q_tokens + token] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0.0f ? kNone : l;
+}
+
+// Joins a tile's slices: one wave a row, in the slices' order.
+template <int DT, int DP> __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs a) {
+  using T = typename OpElem<DT>::T;
+  const int head = blockIdx.x % a.k_heads, rest = blockIdx.x / a.k_heads;
+  const Place p = place(a, a.slots - 1 - rest, false);
+  const int r = blockIdx.y * kWaves + (threadIdx.x >> 6), lane = threadIdx.x & 63, row = p.row0 + r;
+  if (!p.any || row >= p.rows) return;
+  const int64_t step = static_cast<int64_t>(a.k_heads) * a.slots * slice_floats(DP);
+  const float* part = a.part + static_cast<int64_t>(blockIdx.x) * slice_floats(DP);
+  const float* ml = part + static_cast<int64_t>(kAttnTile) * DP + 2 * r;
+  float m = kNone;
+  for (int s = 0; s < a.slices; ++s) m = fmaxf(m, gmem(ml)[s * step]);
+  const float ms = m == kNone ? 0.0f : m;
+  float l = 0.0f, o[DP / 64 + 1] = {};
+  for (int s = 0; s < a.slices; ++s) {
+    const float by = __builtin_amdgcn_exp2f(gmem(ml)[s * step] - ms);
+    l += by * gmem(ml)[s * step + 1];
+#pragma unroll
+    for (int k = 0; k < DP / 64 + 1; ++k)
+      if (64 * k + lane < DP) o[k] += by * gmem(part)[s * step + static_cast<int64_t>(r) * DP + 64 * k + lane];
+  }
+  const int qi = query_of(a, row), qh = head * a.group + row - qi * a.group;
+  const int64_t token = p.q0 + qi;
+  T* out = static_cast<T*>(a.o) + token * a.os + static_cast<int64_t>(qh) * a.dim;
+  const float by = l > 0.0f ? 1.0f / l : l;
+#pragma unroll
+  for (int k = 0; k < DP / 64 + 1; ++k)
+    if (64 * k + lane < a.dim) gmem(out)[64 * k + lane] = static_cast<T>(o[k] * by);
+  if (lane == 0) gmem(a.lse)[static_cast<int64_t>(qh) * a.q_tokens + token] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0.0f ? kNone : l;
+}
+
+template <int DT, int DP> hipError_t run(const AttnArgs& a, hipStream_t stream) {
+  const unsigned tiles = static_cast<unsigned>(a.slots) * a.k_heads;
+  attention_kernel<DT, DP><<<dim3(tiles * a.slices), dim3(kThreads), 0, stream>>>(a);
+  if (a.slices > 1) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    attention_join_kernel<DT, DP><<<dim3(tiles, kAttnTile / kWaves), dim3(kThreads), 0, stream>>>(a);
+  }
+  return hipGetLastError();
+}
+template <int DT> hipError_t run_any(const AttnArgs& a, hipStream_t stream) {
+  switch (attn_padded(a.dim)) {
+    case 64: return run<DT, 64>(a, stream);
+    case 96: return run<DT, 96>(a, stream);
+    case 128: return run<DT, 128>(a, stream);
+    case 192: return run<DT, 192>(a, stream);
+    default: return run<DT, 256>(a, stream);
+  }
+}
+
+}  // namespace
+}  // namespace attn
+
+hipError_t launch_attention(int dt, const AttnArgs& a, hipStream_t stream) {
+  return dt == kF32 ? attn::run_any<kF32>(a, stream) : attn::run_any<kBF16>(a, stream);
+}
+
+}  // namespace dmuon

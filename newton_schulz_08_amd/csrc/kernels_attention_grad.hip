@@ -1,0 +1,296 @@
+// Gradients of attention over packed sequences, on gfx950 (MFMA-bound).
+//
+// With the forward's lse, the probabilities are formed again, tile by tile:
+//
+//   p  = exp(scale q . k - lse),       delta = dout . out  of each row
+//   ds = p (dout . v - delta) scale
+//   dq = sum over keys of ds k,   dk = sum over rows of ds q,   dv = sum of p dout
+//
+// Three launches.  The first forms delta.  dq's blocks keep a tile of rows
+// (queries x the heads that share a key head) and pass over the keys; dk's and
+// dv's keep a tile of keys and pass over the rows, those of all heads that
+// share it, so a shared head's gradient is one sum in one block.  Each forms
+// the scores for itself: seven products in all instead of five, but every sum
+// has one owner and one order, with no atomics and no partial results in
+// memory.
+//
+// Rows without visible keys (lse -infinity) and rows behind the sequence take
+// lse = +infinity, which makes their probabilities exp2(-infinity) = 0.
+#include <hip/hip_runtime.h>
+
+#include "attention.hpp"
+
+namespace dmuon {
+namespace attn {
+namespace {
+
+// Base-2 log-sum-exp of a row, +infinity where it must have no probabilities.
+__device__ __forceinline__ float row_lse(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+
+// One wave per token and run of heads.
+template <int DT> __global__ __launch_bounds__(kThreads) void attention_delta_kernel(AttnArgs a) {
+  using T = typename OpElem<DT>::T;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+  const int64_t token = unit / a.q_heads;
+  const int head = static_cast<int>(unit % a.q_heads), lane = threadIdx.x & 63;
+  if (token >= a.q_tokens) return;
+  const T* o = static_cast<const T*>(a.out) + token * a.os + static_cast<int64_t>(head) * a.dim;
+  const T* d = static_cast<const T*>(a.dout) + token * a.dos + static_cast<int64_t>(head) * a.dim;
+  float s = 0.0f;
+  for (int e = lane; e < a.dim; e += 64) s += static_cast<float>(gmem(o)[e]) * static_cast<float>(gmem(d)[e]);
+#pragma unroll
+  for (int x = 32; x > 0; x >>= 1) s += __shfl_xor(s, x, 64);
+  if (lane == 0) gmem(a.delta)[static_cast<int64_t>(head) * a.q_tokens + token] = s;
+}
+
+template <int DT, int DP> __global__ __launch_bounds__(kThreads) void attention_dq_kernel(AttnArgs a) {
+  using S = Shape<DT, DP>;
+  using T = typename S::T;
+  constexpr int kKeys = S::kPitch <= 256 ? 64 : 32;
+  constexpr int kTileBytes = kKeys * S::kPitch;
+  __shared__ __attribute__((aligned(16))) char lds[4 * kTileBytes];   // K, V; twice
+
+  const int head = blockIdx.x % a.k_heads, rest = blockIdx.x / a.k_heads;
+  const Place p = place(a, a.slots - 1 - rest, false);
+  if (!p.any) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int shift = p.lk - p.lq;
+  const int last = (p.rows < p.row0 + kAttnTile ? p.rows : p.row0 + kAttnTile) - 1;
+  int end = p.lk, begin = 0;
+  if (a.causal) end = min(end, query_of(a, last) + shift + 1);
+  if (a.window) begin = max(0, query_of(a, p.row0) + shift - a.window + 1) / kKeys * kKeys;
+  const int tiles = end > begin ? (end - begin + kKeys - 1) / kKeys : 0;
+
+  const int row = p.row0 + wave * 32 + (lane & 31);
+  const bool any = row < p.rows;
+  const int qi = query_of(a, any ? row : last), g = (any ? row : last) - qi * a.group;
+  const int64_t token = p.q0 + qi;
+  const int qh = head * a.group + g;
+  const int hi = a.causal ? min(qi + shift, p.lk - 1) : p.lk - 1, lo = a.window ? qi + shift - a.window + 1 : 0;
+  const int w0 = p.row0 + wave * 32;
+  const bool wave_any = w0 < p.rows;
+  const int wlo = query_of(a, min(w0, last)), whi = query_of(a, min(w0 + 31, last));
+
+  const T* qrow = static_cast<const T*>(a.q) + token * a.qs + static_cast<int64_t>(qh) * a.dim;
+  const T* drow = static_cast<const T*>(a.dout) + token * a.dos + static_cast<int64_t>(qh) * a.dim;
+  Frag<DT> qf[S::kSteps], df[S::kSteps];
+#pragma unroll
+  for (int s = 0; s < S::kSteps; ++s) {
+    qf[s] = frag_global<DT>(qrow, any, s, a.dim, a.vec);
+    df[s] = frag_global<DT>(drow, any, s, a.dim, a.vec);
+  }
+  const int64_t stat = static_cast<int64_t>(qh) * a.q_tokens + token;
+  const float lse = any ? row_lse(gmem(a.lse)[stat]) : INFINITY, delta = gmem(a.delta)[stat];
+
+  const T* kbase = static_cast<const T*>(a.k) + p.k0 * a.ks + static_cast<int64_t>(head) * a.dim;
+  const T* vbase = static_cast<const T*>(a.v) + p.k0 * a.vs + static_cast<int64_t>(head) * a.dim;
+  auto fetch = [&](int tile) {
+    char* to = lds + (tile & 1) * 2 * kTileBytes;
+    const int key0 = begin + tile * kKeys, most_ = p.lk - 1;
+    fill_tile<DT, DP, kKeys>(to, a.dim, a.vec, [&](int r) { return kbase + static_cast<int64_t>(min(key0 + r, most_)) * a.ks; });
+    fill_tile<DT, DP, kKeys>(to + kTileBytes, a.dim, a.vec,
+                             [&](int r) { return vbase + static_cast<int64_t>(min(key0 + r, most_)) * a.vs; });
+  };
+  f32x16 dq[S::kBlocks];
+#pragma unroll
+  for (int b = 0; b < S::kBlocks; ++b) dq[b] = f32x16{};
+  const float c = a.scale * kLog2e;
+  if (tiles > 0) {
+    if (a.vec && a.dim < DP) {
+      clear_tiles(lds, 4 * kTileBytes);
+      __syncthreads();
+    }
+    fetch(0);
+    tiles_landed();
+  }
+  for (int tile = 0; tile < tiles; ++tile) {
+    if (tile + 1 < tiles) fetch(tile + 1);
+    const char* kt = lds + (tile & 1) * 2 * kTileBytes;
+    const char* vt = kt + kTileBytes;
+#pragma unroll 1
+    for (int kb = 0; kb < kKeys; kb += 32) {
+      const int key0 = begin + tile * kKeys + kb;
+      const bool see = wave_any && key0 < p.lk && (!a.causal || key0 <= whi + shift) &&
+                       (!a.window || key0 + 32 > wlo + shift - a.window + 1);
+      if (!see) continue;
+      f32x16 s{}, dp{};
+#pragma unroll
+      for (int st = 0; st < S::kSteps; ++st) s = mma(frag_rows<DT, DP>(kt, kb, st), qf[st], s);
+#pragma unroll
+      for (int st = 0; st < S::kSteps; ++st) dp = mma(frag_rows<DT, DP>(vt, kb, st), df[st], dp);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        dp[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -lse)) * (dp[i] - delta);
+      const bool mask = key0 + 32 > p.lk || (a.causal && key0 + 31 > wlo + shift) ||
+                        (a.window && key0 < whi + shift - a.window + 1);
+      if (mask) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int key = key0 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
+          if (key > hi || key < lo) dp[i] = 0.0f;
+        }
+      }
+      Frag<DT> ds[2];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ds[i >> 3].set(i & 7, dp[i]);
+#pragma unroll
+      for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) dq[b] = mma(frag_cols<DT, DP>(kt, kb + 16 * h, b), ds[h], dq[b]);
+    }
+    tiles_landed();
+  }
+  if (any)
+    store_row<DT, DP>(static_cast<T*>(a.dq) + token * a.dqs + static_cast<int64_t>(qh) * a.dim, dq, a.scale, a.dim, a.vec);
+}
+
+// HELD: the keys' and values' fragments stay in registers; else they are read
+// again for every tile of rows (fp32 heads beyond 128, whose two fragments and
+// two sums are 512 registers).
+template <int DT, int DP, bool HELD> __global__ __launch_bounds__(kThreads) void attention_dkv_kernel(AttnArgs a) {
+  using S = Shape<DT, DP>;
+  using T = typename S::T;
+  constexpr int kTileBytes = 32 * S::kPitch;
+  __shared__ __attribute__((aligned(16))) char lds[4 * kTileBytes];   // Q, dout; twice
+  __shared__ float stats[2][2][32];                                   // lse, delta; twice
+
+  const int head = blockIdx.x % a.k_heads;
+  const Place p = place(a, blockIdx.x / a.k_heads, true);
+  if (!p.any) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, hf = lane >> 5;
+  const int shift = p.lk - p.lq;
+  const int last = min(p.lk, p.row0 + kAttnTile) - 1;
+  // rows that see any of the tile's keys
+  int first_q = 0, end_q = p.lq;
+  if (a.causal) first_q = max(0, p.row0 - shift);
+  if (a.window) end_q = min(end_q, last - shift + a.window);
+  const int begin = first_q * a.group, end = end_q * a.group;
+  const int tiles = end > begin ? (end - begin + 31) / 32 : 0;
+
+  const int key = p.row0 + wave * 32 + (lane & 31);
+  const bool any = key < p.lk;
+  const int64_t token = p.k0 + (any ? key : last);
+  const T* krow = static_cast<const T*>(a.k) + token * a.ks + static_cast<int64_t>(head) * a.dim;
+  const T* vrow = static_cast<const T*>(a.v) + token * a.vs + static_cast<int64_t>(head) * a.dim;
+  const int w0 = p.row0 + wave * 32, w1 = min(w0 + 31, p.lk - 1);   // this wave's keys
+  const bool wave_any = w0 < p.lk;
+  Frag<DT> kf[HELD ? S::kSteps : 1], vf[HELD ? S::kSteps : 1];
+  if constexpr (HELD)
+#pragma unroll
+    for (int s = 0; s < S::kSteps; ++s) {
+      kf[s] = frag_global<DT>(krow, any, s, a.dim, a.vec);
+      vf[s] = frag_global<DT>(vrow, any, s, a.dim, a.vec);
+    }
+
+  const T* qbase = static_cast<const T*>(a.q) + p.q0 * a.qs + static_cast<int64_t>(head) * a.group * a.dim;
+  const T* dbase = static_cast<const T*>(a.dout) + p.q0 * a.dos + static_cast<int64_t>(head) * a.group * a.dim;
+  auto fetch = [&](int tile) {
+    char* to = lds + (tile & 1) * 2 * kTileBytes;
+    const int r0 = begin + tile * 32;
+    auto at = [&](const T* base, int64_t stride, int r) {
+      const int row = min(r0 + r, end - 1), i = query_of(a, row);
+      return base + i * stride + static_cast<int64_t>(row - i * a.group) * a.dim;
+    };
+    fill_tile<DT, DP, 32>(to, a.dim, a.vec, [&](int r) { return at(qbase, a.qs, r); });
+    fill_tile<DT, DP, 32>(to + kTileBytes, a.dim, a.vec, [&](int r) { return at(dbase, a.dos, r); });
+    if (threadIdx.x < 64) {
+      const int r = threadIdx.x & 31, row = min(r0 + r, end - 1), i = query_of(a, row);
+      const int64_t stat = static_cast<int64_t>(head * a.group + row - i * a.group) * a.q_tokens + p.q0 + i;
+      if (threadIdx.x < 32) stats[tile & 1][0][r] = r0 + r < end ? row_lse(gmem(a.lse)[stat]) : INFINITY;
+      else stats[tile & 1][1][r] = gmem(a.delta)[stat];
+    }
+  };
+  f32x16 dk[S::kBlocks], dv[S::kBlocks];
+#pragma unroll
+  for (int b = 0; b < S::kBlocks; ++b) dk[b] = dv[b] = f32x16{};
+  const float c = a.scale * kLog2e;
+  if (tiles > 0) {
+    if (a.vec && a.dim < DP) {
+      clear_tiles(lds, 4 * kTileBytes);
+      __syncthreads();
+    }
+    fetch(0);
+    tiles_landed();
+  }
+  for (int tile = 0; tile < tiles; ++tile) {
+    if (tile + 1 < tiles) fetch(tile + 1);
+    const char* qt = lds + (tile & 1) * 2 * kTileBytes;
+    const char* dt = qt + kTileBytes;
+    const int r0 = begin + tile * 32, r1 = min(r0 + 31, end - 1);
+    const int qlo = query_of(a, r0), qhi = query_of(a, r1);
+    const bool see = wave_any && (!a.causal || w0 <= qhi + shift) && (!a.window || w1 > qlo + shift - a.window);
+    if (see) {
+      f32x16 s{}, dp{};
+#pragma unroll
+      for (int st = 0; st < S::kSteps; ++st)
+        s = mma(frag_rows<DT, DP>(qt, 0, st), HELD ? kf[HELD ? st : 0] : frag_global<DT>(krow, any, st, a.dim, a.vec), s);
+#pragma unroll
+      for (int st = 0; st < S::kSteps; ++st)
+        dp = mma(frag_rows<DT, DP>(dt, 0, st), HELD ? vf[HELD ? st : 0] : frag_global<DT>(vrow, any, st, a.dim, a.vec), dp);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int r = 8 * (i >> 2) + 4 * hf + (i & 3);
+        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -stats[tile & 1][0][r]));
+        dp[i] = s[i] * (dp[i] - stats[tile & 1][1][r]);
+      }
+      const bool mask = (a.causal && w1 > qlo + shift) || (a.window && w0 <= qhi + shift - a.window);
+      if (mask) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int q = query_of(a, min(r0 + 8 * (i >> 2) + 4 * hf + (i & 3), end - 1)) + shift;
+          if (key > q || (a.window && key <= q - a.window)) s[i] = dp[i] = 0.0f;
+        }
+      }
+      Frag<DT> pf[2], ds[2];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        pf[i >> 3].set(i & 7, s[i]);
+        ds[i >> 3].set(i & 7, dp[i]);
+      }
+#pragma unroll
+      for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          dv[b] = mma(frag_cols<DT, DP>(dt, 16 * h, b), pf[h], dv[b]);
+          dk[b] = mma(frag_cols<DT, DP>(qt, 16 * h, b), ds[h], dk[b]);
+        }
+    }
+    tiles_landed();
+  }
+  if (!any) return;
+  store_row<DT, DP>(static_cast<T*>(a.dk) + token * a.dks + static_cast<int64_t>(head) * a.dim, dk, a.scale, a.dim, a.vec);
+  store_row<DT, DP>(static_cast<T*>(a.dv) + token * a.dvs + static_cast<int64_t>(head) * a.dim, dv, 1.0f, a.dim, a.vec);
+}
+
+template <int DT, int DP> hipError_t run(const AttnArgs& a, int k_slots, hipStream_t stream) {
+  if (a.q_tokens > 0) {
+    const int64_t units = static_cast<int64_t>(a.q_tokens) * a.q_heads;
+    attention_delta_kernel<DT><<<dim3(static_cast<unsigned>((units + kWaves - 1) / kWaves)), dim3(kThreads), 0, stream>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    attention_dq_kernel<DT, DP><<<dim3(static_cast<unsigned>(a.slots) * a.k_heads), dim3(kThreads), 0, stream>>>(a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (a.k_tokens > 0)
+    attention_dkv_kernel<DT, DP, DT == kBF16 || DP <= 128>
+        <<<dim3(static_cast<unsigned>(k_slots) * a.k_heads), dim3(kThreads), 0, stream>>>(a);
+  return hipGetLastError();
+}
+template <int DT> hipError_t run_any(const AttnArgs& a, int k_slots, hipStream_t stream) {
+  switch (attn_padded(a.dim)) {
+    case 64: return run<DT, 64>(a, k_slots, stream);
+    case 96: return run<DT, 96>(a, k_slots, stream);
+    case 128: return run<DT, 128>(a, k_slots, stream);
+    case 192: return run<DT, 192>(a, k_slots, stream);
+    default: return run<DT, 256>(a, k_slots, stream);
+  }
+}
+
+}  // namespace
+}  // namespace attn
+
+hipError_t launch_attention_grad(int dt, const AttnArgs& a, int k_slots, hipStream_t stream) {
+  return dt == kF32 ? attn::run_any<kF32>(a, k_slots, stream) : attn::run_any<kBF16>(a, k_slots, stream);
+}
+
+}  // namespace dmuon
