@@ -655,6 +655,52 @@ int dmuon_attention_backward(const dmuon_attention_shape* shape, const void* dou
                              void* dv, int64_t dv_stride, void* workspace, size_t workspace_bytes, void* hip_stream);
 
 /*
+ * Shape and types of dmuon_gated_ffn_forward and _backward.
+ */
+#define DMUON_ACT_SILU 0   /* g / (1 + exp(-g)) */
+#define DMUON_ACT_GELU 1   /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+typedef struct {
+    int64_t tokens;       /* 0 .. DMUON_MAX_TOKENS */
+    int64_t dim;          /* 1 .. DMUON_MAX_DIM */
+    int64_t hidden;       /* 1 .. DMUON_MAX_DIM */
+    int activation;       /* DMUON_ACT_SILU or DMUON_ACT_GELU */
+    int dtype;            /* inputs, weights, output and their gradients */
+} dmuon_gated_ffn_shape;
+
+/*
+ * The gated half of a feed-forward block: both projections, the activation and
+ * the product in one pass,
+ *
+ *   h = act(x Wg^T) * (x Wu^T).
+ *
+ * x      : device, tokens x dim, row r at element r * x_stride.
+ * w_gate, w_up : device, hidden x dim, contiguous.
+ * h      : device, tokens x hidden, row r at element r * h_stride.
+ * Sums are float32, and so is everything up to h.  workspace: for DMUON_BF16
+ * it takes padded copies of the operands unless dim is a multiple of 64 and they
+ * are aligned: x, w_gate and w_up at multiples of 16 bytes, rows of x a
+ * multiple of 16 bytes apart and at most 8 MiB.  The query is told whether they
+ * are; a call needs no more than that.
+ */
+int dmuon_gated_ffn_workspace_bytes(const dmuon_gated_ffn_shape* shape, int is_aligned, size_t* bytes_out);
+int dmuon_gated_ffn_forward(const dmuon_gated_ffn_shape* shape, const void* x, int64_t x_stride, const void* w_gate,
+                            const void* w_up, void* h, int64_t h_stride, void* workspace, size_t workspace_bytes,
+                            void* hip_stream);
+
+/*
+ * Gradients of dmuon_gated_ffn_forward from dh and its inputs: dx, and the
+ * weights' gradients as the Muon step takes them.  Both projections are formed
+ * again; their gradients are rounded to dtype once, as operands of the products
+ * that give the results, whose sums are float32 in a fixed order.
+ *
+ * dw_gate, dw_up : device, hidden x dim, contiguous.
+ */
+int dmuon_gated_ffn_backward_workspace_bytes(const dmuon_gated_ffn_shape* shape, int is_aligned, size_t* bytes_out);
+int dmuon_gated_ffn_backward(const dmuon_gated_ffn_shape* shape, const void* dh, int64_t dh_stride, const void* x,
+                             int64_t x_stride, const void* w_gate, const void* w_up, void* dx, int64_t dx_stride,
+                             void* dw_gate, void* dw_up, void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
  * The plan of a call as text: routes (numel < DMUON_MIN_NS_NUMEL goes
  * elementwise when muon_step is nonzero), shape groups with their transposed
  * count, tiles and K slices, launches per Newton-Schulz step, algorithmic

@@ -47,5 +47,9 @@ from .block import (  # noqa: F401
     block_norm,
     block_norm_grad,
     block_norm_grad_workspace_bytes,
+    gated_ffn,
+    gated_ffn_grad,
+    gated_ffn_grad_workspace_bytes,
+    gated_ffn_workspace_bytes,
 )
 from ._lib import DmuonError, load  # noqa: F401

@@ -43,6 +43,8 @@ DMUON_MAX_HEAD_DIM = 512
 DMUON_MAX_HEADS = 1024
 DMUON_MAX_TEACHER_K = 1024
 DMUON_MAX_ATTENTION_DIM = 256
+DMUON_ACT_SILU = 0
+DMUON_ACT_GELU = 1
 DMUON_EMBED_DENSE = 0
 DMUON_EMBED_ADD = 1
 DMUON_EMBED_ROWS = 2
@@ -117,6 +119,17 @@ class AttentionShape(ctypes.Structure):
     ]
 
 
+class GatedFfnShape(ctypes.Structure):
+    """dmuon_gated_ffn_shape."""
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("dim", ctypes.c_int64),
+        ("hidden", ctypes.c_int64),
+        ("activation", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+    ]
+
+
 _P = ctypes.c_void_p
 _PP = ctypes.POINTER(ctypes.c_void_p)
 _I64P = ctypes.POINTER(ctypes.c_int64)
@@ -127,6 +140,7 @@ _I, _I64, _F, _SZ = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_
 _QKP = ctypes.POINTER(QkShape)
 _BNP = ctypes.POINTER(BlockNormShape)
 _ATP = ctypes.POINTER(AttentionShape)
+_FFP = ctypes.POINTER(GatedFfnShape)
 
 # name -> (restype, argtypes); mirrors include/dmuon.h
 SIGNATURES = {
@@ -176,6 +190,10 @@ SIGNATURES = {
     "dmuon_attention_backward_workspace_bytes": (_I, [_ATP, _SZP]),
     "dmuon_attention_backward": (_I, [_ATP, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P,
                                       _I64, _P, _I64, _P, _SZ, _P]),
+    "dmuon_gated_ffn_workspace_bytes": (_I, [_FFP, _I, _SZP]),
+    "dmuon_gated_ffn_forward": (_I, [_FFP, _P, _I64, _P, _P, _P, _I64, _P, _SZ, _P]),
+    "dmuon_gated_ffn_backward_workspace_bytes": (_I, [_FFP, _I, _SZP]),
+    "dmuon_gated_ffn_backward": (_I, [_FFP, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P, _P, _SZ, _P]),
     "dmuon_plan_summary": (ctypes.c_int, [ctypes.c_int, _I64P, _I64P, ctypes.c_int, _CFGP, ctypes.c_int, ctypes.c_int,
                                           ctypes.c_char_p, ctypes.c_size_t, _SZP]),
     "dmuon_status_string": (ctypes.c_char_p, [ctypes.c_int]),

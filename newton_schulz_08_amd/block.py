@@ -1,5 +1,5 @@
 """Python binding of the operators between a decoder block's projections: norms
-around the block, attention over packed sequences.
+around the block, attention over packed sequences, gated feed-forward.
 
 Everything that ops.py says of its calls (allocation, devices, streams, graphs,
 autograd) holds here too.
@@ -13,6 +13,8 @@ import torch
 from . import _lib
 from .api import _alloc, dtype_code
 from .ops import _heads, _query, _rows, _run, _tensor, _workspace
+
+_ACTIVATIONS = {"silu": _lib.DMUON_ACT_SILU, "gelu": _lib.DMUON_ACT_GELU}
 
 
 def _row(t, name: str, like: Optional[torch.Tensor] = None) -> Tuple[int, int]:
@@ -184,3 +186,80 @@ def attention_grad(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
 def attention_grad_workspace_bytes(q_tokens: int, q_heads: int) -> int:
     return _query("dmuon_attention_backward_workspace_bytes",
                   _lib.AttentionShape(q_tokens, 0, 1, q_heads, q_heads, 1, scale=1.0))
+
+
+# ---------------------------------------------------------------- gated feed-forward
+def _ffn_args(x, w_gate, w_up, activation):
+    """(device index, dmuon_gated_ffn_shape, [x, stride, w_gate, w_up], whether they are aligned)."""
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be 'silu' or 'gelu', got {activation!r}")
+    head = [*_row(x, "x")]
+    dev, (n, dim) = x.get_device(), x.shape
+    head.append(_tensor(w_gate, "w_gate", dev, x.dtype))
+    if w_gate.dim() != 2 or w_gate.shape[1] != dim:
+        raise ValueError(f"w_gate has shape {tuple(w_gate.shape)}, expected (hidden, {dim})")
+    head.append(_tensor(w_up, "w_up", dev, x.dtype, w_gate.shape))
+    pitch = head[1] * x.element_size() if n > 1 else 0
+    fits = not (head[0] | head[2] | head[3] | pitch) % 16 and pitch <= 1 << 23
+    return dev, _lib.GatedFfnShape(n, dim, w_gate.shape[0], _ACTIVATIONS[activation], dtype_code(x.dtype)), head, fits
+
+
+def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, activation: str = "silu", *,
+              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """dmuon_gated_ffn_forward: act(x w_gate^T) * (x w_up^T), (tokens, hidden).
+
+    x (tokens, dim), rows contiguous; w_gate, w_up (hidden, dim), all of one
+    type; activation "silu" or "gelu" (its tanh form).  Outside autograd: the
+    gradients are gated_ffn_grad's."""
+    dev, s, head, fits = _ffn_args(x, w_gate, w_up, activation)
+    if out is None:
+        new, shape = x.new_empty, (x.shape[0], w_gate.shape[0])
+        out = new(shape) if stream is None else _alloc(stream, new, shape)
+        at = out.data_ptr(), shape[1]
+    else:
+        at = _row(out, "out")
+        if out.dtype != x.dtype or out.get_device() != dev or out.shape != (x.shape[0], w_gate.shape[0]):
+            raise ValueError(f"out is {out.dtype} {tuple(out.shape)} on {out.device}, expected {x.dtype} "
+                             f"{(x.shape[0], w_gate.shape[0])} on {x.device}")
+    _ws, ptr, nbytes = _workspace(workspace, _query("dmuon_gated_ffn_workspace_bytes", s, fits), dev, stream)
+    _run("dmuon_gated_ffn_forward", dev, stream, s, *head, *at, ptr, nbytes)
+    return out
+
+
+def gated_ffn_workspace_bytes(tokens: int, dim: int, hidden: int, dtype: torch.dtype, aligned: bool = True) -> int:
+    """aligned: x and the weights begin at multiples of 16 bytes, and x's rows
+    are a multiple of 16 bytes, at most 8 MiB, apart."""
+    return _query("dmuon_gated_ffn_workspace_bytes", _lib.GatedFfnShape(tokens, dim, hidden, 0, dtype_code(dtype)), aligned)
+
+
+def gated_ffn_grad(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                   activation: str = "silu", *, dx: Optional[torch.Tensor] = None,
+                   dw_gate: Optional[torch.Tensor] = None, dw_up: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """dmuon_gated_ffn_backward: (dx, dw_gate, dw_up) from the gradient of
+    gated_ffn's result and its inputs; the weights' gradients have the weights'
+    type and shape, as muon_step takes them."""
+    dev, s, head, fits = _ffn_args(x, w_gate, w_up, activation)
+    first = _row(dh, "dh")
+    if dh.dtype != x.dtype or dh.get_device() != dev or dh.shape != (x.shape[0], w_gate.shape[0]):
+        raise ValueError(f"dh is {dh.dtype} {tuple(dh.shape)} on {dh.device}, expected {x.dtype} "
+                         f"{(x.shape[0], w_gate.shape[0])} on {x.device}")
+    dx, *dxo = _out(dx, "dx", x, stream)
+    grads = []
+    for dw, w, name in ((dw_gate, w_gate, "dw_gate"), (dw_up, w_up, "dw_up")):
+        if dw is None:
+            dw = torch.empty_like(w) if stream is None else _alloc(stream, torch.empty_like, w)
+        else:
+            _tensor(dw, name, dev, w.dtype, w.shape)
+        grads.append(dw)
+    _ws, ptr, nbytes = _workspace(workspace, _query("dmuon_gated_ffn_backward_workspace_bytes", s, fits), dev, stream)
+    _run("dmuon_gated_ffn_backward", dev, stream, s, *first, *head, *dxo, *[t.data_ptr() for t in grads], ptr, nbytes)
+    return dx, grads[0], grads[1]
+
+
+def gated_ffn_grad_workspace_bytes(tokens: int, dim: int, hidden: int, dtype: torch.dtype, aligned: bool = True) -> int:
+    """aligned: as in gated_ffn_workspace_bytes."""
+    return _query("dmuon_gated_ffn_backward_workspace_bytes",
+                  _lib.GatedFfnShape(tokens, dim, hidden, 0, dtype_code(dtype)), aligned)

@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["kernels_elementwise.hip", "kernels_mfma.hip", "kernels_clip.hip", "kernels_adamw.hip",
            "kernels_embedding.hip", "kernels_adamw_rows.hip", "kernels_distill.hip", "kernels_qknorm.hip",
            "kernels_blocknorm.hip", "kernels_attention.hip", "kernels_attention_grad.hip",
-           "api_util.cpp", "dmuon_api.cpp", "dmuon_ops_api.cpp", "dmuon_block_api.cpp"]
+           "kernels_ffn.hip", "api_util.cpp", "dmuon_api.cpp", "dmuon_ops_api.cpp", "dmuon_block_api.cpp"]
 ARCH = "gfx950"
 
 COMMON_FLAGS = [

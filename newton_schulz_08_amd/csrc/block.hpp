@@ -71,4 +71,37 @@ inline int64_t attn_slots(int64_t rows, int64_t sequences) { return rows / kAttn
 // Head sizes that have kernels; a smaller head is padded with zeros.
 inline int attn_padded(int dim) { return dim <= 64 ? 64 : dim <= 96 ? 96 : dim <= 128 ? 128 : dim <= 192 ? 192 : 256; }
 
+// ---------------------------------------------------------------- gated feed-forward
+enum Activation : int { kSilu = 0, kGelu = 1 };
+// What a launch of the products computes.
+enum FfnMode : int {
+  kFfnOut = 0,    // h = act(x Wg^T) * (x Wu^T)
+  kFfnMid = 1,    // both projections again; their gradients from dh
+  kFfnDx = 2,     // dx = dg Wg + du Wu
+  kFfnDw = 3,     // dWg = dg^T x, dWu = du^T x
+};
+struct FfnArgs {
+  const void* x;           // tokens x dim, xs apart
+  const void* wg;          // hidden x dim, ws apart
+  const void* wu;
+  const void* dh;          // backward: tokens x hidden
+  void* out;               // forward: h; backward: dx
+  void* dwg;               // backward: hidden x dim
+  void* dwu;
+  void* mid;               // backward: mid_rows x 2 hp, the projections' gradients side by side
+  int64_t xs, ws, dhs, outs;
+  int64_t n, mid_rows;     // tokens; rounded up to whole contraction stages
+  int dim, kdim;           // kdim: dim, or for bf16 rounded up to whole stages (zeros)
+  int hidden, hp;          // hp: hidden rounded up to whole stages
+  int act;
+  int vec;                 // operands' and results' runs of 16 bytes are aligned
+};
+constexpr int kFfnStage = 64;      // contraction steps of a bf16 stage
+constexpr int kFfnFewTokens = 64;  // most tokens that the forward pass takes without tiles
+hipError_t launch_ffn_few(int dt, const FfnArgs& a, hipStream_t stream);
+hipError_t launch_ffn(int dt, int mode, const FfnArgs& a, hipStream_t stream);
+// Copies rows of `width` elements to rows of `padded`, zeros behind them.
+hipError_t launch_ffn_pad(int dt, const void* src, int64_t stride, void* dst, int64_t rows, int width, int padded,
+                          hipStream_t stream);
+
 }  // namespace dmuon

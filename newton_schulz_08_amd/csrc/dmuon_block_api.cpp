@@ -145,6 +145,74 @@ void fill_attn(const dmuon_attention_shape& s, AttnArgs* a) {
   a->slots = static_cast<int>(attn_q_slots(s));
 }
 
+// ---------------------------------------------------------------- gated feed-forward
+int check_ffn(const dmuon_gated_ffn_shape* s) {
+  if (!s) return invalid("shape is NULL");
+  DMUON_TRY(check_float(s->dtype, "dtype"));
+  DMUON_TRY(check_range(s->tokens, 0, DMUON_MAX_TOKENS, "tokens"));
+  DMUON_TRY(check_range(s->dim, 1, DMUON_MAX_DIM, "dim"));
+  DMUON_TRY(check_range(s->hidden, 1, DMUON_MAX_DIM, "hidden"));
+  return check_range(s->activation, DMUON_ACT_SILU, DMUON_ACT_GELU, "activation");
+}
+
+int64_t whole_stages(int64_t v) { return (v + kFfnStage - 1) / kFfnStage * kFfnStage; }
+
+// The projections' gradients (backward), and padded copies of the operands.
+struct FfnLayout { size_t off_mid, off_x, off_g, off_u, total; int64_t mid_rows, kdim, hp; bool copies; };
+FfnLayout ffn_layout(const dmuon_gated_ffn_shape& s, bool back, bool in_place) {
+  FfnLayout l{};
+  const int64_t es = size_of(s.dtype);
+  l.kdim = s.dtype == DMUON_BF16 ? whole_stages(s.dim) : s.dim;
+  l.hp = whole_stages(s.hidden);
+  l.mid_rows = whole_stages(s.tokens);
+  if (back) l.total = align_up(static_cast<size_t>(l.mid_rows * 2 * l.hp * es));
+  l.copies = s.dtype == DMUON_BF16 && !(in_place && s.dim % kFfnStage == 0) && (back || s.tokens > kFfnFewTokens);
+  if (l.copies) {
+    l.off_x = l.total;
+    l.off_g = l.off_x + align_up(static_cast<size_t>(s.tokens * l.kdim * es));
+    l.off_u = l.off_g + align_up(static_cast<size_t>(s.hidden * l.kdim * es));
+    l.total = l.off_u + align_up(static_cast<size_t>(s.hidden * l.kdim * es));
+  }
+  return l;
+}
+
+bool ffn_vec(std::initializer_list<const Buf*> bufs) {
+  for (const Buf* b : bufs)
+    if (!b->empty() && (!aligned(b->p, 16) || (b->rows > 1 && b->pitch % 16))) return false;
+  return true;
+}
+// The bf16 tiles read the operands in place when their rows are whole stages at
+// multiples of 16 bytes, and 256 of them lie within 32 bits of offset.
+bool ffn_in_place(const Buf& x, const Buf& wg, const Buf& wu) {
+  return ffn_vec({&x, &wg, &wu}) && (x.rows <= 1 || x.pitch <= (int64_t{1} << 23));
+}
+
+// Sets the operands of the tile kernels, behind copies where they cannot be read in place.
+hipError_t ffn_operands(const dmuon_gated_ffn_shape& s, const FfnLayout& l, void* workspace, FfnArgs* a, hipStream_t stream) {
+  if (!l.copies) return hipSuccess;
+  char* ws = static_cast<char*>(workspace);
+  const int dim = static_cast<int>(s.dim);
+  hipError_t e = launch_ffn_pad(s.dtype, a->x, a->xs, ws + l.off_x, s.tokens, dim, a->kdim, stream);
+  if (e == hipSuccess) e = launch_ffn_pad(s.dtype, a->wg, s.dim, ws + l.off_g, s.hidden, dim, a->kdim, stream);
+  if (e == hipSuccess) e = launch_ffn_pad(s.dtype, a->wu, s.dim, ws + l.off_u, s.hidden, dim, a->kdim, stream);
+  a->x = ws + l.off_x;
+  a->wg = ws + l.off_g;
+  a->wu = ws + l.off_u;
+  a->xs = a->ws = l.kdim;
+  return e;
+}
+
+void fill_ffn(const dmuon_gated_ffn_shape& s, const FfnLayout& l, FfnArgs* a) {
+  a->n = s.tokens;
+  a->mid_rows = l.mid_rows;
+  a->dim = static_cast<int>(s.dim);
+  a->hidden = static_cast<int>(s.hidden);
+  a->hp = static_cast<int>(l.hp);
+  a->act = s.activation;
+  a->kdim = static_cast<int>(l.kdim);
+  a->ws = s.dim;
+}
+
 }  // namespace
 }  // namespace dmuon
 
@@ -387,6 +455,119 @@ int dmuon_attention_backward(const dmuon_attention_shape* shape, const void* dou
     return launched("attention gradient", kKAttentionGrad, 10.0 * qe * (static_cast<double>(s.k_tokens) / s.sequences),
                     4.0 * (qe + ke) * size_of(s.dtype), hip_stream, capturing,
                     [&] { return launch_attention_grad(s.dtype, a, k_slots, static_cast<hipStream_t>(hip_stream)); });
+  });
+}
+
+int dmuon_gated_ffn_workspace_bytes(const dmuon_gated_ffn_shape* shape, int is_aligned, size_t* bytes_out) {
+  return guarded([&]() -> int {
+    if (!bytes_out) return invalid("bytes_out is NULL");
+    DMUON_TRY(check_ffn(shape));
+    *bytes_out = ffn_layout(*shape, false, is_aligned != 0).total;
+    return DMUON_OK;
+  });
+}
+
+int dmuon_gated_ffn_forward(const dmuon_gated_ffn_shape* shape, const void* x, int64_t x_stride, const void* w_gate,
+                            const void* w_up, void* h, int64_t h_stride, void* workspace, size_t workspace_bytes,
+                            void* hip_stream) {
+  return guarded([&]() -> int {
+    DMUON_TRY(check_ffn(shape));
+    const dmuon_gated_ffn_shape& s = *shape;
+    const int64_t es = size_of(s.dtype), wbytes = s.tokens ? s.hidden * s.dim * es : 0;
+    Buf b[5];
+    DMUON_TRY(row_buf("x", x, s.tokens, s.dim, x_stride, s.dtype, false, &b[0]));
+    DMUON_TRY(row_buf("h", h, s.tokens, s.hidden, h_stride, s.dtype, true, &b[1]));
+    b[2] = flat("w_gate", w_gate, wbytes, es, false);
+    b[3] = flat("w_up", w_up, wbytes, es, false);
+    const Buf wg{"w_gate", w_gate, s.hidden, s.dim * es, s.dim * es, es, false};
+    const Buf wu{"w_up", w_up, s.hidden, s.dim * es, s.dim * es, es, false};
+    const FfnLayout l = ffn_layout(s, false, ffn_in_place(b[0], wg, wu));
+    DMUON_TRY(check_workspace(workspace, workspace_bytes, l.total));
+    b[4] = flat("workspace", workspace, static_cast<int64_t>(l.total), 1, true);
+    DMUON_TRY(check_bufs(b, 5));
+    bool capturing = false;
+    DMUON_TRY(check_device(hip_stream, &capturing));
+    if (s.tokens == 0) return DMUON_OK;
+    FfnArgs a{};
+    fill_ffn(s, l, &a);
+    a.x = x;
+    a.xs = x_stride;
+    a.wg = w_gate;
+    a.wu = w_up;
+    a.out = h;
+    a.outs = h_stride;
+    a.vec = ffn_vec({&b[0], &b[1], &wg, &wu});
+    const double flops = 4.0 * s.tokens * s.dim * s.hidden;
+    const double bytes = static_cast<double>(es) * (s.tokens * (s.dim + s.hidden) + 2 * s.hidden * s.dim);
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    return launched("gated feed-forward", kKFfn, flops, bytes, hip_stream, capturing, [&] {
+      if (s.tokens <= kFfnFewTokens) return launch_ffn_few(s.dtype, a, stream);
+      const hipError_t e = ffn_operands(s, l, workspace, &a, stream);
+      return e != hipSuccess ? e : launch_ffn(s.dtype, kFfnOut, a, stream);
+    });
+  });
+}
+
+int dmuon_gated_ffn_backward_workspace_bytes(const dmuon_gated_ffn_shape* shape, int is_aligned, size_t* bytes_out) {
+  return guarded([&]() -> int {
+    if (!bytes_out) return invalid("bytes_out is NULL");
+    DMUON_TRY(check_ffn(shape));
+    *bytes_out = ffn_layout(*shape, true, is_aligned != 0).total;
+    return DMUON_OK;
+  });
+}
+
+int dmuon_gated_ffn_backward(const dmuon_gated_ffn_shape* shape, const void* dh, int64_t dh_stride, const void* x,
+                             int64_t x_stride, const void* w_gate, const void* w_up, void* dx, int64_t dx_stride,
+                             void* dw_gate, void* dw_up, void* workspace, size_t workspace_bytes, void* hip_stream) {
+  return guarded([&]() -> int {
+    DMUON_TRY(check_ffn(shape));
+    const dmuon_gated_ffn_shape& s = *shape;
+    const int64_t es = size_of(s.dtype), wbytes = s.hidden * s.dim * es;
+    Buf b[8];
+    DMUON_TRY(row_buf("dh", dh, s.tokens, s.hidden, dh_stride, s.dtype, false, &b[0]));
+    DMUON_TRY(row_buf("x", x, s.tokens, s.dim, x_stride, s.dtype, false, &b[1]));
+    DMUON_TRY(row_buf("dx", dx, s.tokens, s.dim, dx_stride, s.dtype, true, &b[2]));
+    b[3] = flat("w_gate", w_gate, s.tokens ? wbytes : 0, es, false);
+    b[4] = flat("w_up", w_up, s.tokens ? wbytes : 0, es, false);
+    b[5] = flat("dw_gate", dw_gate, wbytes, es, true);
+    b[6] = flat("dw_up", dw_up, wbytes, es, true);
+    const Buf wg{"w_gate", w_gate, s.hidden, s.dim * es, s.dim * es, es, false};
+    const Buf wu{"w_up", w_up, s.hidden, s.dim * es, s.dim * es, es, false};
+    const FfnLayout l = ffn_layout(s, true, ffn_in_place(b[1], wg, wu));
+    DMUON_TRY(check_workspace(workspace, workspace_bytes, l.total));
+    b[7] = flat("workspace", workspace, static_cast<int64_t>(l.total), 1, true);
+    DMUON_TRY(check_bufs(b, 8));
+    bool capturing = false;
+    DMUON_TRY(check_device(hip_stream, &capturing));
+    const Buf dwg{"dw_gate", dw_gate, s.hidden, s.dim * es, s.dim * es, es, true};
+    const Buf dwu{"dw_up", dw_up, s.hidden, s.dim * es, s.dim * es, es, true};
+    FfnArgs a{};
+    fill_ffn(s, l, &a);
+    a.x = x;
+    a.xs = x_stride;
+    a.wg = w_gate;
+    a.wu = w_up;
+    a.dh = dh;
+    a.dhs = dh_stride;
+    a.out = dx;
+    a.outs = dx_stride;
+    a.dwg = dw_gate;
+    a.dwu = dw_up;
+    a.mid = static_cast<char*>(workspace) + l.off_mid;
+    a.vec = ffn_vec({&b[0], &b[1], &b[2], &wg, &wu, &dwg, &dwu});
+    const double flops = 12.0 * s.tokens * s.dim * s.hidden;
+    const double bytes = static_cast<double>(es) * (s.tokens * (2 * s.dim + s.hidden) + 4 * s.hidden * s.dim);
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    return launched("gated feed-forward gradient", kKFfnGrad, flops, bytes, hip_stream, capturing, [&] {
+      hipError_t e = hipSuccess;
+      if (s.tokens > 0) {
+        e = ffn_operands(s, l, workspace, &a, stream);
+        if (e == hipSuccess) e = launch_ffn(s.dtype, kFfnMid, a, stream);
+        if (e == hipSuccess) e = launch_ffn(s.dtype, kFfnDx, a, stream);
+      }
+      return e != hipSuccess ? e : launch_ffn(s.dtype, kFfnDw, a, stream);
+    });
   });
 }
 

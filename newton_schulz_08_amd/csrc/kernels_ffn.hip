@@ -1,0 +1,690 @@
+// The gated feed-forward product and its gradients, on gfx950 (MFMA-bound for
+// batches, HBM-bound for few tokens).
+//
+//   g = x Wg^T,  u = x Wu^T,  h = act(g) u                     (forward)
+//   dg = dh u act'(g),  du = dh act(g)                         (backward)
+//   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
+//
+// act is silu, g s(g), or gelu in its tanh form, which is g s(2 y) with
+// y = sqrt(2 / pi) (g + 0.044715 g^3); s is the logistic function.  The backward
+// pass forms both projections again (nothing but the inputs is kept between the
+// passes), stores dg and du side by side, rounded to the inputs' type for the
+// products that read them, and runs those two products.
+//
+// bf16 batches: 256 x 256 tiles on v_mfma_f32_16x16x32_bf16, eight waves of
+// 128 x 64, stages of 64 contraction steps double-buffered in LDS (2 x 64 KB),
+// filled straight from memory while the stage before is multiplied, in the
+// manner of the Newton-Schulz products.  The forward's Q panel takes 32 rows
+// of Wg and 32 of Wu by turns, so a lane holds g and u of the same elements and
+// the epilogue needs no exchange.  An operand lies with its contraction steps
+// along a row, or (Q of dx, both of dW) with one step a row, and is then read
+// from LDS through transposing reads: no matrix is transposed in memory.
+//
+// fp32: 128 x 128 tiles on v_mfma_f32_32x32x2_f32, loaded through registers
+// with every bound checked.
+//
+// Few tokens: the weights are read once, straight into fragments, by waves
+// that split the contraction; at most 64 tokens a wave.
+#include <hip/hip_runtime.h>
+
+#include "block.hpp"
+
+namespace dmuon {
+namespace ffn {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) char* lds_t;
+typedef __attribute__((address_space(3))) bf16x4* lds_bf16x4_t;
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// act(g) and act'(g).  e = exp(-2 y) is held below 2^126, so that e s(2 y),
+// which is 1 - s(2 y), stays a number.
+__device__ __forceinline__ void activate(int kind, float g, float* a, float* da) {
+  float y2 = g, dy2 = 1.0f;
+  if (kind == kGelu) {
+    constexpr float c = 1.5957691216057308f, k = 0.044715f;   // 2 sqrt(2 / pi)
+    y2 = c * (g + k * g * g * g);
+    dy2 = c * (1.0f + 3.0f * k * g * g);
+  }
+  const float e = __builtin_amdgcn_exp2f(fminf(-y2 * kLog2e, 126.0f));
+  const float s = 1.0f / (1.0f + e);
+  *a = g * s;
+  *da = s + g * dy2 * s * (e * s);
+}
+
+// Four consecutive elements of a row, as far as it reaches.
+template <typename T> __device__ __forceinline__ void load4(const T* row, int c, int cols, int vec, float* v) {
+  if (vec && c + 4 <= cols) {
+    load_n<4>(row + c, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = c + i < cols ? static_cast<float>(gmem(row)[c + i]) : 0.0f;
+  }
+}
+template <typename T> __device__ __forceinline__ void store4(T* row, int c, int cols, int vec, const float* v) {
+  if (vec && c + 4 <= cols) {
+    store_n<4>(row + c, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < cols) gmem(row)[c + i] = static_cast<T>(v[i]);
+  }
+}
+
+// What becomes of four elements of row r: both projections' (kFfnOut, kFfnMid), at
+// columns f .. f + 3 of the hidden width.
+template <int DT, int MODE> __device__ __forceinline__ void finish_gated(const FfnArgs& a, int64_t r, int f, const float* g, const float* u) {
+  using T = typename OpElem<DT>::T;
+  float act[4], dact[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) activate(a.act, g[i], act + i, dact + i);
+  if constexpr (MODE == kFfnOut) {
+    if (r >= a.n) return;
+    float h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = act[i] * u[i];
+    store4(static_cast<T*>(a.out) + r * a.outs, f, a.hidden, a.vec, h);
+  } else {
+    // rows and columns up to whole stages take zeros: they enter sums
+    if (r >= a.mid_rows || f >= a.hp) return;
+    float dh[4] = {}, dg[4], du[4];
+    if (r < a.n) load4(static_cast<const T*>(a.dh) + r * a.dhs, f, a.hidden, a.vec, dh);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = r < a.n && f + i < a.hidden;
+      dg[i] = in ? dh[i] * u[i] * dact[i] : 0.0f;
+      du[i] = in ? dh[i] * act[i] : 0.0f;
+    }
+    T* mid = static_cast<T*>(a.mid) + r * (2 * static_cast<int64_t>(a.hp));
+    store_n<4>(mid + f, dg);
+    store_n<4>(mid + a.hp + f, du);
+  }
+}
+// ... and of one product's (kFfnDx: row r of dx; kFfnDw: row r of the gradient of
+// weight `which`), columns c .. c + 3.
+template <int DT, int MODE> __device__ __forceinline__ void finish_plain(const FfnArgs& a, int which, int64_t r, int c, const float* v) {
+  using T = typename OpElem<DT>::T;
+  if constexpr (MODE == kFfnDx) {
+    if (r < a.n) store4(static_cast<T*>(a.out) + r * a.outs, c, a.dim, a.vec, v);
+  } else {
+    if (r < a.hidden) store4(static_cast<T*>(which ? a.dwu : a.dwg) + r * a.dim, c, a.dim, a.vec, v);
+  }
+}
+
+// Tiles of a launch: rows x cols, and, for dW, both weights one behind the other.
+struct Grid { int rows, cols, all; };
+template <int MODE> __host__ __device__ Grid grid_of(const FfnArgs& a, int tile) {
+  auto up = [&](int64_t v, int t) { return static_cast<int>((v + t - 1) / t); };
+  Grid g{};
+  if (MODE == kFfnOut || MODE == kFfnMid) {
+    g.rows = up(MODE == kFfnMid ? a.mid_rows : a.n, tile);
+    g.cols = up(MODE == kFfnMid ? a.hp : a.hidden, tile / 2);
+  } else if (MODE == kFfnDx) {
+    g.rows = up(a.n, tile);
+    g.cols = up(a.dim, tile);
+  } else {
+    g.rows = 2 * up(a.hidden, tile);
+    g.cols = up(a.dim, tile);
+  }
+  g.all = g.rows * g.cols;
+  return g;
+}
+// Blocks go round-robin over the eight XCDs.  In each round of 256 an XCD takes 32
+// consecutive tiles, a compact patch of the grid (groups of eight tile rows,
+// column by column), whose operand panels its L2 holds.
+__device__ __forceinline__ void tile_of(const Grid& g, int block, int* ti, int* tj) {
+  const int base = g.all >> 8 << 8;
+  int t = block;
+  if (block < base) {
+    t = (block & ~255) + (block & 7) * 32 + ((block >> 3) & 31);
+  } else {
+    const int n = g.all - base, l = block - base, x = l & 7, each = n >> 3, more = n & 7;
+    t = base + x * each + (x < more ? x : more) + (l >> 3);
+  }
+  constexpr int kGroup = 8;
+  const int per = kGroup * g.cols, first = t / per * kGroup, within = t % per;
+  const int h = g.rows - first < kGroup ? g.rows - first : kGroup;
+  *ti = first + within % h;
+  *tj = within / h;
+}
+
+// ---------------------------------------------------------------- bf16 tiles
+constexpr int kTileThreads = 512;
+constexpr int kOperandBytes = 32768, kStageBytes = 65536;
+
+__device__ __forceinline__ uint32_t lds_address(const char* p) {
+  return static_cast<uint32_t>(reinterpret_cast<size_t>((lds_t)p));   // address-space cast
+}
+__device__ __forceinline__ const char* uniform_ptr(const void* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return reinterpret_cast<const char*>((static_cast<uint64_t>(hi) << 32) | lo);
+}
+// 16 bytes from base + voff (per lane) to LDS[dst + 16 lane].  Through asm, so
+// that the compiler does not make every LDS read wait for it; readers wait for
+// vmcnt(0) and a barrier.
+__device__ __forceinline__ void dma16(const char* base, uint32_t voff, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(dst) : "memory");
+}
+
+// One operand's 256 rows (or columns) of a tile.
+//
+// Steps along a row: stage row r (128 bytes: 64 steps) keeps 16-byte chunk c
+// at c ^ (r & 7) ^ ((r >> 3) & 1).  Rows behind the last take the last one's.
+// Steps as rows (TR): stage row k (512 bytes: 256 columns) keeps chunk c at
+// c ^ 4 (k & 3) ^ 2 ((k >> 4) & 1); columns behind the last take the last
+// aligned eight's, steps behind the last the last one's (the other operand
+// holds zeros there).  Both orders keep the reads below in distinct banks.
+template <bool TR> struct Operand {
+  const char* base;     // of the tile's first row, or of the steps' first row at the tile's first column
+  uint32_t off[4];
+  uint32_t pitch;       // bytes
+  int lane, wave;
+  uint32_t col;         // TR: this lane's bytes along a row, loads 0, 2 and 1, 3
+  uint32_t col1;
+
+  // rows: rows that exist from the tile's first on (TR: columns)
+  __device__ __forceinline__ void init(const void* p, uint32_t pitch_bytes, int rows) {
+    base = uniform_ptr(p);
+    pitch = pitch_bytes;
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if constexpr (TR) {
+      const int k = 8 * wave + (lane >> 5), pc = lane & 31, most_ = rows / 8 - 1;   // load u: row k + 2 u
+      auto at = [&](int row) { return static_cast<uint32_t>(min(pc ^ (4 * (row & 3)) ^ (2 * ((row >> 4) & 1)), most_)) * 16; };
+      col = at(k);
+      col1 = at(k + 2);
+      steps(64);
+    } else {
+      const int r = lane >> 3;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int row = wave * 32 + u * 8 + r;
+        off[u] = static_cast<uint32_t>(min(row, rows - 1)) * pitch + (((lane & 7) ^ r ^ (u & 1)) << 4);
+      }
+    }
+  }
+  // TR: a stage of `left` steps (at least one).
+  __device__ __forceinline__ void steps(int left) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      off[u] = static_cast<uint32_t>(min(8 * wave + (lane >> 5) + 2 * u, left - 1)) * pitch + ((u & 1) ? col1 : col);
+  }
+  __device__ __forceinline__ void load(const char* at, uint32_t lds, int u) const {
+    dma16(at, off[u], lds + static_cast<uint32_t>(wave) * 4096 + u * 1024);
+  }
+};
+
+// Fragment reads.  Lane l holds row (column) l & 15 of a block and, of the 32
+// steps of a sub-step, octet k = (0, 2, 1, 3)[l >> 4], the same for both operands.
+template <bool TR> struct Reader {
+  int at;
+  int sw;
+  int lk;
+  __device__ __forceinline__ void init() {
+    const int lane = threadIdx.x & 63, l16 = lane & 15, lq = lane >> 4;
+    lk = ((lq & 1) << 1) | (lq >> 1);
+    if constexpr (TR) {
+      // in each group of 16 lanes, lane 4 t + a points at step t, columns 4 a .. + 3,
+      // and receives column (lane & 15) of four steps
+      const int t = (lane >> 2) & 3;
+      sw = (4 * t) ^ (2 * ((lk >> 1) & 1));
+      at = (8 * lk + t) * 512 + 8 * (lane & 1);
+    } else {
+      sw = (l16 & 7) ^ ((l16 >> 3) & 1);
+      at = l16 * 128;
+    }
+  }
+  __device__ __forceinline__ bf16x8 read(const char* operand, int sub, int block) const {
+    if constexpr (TR) {
+      const int a = threadIdx.x & 3, ch = 2 * block + (a >> 1);
+      const char* p = operand + at + ((ch ^ sw) << 4) + 32 * sub * 512;
+      const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(reinterpret_cast<lds_bf16x4_t>((lds_t)p));
+      const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(reinterpret_cast<lds_bf16x4_t>((lds_t)(p + 4 * 512)));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      return *reinterpret_cast<const bf16x8*>(operand + at + (((4 * sub + lk) ^ sw) << 4) + block * 16 * 128);
+    }
+  }
+};
+
+// acc[mi][ni] of wave (wr, wc): row 16 mi + (l & 15) of its 128, columns
+// 16 ni + 4 (l >> 4) .. + 3 of its 64.  stage(kt) gives a stage's addresses
+// and sets the operands' offsets for it.
+template <bool PT, bool QT, typename Stage>
+__device__ __forceinline__ void product(Operand<PT>& P, Operand<QT>& Q, int nk, char* lds, f32x4 (&acc)[8][4], Stage&& stage) {
+  if (nk <= 0) return;   // no tokens: the sums are empty, and there is nothing to load
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave >> 2, wc = wave & 3;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(lds));
+  Reader<PT> rp;
+  Reader<QT> rq;
+  rp.init();
+  rq.init();
+  bf16x8 fa[2][4], fb[2][4];
+  auto read_p = [&](int b, int sub, int h, int i) { fa[h][i] = rp.read(lds + b * kStageBytes, sub, wr * 8 + 4 * h + i); };
+  auto read_q = [&](int b, int sub, int i) { fb[sub][i] = rq.read(lds + b * kStageBytes + kOperandBytes, sub, wc * 4 + i); };
+  // A stage is four quarter-steps of 16 MFMAs: (sub-step s, half h of the P
+  // blocks); each reads what the next one needs, one read behind each of its
+  // first MFMAs, and the last spreads the loads of the stage after the next.
+  auto quarter = [&](int s, int h, auto&& rd, int nr, auto&& dma, int nd) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int mi = 4 * h + j / 4, ni = j % 4;
+      acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[s][ni], fa[h][j / 4], acc[mi][ni], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (j < nr) rd(j);
+#pragma unroll
+      for (int i = j * nd / 16; i < (j + 1) * nd / 16; ++i) dma(i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto none = [](int) {};
+  auto fetch = [&](int kt, int i, const char* p, const char* q) {
+    const uint32_t at = lds0 + (kt & 1) * kStageBytes;
+    if (i & 1) Q.load(q, at + kOperandBytes, i >> 1);
+    else P.load(p, at, i >> 1);
+  };
+  const char *p, *q;
+  stage(0, &p, &q);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) fetch(0, i, p, q);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (nk > 1) {
+    stage(1, &p, &q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) fetch(1, i, p, q);
+  }
+  auto first = [&](int b) { return [&, b](int i) { if (i < 4) read_q(b, 0, i); else read_p(b, 0, 0, i - 4); }; };
+#pragma unroll
+  for (int i = 0; i < 8; ++i) first(0)(i);
+  __builtin_amdgcn_sched_barrier(0);
+  for (int kt = 0; kt < nk; ++kt) {
+    const int b = kt & 1;
+    quarter(0, 0, [&](int i) { read_p(b, 0, 1, i); }, 4, none, 0);
+    quarter(0, 1, [&](int i) { if (i < 4) read_q(b, 1, i); else read_p(b, 1, 0, i - 4); }, 8, none, 0);
+    quarter(1, 0, [&](int i) { read_p(b, 1, 1, i); }, 4, none, 0);
+    // stage kt + 1 has landed, and every read of this buffer is done
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (kt + 2 < nk) {
+      stage(kt + 2, &p, &q);
+      quarter(1, 1, first(b ^ 1), 8, [&](int i) { fetch(kt, i, p, q); }, 8);
+    } else {
+      quarter(1, 1, first(b ^ 1), 8, none, 0);   // behind the last stage: read, and not used
+    }
+  }
+}
+
+template <int MODE> __global__ __launch_bounds__(kTileThreads, 2) void ffn_tile_kernel(FfnArgs a) {
+  constexpr bool kPT = MODE == kFfnDw, kQT = MODE == kFfnDx || MODE == kFfnDw;
+  constexpr bool kGated = MODE == kFfnOut || MODE == kFfnMid;
+  __shared__ __attribute__((aligned(16))) char lds[2 * kStageBytes];
+  const Grid grid = grid_of<MODE>(a, 256);
+  int ti, tj;
+  tile_of(grid, blockIdx.x, &ti, &tj);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  f32x4 acc[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
+  const char* x = static_cast<const char*>(a.x);
+  const char* mid = static_cast<const char*>(a.mid);
+  const uint32_t xp = static_cast<uint32_t>(a.xs * 2), wp = static_cast<uint32_t>(a.ws * 2), mp = static_cast<uint32_t>(a.hp) * 4;
+  Operand<kPT> P;
+  Operand<kQT> Q;
+  int which = 0;
+  if constexpr (kGated) {
+    const int64_t r0 = static_cast<int64_t>(ti) * 256;
+    P.init(x + r0 * xp, xp, static_cast<int>(least<int64_t>(a.n - r0, 256)));
+    // this wave's 32 stage rows: 32 of one weight, for columns 32 (wave / 2) .. of the tile's 128
+    const int f0 = tj * 128 + (wave >> 1) * 32;
+    const char* w = static_cast<const char*>((wave & 1) ? a.wu : a.wg);
+    // the offsets count from the wave's own rows: rows() below is written for a tile's 256
+    Q.base = uniform_ptr(w);
+    Q.pitch = wp;
+    Q.lane = lane;
+    Q.wave = wave;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = lane >> 3, row = min(f0 + u * 8 + r, a.hidden - 1) - min(f0, a.hidden - 1);
+      Q.off[u] = static_cast<uint32_t>(row) * wp + (((lane & 7) ^ r ^ (u & 1)) << 4);
+    }
+    Q.base = uniform_ptr(w + static_cast<int64_t>(min(f0, a.hidden - 1)) * wp);
+    product<kPT, kQT>(P, Q, a.kdim / kFfnStage, lds, acc, [&](int kt, const char** p, const char** q) {
+      *p = P.base + kt * (kFfnStage * 2);
+      *q = Q.base + kt * (kFfnStage * 2);
+    });
+  } else if constexpr (MODE == kFfnDx) {
+    const int64_t r0 = static_cast<int64_t>(ti) * 256;
+    P.init(mid + r0 * mp, mp, static_cast<int>(least<int64_t>(a.n - r0, 256)));
+    Q.init(a.wg, wp, a.kdim - tj * 256);
+    const int half = a.hp / kFfnStage;
+    product<kPT, kQT>(P, Q, 2 * half, lds, acc, [&](int kt, const char** p, const char** q) {
+      *p = P.base + kt * (kFfnStage * 2);
+      const int k = (kt < half ? kt : kt - half) * kFfnStage;
+      *q = uniform_ptr(static_cast<const char*>(kt < half ? a.wg : a.wu) + static_cast<int64_t>(k) * wp + tj * 512);
+      if (a.hidden < a.hp) Q.steps(min(a.hidden - k, kFfnStage));
+    });
+  } else {
+    const int per = grid.rows / 2;
+    which = ti >= per;
+    const int f0 = (ti - which * per) * 256;
+    P.init(mid + (static_cast<int64_t>(which) * a.hp + f0) * 2, mp, a.hp - f0);
+    Q.init(x + tj * 512, xp, a.kdim - tj * 256);
+    product<kPT, kQT>(P, Q, static_cast<int>(a.mid_rows / kFfnStage), lds, acc, [&](int kt, const char** p, const char** q) {
+      *p = P.base + static_cast<int64_t>(kt) * kFfnStage * mp;
+      *q = Q.base + static_cast<int64_t>(kt) * kFfnStage * xp;
+      if (a.n < a.mid_rows) Q.steps(static_cast<int>(least<int64_t>(a.n - static_cast<int64_t>(kt) * kFfnStage, kFfnStage)));
+    });
+    ti -= which * per;
+  }
+  const int wr = wave >> 2, wc = wave & 3;
+#pragma unroll
+  for (int mi = 0; mi < 8; ++mi) {
+    const int64_t r = static_cast<int64_t>(ti) * 256 + wr * 128 + 16 * mi + (lane & 15);
+    if constexpr (kGated) {
+#pragma unroll
+      for (int ni = 0; ni < 2; ++ni) {
+        float g[4], u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          g[i] = acc[mi][ni][i];
+          u[i] = acc[mi][ni + 2][i];
+        }
+        finish_gated<kBF16, MODE>(a, r, tj * 128 + wc * 32 + 16 * ni + 4 * (lane >> 4), g, u);
+      }
+    } else {
+#pragma unroll
+      for (int ni = 0; ni < 4; ++ni) {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = acc[mi][ni][i];
+        finish_plain<kBF16, MODE>(a, which, r, tj * 256 + wc * 64 + 16 * ni + 4 * (lane >> 4), v);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- fp32 tiles
+constexpr int kTile32 = 128, kStep32 = 32, kPitch32 = 36;   // floats: 16-byte rows of LDS that start in different banks
+
+// Element (row, k) of an operand: 128 rows from row0, 32 steps from k0, zero outside.
+// TR: the steps are the memory's rows.
+template <bool TR> __device__ __forceinline__ void fill32(float* lds, const float* p, int64_t pitch, int64_t rows, int64_t steps,
+                                                          int64_t row0, int64_t k0, int vec) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int id = u * 256 + threadIdx.x;
+    float v[4] = {};
+    if constexpr (!TR) {
+      const int64_t r = row0 + (id >> 3), k = k0 + (id & 7) * 4;
+      if (r < rows) load4(p + r * pitch, static_cast<int>(k), static_cast<int>(steps), vec, v);
+      *reinterpret_cast<f32x4*>(lds + (id >> 3) * kPitch32 + (id & 7) * 4) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+      const int64_t k = k0 + (id >> 5), r = row0 + (id & 31) * 4;
+      if (k < steps) load4(p + k * pitch, static_cast<int>(r), static_cast<int>(rows), vec, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lds[((id & 31) * 4 + i) * kPitch32 + (id >> 5)] = v[i];
+    }
+  }
+}
+
+template <int MODE> __global__ __launch_bounds__(256) void ffn_tile32_kernel(FfnArgs a) {
+  constexpr bool kGated = MODE == kFfnOut || MODE == kFfnMid;
+  __shared__ __attribute__((aligned(16))) float lp[kTile32 * kPitch32], lq[kTile32 * kPitch32];
+  const Grid grid = grid_of<MODE>(a, kTile32);
+  int ti, tj;
+  tile_of(grid, blockIdx.x, &ti, &tj);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wr = wave >> 1, wc = wave & 1, li = lane & 31, lh = lane >> 5;
+  const float *x = static_cast<const float*>(a.x), *wg = static_cast<const float*>(a.wg), *wu = static_cast<const float*>(a.wu);
+  const float* mid = static_cast<const float*>(a.mid);
+  const int64_t mp = 2 * static_cast<int64_t>(a.hp);
+  int which = 0;
+  int64_t steps;
+  if constexpr (MODE == kFfnDw) {
+    const int per = grid.rows / 2;
+    which = ti >= per;
+    ti -= which * per;
+    steps = a.n;
+  } else if constexpr (MODE == kFfnDx) {
+    steps = 2 * static_cast<int64_t>(a.hp);
+  } else {
+    steps = a.dim;
+  }
+  const int64_t r0 = static_cast<int64_t>(ti) * kTile32;
+  const int c0 = tj * (kGated ? kTile32 / 2 : kTile32);
+  f32x16 acc[2][2] = {};
+  for (int64_t k0 = 0; k0 < steps; k0 += kStep32) {
+    if constexpr (kGated) {
+      fill32<false>(lp, x, a.xs, a.n, a.dim, r0, k0, a.vec);
+      // rows of the tile: 32 of one weight and 32 of the other by turns
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int id = u * 256 + threadIdx.x, row = id >> 3, f = c0 + (row >> 6) * 32 + (row & 31);
+        float v[4] = {};
+        if (f < a.hidden)
+          load4((row & 32 ? wu : wg) + f * a.ws, static_cast<int>(k0) + (id & 7) * 4, a.dim, a.vec, v);
+        *reinterpret_cast<f32x4*>(lq + row * kPitch32 + (id & 7) * 4) = f32x4{v[0], v[1], v[2], v[3]};
+      }
+    } else if constexpr (MODE == kFfnDx) {
+      const bool second = k0 >= a.hp;   // hp holds whole stages
+      fill32<false>(lp, mid, mp, a.n, mp, r0, k0, 1);
+      fill32<true>(lq, second ? wu : wg, a.ws, a.dim, a.hidden, c0, k0 - (second ? a.hp : 0), a.vec);
+    } else {
+      fill32<true>(lp, mid + (which ? a.hp : 0), mp, a.hidden, a.n, r0, k0, 1);
+      fill32<true>(lq, x, a.xs, a.dim, a.n, c0, k0, a.vec);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < kStep32 / 8; ++s) {
+      f32x4 fp[2], fq[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        fp[b] = *reinterpret_cast<const f32x4*>(lp + (wr * 64 + b * 32 + li) * kPitch32 + 8 * s + 4 * lh);
+        fq[b] = *reinterpret_cast<const f32x4*>(lq + (wc * 64 + b * 32 + li) * kPitch32 + 8 * s + 4 * lh);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fq[j][e], fp[i][e], acc[i][j], 0, 0, 0);
+    }
+    __syncthreads();
+  }
+  // lane l: row 32 i + (l & 31) of the wave's 64, columns 32 j + 8 g + 4 (l >> 5) .. + 3
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t r = r0 + wr * 64 + 32 * i + li;
+#pragma unroll
+    for (int g4 = 0; g4 < 4; ++g4) {
+      if constexpr (kGated) {
+        float g[4], u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          g[e] = acc[i][0][4 * g4 + e];
+          u[e] = acc[i][1][4 * g4 + e];
+        }
+        finish_gated<kF32, MODE>(a, r, c0 + wc * 32 + 8 * g4 + 4 * lh, g, u);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g4 + e];
+          finish_plain<kF32, MODE>(a, which, r, c0 + wc * 64 + 32 * j + 8 * g4 + 4 * lh, v);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- few tokens
+constexpr int kFewWaves = 4;
+
+template <int DT> struct Oct;   // eight consecutive steps of a row
+template <> struct Oct<kBF16> { bf16x8 v; };
+template <> struct Oct<kF32> { f32x4 v[2]; };
+
+template <int DT> __device__ __forceinline__ Oct<DT> octet(const void* row, bool any, int k, int dim, int vec) {
+  using T = typename OpElem<DT>::T;
+  const T* p = static_cast<const T*>(row);
+  Oct<DT> o{};
+  if (!any || k >= dim) return o;
+  if (vec && k + 8 <= dim) {
+    if constexpr (DT == kBF16) {
+      o.v = *reinterpret_cast<gptr<const bf16x8>>(gmem(p + k));
+    } else {
+      o.v[0] = *reinterpret_cast<gptr<const f32x4>>(gmem(p + k));
+      o.v[1] = *reinterpret_cast<gptr<const f32x4>>(gmem(p + k + 4));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const T x = k + i < dim ? gmem(p)[k + i] : static_cast<T>(0.0f);
+      if constexpr (DT == kBF16) o.v[i] = x;
+      else o.v[i >> 2][i & 3] = x;
+    }
+  }
+  return o;
+}
+__device__ __forceinline__ f32x4 mma(const Oct<kBF16>& a, const Oct<kBF16>& b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma(const Oct<kF32>& a, const Oct<kF32>& b, f32x4 c) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[i >> 2][i & 3], b.v[i >> 2][i & 3], c, 0, 0, 0);
+  return c;
+}
+
+// 16 rows of both weights a block, up to 16 G tokens; the waves take the steps
+// by turns, 32 at a time, and their sums meet in LDS in the waves' order.
+template <int DT, int G> __global__ __launch_bounds__(64 * kFewWaves) void ffn_few_kernel(FfnArgs a) {
+  using T = typename OpElem<DT>::T;
+  __shared__ float sums[kFewWaves - 1][2 * G][4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, oct = lane >> 4;
+  const int f0 = blockIdx.x * 16, f = f0 + l16;
+  const bool any = f < a.hidden;
+  const T* wg = static_cast<const T*>(a.wg) + static_cast<int64_t>(any ? f : 0) * a.ws;
+  const T* wu = static_cast<const T*>(a.wu) + static_cast<int64_t>(any ? f : 0) * a.ws;
+  f32x4 acc[2][G] = {};
+  constexpr int kUnroll = G == 1 ? 4 : G == 2 ? 2 : 1;   // fragments under way in front of their products
+  for (int k0 = wave * 32 * kUnroll; k0 < a.dim; k0 += 32 * kUnroll * kFewWaves) {
+    Oct<DT> og[kUnroll], ou[kUnroll], ox[kUnroll][G];
+#pragma unroll
+    for (int n = 0; n < kUnroll; ++n) {
+      const int k = k0 + 32 * n + 8 * oct;
+      og[n] = octet<DT>(wg, any, k, a.dim, a.vec);
+      ou[n] = octet<DT>(wu, any, k, a.dim, a.vec);
+#pragma unroll
+      for (int t = 0; t < G; ++t) {
+        const int token = 16 * t + l16;
+        ox[n][t] = octet<DT>(static_cast<const T*>(a.x) + (token < a.n ? token : 0) * a.xs, token < a.n, k, a.dim, a.vec);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kUnroll; ++n)
+#pragma unroll
+      for (int t = 0; t < G; ++t) {
+        acc[0][t] = mma(og[n], ox[n][t], acc[0][t]);
+        acc[1][t] = mma(ou[n], ox[n][t], acc[1][t]);
+      }
+  }
+  if (wave > 0)
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int t = 0; t < G; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums[wave - 1][w * G + t][i][lane] = acc[w][t][i];
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int t = 0; t < G; ++t) {
+    float g[4], u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      g[i] = acc[0][t][i];
+      u[i] = acc[1][t][i];
+#pragma unroll
+      for (int w = 0; w < kFewWaves - 1; ++w) {
+        g[i] += sums[w][t][i][lane];
+        u[i] += sums[w][G + t][i][lane];
+      }
+    }
+    // lane l: token l & 15, rows 4 (l >> 4) .. + 3 of the weights
+    finish_gated<DT, kFfnOut>(a, 16 * t + l16, f0 + 4 * oct, g, u);
+  }
+}
+
+// ---------------------------------------------------------------- padding
+template <int DT> __global__ __launch_bounds__(256) void ffn_pad_kernel(const void* src, int64_t stride, void* dst, int64_t rows,
+                                                                        int width, int padded) {
+  using T = typename OpElem<DT>::T;
+  const int per = padded / 8;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t r = id / per;
+  const int c = static_cast<int>(id % per) * 8;
+  if (r >= rows) return;
+  const T* s = static_cast<const T*>(src) + r * stride;
+  float v[8];
+  if (c + 8 <= width) load_any<8>(s + c, v);
+  else
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < width ? static_cast<float>(gmem(s)[c + i]) : 0.0f;
+  store_n<8>(static_cast<T*>(dst) + r * padded + c, v);
+}
+
+template <int DT, int MODE> hipError_t run(const FfnArgs& a, hipStream_t stream) {
+  if constexpr (DT == kBF16) {
+    const unsigned blocks = static_cast<unsigned>(grid_of<MODE>(a, 256).all);
+    ffn_tile_kernel<MODE><<<dim3(blocks), dim3(kTileThreads), 0, stream>>>(a);
+  } else {
+    const unsigned blocks = static_cast<unsigned>(grid_of<MODE>(a, kTile32).all);
+    ffn_tile32_kernel<MODE><<<dim3(blocks), dim3(256), 0, stream>>>(a);
+  }
+  return hipGetLastError();
+}
+template <int DT> hipError_t run_any(int mode, const FfnArgs& a, hipStream_t stream) {
+  switch (mode) {
+    case kFfnOut: return run<DT, kFfnOut>(a, stream);
+    case kFfnMid: return run<DT, kFfnMid>(a, stream);
+    case kFfnDx: return run<DT, kFfnDx>(a, stream);
+    default: return run<DT, kFfnDw>(a, stream);
+  }
+}
+template <int DT> hipError_t few(const FfnArgs& a, hipStream_t stream) {
+  const dim3 blocks((a.hidden + 15) / 16), threads(64 * kFewWaves);
+  if (a.n <= 16) ffn_few_kernel<DT, 1><<<blocks, threads, 0, stream>>>(a);
+  else if (a.n <= 32) ffn_few_kernel<DT, 2><<<blocks, threads, 0, stream>>>(a);
+  else ffn_few_kernel<DT, 4><<<blocks, threads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace ffn
+
+hipError_t launch_ffn(int dt, int mode, const FfnArgs& a, hipStream_t stream) {
+  return dt == kF32 ? ffn::run_any<kF32>(mode, a, stream) : ffn::run_any<kBF16>(mode, a, stream);
+}
+hipError_t launch_ffn_few(int dt, const FfnArgs& a, hipStream_t stream) {
+  return dt == kF32 ? ffn::few<kF32>(a, stream) : ffn::few<kBF16>(a, stream);
+}
+hipError_t launch_ffn_pad(int dt, const void* src, int64_t stride, void* dst, int64_t rows, int width, int padded,
+                          hipStream_t stream) {
+  const int64_t units = rows * (padded / 8);
+  const dim3 blocks(static_cast<unsigned>((units + 255) / 256));
+  if (dt == kF32) ffn::ffn_pad_kernel<kF32><<<blocks, dim3(256), 0, stream>>>(src, stride, dst, rows, width, padded);
+  else ffn::ffn_pad_kernel<kBF16><<<blocks, dim3(256), 0, stream>>>(src, stride, dst, rows, width, padded);
+  return hipGetLastError();
+}
+
+}  // namespace dmuon
