@@ -305,20 +305,24 @@ __device__ __forceinline__ void product(Operand<PT>& P, Operand<QT>& Q, int nk, 
 #pragma unroll
   for (int i = 0; i < 8; ++i) first(0)(i);
   __builtin_amdgcn_sched_barrier(0);
-  for (int kt = 0; kt < nk; ++kt) {
-    const int b = kt & 1;
+  auto most_of = [&](int b) {
     quarter(0, 0, [&](int i) { read_p(b, 0, 1, i); }, 4, none, 0);
     quarter(0, 1, [&](int i) { if (i < 4) read_q(b, 1, i); else read_p(b, 1, 0, i - 4); }, 8, none, 0);
     quarter(1, 0, [&](int i) { read_p(b, 1, 1, i); }, 4, none, 0);
-    // stage kt + 1 has landed, and every read of this buffer is done
+    // the next stage has landed, and every read of this buffer is done
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (kt + 2 < nk) {
-      stage(kt + 2, &p, &q);
-      quarter(1, 1, first(b ^ 1), 8, [&](int i) { fetch(kt, i, p, q); }, 8);
-    } else {
-      quarter(1, 1, first(b ^ 1), 8, none, 0);   // behind the last stage: read, and not used
-    }
+  };
+  for (int kt = 0; kt < nk - 2; ++kt) {
+    most_of(kt & 1);
+    stage(kt + 2, &p, &q);
+    quarter(1, 1, first((kt & 1) ^ 1), 8, [&](int i) { fetch(kt, i, p, q); }, 8);
+  }
+  // the last two stages (or the only one); behind the last the other buffer is read and not used
+#pragma unroll 1
+  for (int kt = nk > 1 ? nk - 2 : 0; kt < nk; ++kt) {
+    most_of(kt & 1);
+    quarter(1, 1, first((kt & 1) ^ 1), 8, none, 0);
   }
 }
 
