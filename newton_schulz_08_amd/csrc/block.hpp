@@ -23,8 +23,9 @@ struct BlockNormArgs {
   int64_t xs, hs, dxs, dys, xos, ys;   // elements between rows
   int64_t rows;
   int dim, post_norm, w_bf16;
+  int in_place;            // x_out is x (backward: dx_out)
   float eps, scale, offset;
-  float* part;             // backward: blocks x 3 x dim
+  float* part;             // backward: blocks x 2 x dim
   float* stats;            // backward, wide rows: rows x 3, the reciprocal lengths of x and h, and mean(dy g_pre xh)
   int stats_only;          // set by the launch: a pass over wide rows that only fills `stats`
   int64_t col_rows;        // backward, wide rows: rows of a block of the pass over columns
@@ -34,7 +35,7 @@ hipError_t launch_block_norm(int dt, int branch_dt, const BlockNormArgs& a, hipS
 hipError_t launch_block_norm_grad(int dt, int branch_dt, const BlockNormArgs& a, hipStream_t stream);
 constexpr int kBnMaxFused = 8192;   // widest row whose column sums stay in registers beside the row
 // Rows that a block of the backward pass works on at once.
-inline int bn_rows_at_once(int64_t dim) { return dim <= 1024 ? 4 : 1; }
+inline int bn_rows_at_once(int64_t dim) { return dim <= 512 ? 4 : 1; }
 
 // ---------------------------------------------------------------- attention over packed sequences
 constexpr int kAttnMaxDim = 256;
@@ -95,7 +96,12 @@ struct FfnArgs {
   int hidden, hp;          // hp: hidden rounded up to whole stages
   int act;
   int vec;                 // operands' and results' runs of 16 bytes are aligned
+  int dx_slices, dw_slices;   // parts of those products' contractions
+  int slices;              // set by the launch: its own
+  float* part;             // slices x rows x dim rounded up to four: their sums
 };
+// Sets both slices, from the sizes alone.
+void ffn_slices(int dt, FfnArgs* a);
 constexpr int kFfnStage = 64;      // contraction steps of a bf16 stage
 constexpr int kFfnFewTokens = 64;  // most tokens that the forward pass takes without tiles
 hipError_t launch_ffn_few(int dt, const FfnArgs& a, hipStream_t stream);

@@ -40,22 +40,24 @@ int check_bn(const dmuon_block_norm_shape* s) {
   return DMUON_OK;
 }
 
-// Blocks of the backward pass, each leaving one row of sums: three a CU, and
-// no more than there are runs of rows.  Wide rows: blocks of the pass over columns.
+// Blocks of the backward pass, each leaving one row of sums: as many as are at
+// work at once, and, since a row of sums is moved twice, four runs of rows each
+// where that leaves a block a CU.  Wide rows: blocks of the pass over columns.
 int bn_grad_blocks(const dmuon_block_norm_shape& s) {
   if (s.dim > kBnMaxFused) {
     const int64_t per = std::max<int64_t>(64, (s.rows + 4095) / 4096);
     return static_cast<int>((s.rows + per - 1) / per);
   }
-  const int64_t once = bn_rows_at_once(s.dim);
-  return static_cast<int>(std::min<int64_t>((s.rows + once - 1) / once, 768));
+  const int64_t once = bn_rows_at_once(s.dim), most = s.dim <= 512 ? 1024 : s.dim <= 1024 ? 2048 : s.dim <= 2048 ? 1024 : 512;
+  const int64_t runs = (s.rows + once - 1) / once;
+  return static_cast<int>(std::min<int64_t>(runs, std::min<int64_t>(most, std::max<int64_t>(256, runs / 4))));
 }
 
 struct BnLayout { size_t part, total; };
 BnLayout bn_layout(const dmuon_block_norm_shape& s) {
   BnLayout l{};
   l.part = s.dim > kBnMaxFused ? align_up(sizeof(float) * 3 * s.rows) : 0;   // the stats come first
-  l.total = l.part + align_up(sizeof(float) * 3 * s.dim * bn_grad_blocks(s));
+  l.total = l.part + align_up(sizeof(float) * 2 * s.dim * bn_grad_blocks(s));
   return l;
 }
 
@@ -157,21 +159,37 @@ int check_ffn(const dmuon_gated_ffn_shape* s) {
 
 int64_t whole_stages(int64_t v) { return (v + kFfnStage - 1) / kFfnStage * kFfnStage; }
 
-// The projections' gradients (backward), and padded copies of the operands.
-struct FfnLayout { size_t off_mid, off_x, off_g, off_u, total; int64_t mid_rows, kdim, hp; bool copies; };
+void fill_ffn(const dmuon_gated_ffn_shape& s, FfnArgs* a) {
+  a->n = s.tokens;
+  a->mid_rows = whole_stages(s.tokens);
+  a->dim = static_cast<int>(s.dim);
+  a->kdim = static_cast<int>(s.dtype == DMUON_BF16 ? whole_stages(s.dim) : s.dim);
+  a->hidden = static_cast<int>(s.hidden);
+  a->hp = static_cast<int>(whole_stages(s.hidden));
+  a->act = s.activation;
+  a->ws = s.dim;
+}
+
+// The projections' gradients and the slices' sums (backward), and padded copies
+// of the operands.  dx is done with its slices before the weights' begin.
+struct FfnLayout { size_t off_part, off_x, off_g, off_u, total; bool copies; };
 FfnLayout ffn_layout(const dmuon_gated_ffn_shape& s, bool back, bool in_place) {
   FfnLayout l{};
   const int64_t es = size_of(s.dtype);
-  l.kdim = s.dtype == DMUON_BF16 ? whole_stages(s.dim) : s.dim;
-  l.hp = whole_stages(s.hidden);
-  l.mid_rows = whole_stages(s.tokens);
-  if (back) l.total = align_up(static_cast<size_t>(l.mid_rows * 2 * l.hp * es));
+  FfnArgs a{};
+  fill_ffn(s, &a);
+  if (back) {
+    l.off_part = align_up(static_cast<size_t>(a.mid_rows * 2 * a.hp * es));
+    ffn_slices(s.dtype, &a);
+    const int64_t dx = a.dx_slices > 1 ? a.dx_slices * s.tokens : 0, dw = a.dw_slices > 1 ? a.dw_slices * 2 * s.hidden : 0;
+    l.total = l.off_part + align_up(static_cast<size_t>(std::max(dx, dw) * ((s.dim + 3) / 4 * 4) * int64_t{4}));
+  }
   l.copies = s.dtype == DMUON_BF16 && !(in_place && s.dim % kFfnStage == 0) && (back || s.tokens > kFfnFewTokens);
   if (l.copies) {
     l.off_x = l.total;
-    l.off_g = l.off_x + align_up(static_cast<size_t>(s.tokens * l.kdim * es));
-    l.off_u = l.off_g + align_up(static_cast<size_t>(s.hidden * l.kdim * es));
-    l.total = l.off_u + align_up(static_cast<size_t>(s.hidden * l.kdim * es));
+    l.off_g = l.off_x + align_up(static_cast<size_t>(s.tokens * a.kdim * es));
+    l.off_u = l.off_g + align_up(static_cast<size_t>(s.hidden * a.kdim * es));
+    l.total = l.off_u + align_up(static_cast<size_t>(s.hidden * a.kdim * es));
   }
   return l;
 }
@@ -198,19 +216,8 @@ hipError_t ffn_operands(const dmuon_gated_ffn_shape& s, const FfnLayout& l, void
   a->x = ws + l.off_x;
   a->wg = ws + l.off_g;
   a->wu = ws + l.off_u;
-  a->xs = a->ws = l.kdim;
+  a->xs = a->ws = a->kdim;
   return e;
-}
-
-void fill_ffn(const dmuon_gated_ffn_shape& s, const FfnLayout& l, FfnArgs* a) {
-  a->n = s.tokens;
-  a->mid_rows = l.mid_rows;
-  a->dim = static_cast<int>(s.dim);
-  a->hidden = static_cast<int>(s.hidden);
-  a->hp = static_cast<int>(l.hp);
-  a->act = s.activation;
-  a->kdim = static_cast<int>(l.kdim);
-  a->ws = s.dim;
 }
 
 }  // namespace
@@ -246,6 +253,7 @@ int dmuon_block_norm_forward(const dmuon_block_norm_shape* shape, const void* x,
     a.x = x;
     a.h = h;
     a.x_out = x_out;
+    a.in_place = x_out == x;
     a.y = y;
     a.xs = x_stride;
     a.hs = h_stride;
@@ -306,6 +314,7 @@ int dmuon_block_norm_backward(const dmuon_block_norm_shape* shape, const void* d
     a.dx_out = dx_out;
     a.dy = dy;
     a.x_out = dx;
+    a.in_place = dx == dx_out;
     a.y = dh;
     a.xs = x_out_stride;
     a.hs = h_stride;
@@ -489,7 +498,7 @@ int dmuon_gated_ffn_forward(const dmuon_gated_ffn_shape* shape, const void* x, i
     DMUON_TRY(check_device(hip_stream, &capturing));
     if (s.tokens == 0) return DMUON_OK;
     FfnArgs a{};
-    fill_ffn(s, l, &a);
+    fill_ffn(s, &a);
     a.x = x;
     a.xs = x_stride;
     a.wg = w_gate;
@@ -543,7 +552,7 @@ int dmuon_gated_ffn_backward(const dmuon_gated_ffn_shape* shape, const void* dh,
     const Buf dwg{"dw_gate", dw_gate, s.hidden, s.dim * es, s.dim * es, es, true};
     const Buf dwu{"dw_up", dw_up, s.hidden, s.dim * es, s.dim * es, es, true};
     FfnArgs a{};
-    fill_ffn(s, l, &a);
+    fill_ffn(s, &a);
     a.x = x;
     a.xs = x_stride;
     a.wg = w_gate;
@@ -554,7 +563,9 @@ int dmuon_gated_ffn_backward(const dmuon_gated_ffn_shape* shape, const void* dh,
     a.outs = dx_stride;
     a.dwg = dw_gate;
     a.dwu = dw_up;
-    a.mid = static_cast<char*>(workspace) + l.off_mid;
+    a.mid = workspace;
+    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.off_part);
+    ffn_slices(s.dtype, &a);
     a.vec = ffn_vec({&b[0], &b[1], &b[2], &wg, &wu, &dwg, &dwu});
     const double flops = 12.0 * s.tokens * s.dim * s.hidden;
     const double bytes = static_cast<double>(es) * (s.tokens * (2 * s.dim + s.hidden) + 4 * s.hidden * s.dim);

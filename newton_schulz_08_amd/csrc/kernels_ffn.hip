@@ -20,12 +20,15 @@
 // along a row, or (Q of dx, both of dW) with one step a row, and is then read
 // from LDS through transposing reads: no matrix is transposed in memory.
 //
-// fp32: 128 x 128 tiles on v_mfma_f32_32x32x2_f32, loaded through registers
-// with every bound checked.
+// fp32: 64 x 64 tiles on v_mfma_f32_16x16x4_f32, loaded through registers with
+// every bound checked.  Products with few tiles cut their contraction into
+// slices, whose sums another launch adds in order.
 //
 // Few tokens: the weights are read once, straight into fragments, by waves
 // that split the contraction; at most 64 tokens a wave.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "block.hpp"
 
@@ -106,13 +109,19 @@ template <int DT, int MODE> __device__ __forceinline__ void finish_gated(const F
   }
 }
 // ... and of one product's (kFfnDx: row r of dx; kFfnDw: row r of the gradient of
-// weight `which`), columns c .. c + 3.
-template <int DT, int MODE> __device__ __forceinline__ void finish_plain(const FfnArgs& a, int which, int64_t r, int c, const float* v) {
+// weight `which`), columns c .. c + 3; of a slice, the partial sums.
+template <int DT, int MODE>
+__device__ __forceinline__ void finish_plain(const FfnArgs& a, int which, int slice, int64_t r, int c, const float* v) {
   using T = typename OpElem<DT>::T;
-  if constexpr (MODE == kFfnDx) {
-    if (r < a.n) store4(static_cast<T*>(a.out) + r * a.outs, c, a.dim, a.vec, v);
+  const int64_t rows = MODE == kFfnDx ? a.n : a.hidden;
+  if (r >= rows || c >= a.dim) return;
+  if (a.slices > 1) {
+    const int64_t line = MODE == kFfnDx ? slice * rows + r : (2 * static_cast<int64_t>(slice) + which) * rows + r;
+    store_n<4>(a.part + line * ((a.dim + 3) / 4 * 4) + c, v);
+  } else if constexpr (MODE == kFfnDx) {
+    store4(static_cast<T*>(a.out) + r * a.outs, c, a.dim, a.vec, v);
   } else {
-    if (r < a.hidden) store4(static_cast<T*>(which ? a.dwu : a.dwg) + r * a.dim, c, a.dim, a.vec, v);
+    store4(static_cast<T*>(which ? a.dwu : a.dwg) + r * a.dim, c, a.dim, a.vec, v);
   }
 }
 
@@ -133,6 +142,11 @@ template <int MODE> __host__ __device__ Grid grid_of(const FfnArgs& a, int tile)
   }
   g.all = g.rows * g.cols;
   return g;
+}
+// Contraction stages of a launch.
+template <int MODE> __host__ __device__ int64_t stages_of(const FfnArgs& a, int step) {
+  const int64_t steps = MODE == kFfnDx ? 2 * static_cast<int64_t>(a.hp) : MODE == kFfnDw ? a.n : a.kdim;
+  return (steps + step - 1) / step;
 }
 // Blocks go round-robin over the eight XCDs.  In each round of 256 an XCD takes 32
 // consecutive tiles, a compact patch of the grid (groups of eight tile rows,
@@ -332,8 +346,11 @@ template <int MODE> __global__ __launch_bounds__(kTileThreads, 2) void ffn_tile_
   __shared__ __attribute__((aligned(16))) char lds[2 * kStageBytes];
   const Grid grid = grid_of<MODE>(a, 256);
   int ti, tj;
-  tile_of(grid, blockIdx.x, &ti, &tj);
+  tile_of(grid, blockIdx.x / a.slices, &ti, &tj);
+  const int slice = blockIdx.x % a.slices;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t all = stages_of<MODE>(a, kFfnStage);
+  const int first = static_cast<int>(all * slice / a.slices), count = static_cast<int>(all * (slice + 1) / a.slices) - first;
   f32x4 acc[8][4];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -362,7 +379,7 @@ template <int MODE> __global__ __launch_bounds__(kTileThreads, 2) void ffn_tile_
       Q.off[u] = static_cast<uint32_t>(row) * wp + (((lane & 7) ^ r ^ (u & 1)) << 4);
     }
     Q.base = uniform_ptr(w + static_cast<int64_t>(min(f0, a.hidden - 1)) * wp);
-    product<kPT, kQT>(P, Q, a.kdim / kFfnStage, lds, acc, [&](int kt, const char** p, const char** q) {
+    product<kPT, kQT>(P, Q, count, lds, acc, [&](int kt, const char** p, const char** q) {
       *p = P.base + kt * (kFfnStage * 2);
       *q = Q.base + kt * (kFfnStage * 2);
     });
@@ -371,7 +388,8 @@ template <int MODE> __global__ __launch_bounds__(kTileThreads, 2) void ffn_tile_
     P.init(mid + r0 * mp, mp, static_cast<int>(least<int64_t>(a.n - r0, 256)));
     Q.init(a.wg, wp, a.kdim - tj * 256);
     const int half = a.hp / kFfnStage;
-    product<kPT, kQT>(P, Q, 2 * half, lds, acc, [&](int kt, const char** p, const char** q) {
+    product<kPT, kQT>(P, Q, count, lds, acc, [&](int kt, const char** p, const char** q) {
+      kt += first;
       *p = P.base + kt * (kFfnStage * 2);
       const int k = (kt < half ? kt : kt - half) * kFfnStage;
       *q = uniform_ptr(static_cast<const char*>(kt < half ? a.wg : a.wu) + static_cast<int64_t>(k) * wp + tj * 512);
@@ -383,7 +401,8 @@ template <int MODE> __global__ __launch_bounds__(kTileThreads, 2) void ffn_tile_
     const int f0 = (ti - which * per) * 256;
     P.init(mid + (static_cast<int64_t>(which) * a.hp + f0) * 2, mp, a.hp - f0);
     Q.init(x + tj * 512, xp, a.kdim - tj * 256);
-    product<kPT, kQT>(P, Q, static_cast<int>(a.mid_rows / kFfnStage), lds, acc, [&](int kt, const char** p, const char** q) {
+    product<kPT, kQT>(P, Q, count, lds, acc, [&](int kt, const char** p, const char** q) {
+      kt += first;
       *p = P.base + static_cast<int64_t>(kt) * kFfnStage * mp;
       *q = Q.base + static_cast<int64_t>(kt) * kFfnStage * xp;
       if (a.n < a.mid_rows) Q.steps(static_cast<int>(least<int64_t>(a.n - static_cast<int64_t>(kt) * kFfnStage, kFfnStage)));
@@ -411,124 +430,181 @@ template <int MODE> __global__ __launch_bounds__(kTileThreads, 2) void ffn_tile_
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = acc[mi][ni][i];
-        finish_plain<kBF16, MODE>(a, which, r, tj * 256 + wc * 64 + 16 * ni + 4 * (lane >> 4), v);
+        finish_plain<kBF16, MODE>(a, which, slice, r, tj * 256 + wc * 64 + 16 * ni + 4 * (lane >> 4), v);
       }
     }
   }
 }
 
 // ---------------------------------------------------------------- fp32 tiles
-constexpr int kTile32 = 128, kStep32 = 32, kPitch32 = 36;   // floats: 16-byte rows of LDS that start in different banks
+// 64 x 64, four waves of 16 x 64 on v_mfma_f32_16x16x4_f32, stages of 64 steps
+// in two LDS buffers, the next stage's loads under way in registers.  At 32
+// cycles a matrix instruction the LDS reads need a third of its bandwidth, so
+// small tiles cost little and give small matrices enough blocks.
+constexpr int kTile32 = 64, kStep32 = 64;
+constexpr int kPitch32 = 68;   // floats: reads along a row and across rows start in different banks
 
-// Element (row, k) of an operand: 128 rows from row0, 32 steps from k0, zero outside.
-// TR: the steps are the memory's rows.
-template <bool TR> __device__ __forceinline__ void fill32(float* lds, const float* p, int64_t pitch, int64_t rows, int64_t steps,
-                                                          int64_t row0, int64_t k0, int vec) {
+// Part of one operand's stage that a thread moves: 64 rows x 64 steps, zero
+// outside.  In LDS as in memory: rows of steps, or (TR) steps of rows.
+template <bool TR> struct Stage32 {
+  f32x4 v[4];
+  // Whole runs of four: every lane loads, from the last line and run if it has
+  // none of its own, and store() writes zeros for it: a branch around a load
+  // would make the next one wait for it.
+  template <typename Row> __device__ __forceinline__ void load(Row&& row, int64_t lines, int64_t line0, int cols, int col0, int vec) {
+    const int last = static_cast<int>(least<int64_t>(lines - line0, 64)) - 1;
+    const int col = col0 + (threadIdx.x & 15) * 4;
+    if (vec && cols % 4 == 0) {
+      const int at = col < cols ? col : cols - 4;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int id = u * 256 + threadIdx.x;
-    float v[4] = {};
-    if constexpr (!TR) {
-      const int64_t r = row0 + (id >> 3), k = k0 + (id & 7) * 4;
-      if (r < rows) load4(p + r * pitch, static_cast<int>(k), static_cast<int>(steps), vec, v);
-      *reinterpret_cast<f32x4*>(lds + (id >> 3) * kPitch32 + (id & 7) * 4) = f32x4{v[0], v[1], v[2], v[3]};
+      for (int u = 0; u < 4; ++u)
+        v[u] = *reinterpret_cast<gptr<const f32x4>>(gmem(row(min(u * 16 + static_cast<int>(threadIdx.x >> 4), last)) + at));
     } else {
-      const int64_t k = k0 + (id >> 5), r = row0 + (id & 31) * 4;
-      if (k < steps) load4(p + k * pitch, static_cast<int>(r), static_cast<int>(rows), vec, v);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) lds[((id & 31) * 4 + i) * kPitch32 + (id >> 5)] = v[i];
+      for (int u = 0; u < 4; ++u) {
+        const float* p = row(min(u * 16 + static_cast<int>(threadIdx.x >> 4), last));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u][i] = col + i < cols ? gmem(p)[col + i] : 0.0f;
+      }
     }
   }
-}
+  __device__ __forceinline__ void store(float* lds, int64_t lines, int64_t line0, int cols, int col0) const {
+    const int count = static_cast<int>(least<int64_t>(lines - line0, 64));
+    const bool any = col0 + static_cast<int>(threadIdx.x & 15) * 4 < cols;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int line = u * 16 + (threadIdx.x >> 4);
+      *reinterpret_cast<f32x4*>(lds + line * kPitch32 + (threadIdx.x & 15) * 4) = any && line < count ? v[u] : f32x4{};
+    }
+  }
+  // Steps 16 s + 4 oct .. + 3 of row (block, l & 15).
+  __device__ static __forceinline__ f32x4 read(const float* lds, int s, int block) {
+    const int l16 = threadIdx.x & 15, oct = (threadIdx.x >> 4) & 3;
+    if constexpr (!TR) {
+      return *reinterpret_cast<const f32x4*>(lds + (16 * block + l16) * kPitch32 + 16 * s + 4 * oct);
+    } else {
+      f32x4 x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = lds[(16 * s + 4 * oct + e) * kPitch32 + 16 * block + l16];
+      return x;
+    }
+  }
+};
 
-template <int MODE> __global__ __launch_bounds__(256) void ffn_tile32_kernel(FfnArgs a) {
-  constexpr bool kGated = MODE == kFfnOut || MODE == kFfnMid;
-  __shared__ __attribute__((aligned(16))) float lp[kTile32 * kPitch32], lq[kTile32 * kPitch32];
+template <int MODE> __global__ __launch_bounds__(256, 2) void ffn_tile32_kernel(FfnArgs a) {
+  constexpr bool kGated = MODE == kFfnOut || MODE == kFfnMid, kPT = MODE == kFfnDw, kQT = !kGated;
+  __shared__ __attribute__((aligned(16))) float lds[2][2][64 * kPitch32];
   const Grid grid = grid_of<MODE>(a, kTile32);
   int ti, tj;
-  tile_of(grid, blockIdx.x, &ti, &tj);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wr = wave >> 1, wc = wave & 1, li = lane & 31, lh = lane >> 5;
+  tile_of(grid, blockIdx.x / a.slices, &ti, &tj);
+  const int slice = blockIdx.x % a.slices;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float *x = static_cast<const float*>(a.x), *wg = static_cast<const float*>(a.wg), *wu = static_cast<const float*>(a.wu);
   const float* mid = static_cast<const float*>(a.mid);
   const int64_t mp = 2 * static_cast<int64_t>(a.hp);
   int which = 0;
-  int64_t steps;
   if constexpr (MODE == kFfnDw) {
     const int per = grid.rows / 2;
     which = ti >= per;
     ti -= which * per;
-    steps = a.n;
-  } else if constexpr (MODE == kFfnDx) {
-    steps = 2 * static_cast<int64_t>(a.hp);
-  } else {
-    steps = a.dim;
   }
   const int64_t r0 = static_cast<int64_t>(ti) * kTile32;
   const int c0 = tj * (kGated ? kTile32 / 2 : kTile32);
-  f32x16 acc[2][2] = {};
-  for (int64_t k0 = 0; k0 < steps; k0 += kStep32) {
+  const int64_t all = stages_of<MODE>(a, kStep32);
+  const int64_t first = all * slice / a.slices, end = all * (slice + 1) / a.slices;
+  Stage32<kPT> p;
+  Stage32<kQT> q;
+  auto load = [&](int64_t stage) {
+    const int64_t k0 = stage * kStep32;
     if constexpr (kGated) {
-      fill32<false>(lp, x, a.xs, a.n, a.dim, r0, k0, a.vec);
-      // rows of the tile: 32 of one weight and 32 of the other by turns
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int id = u * 256 + threadIdx.x, row = id >> 3, f = c0 + (row >> 6) * 32 + (row & 31);
-        float v[4] = {};
-        if (f < a.hidden)
-          load4((row & 32 ? wu : wg) + f * a.ws, static_cast<int>(k0) + (id & 7) * 4, a.dim, a.vec, v);
-        *reinterpret_cast<f32x4*>(lq + row * kPitch32 + (id & 7) * 4) = f32x4{v[0], v[1], v[2], v[3]};
-      }
+      p.load([&](int line) { return x + (r0 + line) * a.xs; }, a.n, r0, a.dim, static_cast<int>(k0), a.vec);
+      // 32 rows of one weight, then the same of the other
+      q.load([&](int line) { return (line & 32 ? wu : wg) + static_cast<int64_t>(min(c0 + (line & 31), a.hidden - 1)) * a.ws; }, 64, 0,
+             a.dim, static_cast<int>(k0), a.vec);
     } else if constexpr (MODE == kFfnDx) {
       const bool second = k0 >= a.hp;   // hp holds whole stages
-      fill32<false>(lp, mid, mp, a.n, mp, r0, k0, 1);
-      fill32<true>(lq, second ? wu : wg, a.ws, a.dim, a.hidden, c0, k0 - (second ? a.hp : 0), a.vec);
+      const int64_t k = k0 - (second ? a.hp : 0);
+      p.load([&](int line) { return mid + (r0 + line) * mp; }, a.n, r0, 2 * a.hp, static_cast<int>(k0), 1);
+      q.load([&](int line) { return (second ? wu : wg) + (k + line) * a.ws; }, a.hidden, k, a.dim, c0, a.vec);
     } else {
-      fill32<true>(lp, mid + (which ? a.hp : 0), mp, a.hidden, a.n, r0, k0, 1);
-      fill32<true>(lq, x, a.xs, a.dim, a.n, c0, k0, a.vec);
+      p.load([&](int line) { return mid + (k0 + line) * mp + (which ? a.hp : 0); }, a.n, k0, a.hp, static_cast<int>(r0), 1);
+      q.load([&](int line) { return x + (k0 + line) * a.xs; }, a.n, k0, a.dim, c0, a.vec);
     }
-    __syncthreads();
+  };
+  auto store = [&](int b, int64_t stage) {
+    const int64_t k0 = stage * kStep32;
+    if constexpr (kGated) {
+      p.store(lds[b][0], a.n, r0, a.dim, static_cast<int>(k0));
+      q.store(lds[b][1], 64, 0, a.dim, static_cast<int>(k0));
+    } else if constexpr (MODE == kFfnDx) {
+      p.store(lds[b][0], a.n, r0, 2 * a.hp, static_cast<int>(k0));
+      q.store(lds[b][1], a.hidden, k0 - (k0 >= a.hp ? a.hp : 0), a.dim, c0);
+    } else {
+      p.store(lds[b][0], a.n, k0, a.hp, static_cast<int>(r0));
+      q.store(lds[b][1], a.n, k0, a.dim, c0);
+    }
+  };
+  f32x4 acc[4] = {};
+  if (first < end) {
+    load(first);
+    store(0, first);
+  }
+  __syncthreads();
+  for (int64_t st = first; st < end; ++st) {
+    const int b = static_cast<int>(st - first) & 1;
+    if (st + 1 < end) load(st + 1);
 #pragma unroll
-    for (int s = 0; s < kStep32 / 8; ++s) {
-      f32x4 fp[2], fq[2];
+    for (int s = 0; s < kStep32 / 16; ++s) {
+      const f32x4 fp = Stage32<kPT>::read(lds[b][0], s, wave);
+      f32x4 fq[4];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        fp[b] = *reinterpret_cast<const f32x4*>(lp + (wr * 64 + b * 32 + li) * kPitch32 + 8 * s + 4 * lh);
-        fq[b] = *reinterpret_cast<const f32x4*>(lq + (wc * 64 + b * 32 + li) * kPitch32 + 8 * s + 4 * lh);
-      }
+      for (int j = 0; j < 4; ++j) fq[j] = Stage32<kQT>::read(lds[b][1], s, j);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fq[j][e], fp[i][e], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < 4; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fq[j][e], fp[e], acc[j], 0, 0, 0);
     }
+    if (st + 1 < end) store(b ^ 1, st + 1);
     __syncthreads();
   }
-  // lane l: row 32 i + (l & 31) of the wave's 64, columns 32 j + 8 g + 4 (l >> 5) .. + 3
+  // lane l: row l & 15 of the wave's 16, columns 16 j + 4 (l >> 4) .. + 3
+  const int64_t r = r0 + wave * 16 + (lane & 15);
+  const int c = c0 + 4 * (lane >> 4);
+  if constexpr (kGated) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t r = r0 + wr * 64 + 32 * i + li;
+    for (int j = 0; j < 2; ++j) {
+      const float g[4] = {acc[j][0], acc[j][1], acc[j][2], acc[j][3]};
+      const float u[4] = {acc[j + 2][0], acc[j + 2][1], acc[j + 2][2], acc[j + 2][3]};
+      finish_gated<kF32, MODE>(a, r, c + 16 * j, g, u);
+    }
+  } else {
 #pragma unroll
-    for (int g4 = 0; g4 < 4; ++g4) {
-      if constexpr (kGated) {
-        float g[4], u[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          g[e] = acc[i][0][4 * g4 + e];
-          u[e] = acc[i][1][4 * g4 + e];
-        }
-        finish_gated<kF32, MODE>(a, r, c0 + wc * 32 + 8 * g4 + 4 * lh, g, u);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g4 + e];
-          finish_plain<kF32, MODE>(a, which, r, c0 + wc * 64 + 32 * j + 8 * g4 + 4 * lh, v);
-        }
-      }
+    for (int j = 0; j < 4; ++j) {
+      const float v[4] = {acc[j][0], acc[j][1], acc[j][2], acc[j][3]};
+      finish_plain<kF32, MODE>(a, which, slice, r, c + 16 * j, v);
     }
   }
+}
+
+// ---------------------------------------------------------------- joining slices
+// Adds the slices of dx (kFfnDx) or of both weights' gradients, in order.
+template <int DT, int MODE> __global__ __launch_bounds__(256) void ffn_join_kernel(FfnArgs a) {
+  const int per = (a.dim + 3) / 4;
+  const int64_t rows = MODE == kFfnDx ? a.n : 2 * static_cast<int64_t>(a.hidden);
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, r = id / per;
+  const int c = static_cast<int>(id % per) * 4;
+  if (r >= rows) return;
+  const int64_t pitch = 4 * static_cast<int64_t>(per);
+  float v[4] = {};
+  for (int s = 0; s < a.slices; ++s) {
+    const f32x4 x = *reinterpret_cast<gptr<const f32x4>>(gmem(a.part + (s * rows + r) * pitch + c));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += x[i];
+  }
+  const int which = MODE == kFfnDw && r >= a.hidden;
+  FfnArgs one = a;
+  one.slices = 1;
+  finish_plain<DT, MODE>(one, which, 0, r - (which ? a.hidden : 0), c, v);
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -647,13 +723,24 @@ template <int DT> __global__ __launch_bounds__(256) void ffn_pad_kernel(const vo
   store_n<8>(static_cast<T*>(dst) + r * padded + c, v);
 }
 
-template <int DT, int MODE> hipError_t run(const FfnArgs& a, hipStream_t stream) {
+template <int DT, int MODE> hipError_t run(const FfnArgs& args, hipStream_t stream) {
+  FfnArgs a = args;
+  if (MODE == kFfnOut || MODE == kFfnMid) a.slices = 1;
+  else a.slices = MODE == kFfnDx ? a.dx_slices : a.dw_slices;
   if constexpr (DT == kBF16) {
-    const unsigned blocks = static_cast<unsigned>(grid_of<MODE>(a, 256).all);
+    const unsigned blocks = static_cast<unsigned>(grid_of<MODE>(a, 256).all) * a.slices;
     ffn_tile_kernel<MODE><<<dim3(blocks), dim3(kTileThreads), 0, stream>>>(a);
   } else {
-    const unsigned blocks = static_cast<unsigned>(grid_of<MODE>(a, kTile32).all);
+    const unsigned blocks = static_cast<unsigned>(grid_of<MODE>(a, kTile32).all) * a.slices;
     ffn_tile32_kernel<MODE><<<dim3(blocks), dim3(256), 0, stream>>>(a);
+  }
+  if constexpr (MODE == kFfnDx || MODE == kFfnDw) {
+    if (a.slices > 1) {
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      const int64_t units = (MODE == kFfnDx ? a.n : 2 * static_cast<int64_t>(a.hidden)) * ((a.dim + 3) / 4);
+      ffn_join_kernel<DT, MODE><<<dim3(static_cast<unsigned>((units + 255) / 256)), dim3(256), 0, stream>>>(a);
+    }
   }
   return hipGetLastError();
 }
@@ -664,6 +751,14 @@ template <int DT> hipError_t run_any(int mode, const FfnArgs& a, hipStream_t str
     case kFfnDx: return run<DT, kFfnDx>(a, stream);
     default: return run<DT, kFfnDw>(a, stream);
   }
+}
+// Slices of a product's contraction: where its tiles alone leave CUs idle, at
+// least eight stages each.
+template <int DT, int MODE> int slices_of(const FfnArgs& a) {
+  const int64_t tiles = grid_of<MODE>(a, DT == kBF16 ? 256 : kTile32).all;
+  if (tiles == 0 || tiles > 128) return 1;
+  const int64_t most_ = stages_of<MODE>(a, kFfnStage) / 8;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(DT == kBF16 ? 256 : 512) / tiles, most_, 16})));
 }
 template <int DT> hipError_t few(const FfnArgs& a, hipStream_t stream) {
   const dim3 blocks((a.hidden + 15) / 16), threads(64 * kFewWaves);
@@ -676,6 +771,10 @@ template <int DT> hipError_t few(const FfnArgs& a, hipStream_t stream) {
 }  // namespace
 }  // namespace ffn
 
+void ffn_slices(int dt, FfnArgs* a) {
+  a->dx_slices = dt == kF32 ? ffn::slices_of<kF32, kFfnDx>(*a) : ffn::slices_of<kBF16, kFfnDx>(*a);
+  a->dw_slices = dt == kF32 ? ffn::slices_of<kF32, kFfnDw>(*a) : ffn::slices_of<kBF16, kFfnDw>(*a);
+}
 hipError_t launch_ffn(int dt, int mode, const FfnArgs& a, hipStream_t stream) {
   return dt == kF32 ? ffn::run_any<kF32>(mode, a, stream) : ffn::run_any<kBF16>(mode, a, stream);
 }

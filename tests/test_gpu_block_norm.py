@@ -144,10 +144,13 @@ def test_strides_do_not_change_a_bit():
         assert all(torch.equal(a, b) for a, b in zip(back[0], other))
 
 
-@pytest.mark.parametrize("dim", [100, 5000, 9000])
-def test_in_place(dim):
+# 513, 1030, 4099, 16390: the last run begins in one wave and is loaded together with another's last elements
+@pytest.mark.parametrize("dim", [5, 100, 513, 1030, 4099, 5000, 9000, 16390])
+@pytest.mark.parametrize("post_norm", [False, True])
+def test_in_place(dim, post_norm):
     x, h, dx, dy, pre, post, gate = make(20, dim, F32, BF16, F32, 7)
-    kw = dict(post_norm=True, residual_scale=0.5)
+    post = post if post_norm else None
+    kw = dict(post_norm=post_norm, residual_scale=0.5)
     want = nsa.block_norm(x, h, pre, post, gate, **kw)
     back = nsa.block_norm_grad(dx, dy, want[0], h, pre, post, gate, **kw)
     got = nsa.block_norm_grad(dx, dy, want[0], h, pre, post, gate, dx=dx, **kw)
