@@ -111,8 +111,9 @@ template <int DT, int DP> __device__ __forceinline__ Frag<DT> frag_cols(const ch
   }
   return f;
 }
-// Fragment `step` of one row in memory: zeros behind the head and where there is no row.
-template <int DT> __device__ __forceinline__ Frag<DT> frag_global(const void* row, bool any, int step, int dim, int vec) {
+// Fragment `step` of one row in memory, zeros behind the head.  VEC: runs of 16
+// bytes are aligned and whole.
+template <int DT, bool VEC> __device__ __forceinline__ Frag<DT> frag_global(const void* row, int step, int dim) {
   using T = typename OpElem<DT>::T;
   constexpr int M = 16 / static_cast<int>(sizeof(T));
   typedef T V __attribute__((ext_vector_type(M)));
@@ -121,15 +122,14 @@ template <int DT> __device__ __forceinline__ Frag<DT> frag_global(const void* ro
   Frag<DT> f;
 #pragma unroll
   for (int h = 0; h < 8 / M; ++h) {
-    V x{};
-    if (any) {
-      if (vec) {
-        if (d0 + M * h < dim) x = *reinterpret_cast<gptr<const V>>(gmem(p + d0 + M * h));
-      } else {
+    const int d = d0 + M * h;
+    V x;
+    if constexpr (VEC) {   // every lane loads, so that no load waits for another
+      x = *reinterpret_cast<gptr<const V>>(gmem(p + (d < dim ? d : 0)));
+      if (d >= dim) x = V{};
+    } else {
 #pragma unroll
-        for (int i = 0; i < M; ++i)
-          if (d0 + M * h + i < dim) x[i] = gmem(p)[d0 + M * h + i];
-      }
+      for (int i = 0; i < M; ++i) x[i] = d + i < dim ? gmem(p)[d + i] : static_cast<T>(0.0f);
     }
 #pragma unroll
     for (int i = 0; i < M; ++i) f.v[M * h + i] = x[i];
@@ -145,14 +145,21 @@ __device__ __forceinline__ int query_of(const AttnArgs& a, int r) {
   return i;
 }
 
-// 16 bytes from `src` to LDS[dst + 16 lane], with no register between.  Issued
-// through asm so that the compiler's count of outstanding accesses does not
-// make every LDS read wait for it; the reader waits for vmcnt(0) and a barrier.
-__device__ __forceinline__ void dma16(const void* src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory");
+// 16 bytes from base + voff (per lane) to LDS[dst + 16 lane], with no register
+// between.  Issued through asm so that the compiler's count of outstanding
+// accesses does not make every LDS read wait for it; the reader waits for
+// vmcnt(0) and a barrier.
+__device__ __forceinline__ void dma16(const void* base, uint32_t voff, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(dst) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_address(const char* p) {
   return static_cast<uint32_t>(reinterpret_cast<size_t>((lds_t)p));   // address-space cast
+}
+__device__ __forceinline__ const char* uniform_ptr(const void* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return reinterpret_cast<const char*>((static_cast<uint64_t>(hi) << 32) | lo);
 }
 // Everything that the block has on its way into LDS is there behind this.
 __device__ __forceinline__ void tiles_landed() {
@@ -160,35 +167,64 @@ __device__ __forceinline__ void tiles_landed() {
   __syncthreads();
 }
 
-// Fills a tile of R rows; address(row) is where the row's head begins (rows
-// that do not exist take one that does).  Heads with aligned runs go straight
-// to LDS and leave the padding alone (clear_tiles), others element by element.
-template <int DT, int DP, int R, typename Address>
-__device__ __forceinline__ void fill_tile(char* tile, int dim, int vec, Address&& address) {
+// Fills tiles of R rows, straight to LDS (VEC; the padding behind a head is left
+// alone, clear_tiles) or element by element.
+template <int DT, int DP, int R, bool VEC> struct Filler {
   using S = Shape<DT, DP>;
   using T = typename S::T;
-  if (vec) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const uint32_t base = lds_address(tile);
-    constexpr int kLoads = R * S::kChunks / 64;          // of 1 KB
+  static constexpr int kLoads = R * S::kChunks / 64 / kWaves;   // of 1 KB, per wave
+  static_assert(R * S::kChunks % (64 * kWaves) == 0, "whole loads for every wave");
+  static constexpr uint32_t kNone = 0xFFFFFFFFu;
+  uint32_t off[VEC ? kLoads : 1];
+
+  __device__ static __forceinline__ int row_of(int u) {
+    return ((u * kWaves + static_cast<int>(threadIdx.x >> 6)) * 64 + static_cast<int>(threadIdx.x & 63)) / S::kChunks;
+  }
+  // offset(row): bytes from the tile's first row to this one; every row's are
+  // the same in every whole tile.
+  template <typename Offset> __device__ __forceinline__ void init(int dim, Offset&& offset) {
+    if constexpr (VEC)
 #pragma unroll
-    for (int u = 0; u < (kLoads + kWaves - 1) / kWaves; ++u) {
-      const int load = u * kWaves + wave;
-      if (kLoads % kWaves != 0 && load >= kLoads) break;
-      const int slot = load * 64 + lane, row = slot / S::kChunks;
-      const int chunk = (slot % S::kChunks) ^ S::swizzle(row);
-      if (chunk * 16 < dim * S::kElem)
-        dma16(reinterpret_cast<const char*>(address(row)) + chunk * 16,
-              __builtin_amdgcn_readfirstlane(base + static_cast<uint32_t>(load) * 1024));
-    }
-  } else {
-    for (int e = threadIdx.x; e < R * DP; e += kThreads) {
-      const int row = e / DP, d = e % DP, byte = d * S::kElem;
-      const T x = d < dim ? gmem(address(row))[d] : static_cast<T>(0.0f);
-      *reinterpret_cast<T*>(tile + row * S::kPitch + (((byte >> 4) ^ S::swizzle(row)) << 4) + (byte & 15)) = x;
+      for (int u = 0; u < kLoads; ++u) {
+        const int row = row_of(u), chunk = (static_cast<int>(threadIdx.x & 63) % S::kChunks) ^ S::swizzle(row);
+        off[u] = chunk * 16 < dim * S::kElem ? offset(row) + chunk * 16 : kNone;
+      }
+  }
+  __device__ static __forceinline__ void move(const char* base, uint32_t voff, uint32_t lds, int u, bool full) {
+    const uint32_t dst = lds + static_cast<uint32_t>(u * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * 1024;
+    if (full) dma16(base, voff, dst);
+    else if (voff != kNone) dma16(base, voff, dst);
+  }
+  // A whole tile whose first row begins at `first`.
+  __device__ __forceinline__ void whole(char* tile, const void* first, int dim) const {
+    static_assert(VEC, "by element: any()");
+    const char* base = uniform_ptr(first);
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_address(tile));
+    const bool full = dim * S::kElem == S::kPitch;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) move(base, off[u], lds, u, full);
+  }
+  // Any tile: address(row) is where the row's head begins; rows that do not
+  // exist take one that does.
+  template <typename Address> __device__ __forceinline__ void any(char* tile, int dim, Address&& address) const {
+    if constexpr (VEC) {
+      const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_address(tile));
+      const char* base = uniform_ptr(address(0));
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const int row = row_of(u), chunk = (static_cast<int>(threadIdx.x & 63) % S::kChunks) ^ S::swizzle(row);
+        const uint32_t at = static_cast<uint32_t>(reinterpret_cast<const char*>(address(row)) - base) + chunk * 16;
+        move(base, chunk * 16 < dim * S::kElem ? at : kNone, lds, u, false);
+      }
+    } else {
+      for (int e = threadIdx.x; e < R * DP; e += kThreads) {
+        const int row = e / DP, d = e % DP, byte = d * S::kElem;
+        const T x = d < dim ? gmem(address(row))[d] : static_cast<T>(0.0f);
+        *reinterpret_cast<T*>(tile + row * S::kPitch + (((byte >> 4) ^ S::swizzle(row)) << 4) + (byte & 15)) = x;
+      }
     }
   }
-}
+};
 __device__ __forceinline__ void clear_tiles(char* lds, int bytes) {
   for (int i = threadIdx.x * 16; i < bytes; i += kThreads * 16) *reinterpret_cast<f32v4*>(lds + i) = f32v4{};
 }
@@ -241,8 +277,8 @@ __device__ __forceinline__ Place place(const AttnArgs& a, int slot, bool keys) {
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, 64); }
 
 // One lane's row of a result: four elements at a time, scaled.
-template <int DT, int DP>
-__device__ __forceinline__ void store_row(void* row, const f32x16 (&o)[DP / 32], float by, int dim, int vec) {
+template <int DT, int DP, bool VEC>
+__device__ __forceinline__ void store_row(void* row, const f32x16 (&o)[DP / 32], float by, int dim) {
   using T = typename OpElem<DT>::T;
   T* p = static_cast<T*>(row);
   const int hf = (threadIdx.x & 63) >> 5;
@@ -254,7 +290,7 @@ __device__ __forceinline__ void store_row(void* row, const f32x16 (&o)[DP / 32],
       float x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = o[b][4 * g + i] * by;
-      if (vec) {
+      if constexpr (VEC) {
         if (d < dim) store_n<4>(p + d, x);
       } else {
 #pragma unroll

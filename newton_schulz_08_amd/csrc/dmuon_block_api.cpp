@@ -118,11 +118,12 @@ int head_buf(const dmuon_attention_shape& s, const char* name, const void* p, in
   return row_buf(name, p, tokens, heads * s.head_dim, stride, s.dtype, written, out);
 }
 
-// Every 16-byte run of every head lies at a multiple of 16 bytes.
+// Every 16-byte run of every head lies at a multiple of 16 bytes, and a tile
+// within 32 bits of offset.
 bool attn_vec(const dmuon_attention_shape& s, std::initializer_list<const Buf*> bufs) {
   if (s.head_dim * size_of(s.dtype) % 16) return false;
   for (const Buf* b : bufs)
-    if (!b->empty() && (!aligned(b->p, 16) || (b->rows > 1 && b->pitch % 16))) return false;
+    if (!b->empty() && (!aligned(b->p, 16) || (b->rows > 1 && (b->pitch % 16 || b->pitch > (int64_t{1} << 23))))) return false;
   return true;
 }
 

@@ -28,11 +28,19 @@ namespace attn {
 namespace {
 
 constexpr float kNone = -INFINITY;
+// Two blocks a CU where their tiles fit its LDS and 256 registers hold a wave:
+// one's softmax runs beside the other's matrix instructions.
+template <int DT, int DP> constexpr int waves_per_simd() { return Shape<DT, DP>::kPitch <= 256 ? 2 : 1; }
+// A row's sums are scaled to a new maximum only when it lies this far (a factor
+// of 2^8) above the one they were formed with: fp32 has room for that, and the
+// result does not depend on which maximum was taken off.
+constexpr float kSlack = 8.0f;
 
 // Unnormed sums of a slice: rows x DP, then maximum and weight of each row.
 __host__ __device__ constexpr int64_t slice_floats(int dp) { return static_cast<int64_t>(kAttnTile) * (dp + 2); }
 
-template <int DT, int DP> __global__ __launch_bounds__(kThreads) void attention_kernel(AttnArgs a) {
+template <int DT, int DP, bool VEC>
+__global__ __launch_bounds__(kThreads, (waves_per_simd<DT, DP>())) void attention_kernel(AttnArgs a) {
   using S = Shape<DT, DP>;
   using T = typename S::T;
   constexpr int kKeys = S::kPitch <= 512 ? 64 : 32;          // of a tile
@@ -77,16 +85,24 @@ template <int DT, int DP> __global__ __launch_bounds__(kThreads) void attention_
 
   Frag<DT> qf[S::kSteps];
 #pragma unroll
-  for (int s = 0; s < S::kSteps; ++s) qf[s] = frag_global<DT>(qrow, any, s, a.dim, a.vec);
+  for (int s = 0; s < S::kSteps; ++s) qf[s] = frag_global<DT, VEC>(qrow, s, a.dim);
 
   const T* kbase = static_cast<const T*>(a.k) + p.k0 * a.ks + static_cast<int64_t>(head) * a.dim;
   const T* vbase = static_cast<const T*>(a.v) + p.k0 * a.vs + static_cast<int64_t>(head) * a.dim;
+  Filler<DT, DP, kKeys, VEC> fill_k, fill_v;
+  fill_k.init(a.dim, [&](int r) { return static_cast<uint32_t>(r) * static_cast<uint32_t>(a.ks * S::kElem); });
+  fill_v.init(a.dim, [&](int r) { return static_cast<uint32_t>(r) * static_cast<uint32_t>(a.vs * S::kElem); });
   auto fetch = [&](int tile) {
     char* to = lds + (tile & 1) * 2 * kTileBytes;
-    const int key0 = begin + tile * kKeys, most_ = p.lk - 1;
-    fill_tile<DT, DP, kKeys>(to, a.dim, a.vec, [&](int r) { return kbase + static_cast<int64_t>(min(key0 + r, most_)) * a.ks; });
-    fill_tile<DT, DP, kKeys>(to + kTileBytes, a.dim, a.vec,
-                             [&](int r) { return vbase + static_cast<int64_t>(min(key0 + r, most_)) * a.vs; });
+    const int key0 = begin + tile * kKeys;
+    if constexpr (VEC)
+      if (key0 + kKeys <= p.lk) {
+        fill_k.whole(to, kbase + key0 * a.ks, a.dim);
+        fill_v.whole(to + kTileBytes, vbase + key0 * a.vs, a.dim);
+        return;
+      }
+    fill_k.any(to, a.dim, [&](int r) { return kbase + min(key0 + r, p.lk - 1) * a.ks; });
+    fill_v.any(to + kTileBytes, a.dim, [&](int r) { return vbase + min(key0 + r, p.lk - 1) * a.vs; });
   };
 
   f32x16 o[S::kBlocks];
@@ -96,7 +112,7 @@ template <int DT, int DP> __global__ __launch_bounds__(kThreads) void attention_
   const float c = a.scale * kLog2e;
 
   if (tiles > 0) {
-    if (a.vec && a.dim < DP) {
+    if (VEC && a.dim < DP) {
       clear_tiles(lds, 4 * kTileBytes);
       __syncthreads();
     }
@@ -134,15 +150,15 @@ template <int DT, int DP> __global__ __launch_bounds__(kThreads) void attention_
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
       top = fmaxf(top, other_half(top)) * c;
-      const float mn = fmaxf(m, top);
-      const float ms = mn == kNone ? 0.0f : mn;   // nothing visible so far: exp2(-inf - 0) = 0
-      if (__any(mn > m)) {
-        const float by = __builtin_amdgcn_exp2f(m - ms);
+      // nothing visible so far: any finite maximum will do, exp2(-inf) is 0
+      if (__any(top > m + kSlack)) {
+        const float mn = fmaxf(m, top), by = __builtin_amdgcn_exp2f(m - (mn == kNone ? 0.0f : mn));
+        m = mn;
         l *= by;
 #pragma unroll
         for (int b = 0; b < S::kBlocks; ++b) o[b] *= by;
       }
-      m = mn;
+      const float ms = m == kNone ? 0.0f : m;
       Frag<DT> pf[kKb][2];
 #pragma unroll
       for (int kb = 0; kb < kKb; ++kb)
@@ -167,7 +183,7 @@ template <int DT, int DP> __global__ __launch_bounds__(kThreads) void attention_
     if (!any) return;
     float* part = a.part + (static_cast<int64_t>(blockIdx.x)) * slice_floats(DP);
     const int r = wave * 32 + (lane & 31);
-    store_row<kF32, DP>(part + static_cast<int64_t>(r) * DP, o, 1.0f, DP, 1);
+    store_row<kF32, DP, true>(part + static_cast<int64_t>(r) * DP, o, 1.0f, DP);
     if (lane < 32) {
       gmem(part)[static_cast<int64_t>(kAttnTile) * DP + 2 * r] = m;
       gmem(part)[static_cast<int64_t>(kAttnTile) * DP + 2 * r + 1] = l;
@@ -175,8 +191,7 @@ template <int DT, int DP> __global__ __launch_bounds__(kThreads) void attention_
     return;
   }
   if (!any) return;
-  store_row<DT, DP>(static_cast<T*>(a.o) + token * a.os + static_cast<int64_t>(qh) * a.dim, o, l > 0.0f ? 1.0f / l : l, a.dim,
-                    a.vec);
+  store_row<DT, DP, VEC>(static_cast<T*>(a.o) + token * a.os + static_cast<int64_t>(qh) * a.dim, o, l > 0.0f ? 1.0f / l : l, a.dim);
   if (lane < 32) gmem(a.lse)[static_cast<int64_t>(qh) * a.q_tokens + token] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0.0f ? kNone : l;
 }
 
@@ -213,7 +228,9 @@ template <int DT, int DP> __global__ __launch_bounds__(kThreads) void attention_
 
 template <int DT, int DP> hipError_t run(const AttnArgs& a, hipStream_t stream) {
   const unsigned tiles = static_cast<unsigned>(a.slots) * a.k_heads;
-  attention_kernel<DT, DP><<<dim3(tiles * a.slices), dim3(kThreads), 0, stream>>>(a);
+  const dim3 blocks(tiles * a.slices);
+  if (a.vec) attention_kernel<DT, DP, true><<<blocks, dim3(kThreads), 0, stream>>>(a);
+  else attention_kernel<DT, DP, false><<<blocks, dim3(kThreads), 0, stream>>>(a);
   if (a.slices > 1) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

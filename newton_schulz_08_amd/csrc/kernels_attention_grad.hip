@@ -43,7 +43,8 @@ template <int DT> __global__ __launch_bounds__(kThreads) void attention_delta_ke
   if (lane == 0) gmem(a.delta)[static_cast<int64_t>(head) * a.q_tokens + token] = s;
 }
 
-template <int DT, int DP> __global__ __launch_bounds__(kThreads) void attention_dq_kernel(AttnArgs a) {
+template <int DT, int DP, bool VEC>
+__global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void attention_dq_kernel(AttnArgs a) {
   using S = Shape<DT, DP>;
   using T = typename S::T;
   constexpr int kKeys = S::kPitch <= 256 ? 64 : 32;
@@ -76,27 +77,35 @@ template <int DT, int DP> __global__ __launch_bounds__(kThreads) void attention_
   Frag<DT> qf[S::kSteps], df[S::kSteps];
 #pragma unroll
   for (int s = 0; s < S::kSteps; ++s) {
-    qf[s] = frag_global<DT>(qrow, any, s, a.dim, a.vec);
-    df[s] = frag_global<DT>(drow, any, s, a.dim, a.vec);
+    qf[s] = frag_global<DT, VEC>(qrow, s, a.dim);
+    df[s] = frag_global<DT, VEC>(drow, s, a.dim);
   }
   const int64_t stat = static_cast<int64_t>(qh) * a.q_tokens + token;
   const float lse = any ? row_lse(gmem(a.lse)[stat]) : INFINITY, delta = gmem(a.delta)[stat];
 
   const T* kbase = static_cast<const T*>(a.k) + p.k0 * a.ks + static_cast<int64_t>(head) * a.dim;
   const T* vbase = static_cast<const T*>(a.v) + p.k0 * a.vs + static_cast<int64_t>(head) * a.dim;
+  Filler<DT, DP, kKeys, VEC> fill_k, fill_v;
+  fill_k.init(a.dim, [&](int r) { return static_cast<uint32_t>(r) * static_cast<uint32_t>(a.ks * S::kElem); });
+  fill_v.init(a.dim, [&](int r) { return static_cast<uint32_t>(r) * static_cast<uint32_t>(a.vs * S::kElem); });
   auto fetch = [&](int tile) {
     char* to = lds + (tile & 1) * 2 * kTileBytes;
-    const int key0 = begin + tile * kKeys, most_ = p.lk - 1;
-    fill_tile<DT, DP, kKeys>(to, a.dim, a.vec, [&](int r) { return kbase + static_cast<int64_t>(min(key0 + r, most_)) * a.ks; });
-    fill_tile<DT, DP, kKeys>(to + kTileBytes, a.dim, a.vec,
-                             [&](int r) { return vbase + static_cast<int64_t>(min(key0 + r, most_)) * a.vs; });
+    const int key0 = begin + tile * kKeys;
+    if constexpr (VEC)
+      if (key0 + kKeys <= p.lk) {
+        fill_k.whole(to, kbase + key0 * a.ks, a.dim);
+        fill_v.whole(to + kTileBytes, vbase + key0 * a.vs, a.dim);
+        return;
+      }
+    fill_k.any(to, a.dim, [&](int r) { return kbase + min(key0 + r, p.lk - 1) * a.ks; });
+    fill_v.any(to + kTileBytes, a.dim, [&](int r) { return vbase + min(key0 + r, p.lk - 1) * a.vs; });
   };
   f32x16 dq[S::kBlocks];
 #pragma unroll
   for (int b = 0; b < S::kBlocks; ++b) dq[b] = f32x16{};
   const float c = a.scale * kLog2e;
   if (tiles > 0) {
-    if (a.vec && a.dim < DP) {
+    if (VEC && a.dim < DP) {
       clear_tiles(lds, 4 * kTileBytes);
       __syncthreads();
     }
@@ -141,13 +150,13 @@ template <int DT, int DP> __global__ __launch_bounds__(kThreads) void attention_
     tiles_landed();
   }
   if (any)
-    store_row<DT, DP>(static_cast<T*>(a.dq) + token * a.dqs + static_cast<int64_t>(qh) * a.dim, dq, a.scale, a.dim, a.vec);
+    store_row<DT, DP, VEC>(static_cast<T*>(a.dq) + token * a.dqs + static_cast<int64_t>(qh) * a.dim, dq, a.scale, a.dim);
 }
 
 // HELD: the keys' and values' fragments stay in registers; else they are read
 // again for every tile of rows (fp32 heads beyond 128, whose two fragments and
 // two sums are 512 registers).
-template <int DT, int DP, bool HELD> __global__ __launch_bounds__(kThreads) void attention_dkv_kernel(AttnArgs a) {
+template <int DT, int DP, bool HELD, bool VEC> __global__ __launch_bounds__(kThreads) void attention_dkv_kernel(AttnArgs a) {
   using S = Shape<DT, DP>;
   using T = typename S::T;
   constexpr int kTileBytes = 32 * S::kPitch;
@@ -178,21 +187,35 @@ template <int DT, int DP, bool HELD> __global__ __launch_bounds__(kThreads) void
   if constexpr (HELD)
 #pragma unroll
     for (int s = 0; s < S::kSteps; ++s) {
-      kf[s] = frag_global<DT>(krow, any, s, a.dim, a.vec);
-      vf[s] = frag_global<DT>(vrow, any, s, a.dim, a.vec);
+      kf[s] = frag_global<DT, VEC>(krow, s, a.dim);
+      vf[s] = frag_global<DT, VEC>(vrow, s, a.dim);
     }
 
   const T* qbase = static_cast<const T*>(a.q) + p.q0 * a.qs + static_cast<int64_t>(head) * a.group * a.dim;
   const T* dbase = static_cast<const T*>(a.dout) + p.q0 * a.dos + static_cast<int64_t>(head) * a.group * a.dim;
+  // whole tiles begin with a query's first head where the group divides 32
+  Filler<DT, DP, 32, VEC> fill_q, fill_d;
+  const bool even = 32 % a.group == 0;
+  auto at = [&](int r, int64_t stride) {
+    const int i = query_of(a, r);
+    return i * stride + static_cast<int64_t>(r - i * a.group) * a.dim;
+  };
+  fill_q.init(a.dim, [&](int r) { return static_cast<uint32_t>(at(r, a.qs) * S::kElem); });
+  fill_d.init(a.dim, [&](int r) { return static_cast<uint32_t>(at(r, a.dos) * S::kElem); });
   auto fetch = [&](int tile) {
     char* to = lds + (tile & 1) * 2 * kTileBytes;
     const int r0 = begin + tile * 32;
-    auto at = [&](const T* base, int64_t stride, int r) {
-      const int row = min(r0 + r, end - 1), i = query_of(a, row);
-      return base + i * stride + static_cast<int64_t>(row - i * a.group) * a.dim;
-    };
-    fill_tile<DT, DP, 32>(to, a.dim, a.vec, [&](int r) { return at(qbase, a.qs, r); });
-    fill_tile<DT, DP, 32>(to + kTileBytes, a.dim, a.vec, [&](int r) { return at(dbase, a.dos, r); });
+    bool done = false;
+    if constexpr (VEC)
+      if (even && r0 + 32 <= end) {
+        fill_q.whole(to, qbase + at(r0, a.qs), a.dim);
+        fill_d.whole(to + kTileBytes, dbase + at(r0, a.dos), a.dim);
+        done = true;
+      }
+    if (!done) {
+      fill_q.any(to, a.dim, [&](int r) { return qbase + at(min(r0 + r, end - 1), a.qs); });
+      fill_d.any(to + kTileBytes, a.dim, [&](int r) { return dbase + at(min(r0 + r, end - 1), a.dos); });
+    }
     if (threadIdx.x < 64) {
       const int r = threadIdx.x & 31, row = min(r0 + r, end - 1), i = query_of(a, row);
       const int64_t stat = static_cast<int64_t>(head * a.group + row - i * a.group) * a.q_tokens + p.q0 + i;
@@ -205,7 +228,7 @@ template <int DT, int DP, bool HELD> __global__ __launch_bounds__(kThreads) void
   for (int b = 0; b < S::kBlocks; ++b) dk[b] = dv[b] = f32x16{};
   const float c = a.scale * kLog2e;
   if (tiles > 0) {
-    if (a.vec && a.dim < DP) {
+    if (VEC && a.dim < DP) {
       clear_tiles(lds, 4 * kTileBytes);
       __syncthreads();
     }
@@ -223,10 +246,10 @@ template <int DT, int DP, bool HELD> __global__ __launch_bounds__(kThreads) void
       f32x16 s{}, dp{};
 #pragma unroll
       for (int st = 0; st < S::kSteps; ++st)
-        s = mma(frag_rows<DT, DP>(qt, 0, st), HELD ? kf[HELD ? st : 0] : frag_global<DT>(krow, any, st, a.dim, a.vec), s);
+        s = mma(frag_rows<DT, DP>(qt, 0, st), HELD ? kf[HELD ? st : 0] : frag_global<DT, VEC>(krow, st, a.dim), s);
 #pragma unroll
       for (int st = 0; st < S::kSteps; ++st)
-        dp = mma(frag_rows<DT, DP>(dt, 0, st), HELD ? vf[HELD ? st : 0] : frag_global<DT>(vrow, any, st, a.dim, a.vec), dp);
+        dp = mma(frag_rows<DT, DP>(dt, 0, st), HELD ? vf[HELD ? st : 0] : frag_global<DT, VEC>(vrow, st, a.dim), dp);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int r = 8 * (i >> 2) + 4 * hf + (i & 3);
@@ -258,23 +281,26 @@ template <int DT, int DP, bool HELD> __global__ __launch_bounds__(kThreads) void
     tiles_landed();
   }
   if (!any) return;
-  store_row<DT, DP>(static_cast<T*>(a.dk) + token * a.dks + static_cast<int64_t>(head) * a.dim, dk, a.scale, a.dim, a.vec);
-  store_row<DT, DP>(static_cast<T*>(a.dv) + token * a.dvs + static_cast<int64_t>(head) * a.dim, dv, 1.0f, a.dim, a.vec);
+  store_row<DT, DP, VEC>(static_cast<T*>(a.dk) + token * a.dks + static_cast<int64_t>(head) * a.dim, dk, a.scale, a.dim);
+  store_row<DT, DP, VEC>(static_cast<T*>(a.dv) + token * a.dvs + static_cast<int64_t>(head) * a.dim, dv, 1.0f, a.dim);
 }
 
-template <int DT, int DP> hipError_t run(const AttnArgs& a, int k_slots, hipStream_t stream) {
+template <int DT, int DP, bool VEC> hipError_t run(const AttnArgs& a, int k_slots, hipStream_t stream) {
   if (a.q_tokens > 0) {
     const int64_t units = static_cast<int64_t>(a.q_tokens) * a.q_heads;
     attention_delta_kernel<DT><<<dim3(static_cast<unsigned>((units + kWaves - 1) / kWaves)), dim3(kThreads), 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attention_dq_kernel<DT, DP><<<dim3(static_cast<unsigned>(a.slots) * a.k_heads), dim3(kThreads), 0, stream>>>(a);
+    attention_dq_kernel<DT, DP, VEC><<<dim3(static_cast<unsigned>(a.slots) * a.k_heads), dim3(kThreads), 0, stream>>>(a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (a.k_tokens > 0)
-    attention_dkv_kernel<DT, DP, DT == kBF16 || DP <= 128>
+    attention_dkv_kernel<DT, DP, DT == kBF16 || DP <= 128, VEC>
         <<<dim3(static_cast<unsigned>(k_slots) * a.k_heads), dim3(kThreads), 0, stream>>>(a);
   return hipGetLastError();
+}
+template <int DT, int DP> hipError_t run(const AttnArgs& a, int k_slots, hipStream_t stream) {
+  return a.vec ? run<DT, DP, true>(a, k_slots, stream) : run<DT, DP, false>(a, k_slots, stream);
 }
 template <int DT> hipError_t run_any(const AttnArgs& a, int k_slots, hipStream_t stream) {
   switch (attn_padded(a.dim)) {
