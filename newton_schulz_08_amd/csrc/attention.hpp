@@ -152,6 +152,10 @@ __device__ __forceinline__ int query_of(const AttnArgs& a, int r) {
 __device__ __forceinline__ void dma16(const void* base, uint32_t voff, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(dst) : "memory");
 }
+// The same of four bytes a lane.
+__device__ __forceinline__ void dma4(const void* base, uint32_t voff, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(dst) : "memory");
+}
 __device__ __forceinline__ uint32_t lds_address(const char* p) {
   return static_cast<uint32_t>(reinterpret_cast<size_t>((lds_t)p));   // address-space cast
 }

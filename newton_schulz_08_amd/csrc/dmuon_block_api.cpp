@@ -113,6 +113,11 @@ int64_t attn_part_bytes(const dmuon_attention_shape& s) {
   return attn_q_slots(s) * s.k_heads * slices * kAttnTile * (attn_padded(s.head_dim) + 2) * int64_t{4};
 }
 
+// Two numbers a row, and room for a tile of rows behind the last.
+size_t attn_stat_bytes(const dmuon_attention_shape& s) {
+  return align_up(2 * sizeof(float) * (static_cast<size_t>(s.q_tokens) * s.q_heads + 32));
+}
+
 int head_buf(const dmuon_attention_shape& s, const char* name, const void* p, int64_t tokens, int64_t heads,
              int64_t stride, bool written, Buf* out) {
   return row_buf(name, p, tokens, heads * s.head_dim, stride, s.dtype, written, out);
@@ -401,7 +406,7 @@ int dmuon_attention_backward_workspace_bytes(const dmuon_attention_shape* shape,
   return guarded([&]() -> int {
     if (!bytes_out) return invalid("bytes_out is NULL");
     DMUON_TRY(check_attn(shape));
-    *bytes_out = align_up(sizeof(float) * shape->q_tokens * shape->q_heads);
+    *bytes_out = attn_stat_bytes(*shape);
     return DMUON_OK;
   });
 }
@@ -416,7 +421,7 @@ int dmuon_attention_backward(const dmuon_attention_shape* shape, const void* dou
     const dmuon_attention_shape& s = *shape;
     DMUON_TRY(check_attn_grid(s));
     DMUON_TRY(check_offsets(q_offsets, k_offsets, s.sequences));
-    const size_t need = align_up(sizeof(float) * s.q_tokens * s.q_heads);
+    const size_t need = attn_stat_bytes(s);
     DMUON_TRY(check_workspace(workspace, workspace_bytes, need));
     Buf b[12];
     DMUON_TRY(head_buf(s, "dout", dout, s.q_tokens, s.q_heads, dout_stride, false, &b[0]));
@@ -456,7 +461,7 @@ int dmuon_attention_backward(const dmuon_attention_shape* shape, const void* dou
     a.dqs = dq_stride;
     a.dks = dk_stride;
     a.dvs = dv_stride;
-    a.delta = static_cast<float*>(workspace);
+    a.stats = static_cast<float*>(workspace);
     a.slices = 1;
     a.vec = attn_vec(s, {&b[0], &b[1], &b[2], &b[3], &b[4], &b[5], &b[6], &b[7]});
     const int k_slots = static_cast<int>(attn_slots(s.k_tokens, s.sequences));

@@ -6,7 +6,7 @@
 //   ds = p (dout . v - delta) scale
 //   dq = sum over keys of ds k,   dk = sum over rows of ds q,   dv = sum of p dout
 //
-// Three launches.  The first forms delta.  dq's blocks keep a tile of rows
+// Three launches.  The first forms delta and puts it beside lse.  dq's blocks keep a tile of rows
 // (queries x the heads that share a key head) and pass over the keys; dk's and
 // dv's keep a tile of keys and pass over the rows, those of all heads that
 // share it, so a shared head's gradient is one sum in one block.  Each forms
@@ -14,8 +14,8 @@
 // has one owner and one order, with no atomics and no partial results in
 // memory.
 //
-// Rows without visible keys (lse -infinity) and rows behind the sequence take
-// lse = +infinity, which makes their probabilities exp2(-infinity) = 0.
+// Rows without visible keys (lse -infinity) take lse = +infinity, which makes
+// their probabilities exp2(-infinity) = 0.
 #include <hip/hip_runtime.h>
 
 #include "attention.hpp"
@@ -24,23 +24,43 @@ namespace dmuon {
 namespace attn {
 namespace {
 
-// Base-2 log-sum-exp of a row, +infinity where it must have no probabilities.
-__device__ __forceinline__ float row_lse(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+// Where a row's base-2 log-sum-exp and delta lie: in the order of a key head's
+// rows (token, head of the group), so that a tile's are one run.
+__device__ __forceinline__ int64_t stat_of(const AttnArgs& a, int head, int64_t token, int g) {
+  return 2 * ((static_cast<int64_t>(head) * a.q_tokens + token) * a.group + g);
+}
 
-// One wave per token and run of heads.
-template <int DT> __global__ __launch_bounds__(kThreads) void attention_delta_kernel(AttnArgs a) {
+// Runs of 16 bytes of (token, query head) rows; LANES lanes a row.
+template <int DT, int LANES, bool VEC> __global__ __launch_bounds__(kThreads) void attention_stats_kernel(AttnArgs a) {
   using T = typename OpElem<DT>::T;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
-  const int64_t token = unit / a.q_heads;
-  const int head = static_cast<int>(unit % a.q_heads), lane = threadIdx.x & 63;
+  constexpr int M = 16 / static_cast<int>(sizeof(T));
+  typedef T V __attribute__((ext_vector_type(M)));
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / LANES;
+  const int64_t token = row / a.q_heads;
+  const int h = static_cast<int>(row - token * a.q_heads), d = threadIdx.x % LANES * M;
   if (token >= a.q_tokens) return;
-  const T* o = static_cast<const T*>(a.out) + token * a.os + static_cast<int64_t>(head) * a.dim;
-  const T* d = static_cast<const T*>(a.dout) + token * a.dos + static_cast<int64_t>(head) * a.dim;
+  const T* o = static_cast<const T*>(a.out) + token * a.os + static_cast<int64_t>(h) * a.dim;
+  const T* g = static_cast<const T*>(a.dout) + token * a.dos + static_cast<int64_t>(h) * a.dim;
   float s = 0.0f;
-  for (int e = lane; e < a.dim; e += 64) s += static_cast<float>(gmem(o)[e]) * static_cast<float>(gmem(d)[e]);
+  if constexpr (VEC) {
+    if (d < a.dim) {
+      const V x = *reinterpret_cast<gptr<const V>>(gmem(o + d)), y = *reinterpret_cast<gptr<const V>>(gmem(g + d));
 #pragma unroll
-  for (int x = 32; x > 0; x >>= 1) s += __shfl_xor(s, x, 64);
-  if (lane == 0) gmem(a.delta)[static_cast<int64_t>(head) * a.q_tokens + token] = s;
+      for (int i = 0; i < M; ++i) s += static_cast<float>(x[i]) * static_cast<float>(y[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+      if (d + i < a.dim) s += static_cast<float>(gmem(o)[d + i]) * static_cast<float>(gmem(g)[d + i]);
+  }
+#pragma unroll
+  for (int x = LANES / 2; x > 0; x >>= 1) s += __shfl_xor(s, x, 64);
+  if (threadIdx.x % LANES) return;
+  const float lse = gmem(a.lse)[static_cast<int64_t>(h) * a.q_tokens + token];
+  const int head = h / a.group;
+  float* at = a.stats + stat_of(a, head, token, h - head * a.group);
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  *reinterpret_cast<gptr<f32x2>>(gmem(at)) = f32x2{lse == -INFINITY ? INFINITY : lse * kLog2e, s};
 }
 
 template <int DT, int DP, bool VEC>
@@ -80,8 +100,8 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
     qf[s] = frag_global<DT, VEC>(qrow, s, a.dim);
     df[s] = frag_global<DT, VEC>(drow, s, a.dim);
   }
-  const int64_t stat = static_cast<int64_t>(qh) * a.q_tokens + token;
-  const float lse = any ? row_lse(gmem(a.lse)[stat]) : INFINITY, delta = gmem(a.delta)[stat];
+  const float* stat = a.stats + stat_of(a, head, token, g);
+  const float lse = any ? gmem(stat)[0] : INFINITY, delta = gmem(stat)[1];
 
   const T* kbase = static_cast<const T*>(a.k) + p.k0 * a.ks + static_cast<int64_t>(head) * a.dim;
   const T* vbase = static_cast<const T*>(a.v) + p.k0 * a.vs + static_cast<int64_t>(head) * a.dim;
@@ -153,20 +173,29 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
     store_row<DT, DP, VEC>(static_cast<T*>(a.dq) + token * a.dqs + static_cast<int64_t>(qh) * a.dim, dq, a.scale, a.dim);
 }
 
-// HELD: the keys' and values' fragments stay in registers; else they are read
-// again for every tile of rows (fp32 heads beyond 128, whose two fragments and
-// two sums are 512 registers).
-template <int DT, int DP, bool HELD, bool VEC> __global__ __launch_bounds__(kThreads) void attention_dkv_kernel(AttnArgs a) {
+// Where the tile's keys and values stay: their fragments in registers, or, where
+// two sums of a head fill those, the values in LDS (bf16 from 128 on: two waves a
+// SIMD at 128, no spilling at 256), or both in memory and read again for every
+// tile of rows (fp32 beyond 128: neither has room).
+template <int DT, int DP> struct Held {
+  static constexpr bool kMemory = DT == kF32 && DP > 128;
+  static constexpr bool kValuesLds = DT == kBF16 && DP >= 128;
+  static constexpr int kWavesPerSimd = DT == kBF16 && DP <= 128 ? 2 : 1;
+};
+
+template <int DT, int DP, bool VEC>
+__global__ __launch_bounds__(kThreads, (Held<DT, DP>::kWavesPerSimd)) void attention_dkv_kernel(AttnArgs a) {
   using S = Shape<DT, DP>;
   using T = typename S::T;
-  constexpr int kTileBytes = 32 * S::kPitch;
-  __shared__ __attribute__((aligned(16))) char lds[4 * kTileBytes];   // Q, dout; twice
-  __shared__ float stats[2][2][32];                                   // lse, delta; twice
+  using H = Held<DT, DP>;
+  constexpr int kTileBytes = 32 * S::kPitch, kValues = H::kValuesLds ? kAttnTile * S::kPitch : 0;
+  constexpr int kStats = 4 * kTileBytes;   // lse, delta of 32 rows; twice
+  __shared__ __attribute__((aligned(16))) char lds[4 * kTileBytes + 512 + kValues];   // Q, dout; twice
 
   const int head = blockIdx.x % a.k_heads;
   const Place p = place(a, blockIdx.x / a.k_heads, true);
   if (!p.any) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, hf = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, hf = lane >> 5;
   const int shift = p.lk - p.lq;
   const int last = min(p.lk, p.row0 + kAttnTile) - 1;
   // rows that see any of the tile's keys
@@ -179,20 +208,33 @@ template <int DT, int DP, bool HELD, bool VEC> __global__ __launch_bounds__(kThr
   const int key = p.row0 + wave * 32 + (lane & 31);
   const bool any = key < p.lk;
   const int64_t token = p.k0 + (any ? key : last);
-  const T* krow = static_cast<const T*>(a.k) + token * a.ks + static_cast<int64_t>(head) * a.dim;
-  const T* vrow = static_cast<const T*>(a.v) + token * a.vs + static_cast<int64_t>(head) * a.dim;
+  const T* kbase = static_cast<const T*>(a.k) + p.k0 * a.ks + static_cast<int64_t>(head) * a.dim;
+  const T* vbase = static_cast<const T*>(a.v) + p.k0 * a.vs + static_cast<int64_t>(head) * a.dim;
+  const T* krow = kbase + (any ? key : last) * a.ks;
+  const T* vrow = vbase + (any ? key : last) * a.vs;
   const int w0 = p.row0 + wave * 32, w1 = min(w0 + 31, p.lk - 1);   // this wave's keys
   const bool wave_any = w0 < p.lk;
-  Frag<DT> kf[HELD ? S::kSteps : 1], vf[HELD ? S::kSteps : 1];
-  if constexpr (HELD)
+  Frag<DT> kf[H::kMemory ? 1 : S::kSteps], vf[H::kMemory || H::kValuesLds ? 1 : S::kSteps];
+  if constexpr (!H::kMemory)
 #pragma unroll
     for (int s = 0; s < S::kSteps; ++s) {
       kf[s] = frag_global<DT, VEC>(krow, s, a.dim);
-      vf[s] = frag_global<DT, VEC>(vrow, s, a.dim);
+      if constexpr (!H::kValuesLds) vf[s] = frag_global<DT, VEC>(vrow, s, a.dim);
     }
+  char* values = lds + kStats + 512;
+  auto key_frag = [&](int st) {
+    if constexpr (H::kMemory) return frag_global<DT, VEC>(krow, st, a.dim);
+    else return kf[st];
+  };
+  auto value_frag = [&](int st) {
+    if constexpr (H::kMemory) return frag_global<DT, VEC>(vrow, st, a.dim);
+    else if constexpr (H::kValuesLds) return frag_rows<DT, DP>(values, wave * 32, st);
+    else return vf[st];
+  };
 
   const T* qbase = static_cast<const T*>(a.q) + p.q0 * a.qs + static_cast<int64_t>(head) * a.group * a.dim;
   const T* dbase = static_cast<const T*>(a.dout) + p.q0 * a.dos + static_cast<int64_t>(head) * a.group * a.dim;
+  const float* sbase = a.stats + stat_of(a, head, p.q0, 0);
   // whole tiles begin with a query's first head where the group divides 32
   Filler<DT, DP, 32, VEC> fill_q, fill_d;
   const bool even = 32 % a.group == 0;
@@ -216,12 +258,10 @@ template <int DT, int DP, bool HELD, bool VEC> __global__ __launch_bounds__(kThr
       fill_q.any(to, a.dim, [&](int r) { return qbase + at(min(r0 + r, end - 1), a.qs); });
       fill_d.any(to + kTileBytes, a.dim, [&](int r) { return dbase + at(min(r0 + r, end - 1), a.dos); });
     }
-    if (threadIdx.x < 64) {
-      const int r = threadIdx.x & 31, row = min(r0 + r, end - 1), i = query_of(a, row);
-      const int64_t stat = static_cast<int64_t>(head * a.group + row - i * a.group) * a.q_tokens + p.q0 + i;
-      if (threadIdx.x < 32) stats[tile & 1][0][r] = r0 + r < end ? row_lse(gmem(a.lse)[stat]) : INFINITY;
-      else stats[tile & 1][1][r] = gmem(a.delta)[stat];
-    }
+    // 32 rows' pairs; those behind the last row (the room holds a tile more) are masked
+    if (wave == 0)
+      dma4(uniform_ptr(sbase + 2 * static_cast<int64_t>(r0)), static_cast<uint32_t>(lane) * 4,
+           __builtin_amdgcn_readfirstlane(lds_address(lds + kStats)) + (tile & 1) * 256);
   };
   f32x16 dk[S::kBlocks], dv[S::kBlocks];
 #pragma unroll
@@ -229,8 +269,12 @@ template <int DT, int DP, bool HELD, bool VEC> __global__ __launch_bounds__(kThr
   const float c = a.scale * kLog2e;
   if (tiles > 0) {
     if (VEC && a.dim < DP) {
-      clear_tiles(lds, 4 * kTileBytes);
+      clear_tiles(lds, sizeof(lds));
       __syncthreads();
+    }
+    if constexpr (H::kValuesLds) {
+      Filler<DT, DP, kAttnTile, VEC> fill_v;
+      fill_v.any(values, a.dim, [&](int r) { return vbase + min(p.row0 + r, last) * a.vs; });
     }
     fetch(0);
     tiles_landed();
@@ -245,23 +289,22 @@ template <int DT, int DP, bool HELD, bool VEC> __global__ __launch_bounds__(kThr
     if (see) {
       f32x16 s{}, dp{};
 #pragma unroll
-      for (int st = 0; st < S::kSteps; ++st)
-        s = mma(frag_rows<DT, DP>(qt, 0, st), HELD ? kf[HELD ? st : 0] : frag_global<DT, VEC>(krow, st, a.dim), s);
+      for (int st = 0; st < S::kSteps; ++st) s = mma(frag_rows<DT, DP>(qt, 0, st), key_frag(st), s);
 #pragma unroll
-      for (int st = 0; st < S::kSteps; ++st)
-        dp = mma(frag_rows<DT, DP>(dt, 0, st), HELD ? vf[HELD ? st : 0] : frag_global<DT, VEC>(vrow, st, a.dim), dp);
+      for (int st = 0; st < S::kSteps; ++st) dp = mma(frag_rows<DT, DP>(dt, 0, st), value_frag(st), dp);
+      const float* stat = reinterpret_cast<const float*>(lds + kStats + (tile & 1) * 256) + 8 * hf;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int r = 8 * (i >> 2) + 4 * hf + (i & 3);
-        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -stats[tile & 1][0][r]));
-        dp[i] = s[i] * (dp[i] - stats[tile & 1][1][r]);
+        const int r = 8 * (i >> 2) + (i & 3);
+        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -stat[2 * r]));
+        dp[i] = s[i] * (dp[i] - stat[2 * r + 1]);
       }
-      const bool mask = (a.causal && w1 > qlo + shift) || (a.window && w0 <= qhi + shift - a.window);
+      const bool mask = r0 + 32 > end || (a.causal && w1 > qlo + shift) || (a.window && w0 <= qhi + shift - a.window);
       if (mask) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int q = query_of(a, min(r0 + 8 * (i >> 2) + 4 * hf + (i & 3), end - 1)) + shift;
-          if (key > q || (a.window && key <= q - a.window)) s[i] = dp[i] = 0.0f;
+          const int r = r0 + 8 * (i >> 2) + 4 * hf + (i & 3), q = query_of(a, r) + shift;
+          if (r >= end || (a.causal && key > q) || (a.window && key <= q - a.window)) s[i] = dp[i] = 0.0f;
         }
       }
       Frag<DT> pf[2], ds[2];
@@ -287,15 +330,17 @@ template <int DT, int DP, bool HELD, bool VEC> __global__ __launch_bounds__(kThr
 
 template <int DT, int DP, bool VEC> hipError_t run(const AttnArgs& a, int k_slots, hipStream_t stream) {
   if (a.q_tokens > 0) {
-    const int64_t units = static_cast<int64_t>(a.q_tokens) * a.q_heads;
-    attention_delta_kernel<DT><<<dim3(static_cast<unsigned>((units + kWaves - 1) / kWaves)), dim3(kThreads), 0, stream>>>(a);
+    constexpr int kLanes = Shape<DT, DP>::kPitch / 16;
+    const int64_t threads = static_cast<int64_t>(a.q_tokens) * a.q_heads * kLanes;
+    attention_stats_kernel<DT, kLanes, VEC>
+        <<<dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     attention_dq_kernel<DT, DP, VEC><<<dim3(static_cast<unsigned>(a.slots) * a.k_heads), dim3(kThreads), 0, stream>>>(a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (a.k_tokens > 0)
-    attention_dkv_kernel<DT, DP, DT == kBF16 || DP <= 128, VEC>
+    attention_dkv_kernel<DT, DP, VEC>
         <<<dim3(static_cast<unsigned>(k_slots) * a.k_heads), dim3(kThreads), 0, stream>>>(a);
   return hipGetLastError();
 }
