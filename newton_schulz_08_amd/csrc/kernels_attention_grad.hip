@@ -159,13 +159,24 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
           if (key > hi || key < lo) dp[i] = 0.0f;
         }
       }
-      Frag<DT> ds[2];
+      // A row's ds add up to 0, so what its keys have in common cancels in dq, but
+      // not in the errors of rounding ds to bf16: with those alone dq of trained
+      // keys is half as far off again as its own rounding.  The product takes ds
+      // as two bf16 numbers, from the same fragments of the keys.
+      Frag<DT> ds[2], low[2];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) ds[i >> 3].set(i & 7, dp[i]);
+      for (int i = 0; i < 16; ++i) {
+        ds[i >> 3].set(i & 7, dp[i]);
+        if constexpr (DT == kBF16) low[i >> 3].set(i & 7, dp[i] - static_cast<float>(ds[i >> 3].v[i & 7]));
+      }
 #pragma unroll
       for (int b = 0; b < S::kBlocks; ++b)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) dq[b] = mma(frag_cols<DT, DP>(kt, kb + 16 * h, b), ds[h], dq[b]);
+        for (int h = 0; h < 2; ++h) {
+          const Frag<DT> k = frag_cols<DT, DP>(kt, kb + 16 * h, b);
+          dq[b] = mma(k, ds[h], dq[b]);
+          if constexpr (DT == kBF16) dq[b] = mma(k, low[h], dq[b]);
+        }
     }
     tiles_landed();
   }
