@@ -221,7 +221,7 @@ template <int DT, int DP, int R, bool VEC> struct Filler {
         move(base, chunk * 16 < dim * S::kElem ? at : kNone, lds, u, false);
       }
     } else {
-      for (int e = threadIdx.x; e < R * DP; e += kThreads) {
+      for (int e = threadIdx.x; e < R * DP; e += 64 * kWaves) {
         const int row = e / DP, d = e % DP, byte = d * S::kElem;
         const T x = d < dim ? gmem(address(row))[d] : static_cast<T>(0.0f);
         *reinterpret_cast<T*>(tile + row * S::kPitch + (((byte >> 4) ^ S::swizzle(row)) << 4) + (byte & 15)) = x;
@@ -230,7 +230,7 @@ template <int DT, int DP, int R, bool VEC> struct Filler {
   }
 };
 __device__ __forceinline__ void clear_tiles(char* lds, int bytes) {
-  for (int i = threadIdx.x * 16; i < bytes; i += kThreads * 16) *reinterpret_cast<f32v4*>(lds + i) = f32v4{};
+  for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16) *reinterpret_cast<f32v4*>(lds + i) = f32v4{};
 }
 
 // A block's place: sequence, tile of it, and the sequence's extent.

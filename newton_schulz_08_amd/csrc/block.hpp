@@ -53,7 +53,7 @@ struct AttnArgs {
   void* dq;
   void* dk;
   void* dv;
-  float* stats;            // backward: base-2 lse and dout . out of every row, in the rows' order, and a tile's room
+  float* stats;            // backward: base-2 lse and dout . out of every row, in the rows' order
   float* part;             // forward in slices: per slice, tile and row the sum, then maximum and weight
   int64_t qs, ks, vs, os, dos, dqs, dks, dvs;   // elements between tokens
   int q_tokens, k_tokens, sequences;

@@ -113,9 +113,9 @@ int64_t attn_part_bytes(const dmuon_attention_shape& s) {
   return attn_q_slots(s) * s.k_heads * slices * kAttnTile * (attn_padded(s.head_dim) + 2) * int64_t{4};
 }
 
-// Two numbers a row, and room for a tile of rows behind the last.
+// Two numbers a row.
 size_t attn_stat_bytes(const dmuon_attention_shape& s) {
-  return align_up(2 * sizeof(float) * (static_cast<size_t>(s.q_tokens) * s.q_heads + 32));
+  return align_up(2 * sizeof(float) * static_cast<size_t>(s.q_tokens) * s.q_heads);
 }
 
 int head_buf(const dmuon_attention_shape& s, const char* name, const void* p, int64_t tokens, int64_t heads,

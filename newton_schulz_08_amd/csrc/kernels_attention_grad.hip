@@ -147,18 +147,17 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
       for (int st = 0; st < S::kSteps; ++st) s = mma(frag_rows<DT, DP>(kt, kb, st), qf[st], s);
 #pragma unroll
       for (int st = 0; st < S::kSteps; ++st) dp = mma(frag_rows<DT, DP>(vt, kb, st), df[st], dp);
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        dp[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -lse)) * (dp[i] - delta);
       const bool mask = key0 + 32 > p.lk || (a.causal && key0 + 31 > wlo + shift) ||
                         (a.window && key0 < whi + shift - a.window + 1);
       if (mask) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int key = key0 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
-          if (key > hi || key < lo) dp[i] = 0.0f;
+          if (key > hi || key < lo) s[i] = -INFINITY;
         }
       }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) dp[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -lse)) * (dp[i] - delta);
       // A row's ds add up to 0, so what its keys have in common cancels in dq, but
       // not in the errors of rounding ds to bf16: with those alone dq of trained
       // keys is half as far off again as its own rounding.  The product takes ds
@@ -185,23 +184,21 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
 }
 
 // Where the tile's keys and values stay: their fragments in registers, or, where
-// two sums of a head fill those, the values in LDS (bf16 from 128 on: two waves a
-// SIMD at 128, no spilling at 256), or both in memory and read again for every
-// tile of rows (fp32 beyond 128: neither has room).
+// two sums of a head fill those, the values in LDS (bf16 from 128 on), or both in
+// memory and read again for every tile of rows (fp32 beyond 128).
 template <int DT, int DP> struct Held {
   static constexpr bool kMemory = DT == kF32 && DP > 128;
   static constexpr bool kValuesLds = DT == kBF16 && DP >= 128;
-  static constexpr int kWavesPerSimd = DT == kBF16 && DP <= 128 ? 2 : 1;
 };
 
 template <int DT, int DP, bool VEC>
-__global__ __launch_bounds__(kThreads, (Held<DT, DP>::kWavesPerSimd)) void attention_dkv_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void attention_dkv_kernel(AttnArgs a) {
   using S = Shape<DT, DP>;
   using T = typename S::T;
   using H = Held<DT, DP>;
   constexpr int kTileBytes = 32 * S::kPitch, kValues = H::kValuesLds ? kAttnTile * S::kPitch : 0;
   constexpr int kStats = 4 * kTileBytes;   // lse, delta of 32 rows; twice
-  __shared__ __attribute__((aligned(16))) char lds[4 * kTileBytes + 512 + kValues];   // Q, dout; twice
+  __shared__ __attribute__((aligned(16))) char lds[kStats + 512 + kValues];   // Q, dout; twice
 
   const int head = blockIdx.x % a.k_heads;
   const Place p = place(a, blockIdx.x / a.k_heads, true);
@@ -216,15 +213,13 @@ __global__ __launch_bounds__(kThreads, (Held<DT, DP>::kWavesPerSimd)) void atten
   const int begin = first_q * a.group, end = end_q * a.group;
   const int tiles = end > begin ? (end - begin + 31) / 32 : 0;
 
-  const int key = p.row0 + wave * 32 + (lane & 31);
-  const bool any = key < p.lk;
-  const int64_t token = p.k0 + (any ? key : last);
+  const int w0 = p.row0 + wave * 32, w1 = min(w0 + 32, p.lk) - 1;   // this wave's keys
+  const bool wave_any = w0 < p.lk;
+  const int key = w0 + (lane & 31);
   const T* kbase = static_cast<const T*>(a.k) + p.k0 * a.ks + static_cast<int64_t>(head) * a.dim;
   const T* vbase = static_cast<const T*>(a.v) + p.k0 * a.vs + static_cast<int64_t>(head) * a.dim;
-  const T* krow = kbase + (any ? key : last) * a.ks;
-  const T* vrow = vbase + (any ? key : last) * a.vs;
-  const int w0 = p.row0 + wave * 32, w1 = min(w0 + 31, p.lk - 1);   // this wave's keys
-  const bool wave_any = w0 < p.lk;
+  const T* krow = kbase + min(key, last) * a.ks;
+  const T* vrow = vbase + min(key, last) * a.vs;
   Frag<DT> kf[H::kMemory ? 1 : S::kSteps], vf[H::kMemory || H::kValuesLds ? 1 : S::kSteps];
   if constexpr (!H::kMemory)
 #pragma unroll
@@ -258,21 +253,18 @@ __global__ __launch_bounds__(kThreads, (Held<DT, DP>::kWavesPerSimd)) void atten
   auto fetch = [&](int tile) {
     char* to = lds + (tile & 1) * 2 * kTileBytes;
     const int r0 = begin + tile * 32;
-    bool done = false;
+    // 32 rows' pairs; behind the last row, the last one's
+    if (wave == 0)
+      dma4(uniform_ptr(sbase + 2 * static_cast<int64_t>(r0)), static_cast<uint32_t>(8 * min(lane >> 1, end - 1 - r0) + 4 * (lane & 1)),
+           __builtin_amdgcn_readfirstlane(lds_address(lds + kStats)) + (tile & 1) * 256);
     if constexpr (VEC)
       if (even && r0 + 32 <= end) {
         fill_q.whole(to, qbase + at(r0, a.qs), a.dim);
         fill_d.whole(to + kTileBytes, dbase + at(r0, a.dos), a.dim);
-        done = true;
+        return;
       }
-    if (!done) {
-      fill_q.any(to, a.dim, [&](int r) { return qbase + at(min(r0 + r, end - 1), a.qs); });
-      fill_d.any(to + kTileBytes, a.dim, [&](int r) { return dbase + at(min(r0 + r, end - 1), a.dos); });
-    }
-    // 32 rows' pairs; those behind the last row (the room holds a tile more) are masked
-    if (wave == 0)
-      dma4(uniform_ptr(sbase + 2 * static_cast<int64_t>(r0)), static_cast<uint32_t>(lane) * 4,
-           __builtin_amdgcn_readfirstlane(lds_address(lds + kStats)) + (tile & 1) * 256);
+    fill_q.any(to, a.dim, [&](int r) { return qbase + at(min(r0 + r, end - 1), a.qs); });
+    fill_d.any(to + kTileBytes, a.dim, [&](int r) { return dbase + at(min(r0 + r, end - 1), a.dos); });
   };
   f32x16 dk[S::kBlocks], dv[S::kBlocks];
 #pragma unroll
@@ -303,26 +295,22 @@ __global__ __launch_bounds__(kThreads, (Held<DT, DP>::kWavesPerSimd)) void atten
       for (int st = 0; st < S::kSteps; ++st) s = mma(frag_rows<DT, DP>(qt, 0, st), key_frag(st), s);
 #pragma unroll
       for (int st = 0; st < S::kSteps; ++st) dp = mma(frag_rows<DT, DP>(dt, 0, st), value_frag(st), dp);
-      const float* stat = reinterpret_cast<const float*>(lds + kStats + (tile & 1) * 256) + 8 * hf;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = 8 * (i >> 2) + (i & 3);
-        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -stat[2 * r]));
-        dp[i] = s[i] * (dp[i] - stat[2 * r + 1]);
-      }
       const bool mask = r0 + 32 > end || (a.causal && w1 > qlo + shift) || (a.window && w0 <= qhi + shift - a.window);
       if (mask) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int r = r0 + 8 * (i >> 2) + 4 * hf + (i & 3), q = query_of(a, r) + shift;
-          if (r >= end || (a.causal && key > q) || (a.window && key <= q - a.window)) s[i] = dp[i] = 0.0f;
+          if (r >= end || (a.causal && key > q) || (a.window && key <= q - a.window)) s[i] = -INFINITY;
         }
       }
+      const float* stat = reinterpret_cast<const float*>(lds + kStats + (tile & 1) * 256) + 8 * hf;
       Frag<DT> pf[2], ds[2];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        pf[i >> 3].set(i & 7, s[i]);
-        ds[i >> 3].set(i & 7, dp[i]);
+        const int r = 8 * (i >> 2) + (i & 3);
+        const float e = __builtin_amdgcn_exp2f(fmaf(s[i], c, -stat[2 * r]));
+        pf[i >> 3].set(i & 7, e);
+        ds[i >> 3].set(i & 7, e * (dp[i] - stat[2 * r + 1]));
       }
 #pragma unroll
       for (int b = 0; b < S::kBlocks; ++b)
@@ -334,7 +322,8 @@ __global__ __launch_bounds__(kThreads, (Held<DT, DP>::kWavesPerSimd)) void atten
     }
     tiles_landed();
   }
-  if (!any) return;
+  if (key >= p.lk) return;
+  const int64_t token = p.k0 + key;
   store_row<DT, DP, VEC>(static_cast<T*>(a.dk) + token * a.dks + static_cast<int64_t>(head) * a.dim, dk, a.scale, a.dim);
   store_row<DT, DP, VEC>(static_cast<T*>(a.dv) + token * a.dvs + static_cast<int64_t>(head) * a.dim, dv, 1.0f, a.dim);
 }
