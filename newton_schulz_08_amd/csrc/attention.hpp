@@ -29,8 +29,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) char* lds_t;
-typedef __attribute__((address_space(3))) bf16x4* lds_bf16x4_t;
+// LDS is addressed as such throughout: a cast from a general pointer would test it for null.
+template <typename T> using lptr = __attribute__((address_space(3))) T*;
+typedef lptr<char> lds_t;
 
 template <int DT, int DP> struct Shape {
   using T = typename OpElem<DT>::T;
@@ -66,17 +67,17 @@ __device__ __forceinline__ f32x16 mma(const Frag<kF32>& a, const Frag<kF32>& b, 
 }
 
 // Fragment `step` of a tile's rows row0 .. row0 + 31, steps along the head.
-template <int DT, int DP> __device__ __forceinline__ Frag<DT> frag_rows(const char* tile, int row0, int step) {
+template <int DT, int DP> __device__ __forceinline__ Frag<DT> frag_rows(lds_t tile, int row0, int step) {
   using S = Shape<DT, DP>;
   const int lane = threadIdx.x & 63, row = row0 + (lane & 31), hf = lane >> 5, sw = S::swizzle(lane & 31);
-  const char* at = tile + row * S::kPitch;
+  const lds_t at = tile + row * S::kPitch;
   Frag<DT> f;
   if constexpr (DT == kBF16) {
-    f.v = *reinterpret_cast<const bf16x8*>(at + (((2 * step + hf) ^ sw) << 4));
+    f.v = *reinterpret_cast<lptr<const bf16x8>>(at + (((2 * step + hf) ^ sw) << 4));
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const f32v4 x = *reinterpret_cast<const f32v4*>(at + (((4 * step + 2 * hf + h) ^ sw) << 4));
+      const f32v4 x = *reinterpret_cast<lptr<const f32v4>>(at + (((4 * step + 2 * hf + h) ^ sw) << 4));
 #pragma unroll
       for (int i = 0; i < 4; ++i) f.v[4 * h + i] = x[i];
     }
@@ -85,7 +86,7 @@ template <int DT, int DP> __device__ __forceinline__ Frag<DT> frag_rows(const ch
 }
 // Fragment of columns 32 block .. + 31 of the head, steps along the tile's
 // rows: the 16 from row0 on, in the order of a result block's registers.
-template <int DT, int DP> __device__ __forceinline__ Frag<DT> frag_cols(const char* tile, int row0, int block) {
+template <int DT, int DP> __device__ __forceinline__ Frag<DT> frag_cols(lds_t tile, int row0, int block) {
   using S = Shape<DT, DP>;
   const int lane = threadIdx.x & 63, hf = lane >> 5;
   Frag<DT> f;
@@ -97,8 +98,8 @@ template <int DT, int DP> __device__ __forceinline__ Frag<DT> frag_cols(const ch
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int row = row0 + 8 * h + 4 * hf + t;
-      const char* at = tile + row * S::kPitch + (((4 * block + 2 * g + (a >> 1)) ^ S::swizzle(row)) << 4) + 8 * (a & 1);
-      part[h] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(reinterpret_cast<lds_bf16x4_t>((lds_t)at));
+      const lds_t at = tile + row * S::kPitch + (((4 * block + 2 * g + (a >> 1)) ^ S::swizzle(row)) << 4) + 8 * (a & 1);
+      part[h] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(reinterpret_cast<lptr<bf16x4>>(at));
     }
     f.v = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
   } else {
@@ -106,7 +107,7 @@ template <int DT, int DP> __device__ __forceinline__ Frag<DT> frag_cols(const ch
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int row = row0 + 8 * (i >> 2) + 4 * hf + (i & 3);
-      f.v[i] = *reinterpret_cast<const float*>(tile + row * S::kPitch + (((col >> 2) ^ S::swizzle(row)) << 4) + 4 * (col & 3));
+      f.v[i] = *reinterpret_cast<lptr<const float>>(tile + row * S::kPitch + (((col >> 2) ^ S::swizzle(row)) << 4) + 4 * (col & 3));
     }
   }
   return f;
@@ -156,9 +157,7 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t voff, uint32_t 
 __device__ __forceinline__ void dma4(const void* base, uint32_t voff, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(dst) : "memory");
 }
-__device__ __forceinline__ uint32_t lds_address(const char* p) {
-  return static_cast<uint32_t>(reinterpret_cast<size_t>((lds_t)p));   // address-space cast
-}
+__device__ __forceinline__ uint32_t lds_address(lds_t p) { return static_cast<uint32_t>(reinterpret_cast<size_t>(p)); }
 __device__ __forceinline__ const char* uniform_ptr(const void* p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
   const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
@@ -200,7 +199,7 @@ template <int DT, int DP, int R, bool VEC> struct Filler {
     else if (voff != kNone) dma16(base, voff, dst);
   }
   // A whole tile whose first row begins at `first`.
-  __device__ __forceinline__ void whole(char* tile, const void* first, int dim) const {
+  __device__ __forceinline__ void whole(lds_t tile, const void* first, int dim) const {
     static_assert(VEC, "by element: any()");
     const char* base = uniform_ptr(first);
     const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_address(tile));
@@ -210,7 +209,7 @@ template <int DT, int DP, int R, bool VEC> struct Filler {
   }
   // Any tile: address(row) is where the row's head begins; rows that do not
   // exist take one that does.
-  template <typename Address> __device__ __forceinline__ void any(char* tile, int dim, Address&& address) const {
+  template <typename Address> __device__ __forceinline__ void any(lds_t tile, int dim, Address&& address) const {
     if constexpr (VEC) {
       const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_address(tile));
       const char* base = uniform_ptr(address(0));
@@ -224,13 +223,13 @@ template <int DT, int DP, int R, bool VEC> struct Filler {
       for (int e = threadIdx.x; e < R * DP; e += 64 * kWaves) {
         const int row = e / DP, d = e % DP, byte = d * S::kElem;
         const T x = d < dim ? gmem(address(row))[d] : static_cast<T>(0.0f);
-        *reinterpret_cast<T*>(tile + row * S::kPitch + (((byte >> 4) ^ S::swizzle(row)) << 4) + (byte & 15)) = x;
+        *reinterpret_cast<lptr<T>>(tile + row * S::kPitch + (((byte >> 4) ^ S::swizzle(row)) << 4) + (byte & 15)) = x;
       }
     }
   }
 };
-__device__ __forceinline__ void clear_tiles(char* lds, int bytes) {
-  for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16) *reinterpret_cast<f32v4*>(lds + i) = f32v4{};
+__device__ __forceinline__ void clear_tiles(lds_t lds, int bytes) {
+  for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16) *reinterpret_cast<lptr<f32v4>>(lds + i) = f32v4{};
 }
 
 // A block's place: sequence, tile of it, and the sequence's extent.

@@ -46,7 +46,8 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<DT, DP>())) void attentio
   constexpr int kKeys = S::kPitch <= 512 ? 64 : 32;          // of a tile
   constexpr int kKb = kKeys / 32;
   constexpr int kTileBytes = kKeys * S::kPitch;
-  __shared__ __attribute__((aligned(16))) char lds[4 * kTileBytes];   // K, V; twice
+  __shared__ __attribute__((aligned(16))) char shared[4 * kTileBytes];   // K, V; twice
+  const lds_t lds = (lds_t)shared;
 
   // heads vary fastest: the blocks of one XCD share few heads' keys.  The last
   // tiles of a causal sequence have the most keys: they start first.
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<DT, DP>())) void attentio
   fill_k.init(a.dim, [&](int r) { return static_cast<uint32_t>(r) * static_cast<uint32_t>(a.ks * S::kElem); });
   fill_v.init(a.dim, [&](int r) { return static_cast<uint32_t>(r) * static_cast<uint32_t>(a.vs * S::kElem); });
   auto fetch = [&](int tile) {
-    char* to = lds + (tile & 1) * 2 * kTileBytes;
+    const lds_t to = lds + (tile & 1) * 2 * kTileBytes;
     const int key0 = begin + tile * kKeys;
     if constexpr (VEC)
       if (key0 + kKeys <= p.lk) {
@@ -121,8 +122,8 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<DT, DP>())) void attentio
   }
   for (int tile = 0; tile < tiles; ++tile) {
     if (tile + 1 < tiles) fetch(tile + 1);
-    const char* kt = lds + (tile & 1) * 2 * kTileBytes;
-    const char* vt = kt + kTileBytes;
+    const lds_t kt = lds + (tile & 1) * 2 * kTileBytes;
+    const lds_t vt = kt + kTileBytes;
     const int key0 = begin + tile * kKeys;
     const bool see = wave_any && (!a.causal || key0 <= whi + shift) && (!a.window || key0 + kKeys > wlo + shift - a.window + 1);
     if (see) {

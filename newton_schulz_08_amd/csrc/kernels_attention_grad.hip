@@ -69,7 +69,8 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
   using T = typename S::T;
   constexpr int kKeys = S::kPitch <= 256 ? 64 : 32;
   constexpr int kTileBytes = kKeys * S::kPitch;
-  __shared__ __attribute__((aligned(16))) char lds[4 * kTileBytes];   // K, V; twice
+  __shared__ __attribute__((aligned(16))) char shared[4 * kTileBytes];   // K, V; twice
+  const lds_t lds = (lds_t)shared;
 
   const int head = blockIdx.x % a.k_heads, rest = blockIdx.x / a.k_heads;
   const Place p = place(a, a.slots - 1 - rest, false);
@@ -109,7 +110,7 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
   fill_k.init(a.dim, [&](int r) { return static_cast<uint32_t>(r) * static_cast<uint32_t>(a.ks * S::kElem); });
   fill_v.init(a.dim, [&](int r) { return static_cast<uint32_t>(r) * static_cast<uint32_t>(a.vs * S::kElem); });
   auto fetch = [&](int tile) {
-    char* to = lds + (tile & 1) * 2 * kTileBytes;
+    const lds_t to = lds + (tile & 1) * 2 * kTileBytes;
     const int key0 = begin + tile * kKeys;
     if constexpr (VEC)
       if (key0 + kKeys <= p.lk) {
@@ -134,8 +135,8 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
   }
   for (int tile = 0; tile < tiles; ++tile) {
     if (tile + 1 < tiles) fetch(tile + 1);
-    const char* kt = lds + (tile & 1) * 2 * kTileBytes;
-    const char* vt = kt + kTileBytes;
+    const lds_t kt = lds + (tile & 1) * 2 * kTileBytes;
+    const lds_t vt = kt + kTileBytes;
 #pragma unroll 1
     for (int kb = 0; kb < kKeys; kb += 32) {
       const int key0 = begin + tile * kKeys + kb;
@@ -198,7 +199,8 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
   using H = Held<DT, DP>;
   constexpr int kTileBytes = 32 * S::kPitch, kValues = H::kValuesLds ? kAttnTile * S::kPitch : 0;
   constexpr int kStats = 4 * kTileBytes;   // lse, delta of 32 rows; twice
-  __shared__ __attribute__((aligned(16))) char lds[kStats + 512 + kValues];   // Q, dout; twice
+  __shared__ __attribute__((aligned(16))) char shared[kStats + 512 + kValues];   // Q, dout; twice
+  const lds_t lds = (lds_t)shared;
 
   const int head = blockIdx.x % a.k_heads;
   const Place p = place(a, blockIdx.x / a.k_heads, true);
@@ -227,7 +229,7 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
       kf[s] = frag_global<DT, VEC>(krow, s, a.dim);
       if constexpr (!H::kValuesLds) vf[s] = frag_global<DT, VEC>(vrow, s, a.dim);
     }
-  char* values = lds + kStats + 512;
+  const lds_t values = lds + kStats + 512;
   auto key_frag = [&](int st) {
     if constexpr (H::kMemory) return frag_global<DT, VEC>(krow, st, a.dim);
     else return kf[st];
@@ -251,7 +253,7 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
   fill_q.init(a.dim, [&](int r) { return static_cast<uint32_t>(at(r, a.qs) * S::kElem); });
   fill_d.init(a.dim, [&](int r) { return static_cast<uint32_t>(at(r, a.dos) * S::kElem); });
   auto fetch = [&](int tile) {
-    char* to = lds + (tile & 1) * 2 * kTileBytes;
+    const lds_t to = lds + (tile & 1) * 2 * kTileBytes;
     const int r0 = begin + tile * 32;
     // 32 rows' pairs; behind the last row, the last one's
     if (wave == 0)
@@ -272,7 +274,7 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
   const float c = a.scale * kLog2e;
   if (tiles > 0) {
     if (VEC && a.dim < DP) {
-      clear_tiles(lds, sizeof(lds));
+      clear_tiles(lds, sizeof(shared));
       __syncthreads();
     }
     if constexpr (H::kValuesLds) {
@@ -284,8 +286,8 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
   }
   for (int tile = 0; tile < tiles; ++tile) {
     if (tile + 1 < tiles) fetch(tile + 1);
-    const char* qt = lds + (tile & 1) * 2 * kTileBytes;
-    const char* dt = qt + kTileBytes;
+    const lds_t qt = lds + (tile & 1) * 2 * kTileBytes;
+    const lds_t dt = qt + kTileBytes;
     const int r0 = begin + tile * 32, r1 = min(r0 + 31, end - 1);
     const int qlo = query_of(a, r0), qhi = query_of(a, r1);
     const bool see = wave_any && (!a.causal || w0 <= qhi + shift) && (!a.window || w1 > qlo + shift - a.window);
@@ -303,7 +305,7 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
           if (r >= end || (a.causal && key > q) || (a.window && key <= q - a.window)) s[i] = -INFINITY;
         }
       }
-      const float* stat = reinterpret_cast<const float*>(lds + kStats + (tile & 1) * 256) + 8 * hf;
+      const lptr<const float> stat = reinterpret_cast<lptr<const float>>(lds + kStats + (tile & 1) * 256) + 8 * hf;
       Frag<DT> pf[2], ds[2];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
