@@ -21,6 +21,8 @@
 // unnormed sum, maximum and weight; a second launch joins them.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "attention.hpp"
 
 namespace dmuon {
@@ -38,6 +40,11 @@ constexpr float kSlack = 8.0f;
 
 // Unnormed sums of a slice: rows x DP, then maximum and weight of each row.
 __host__ __device__ constexpr int64_t slice_floats(int dp) { return static_cast<int64_t>(kAttnTile) * (dp + 2); }
+
+// lse of a row with maximum m (base 2) and weight l.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0.0f ? kNone : l;
+}
 
 template <int DT, int DP, bool VEC>
 __global__ __launch_bounds__(kThreads, (waves_per_simd<DT, DP>())) void attention_kernel(AttnArgs a) {
@@ -193,38 +200,56 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<DT, DP>())) void attentio
   }
   if (!any) return;
   store_row<DT, DP, VEC>(static_cast<T*>(a.o) + token * a.os + static_cast<int64_t>(qh) * a.dim, o, l > 0.0f ? 1.0f / l : l, a.dim);
-  if (lane < 32) gmem(a.lse)[static_cast<int64_t>(qh) * a.q_tokens + token] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0.0f ? kNone : l;
+  if (lane < 32) gmem(a.lse)[static_cast<int64_t>(qh) * a.q_tokens + token] = row_lse(m, l);
 }
 
-// Joins a tile's slices: one wave a row, in the slices' order.
-template <int DT, int DP> __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs a) {
+// Joins a tile's slices: one wave a row, in the slices' order.  The slices' maxima
+// and weights are loaded by a lane each, their sums eight at a time.
+template <int DT, int DP> __global__ __launch_bounds__(64) void attention_join_kernel(AttnArgs a) {
   using T = typename OpElem<DT>::T;
+  constexpr int kRun = (DP + 63) / 64;
   const int head = blockIdx.x % a.k_heads, rest = blockIdx.x / a.k_heads;
   const Place p = place(a, a.slots - 1 - rest, false);
-  const int r = blockIdx.y * kWaves + (threadIdx.x >> 6), lane = threadIdx.x & 63, row = p.row0 + r;
+  const int r = blockIdx.y, lane = threadIdx.x, row = p.row0 + r;
   if (!p.any || row >= p.rows) return;
   const int64_t step = static_cast<int64_t>(a.k_heads) * a.slots * slice_floats(DP);
   const float* part = a.part + static_cast<int64_t>(blockIdx.x) * slice_floats(DP);
   const float* ml = part + static_cast<int64_t>(kAttnTile) * DP + 2 * r;
-  float m = kNone;
-  for (int s = 0; s < a.slices; ++s) m = fmaxf(m, gmem(ml)[s * step]);
-  const float ms = m == kNone ? 0.0f : m;
-  float l = 0.0f, o[DP / 64 + 1] = {};
-  for (int s = 0; s < a.slices; ++s) {
-    const float by = __builtin_amdgcn_exp2f(gmem(ml)[s * step] - ms);
-    l += by * gmem(ml)[s * step + 1];
+  part += static_cast<int64_t>(r) * DP;
+  const bool mine = lane < a.slices;   // at most 64
+  float m = mine ? gmem(ml)[lane * step] : kNone, l = mine ? gmem(ml)[lane * step + 1] : 0.0f;
+  float top = m;
 #pragma unroll
-    for (int k = 0; k < DP / 64 + 1; ++k)
-      if (64 * k + lane < DP) o[k] += by * gmem(part)[s * step + static_cast<int64_t>(r) * DP + 64 * k + lane];
+  for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x, 64));
+  const float by = mine ? __builtin_amdgcn_exp2f(m - (top == kNone ? 0.0f : top)) : 0.0f;
+  l *= by;
+#pragma unroll
+  for (int x = 32; x > 0; x >>= 1) l += __shfl_xor(l, x, 64);
+  float o[kRun] = {};
+  for (int s0 = 0; s0 < a.slices; s0 += 8) {
+    float v[8][kRun];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) {
+        const int64_t at = least(s0 + s, a.slices - 1) * step;   // every lane loads
+        v[s][k] = gmem(part)[at + (64 * k + lane < DP ? 64 * k + lane : 0)];
+      }
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const float w = __shfl(by, s0 + s, 64);                  // 0 behind the last slice
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) o[k] = w == 0.0f ? o[k] : o[k] + w * v[s][k];
+    }
   }
   const int qi = query_of(a, row), qh = head * a.group + row - qi * a.group;
   const int64_t token = p.q0 + qi;
   T* out = static_cast<T*>(a.o) + token * a.os + static_cast<int64_t>(qh) * a.dim;
-  const float by = l > 0.0f ? 1.0f / l : l;
+  const float inv = l > 0.0f ? 1.0f / l : l;
 #pragma unroll
-  for (int k = 0; k < DP / 64 + 1; ++k)
-    if (64 * k + lane < a.dim) gmem(out)[64 * k + lane] = static_cast<T>(o[k] * by);
-  if (lane == 0) gmem(a.lse)[static_cast<int64_t>(qh) * a.q_tokens + token] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0.0f ? kNone : l;
+  for (int k = 0; k < kRun; ++k)
+    if (64 * k + lane < a.dim) gmem(out)[64 * k + lane] = static_cast<T>(o[k] * inv);
+  if (lane == 0) gmem(a.lse)[static_cast<int64_t>(qh) * a.q_tokens + token] = row_lse(top, l);
 }
 
 template <int DT, int DP> hipError_t run(const AttnArgs& a, hipStream_t stream) {
@@ -235,7 +260,9 @@ template <int DT, int DP> hipError_t run(const AttnArgs& a, hipStream_t stream) 
   if (a.slices > 1) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attention_join_kernel<DT, DP><<<dim3(tiles, kAttnTile / kWaves), dim3(kThreads), 0, stream>>>(a);
+    // no tile has more rows than there are
+    const int rows = static_cast<int>(std::min<int64_t>(kAttnTile, static_cast<int64_t>(a.q_tokens) * a.group));
+    attention_join_kernel<DT, DP><<<dim3(tiles, rows), dim3(64), 0, stream>>>(a);
   }
   return hipGetLastError();
 }
