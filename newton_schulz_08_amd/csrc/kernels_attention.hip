@@ -157,9 +157,11 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<DT, DP>())) void attentio
       for (int kb = 0; kb < kKb; ++kb)
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
-      top = fmaxf(top, other_half(top)) * c;
-      // nothing visible so far: any finite maximum will do, exp2(-inf) is 0
-      if (__any(top > m + kSlack)) {
+      // m is the row's, the same in both lanes that share it; the lanes' own maxima
+      // decide whether it still serves.  Nothing visible so far: any finite
+      // maximum will do, exp2(-inf) is 0.
+      if (__any(top * c > m + kSlack)) {
+        top = fmaxf(top, other_half(top)) * c;
         const float mn = fmaxf(m, top), by = __builtin_amdgcn_exp2f(m - (mn == kNone ? 0.0f : mn));
         m = mn;
         l *= by;

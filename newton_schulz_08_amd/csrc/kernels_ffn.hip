@@ -553,6 +553,9 @@ template <int MODE> __global__ __launch_bounds__(256, 2) void ffn_tile32_kernel(
   for (int64_t st = first; st < end; ++st) {
     const int b = static_cast<int>(st - first) & 1;
     if (st + 1 < end) load(st + 1);
+    // a stage's sum is added as a whole: the roundings of a long contraction then
+    // grow with its stages, not with its steps
+    f32x4 part[4] = {};
 #pragma unroll
     for (int s = 0; s < kStep32 / 16; ++s) {
       const f32x4 fp = Stage32<kPT>::read(lds[b][0], s, wave);
@@ -562,8 +565,10 @@ template <int MODE> __global__ __launch_bounds__(256, 2) void ffn_tile32_kernel(
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fq[j][e], fp[e], acc[j], 0, 0, 0);
+        for (int j = 0; j < 4; ++j) part[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fq[j][e], fp[e], part[j], 0, 0, 0);
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] += part[j];
     if (st + 1 < end) store(b ^ 1, st + 1);
     __syncthreads();
   }
@@ -670,13 +675,19 @@ template <int DT, int G> __global__ __launch_bounds__(64 * kFewWaves) void ffn_f
         ox[n][t] = octet<DT>(static_cast<const T*>(a.x) + (token < a.n ? token : 0) * a.xs, token < a.n, k, a.dim, a.vec);
       }
     }
+    f32x4 part[2][G] = {};   // added as a whole, as the fp32 tiles' stages are
 #pragma unroll
     for (int n = 0; n < kUnroll; ++n)
 #pragma unroll
       for (int t = 0; t < G; ++t) {
-        acc[0][t] = mma(og[n], ox[n][t], acc[0][t]);
-        acc[1][t] = mma(ou[n], ox[n][t], acc[1][t]);
+        part[0][t] = mma(og[n], ox[n][t], part[0][t]);
+        part[1][t] = mma(ou[n], ox[n][t], part[1][t]);
       }
+#pragma unroll
+    for (int t = 0; t < G; ++t) {
+      acc[0][t] += part[0][t];
+      acc[1][t] += part[1][t];
+    }
   }
   if (wave > 0)
 #pragma unroll
