@@ -97,7 +97,7 @@ int64_t attn_q_slots(const dmuon_attention_shape& s) {
 }
 int check_attn_grid(const dmuon_attention_shape& s) {
   const int64_t slots = std::max(attn_q_slots(s), attn_slots(s.k_tokens, s.sequences));
-  return check_range(slots * s.k_heads, 0, int64_t{1} << 24, "tiles (tokens / 128 + sequences, times k_heads)");
+  return check_range(slots * s.k_heads, 0, (int64_t{1} << 24) - 1, "tiles (tokens / 128 + sequences, times k_heads)");
 }
 
 // Parts of a tile's keys: where the tiles alone leave CUs idle and the
@@ -161,6 +161,15 @@ int check_ffn(const dmuon_gated_ffn_shape* s) {
   DMUON_TRY(check_range(s->dim, 1, DMUON_MAX_DIM, "dim"));
   DMUON_TRY(check_range(s->hidden, 1, DMUON_MAX_DIM, "hidden"));
   return check_range(s->activation, DMUON_ACT_SILU, DMUON_ACT_GELU, "activation");
+}
+
+// Threads of a launch fit 32 bits: 512 to a 256 x 256 tile of bf16, 256 to a 64 x 64
+// one of fp32 (of the hidden width half of that, twice).
+int check_ffn_grid(const dmuon_gated_ffn_shape& s, bool back) {
+  const int64_t tile = s.dtype == DMUON_BF16 ? 256 : 64, most = s.dtype == DMUON_BF16 ? int64_t{1} << 23 : int64_t{1} << 24;
+  auto up = [](int64_t v, int64_t t) { return v / t + 1; };
+  const int64_t rows = up(s.tokens, tile), gated = rows * up(s.hidden, tile / 2), dx = back ? rows * up(s.dim, tile) : 0;
+  return check_range(std::max(gated, dx), 0, most - 1, "tiles (tokens times hidden or dim)");
 }
 
 int64_t whole_stages(int64_t v) { return (v + kFfnStage - 1) / kFfnStage * kFfnStage; }
@@ -488,6 +497,7 @@ int dmuon_gated_ffn_forward(const dmuon_gated_ffn_shape* shape, const void* x, i
   return guarded([&]() -> int {
     DMUON_TRY(check_ffn(shape));
     const dmuon_gated_ffn_shape& s = *shape;
+    DMUON_TRY(check_ffn_grid(s, false));
     const int64_t es = size_of(s.dtype), wbytes = s.tokens ? s.hidden * s.dim * es : 0;
     Buf b[5];
     DMUON_TRY(row_buf("x", x, s.tokens, s.dim, x_stride, s.dtype, false, &b[0]));
@@ -538,6 +548,7 @@ int dmuon_gated_ffn_backward(const dmuon_gated_ffn_shape* shape, const void* dh,
   return guarded([&]() -> int {
     DMUON_TRY(check_ffn(shape));
     const dmuon_gated_ffn_shape& s = *shape;
+    DMUON_TRY(check_ffn_grid(s, true));
     const int64_t es = size_of(s.dtype), wbytes = s.hidden * s.dim * es;
     Buf b[8];
     DMUON_TRY(row_buf("dh", dh, s.tokens, s.hidden, dh_stride, s.dtype, false, &b[0]));

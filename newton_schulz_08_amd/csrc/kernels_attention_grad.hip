@@ -18,6 +18,8 @@
 // their probabilities exp2(-infinity) = 0.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "attention.hpp"
 
 namespace dmuon {
@@ -35,7 +37,7 @@ template <int DT, int LANES, bool VEC> __global__ __launch_bounds__(kThreads) vo
   using T = typename OpElem<DT>::T;
   constexpr int M = 16 / static_cast<int>(sizeof(T));
   typedef T V __attribute__((ext_vector_type(M)));
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / LANES;
+  const int64_t row = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES;
   const int64_t token = row / a.q_heads;
   const int h = static_cast<int>(row - token * a.q_heads), d = threadIdx.x % LANES * M;
   if (token >= a.q_tokens) return;
@@ -211,7 +213,7 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
   // rows that see any of the tile's keys
   int first_q = 0, end_q = p.lq;
   if (a.causal) first_q = max(0, p.row0 - shift);
-  if (a.window) end_q = min(end_q, last - shift + a.window);
+  if (a.window) end_q = max(0, min(end_q, last - shift + a.window));   // times the group it stays within 32 bits
   const int begin = first_q * a.group, end = end_q * a.group;
   const int tiles = end > begin ? (end - begin + 31) / 32 : 0;
 
@@ -330,12 +332,15 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
   store_row<DT, DP, VEC>(static_cast<T*>(a.dv) + token * a.dvs + static_cast<int64_t>(head) * a.dim, dv, 1.0f, a.dim);
 }
 
+constexpr int64_t kGridLine = int64_t{1} << 20;   // blocks along a grid's first axis; the rows' come in lines of it
+
 template <int DT, int DP, bool VEC> hipError_t run(const AttnArgs& a, int k_slots, hipStream_t stream) {
   if (a.q_tokens > 0) {
     constexpr int kLanes = Shape<DT, DP>::kPitch / 16;
-    const int64_t threads = static_cast<int64_t>(a.q_tokens) * a.q_heads * kLanes;
-    attention_stats_kernel<DT, kLanes, VEC>
-        <<<dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream>>>(a);
+    const int64_t per = kThreads / kLanes, blocks = (static_cast<int64_t>(a.q_tokens) * a.q_heads + per - 1) / per;
+    const int64_t cols = std::min<int64_t>(blocks, kGridLine);
+    attention_stats_kernel<DT, kLanes, VEC><<<dim3(static_cast<unsigned>(cols), static_cast<unsigned>((blocks + cols - 1) / cols)),
+                                              dim3(kThreads), 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     attention_dq_kernel<DT, DP, VEC><<<dim3(static_cast<unsigned>(a.slots) * a.k_heads), dim3(kThreads), 0, stream>>>(a);

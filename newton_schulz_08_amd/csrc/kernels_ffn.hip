@@ -721,7 +721,7 @@ template <int DT> __global__ __launch_bounds__(256) void ffn_pad_kernel(const vo
                                                                         int width, int padded) {
   using T = typename OpElem<DT>::T;
   const int per = padded / 8;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t id = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
   const int64_t r = id / per;
   const int c = static_cast<int>(id % per) * 8;
   if (r >= rows) return;
@@ -794,8 +794,8 @@ hipError_t launch_ffn_few(int dt, const FfnArgs& a, hipStream_t stream) {
 }
 hipError_t launch_ffn_pad(int dt, const void* src, int64_t stride, void* dst, int64_t rows, int width, int padded,
                           hipStream_t stream) {
-  const int64_t units = rows * (padded / 8);
-  const dim3 blocks(static_cast<unsigned>((units + 255) / 256));
+  const int64_t all = (rows * (padded / 8) + 255) / 256, cols = std::min<int64_t>(all, int64_t{1} << 20);
+  const dim3 blocks(static_cast<unsigned>(cols), static_cast<unsigned>((all + cols - 1) / cols));
   if (dt == kF32) ffn::ffn_pad_kernel<kF32><<<blocks, dim3(256), 0, stream>>>(src, stride, dst, rows, width, padded);
   else ffn::ffn_pad_kernel<kBF16><<<blocks, dim3(256), 0, stream>>>(src, stride, dst, rows, width, padded);
   return hipGetLastError();

@@ -192,3 +192,15 @@ def test_binding_refuses_host_tensors_and_wrong_types():
     for f in (nsa.block_norm, lambda a, b: nsa.attention(a, b, b), lambda a, b: nsa.gated_ffn(a, b, b)):
         with pytest.raises(TypeError):
             f("x", t)
+
+
+def test_launches_beyond_a_grid(lib):
+    """As many tiles as a launch cannot hold; one sequence, or one token, fewer is taken as far as the operands."""
+    wide = dict(AT, shape=at_shape(q_tokens=0, k_tokens=0, sequences=1 << 22, q_heads=4, k_heads=4), q=0, k=0, v=0, out=0, lse=0)
+    refused(lib.dmuon_attention_forward, dict(AT, shape=at_shape(k_tokens=6)), [(wide, BAD)])
+    accepted(lib.dmuon_attention_forward, dict(wide, shape=at_shape(q_tokens=0, k_tokens=0, sequences=(1 << 22) - 1, q_heads=4, k_heads=4),
+                                               qo=addr(1), ko=addr(1) + (1 << 25), stream=None))
+    many = E.DMUON_MAX_TOKENS
+    refused(lib.dmuon_gated_ffn_forward, FF, [(dict(shape=ff_shape(tokens=many, hidden=65536), hs=65536), BAD),
+                                              (dict(shape=ff_shape(tokens=many, hidden=8192, dtype=0), hs=8192), BAD)])
+    refused(lib.dmuon_gated_ffn_backward, FFG, [(dict(shape=ff_shape(tokens=many, dim=65536, hidden=16, dtype=0), xs=65536, dxs=65536), BAD)])

@@ -119,3 +119,16 @@ def test_feed_forward_gradient_of_many_tokens(dtype):
     for what, t, d_, e in (("dw_gate", dg, a, ea), ("dw_up", du, b, eb)):
         w, e = d_.T @ x.double(), (e + add * d_.abs()).T @ x.double().abs()
         within(host(t[cols]), w.cpu().numpy(), (e * 1.01 + half * (w.abs() + e)).cpu().numpy(), what)
+
+
+def test_attention_gradient_of_one_query_behind_many_keys():
+    """1024 heads share four million keys, and a window leaves the query the last three of them."""
+    n, heads, window = 1 << 22, 1024, 3
+    q, dout = (torch.randn(1, heads, 1, device="cuda") for _ in range(2))
+    k, v = (torch.randn(n, 1, 1, device="cuda") for _ in range(2))
+    out, lse = nsa.attention(q, k, v, window=window)
+    dq, dk, dv = nsa.attention_grad(dout, q, k, v, out, lse, window=window)
+    assert not dk[:-window].any() and not dv[:-window].any()
+    for g, (w, b) in zip((dq, dk[-window:], dv[-window:]),
+                         ref.backward(dout, q, k[-window:], v[-window:], out, lse, [0, 1], [0, window], True, window, 1.0, F32)):
+        within(host(g), w.cpu().numpy(), b.cpu().numpy(), "gradient")
