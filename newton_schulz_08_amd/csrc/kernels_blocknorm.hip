@@ -235,6 +235,19 @@ template <int XDT, int BDT, int T> __global__ __launch_bounds__(kBlock<T>) void 
   gain(a.w[2], a.w_bf16, 0.0f, e, a.dim, gate);
 #pragma unroll
   for (int i = 0; i < 8; ++i) gd[i] *= gate[i];
+  // Sixteen waves leave 128 registers to each.  The next row beside this one does
+  // not fit them: a row of over 4096 is under way as a whole instead; and the
+  // gains are kept in LDS, each lane its own.
+  constexpr bool kAhead = T < 1024;
+  __shared__ f32v4 kept[kAhead ? 1 : 4][kAhead ? 1 : T];
+  if constexpr (!kAhead)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      kept[k][threadIdx.x] = f32v4{gpre[4 * k], gpre[4 * k + 1], gpre[4 * k + 2], gpre[4 * k + 3]};
+      kept[2 + k][threadIdx.x] = f32v4{gd[4 * k], gd[4 * k + 1], gd[4 * k + 2], gd[4 * k + 3]};
+    }
+  auto pre_gain = [&](int i) { if constexpr (kAhead) return gpre[i]; else return kept[i >> 2][threadIdx.x][i & 3]; };
+  auto post_gain = [&](int i) { if constexpr (kAhead) return gd[i]; else return kept[2 + (i >> 2)][threadIdx.x][i & 3]; };
   float acc[2][8] = {};
   RowSum<T, 3> sum3{red3};
   RowSum<T, 1> sum1{red1};
@@ -254,8 +267,9 @@ template <int XDT, int BDT, int T> __global__ __launch_bounds__(kBlock<T>) void 
     nh.load(h + r * a.hs, e, a.dim);
     if (dx) nd.load(dx + r * a.dxs, e, a.dim);
   };
-  ahead(row);
+  if (kAhead) ahead(row);
   for (; row < a.rows; row += step) {
+    if (!kAhead) ahead(row);
     nx.land(e, a.dim);
     ny.land(e, a.dim);
     nh.land(e, a.dim);
@@ -266,10 +280,10 @@ template <int XDT, int BDT, int T> __global__ __launch_bounds__(kBlock<T>) void 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       s[0] += cx[i] * cx[i];
-      s[1] += cy[i] * gpre[i] * cx[i];
+      s[1] += cy[i] * pre_gain(i) * cx[i];
       s[2] += ch[i] * ch[i];
     }
-    ahead(row + step);
+    if (kAhead) ahead(row + step);
     sum3(s);
     const float rx = 1.0f / sqrtf(s[0] * inv + a.eps);
     const float rh = a.post_norm ? 1.0f / sqrtf(s[2] * inv + a.eps) : 1.0f;
@@ -278,11 +292,11 @@ template <int XDT, int BDT, int T> __global__ __launch_bounds__(kBlock<T>) void 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float xh = cx[i] * rx, hh = ch[i] * rh;
-      out[i] = rx * (cy[i] * gpre[i] - xh * along) + cd[i];
+      out[i] = rx * (cy[i] * pre_gain(i) - xh * along) + cd[i];
       const float st = a.scale * out[i];
       acc[0][i] += cy[i] * xh;
       acc[1][i] += st * hh;
-      d[i] = st * gd[i];
+      d[i] = st * post_gain(i);
       u[0] += d[i] * hh;
     }
     row_loaded<T>(a);
