@@ -112,6 +112,36 @@ template <int DT, int DP> __device__ __forceinline__ Frag<DT> frag_cols(lds_t ti
   }
   return f;
 }
+// The 16 bytes from element d of a head on, wherever it lies, zeros behind it.
+// Every lane loads, from the head's last 16 bytes if its own reach behind them,
+// and moves those into place: a branch around a load would make the next one
+// wait for it.
+template <typename T> using Chunk = T __attribute__((ext_vector_type(16 / sizeof(T))));
+template <typename T> __device__ __forceinline__ Chunk<T> chunk_of(const T* head, int d, int dim) {
+  constexpr int M = 16 / static_cast<int>(sizeof(T));
+  const T zero = static_cast<T>(0.0f);
+  Chunk<T> x;
+  if (dim >= M) {
+    using L = typename Loose<T, M>::V;
+    const L v = *reinterpret_cast<gptr<const L>>(gmem(head + min(d, dim - M)));
+#pragma unroll
+    for (int i = 0; i < M; ++i) x[i] = v[i];
+    const int by = d - (dim - M);   // > 0: the elements lie that far up
+    if (by >= M) x = Chunk<T>{};
+#pragma unroll
+    for (int b = M / 2; b > 0; b >>= 1)
+      if (by > 0 && (by & b))
+#pragma unroll
+        for (int i = 0; i < M; ++i) x[i] = i + b < M ? x[i + b < M ? i + b : 0] : zero;
+  } else {
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      const T v = gmem(head)[min(d + i, dim - 1)];
+      x[i] = d + i < dim ? v : zero;
+    }
+  }
+  return x;
+}
 // Fragment `step` of one row in memory, zeros behind the head.  VEC: runs of 16
 // bytes are aligned and whole.
 template <int DT, bool VEC> __device__ __forceinline__ Frag<DT> frag_global(const void* row, int step, int dim) {
@@ -129,8 +159,7 @@ template <int DT, bool VEC> __device__ __forceinline__ Frag<DT> frag_global(cons
       x = *reinterpret_cast<gptr<const V>>(gmem(p + (d < dim ? d : 0)));
       if (d >= dim) x = V{};
     } else {
-#pragma unroll
-      for (int i = 0; i < M; ++i) x[i] = d + i < dim ? gmem(p)[d + i] : static_cast<T>(0.0f);
+      x = chunk_of(p, d, dim);
     }
 #pragma unroll
     for (int i = 0; i < M; ++i) f.v[M * h + i] = x[i];
@@ -171,7 +200,7 @@ __device__ __forceinline__ void tiles_landed() {
 }
 
 // Fills tiles of R rows, straight to LDS (VEC; the padding behind a head is left
-// alone, clear_tiles) or element by element.
+// alone, clear_tiles) or through registers, 16 bytes at a time.
 template <int DT, int DP, int R, bool VEC> struct Filler {
   using S = Shape<DT, DP>;
   using T = typename S::T;
@@ -200,7 +229,7 @@ template <int DT, int DP, int R, bool VEC> struct Filler {
   }
   // A whole tile whose first row begins at `first`.
   __device__ __forceinline__ void whole(lds_t tile, const void* first, int dim) const {
-    static_assert(VEC, "by element: any()");
+    static_assert(VEC, "through registers: any()");
     const char* base = uniform_ptr(first);
     const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_address(tile));
     const bool full = dim * S::kElem == S::kPitch;
@@ -220,10 +249,20 @@ template <int DT, int DP, int R, bool VEC> struct Filler {
         move(base, chunk * 16 < dim * S::kElem ? at : kNone, lds, u, false);
       }
     } else {
-      for (int e = threadIdx.x; e < R * DP; e += 64 * kWaves) {
-        const int row = e / DP, d = e % DP, byte = d * S::kElem;
-        const T x = d < dim ? gmem(address(row))[d] : static_cast<T>(0.0f);
-        *reinterpret_cast<lptr<T>>(tile + row * S::kPitch + (((byte >> 4) ^ S::swizzle(row)) << 4) + (byte & 15)) = x;
+      constexpr int kC = S::kRow / 16, kAll = R * kC, kAtOnce = 4;   // chunks under way in a thread
+#pragma unroll 1
+      for (int e0 = threadIdx.x; e0 < kAll; e0 += kAtOnce * kThreads) {
+        Chunk<T> x[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int e = min(e0 + u * kThreads, kAll - 1);
+          x[u] = chunk_of(address(e / kC), e % kC * (16 / S::kElem), dim);
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int e = e0 + u * kThreads, row = e / kC;
+          if (e < kAll) *reinterpret_cast<lptr<Chunk<T>>>(tile + row * S::kPitch + ((e % kC ^ S::swizzle(row)) << 4)) = x[u];
+        }
       }
     }
   }
