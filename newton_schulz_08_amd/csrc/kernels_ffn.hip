@@ -613,8 +613,6 @@ template <int DT, int MODE> __global__ __launch_bounds__(256) void ffn_join_kern
 }
 
 // ---------------------------------------------------------------- few tokens
-constexpr int kFewWaves = 4;
-
 template <int DT> struct Oct;   // eight consecutive steps of a row
 template <> struct Oct<kBF16> { bf16x8 v; };
 template <> struct Oct<kF32> { f32x4 v[2]; };
@@ -650,67 +648,82 @@ __device__ __forceinline__ f32x4 mma(const Oct<kF32>& a, const Oct<kF32>& b, f32
   return c;
 }
 
-// 16 rows of both weights a block, up to 16 G tokens; the waves take the steps
-// by turns, 32 at a time, and their sums meet in LDS in the waves' order.
-template <int DT, int G> __global__ __launch_bounds__(64 * kFewWaves) void ffn_few_kernel(FfnArgs a) {
+constexpr int kFewWaves = 4;
+
+// Eight steps from k on of a row whose runs of 16 bytes are whole and aligned:
+// every lane loads, so that no load waits for another.
+template <int DT> __device__ __forceinline__ Oct<DT> whole_octet(const void* row, int k, int dim) {
   using T = typename OpElem<DT>::T;
-  __shared__ float sums[kFewWaves - 1][2 * G][4][64];
+  const T* p = static_cast<const T*>(row) + (k < dim ? k : 0);
+  Oct<DT> o;
+  if constexpr (DT == kBF16) {
+    o.v = *reinterpret_cast<gptr<const bf16x8>>(gmem(p));
+  } else {
+    o.v[0] = *reinterpret_cast<gptr<const f32x4>>(gmem(p));
+    o.v[1] = *reinterpret_cast<gptr<const f32x4>>(gmem(p + 4));
+  }
+  if (k >= dim) o = Oct<DT>{};
+  return o;
+}
+
+// 16 rows of both weights a block, up to 16 G tokens; the waves take the steps by
+// turns, 32 U at a time, and their sums meet in LDS in the waves' order.
+template <int DT, int G, int U, bool VEC> __global__ __launch_bounds__(64 * kFewWaves) void ffn_few_kernel(FfnArgs a) {
+  using T = typename OpElem<DT>::T;
+  constexpr int kSums = 2 * G;   // of each weight with each 16 tokens
+  __shared__ f32x4 sums[kFewWaves - 1][kSums][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, oct = lane >> 4;
   const int f0 = blockIdx.x * 16, f = f0 + l16;
   const bool any = f < a.hidden;
-  const T* wg = static_cast<const T*>(a.wg) + static_cast<int64_t>(any ? f : 0) * a.ws;
-  const T* wu = static_cast<const T*>(a.wu) + static_cast<int64_t>(any ? f : 0) * a.ws;
-  f32x4 acc[2][G] = {};
-  constexpr int kUnroll = G == 1 ? 4 : G == 2 ? 2 : 1;   // fragments under way in front of their products
-  for (int k0 = wave * 32 * kUnroll; k0 < a.dim; k0 += 32 * kUnroll * kFewWaves) {
-    Oct<DT> og[kUnroll], ou[kUnroll], ox[kUnroll][G];
+  const int64_t row = static_cast<int64_t>(any ? f : a.hidden - 1) * a.ws;
+  const T* w[2] = {static_cast<const T*>(a.wg) + row, static_cast<const T*>(a.wu) + row};
+  const T* x[G];
+  bool has[G];
 #pragma unroll
-    for (int n = 0; n < kUnroll; ++n) {
+  for (int t = 0; t < G; ++t) {
+    has[t] = 16 * t + l16 < a.n;
+    x[t] = static_cast<const T*>(a.x) + (has[t] ? 16 * t + l16 : a.n - 1) * a.xs;
+  }
+  f32x4 acc[kSums] = {};
+  for (int k0 = wave * 32 * U; k0 < a.dim; k0 += 32 * U * kFewWaves) {
+    Oct<DT> ow[U][2], ox[U][G];
+#pragma unroll
+    for (int n = 0; n < U; ++n) {
       const int k = k0 + 32 * n + 8 * oct;
-      og[n] = octet<DT>(wg, any, k, a.dim, a.vec);
-      ou[n] = octet<DT>(wu, any, k, a.dim, a.vec);
 #pragma unroll
-      for (int t = 0; t < G; ++t) {
-        const int token = 16 * t + l16;
-        ox[n][t] = octet<DT>(static_cast<const T*>(a.x) + (token < a.n ? token : 0) * a.xs, token < a.n, k, a.dim, a.vec);
-      }
-    }
-    f32x4 part[2][G] = {};   // added as a whole, as the fp32 tiles' stages are
-#pragma unroll
-    for (int n = 0; n < kUnroll; ++n)
-#pragma unroll
-      for (int t = 0; t < G; ++t) {
-        part[0][t] = mma(og[n], ox[n][t], part[0][t]);
-        part[1][t] = mma(ou[n], ox[n][t], part[1][t]);
+      for (int r = 0; r < 2; ++r) {
+        if constexpr (VEC) ow[n][r] = whole_octet<DT>(w[r], k, a.dim);
+        else ow[n][r] = octet<DT>(w[r], any, k, a.dim, a.vec);
       }
 #pragma unroll
-    for (int t = 0; t < G; ++t) {
-      acc[0][t] += part[0][t];
-      acc[1][t] += part[1][t];
+      for (int t = 0; t < G; ++t) {
+        if constexpr (VEC) ox[n][t] = whole_octet<DT>(x[t], k, a.dim);
+        else ox[n][t] = octet<DT>(x[t], has[t], k, a.dim, a.vec);
+      }
     }
+    f32x4 part[kSums] = {};   // added as a whole, as the fp32 tiles' stages are
+#pragma unroll
+    for (int n = 0; n < U; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int t = 0; t < G; ++t) part[r * G + t] = mma(ow[n][r], ox[n][t], part[r * G + t]);
+#pragma unroll
+    for (int s = 0; s < kSums; ++s) acc[s] += part[s];
   }
   if (wave > 0)
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int t = 0; t < G; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sums[wave - 1][w * G + t][i][lane] = acc[w][t][i];
+    for (int s = 0; s < kSums; ++s) sums[wave - 1][s][lane] = acc[s];
   __syncthreads();
   if (wave > 0) return;
 #pragma unroll
+  for (int s = 0; s < kSums; ++s)
+#pragma unroll
+    for (int v = 0; v < kFewWaves - 1; ++v) acc[s] += sums[v][s][lane];
+#pragma unroll
   for (int t = 0; t < G; ++t) {
-    float g[4], u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      g[i] = acc[0][t][i];
-      u[i] = acc[1][t][i];
-#pragma unroll
-      for (int w = 0; w < kFewWaves - 1; ++w) {
-        g[i] += sums[w][t][i][lane];
-        u[i] += sums[w][G + t][i][lane];
-      }
-    }
+    const float g[4] = {acc[t][0], acc[t][1], acc[t][2], acc[t][3]};
+    const float u[4] = {acc[G + t][0], acc[G + t][1], acc[G + t][2], acc[G + t][3]};
     // lane l: token l & 15, rows 4 (l >> 4) .. + 3 of the weights
     finish_gated<DT, kFfnOut>(a, 16 * t + l16, f0 + 4 * oct, g, u);
   }
@@ -771,11 +784,15 @@ template <int DT, int MODE> int slices_of(const FfnArgs& a) {
   const int64_t most_ = stages_of<MODE>(a, kFfnStage) / 8;
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(DT == kBF16 ? 256 : 512) / tiles, most_, 16})));
 }
-template <int DT> hipError_t few(const FfnArgs& a, hipStream_t stream) {
+template <int DT, int G, int U> void few_any(const FfnArgs& a, hipStream_t stream) {
   const dim3 blocks((a.hidden + 15) / 16), threads(64 * kFewWaves);
-  if (a.n <= 16) ffn_few_kernel<DT, 1><<<blocks, threads, 0, stream>>>(a);
-  else if (a.n <= 32) ffn_few_kernel<DT, 2><<<blocks, threads, 0, stream>>>(a);
-  else ffn_few_kernel<DT, 4><<<blocks, threads, 0, stream>>>(a);
+  if (a.vec && a.dim % 8 == 0) ffn_few_kernel<DT, G, U, true><<<blocks, threads, 0, stream>>>(a);
+  else ffn_few_kernel<DT, G, U, false><<<blocks, threads, 0, stream>>>(a);
+}
+template <int DT> hipError_t few(const FfnArgs& a, hipStream_t stream) {
+  if (a.n <= 16) few_any<DT, 1, 4>(a, stream);
+  else if (a.n <= 32) few_any<DT, 2, 4>(a, stream);
+  else few_any<DT, 4, 2>(a, stream);
   return hipGetLastError();
 }
 
