@@ -607,6 +607,8 @@ typedef struct {
     float scale;          /* of q . k; finite, > 0 */
     int dtype;            /* queries, keys, values, outputs and their gradients */
 } dmuon_attention_shape;
+/* A call takes less than 2^24 tiles: of 128 (query, head) rows, and of 128 keys,
+ * a key head, one more of each a sequence. */
 
 /*
  * Attention over packed sequences:
@@ -645,7 +647,9 @@ int dmuon_attention_forward(const dmuon_attention_shape* shape, const void* q, i
  * Gradients of dmuon_attention_forward: dq, dk, dv from dout, the forward's
  * inputs and its out and lse.  The probabilities are formed again from lse; a
  * key head's gradients are summed over the query heads that share it, in fp32,
- * in a fixed order.  Rows behind the last sequence are left as they were.
+ * in a fixed order.  Rows behind the last sequence are left as they were.  An
+ * infinity or NaN in any operand can reach every gradient of its sequence, and
+ * none of another's.
  */
 int dmuon_attention_backward_workspace_bytes(const dmuon_attention_shape* shape, size_t* bytes_out);
 int dmuon_attention_backward(const dmuon_attention_shape* shape, const void* dout, int64_t dout_stride, const void* q,
@@ -666,6 +670,8 @@ typedef struct {
     int activation;       /* DMUON_ACT_SILU or DMUON_ACT_GELU */
     int dtype;            /* inputs, weights, output and their gradients */
 } dmuon_gated_ffn_shape;
+/* A call takes less than 2^32 threads: 512 to 256 tokens x 128 of the hidden width
+ * (backward, also x 256 of dim) for DMUON_BF16, 256 to 64 x 32 (x 64) for DMUON_F32. */
 
 /*
  * The gated half of a feed-forward block: both projections, the activation and

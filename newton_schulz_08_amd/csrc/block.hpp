@@ -61,7 +61,7 @@ struct AttnArgs {
   unsigned group_inv;                 // ceil(2^32 / group), for rows / group
   int causal, window;
   float scale;
-  int vec;                 // every run of 16 bytes of a head is aligned
+  int vec;                 // every run of 16 bytes of a head is aligned (the 16384-token batch 1.16 ms; otherwise 2.5)
   int slots;               // tiles' places over all sequences, of queries or of keys
   int slices;              // forward: parts of a tile's keys
 };
@@ -103,7 +103,11 @@ struct FfnArgs {
 // Sets both slices, from the sizes alone.
 void ffn_slices(int dt, FfnArgs* a);
 constexpr int kFfnStage = 64;      // contraction steps of a bf16 stage
-constexpr int kFfnFewTokens = 64;  // most tokens that the forward pass takes without tiles
+// Most tokens that the forward pass takes without tiles.  64 tokens in us, without
+// and with: 512 -> 2048 bf16 9.5, 14; 2048 -> 8192 26, 40; 4096 -> 14336 89, 73
+// (33 tokens 71, 76); fp32 512 -> 2048 12, 16; 4096 -> 14336 212, 174.  Beyond,
+// a wave's sums would not fit its registers.
+constexpr int kFfnFewTokens = 64;
 hipError_t launch_ffn_few(int dt, const FfnArgs& a, hipStream_t stream);
 hipError_t launch_ffn(int dt, int mode, const FfnArgs& a, hipStream_t stream);
 // Copies rows of `width` elements to rows of `padded`, zeros behind them.

@@ -14,6 +14,15 @@
 // has one owner and one order, with no atomics and no partial results in
 // memory.
 //
+// Measured, 32 heads over 8 key heads of 128 bf16, causal, two sequences of 8192
+// tokens: 4.2 to 4.45 ms (dk and dv 2.35, dq 2.08, statistics 0.055), 0.62 to
+// 0.65 PFLOP/s of five products; with the two that are formed twice and dq's
+// second operand 1.0.  In dk and dv a wave reads 368 LDS cycles a step of 32
+// rows beside 1024 of matrix instructions, eight waves to one LDS: without
+// barriers, exponentials or later loads it would still take 1.9 ms.  Eight
+// waves on 256 keys with three buffers take 2.45 ms; 64 keys a wave, which would
+// halve the reads, spill (13 ms).  fp32, 4096 tokens: 3.6 ms.
+//
 // Rows without visible keys (lse -infinity) take lse = +infinity, which makes
 // their probabilities exp2(-infinity) = 0.
 #include <hip/hip_runtime.h>
@@ -164,7 +173,8 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
       // A row's ds add up to 0, so what its keys have in common cancels in dq, but
       // not in the errors of rounding ds to bf16: with those alone dq of trained
       // keys is half as far off again as its own rounding.  The product takes ds
-      // as two bf16 numbers, from the same fragments of the keys.
+      // as two bf16 numbers, from the same fragments of the keys (0.5 ms of the
+      // 16384-token batch; the relative error of dq falls from 2.5e-3 to 1.8e-3).
       Frag<DT> ds[2], low[2];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -188,7 +198,9 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
 
 // Where the tile's keys and values stay: their fragments in registers, or, where
 // two sums of a head fill those, the values in LDS (bf16 from 128 on), or both in
-// memory and read again for every tile of rows (fp32 beyond 128).
+// memory and read again for every tile of rows (fp32 beyond 128).  With the
+// values in LDS 256 registers hold a wave and two share a SIMD: the 16384-token
+// batch in 4.24 ms, and in 6.8 with one wave.
 template <int DT, int DP> struct Held {
   static constexpr bool kMemory = DT == kF32 && DP > 128;
   static constexpr bool kValuesLds = DT == kBF16 && DP >= 128;

@@ -26,6 +26,12 @@
 // fixed order.  Wider rows are swept several times, out of the caches, and
 // their column sums are a launch of its own behind one that stores each row's
 // lengths and mean.
+//
+// Measured, fp32 stream and bf16 branch: backward of 32768 x 4096 455 us and of
+// 32768 x 8192 884 us, 5.3 and 5.5 TB/s of the bytes it cannot do without (a
+// copy of 1 GiB moves 5.2); forward of 16 x 4096 4.3 us, which is latency.  Two
+// runs of eight a lane, and half the threads, take 852 us at 4096; loads behind
+// branches 1247.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -236,8 +242,9 @@ template <int XDT, int BDT, int T> __global__ __launch_bounds__(kBlock<T>) void 
 #pragma unroll
   for (int i = 0; i < 8; ++i) gd[i] *= gate[i];
   // Sixteen waves leave 128 registers to each.  The next row beside this one does
-  // not fit them: a row of over 4096 is under way as a whole instead; and the
-  // gains are kept in LDS, each lane its own.
+  // not fit them: a row of over 4096 is under way as a whole instead, and the
+  // gains are kept in LDS, each lane its own (32768 x 8192: 884 us; with the next
+  // row and the gains in registers, up to 122 of which spill, 1779).
   constexpr bool kAhead = T < 1024;
   __shared__ f32v4 kept[kAhead ? 1 : 4][kAhead ? 1 : T];
   if constexpr (!kAhead)

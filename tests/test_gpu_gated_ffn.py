@@ -192,3 +192,23 @@ def test_gradient_by_differences():
         got, want = float((g.double() * d.double()).sum()), (values[0] - values[1]) / (2 * step)
         # the third derivative's share (step^2 / 6 of a value of this size) and the results' roundings over the step
         assert abs(got - want) <= 2e-3 * (abs(want) + float((g.double() * d.double()).norm())), which
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", [1, 70])
+def test_activation_is_zero_or_its_argument_far_out(n, dtype, kind):
+    """One input column of 1s: the projections are the weights, and beyond +-200 act is 0 or g and
+    its derivative 0 or 1, to less than half a step of any type.  The gradients of 1 or 64 tokens,
+    a power of two each, add up to 1 without rounding."""
+    tokens = 64 if n == 70 else n
+    g = torch.tensor([s * 2.0 ** e for e in (8, 20, 43, 60, 83, 100) for s in (1, -1)], device="cuda").to(dtype)
+    x, one = torch.ones(n, 1, dtype=dtype, device="cuda"), torch.ones_like(g)[:, None]
+    want = torch.where(g > 0, g, torch.zeros_like(g))
+    out = nsa.gated_ffn(x, g[:, None], one, kind)
+    assert torch.equal(out, want.expand(n, -1))
+    dh = torch.zeros(n, len(g), dtype=dtype, device="cuda")
+    dh[:tokens] = 1 / tokens
+    dx, dg, du = nsa.gated_ffn_grad(dh, x, g[:, None], one, kind)
+    assert torch.equal(dg[:, 0], (g > 0).to(dtype)) and torch.equal(du[:, 0], want)
+    assert torch.isfinite(dx).all()
