@@ -42,7 +42,8 @@ int check_bn(const dmuon_block_norm_shape* s) {
 
 // Blocks of the backward pass, each leaving one row of sums: as many as are at
 // work at once, and, since a row of sums is moved twice, four runs of rows each
-// where that leaves a block a CU.  Wide rows: blocks of the pass over columns.
+// where that leaves a block a CU (1024 x 4096 27 us, without that 31; 2048 x 1024
+// 27, 29; 777 x 1001 28 either way).  Wide rows: blocks of the pass over columns.
 int bn_grad_blocks(const dmuon_block_norm_shape& s) {
   if (s.dim > kBnMaxFused) {
     const int64_t per = std::max<int64_t>(64, (s.rows + 4095) / 4096);
