@@ -24,7 +24,8 @@
 // tokens 1.10 to 1.16 ms, 0.96 to 1.00 PFLOP/s of the visible half (the matrix
 // pipe is busy for 47% of it, the vector pipe for 57%: exponentials, maxima,
 // conversions); one new token of 8 sequences over 65536 keys in all 49 us with
-// the join's 4.8, 5.5 TB/s.  Heads of 64 0.60 ms, of 256 3.3 (one wave a SIMD).
+// the join's 4.8, 5.5 TB/s out of the memory-side cache in part; a fresh cache 63,
+// 4.2 TB/s.  Heads of 64 0.60 ms, of 256 3.3 (one wave a SIMD).
 // fp32, 4096 tokens: 0.62 ms, 0.11 PFLOP/s.
 #include <hip/hip_runtime.h>
 

@@ -30,10 +30,10 @@
 // Measured, 4096 -> 14336 bf16: 8192 tokens 1.45 to 1.49 ms, 1.30 PFLOP/s (a
 // library product of 8192 on each side reaches 1.38); gradient 4.5 ms, 1.28
 // (projections again 1.67, dx 1.40, weights 1.49); 1 to 4 tokens 43 us, 5.5 TB/s
-// of the weights.  512 -> 2048 fp32, gradient of 1001 tokens: 161 us, three
-// products of 55 and a join of 5, where 27 would be the matrix pipe's time:
-// loads of the first stage and stores of the last cost the rest in two rounds of
-// blocks.
+// of the weights as they lie in the memory-side cache (fresh ones 48).  512 ->
+// 2048 fp32, gradient of 1001 tokens: 157 us, three products of 50 and a join of
+// 5, where 27 would be the matrix pipe's time: 64 x 64 tiles ask the L2 for 16
+// bytes a cycle and CU, and a stage of two waves a SIMD is too short for its loads.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -456,36 +456,38 @@ constexpr int kTile32 = 64, kStep32 = 64;
 constexpr int kPitch32 = 68;   // floats: reads along a row and across rows start in different banks
 
 // Part of one operand's stage that a thread moves: 64 rows x 64 steps, zero
-// outside.  In LDS as in memory: rows of steps, or (TR) steps of rows.
-template <bool TR> struct Stage32 {
+// outside.  In LDS as in memory: rows of steps, or (TR) steps of rows.  VEC: runs
+// of four are whole and aligned; otherwise element by element.  Every thread
+// loads, from the last line and run (element) if it has none of its own, and
+// store() writes zeros for it: a branch around a load, or between two ways to
+// load, would make the next load wait for it.
+template <bool TR, bool VEC> struct Stage32 {
   f32x4 v[4];
-  // Whole runs of four: every lane loads, from the last line and run if it has
-  // none of its own, and store() writes zeros for it: a branch around a load
-  // would make the next one wait for it.
-  template <typename Row> __device__ __forceinline__ void load(Row&& row, int64_t lines, int64_t line0, int cols, int col0, int vec) {
+  template <typename Row> __device__ __forceinline__ void load(Row&& row, int64_t lines, int64_t line0, int cols, int col0) {
     const int last = static_cast<int>(least<int64_t>(lines - line0, 64)) - 1;
     const int col = col0 + (threadIdx.x & 15) * 4;
-    if (vec && cols % 4 == 0) {
-      const int at = col < cols ? col : cols - 4;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        v[u] = *reinterpret_cast<gptr<const f32x4>>(gmem(row(min(u * 16 + static_cast<int>(threadIdx.x >> 4), last)) + at));
-    } else {
+    for (int u = 0; u < 4; ++u) {
+      const float* p = row(min(u * 16 + static_cast<int>(threadIdx.x >> 4), last));
+      if constexpr (VEC) {
+        v[u] = *reinterpret_cast<gptr<const f32x4>>(gmem(p + min(col, cols - 4)));
+      } else {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float* p = row(min(u * 16 + static_cast<int>(threadIdx.x >> 4), last));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[u][i] = col + i < cols ? gmem(p)[col + i] : 0.0f;
+        for (int i = 0; i < 4; ++i) v[u][i] = gmem(p)[min(col + i, cols - 1)];
       }
     }
   }
   __device__ __forceinline__ void store(float* lds, int64_t lines, int64_t line0, int cols, int col0) const {
     const int count = static_cast<int>(least<int64_t>(lines - line0, 64));
-    const bool any = col0 + static_cast<int>(threadIdx.x & 15) * 4 < cols;
+    const int left = cols - col0 - static_cast<int>(threadIdx.x & 15) * 4;   // elements of the run that exist
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int line = u * 16 + (threadIdx.x >> 4);
-      *reinterpret_cast<f32x4*>(lds + line * kPitch32 + (threadIdx.x & 15) * 4) = any && line < count ? v[u] : f32x4{};
+      f32x4 x = line < count && left > 0 ? v[u] : f32x4{};
+      if constexpr (!VEC)
+#pragma unroll
+        for (int i = 1; i < 4; ++i) x[i] = i < left ? x[i] : 0.0f;
+      *reinterpret_cast<f32x4*>(lds + line * kPitch32 + (threadIdx.x & 15) * 4) = x;
     }
   }
   // Steps 16 s + 4 oct .. + 3 of row (block, l & 15).
@@ -502,7 +504,8 @@ template <bool TR> struct Stage32 {
   }
 };
 
-template <int MODE> __global__ __launch_bounds__(256, 2) void ffn_tile32_kernel(FfnArgs a) {
+// VEC: of x and the weights (what the kernels themselves stored is always whole runs).
+template <int MODE, bool VEC> __global__ __launch_bounds__(256, 2) void ffn_tile32_kernel(FfnArgs a) {
   constexpr bool kGated = MODE == kFfnOut || MODE == kFfnMid, kPT = MODE == kFfnDw, kQT = !kGated;
   __shared__ __attribute__((aligned(16))) float lds[2][2][64 * kPitch32];
   const Grid grid = grid_of<MODE>(a, kTile32);
@@ -523,23 +526,23 @@ template <int MODE> __global__ __launch_bounds__(256, 2) void ffn_tile32_kernel(
   const int c0 = tj * (kGated ? kTile32 / 2 : kTile32);
   const int64_t all = stages_of<MODE>(a, kStep32);
   const int64_t first = all * slice / a.slices, end = all * (slice + 1) / a.slices;
-  Stage32<kPT> p;
-  Stage32<kQT> q;
+  Stage32<kPT, VEC || !kGated> p;
+  Stage32<kQT, VEC> q;
   auto load = [&](int64_t stage) {
     const int64_t k0 = stage * kStep32;
     if constexpr (kGated) {
-      p.load([&](int line) { return x + (r0 + line) * a.xs; }, a.n, r0, a.dim, static_cast<int>(k0), a.vec);
+      p.load([&](int line) { return x + (r0 + line) * a.xs; }, a.n, r0, a.dim, static_cast<int>(k0));
       // 32 rows of one weight, then the same of the other
       q.load([&](int line) { return (line & 32 ? wu : wg) + static_cast<int64_t>(min(c0 + (line & 31), a.hidden - 1)) * a.ws; }, 64, 0,
-             a.dim, static_cast<int>(k0), a.vec);
+             a.dim, static_cast<int>(k0));
     } else if constexpr (MODE == kFfnDx) {
       const bool second = k0 >= a.hp;   // hp holds whole stages
       const int64_t k = k0 - (second ? a.hp : 0);
-      p.load([&](int line) { return mid + (r0 + line) * mp; }, a.n, r0, 2 * a.hp, static_cast<int>(k0), 1);
-      q.load([&](int line) { return (second ? wu : wg) + (k + line) * a.ws; }, a.hidden, k, a.dim, c0, a.vec);
+      p.load([&](int line) { return mid + (r0 + line) * mp; }, a.n, r0, 2 * a.hp, static_cast<int>(k0));
+      q.load([&](int line) { return (second ? wu : wg) + (k + line) * a.ws; }, a.hidden, k, a.dim, c0);
     } else {
-      p.load([&](int line) { return mid + (k0 + line) * mp + (which ? a.hp : 0); }, a.n, k0, a.hp, static_cast<int>(r0), 1);
-      q.load([&](int line) { return x + (k0 + line) * a.xs; }, a.n, k0, a.dim, c0, a.vec);
+      p.load([&](int line) { return mid + (k0 + line) * mp + (which ? a.hp : 0); }, a.n, k0, a.hp, static_cast<int>(r0));
+      q.load([&](int line) { return x + (k0 + line) * a.xs; }, a.n, k0, a.dim, c0);
     }
   };
   auto store = [&](int b, int64_t stage) {
@@ -567,16 +570,26 @@ template <int MODE> __global__ __launch_bounds__(256, 2) void ffn_tile32_kernel(
     // a stage's sum is added as a whole: the roundings of a long contraction then
     // grow with its stages, not with its steps
     f32x4 part[4] = {};
+    // fragments are read one sub-step ahead of their products: left alone, the
+    // compiler reads them right in front of those and waits (4096 tokens, 512 ->
+    // 2048: the gradient 595 us instead of 586; and 560 with whole runs' loads
+    // free of branches)
+    f32x4 fp[2], fq[2][4];
+    auto read = [&](int s) {
+      fp[s & 1] = decltype(p)::read(lds[b][0], s, wave);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fq[s & 1][j] = decltype(q)::read(lds[b][1], s, j);
+    };
+    read(0);
 #pragma unroll
     for (int s = 0; s < kStep32 / 16; ++s) {
-      const f32x4 fp = Stage32<kPT>::read(lds[b][0], s, wave);
-      f32x4 fq[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) fq[j] = Stage32<kQT>::read(lds[b][1], s, j);
+      if (s + 1 < kStep32 / 16) read(s + 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) part[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fq[j][e], fp[e], part[j], 0, 0, 0);
+        for (int j = 0; j < 4; ++j) part[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fq[s & 1][j][e], fp[s & 1][e], part[j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] += part[j];
@@ -767,7 +780,8 @@ template <int DT, int MODE> hipError_t run(const FfnArgs& args, hipStream_t stre
     ffn_tile_kernel<MODE><<<dim3(blocks), dim3(kTileThreads), 0, stream>>>(a);
   } else {
     const unsigned blocks = static_cast<unsigned>(grid_of<MODE>(a, kTile32).all) * a.slices;
-    ffn_tile32_kernel<MODE><<<dim3(blocks), dim3(256), 0, stream>>>(a);
+    if (a.vec && a.dim % 4 == 0) ffn_tile32_kernel<MODE, true><<<dim3(blocks), dim3(256), 0, stream>>>(a);
+    else ffn_tile32_kernel<MODE, false><<<dim3(blocks), dim3(256), 0, stream>>>(a);
   }
   if constexpr (MODE == kFfnDx || MODE == kFfnDw) {
     if (a.slices > 1) {
