@@ -463,15 +463,21 @@ constexpr int kPitch32 = 68;   // floats: reads along a row and across rows star
 // load, would make the next load wait for it.
 template <bool TR, bool VEC> struct Stage32 {
   f32x4 v[4];
-  template <typename Row> __device__ __forceinline__ void load(Row&& row, int64_t lines, int64_t line0, int cols, int col0) {
+  // base(u): where the lines of load u count from, row(line): rows behind it,
+  // stride elements apart.  VEC: all within 32 bits of offset, which keeps the
+  // addresses' arithmetic short.
+  template <typename Base, typename Row>
+  __device__ __forceinline__ void load(Base&& base, Row&& row, int64_t stride, int64_t lines, int64_t line0, int cols, int col0) {
     const int last = static_cast<int>(least<int64_t>(lines - line0, 64)) - 1;
     const int col = col0 + (threadIdx.x & 15) * 4;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const float* p = row(min(u * 16 + static_cast<int>(threadIdx.x >> 4), last));
+      const int r = row(min(u * 16 + static_cast<int>(threadIdx.x >> 4), last));
       if constexpr (VEC) {
-        v[u] = *reinterpret_cast<gptr<const f32x4>>(gmem(p + min(col, cols - 4)));
+        const uint32_t at = (static_cast<uint32_t>(r) * static_cast<uint32_t>(stride) + min(col, cols - 4)) * 4;
+        v[u] = *reinterpret_cast<gptr<const f32x4>>(gmem(reinterpret_cast<const char*>(base(u)) + at));
       } else {
+        const float* p = base(u) + r * stride;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[u][i] = gmem(p)[min(col + i, cols - 1)];
       }
@@ -530,19 +536,21 @@ template <int MODE, bool VEC> __global__ __launch_bounds__(256, 2) void ffn_tile
   Stage32<kQT, VEC> q;
   auto load = [&](int64_t stage) {
     const int64_t k0 = stage * kStep32;
+    auto same = [](int line) { return line; };
     if constexpr (kGated) {
-      p.load([&](int line) { return x + (r0 + line) * a.xs; }, a.n, r0, a.dim, static_cast<int>(k0));
+      p.load([&](int) { return x + r0 * a.xs; }, same, a.xs, a.n, r0, a.dim, static_cast<int>(k0));
       // 32 rows of one weight, then the same of the other
-      q.load([&](int line) { return (line & 32 ? wu : wg) + static_cast<int64_t>(min(c0 + (line & 31), a.hidden - 1)) * a.ws; }, 64, 0,
-             a.dim, static_cast<int>(k0));
+      const int f0 = min(c0, a.hidden - 1);
+      q.load([&](int u) { return (u & 2 ? wu : wg) + f0 * a.ws; }, [&](int line) { return min(c0 + (line & 31), a.hidden - 1) - f0; }, a.ws,
+             64, 0, a.dim, static_cast<int>(k0));
     } else if constexpr (MODE == kFfnDx) {
       const bool second = k0 >= a.hp;   // hp holds whole stages
       const int64_t k = k0 - (second ? a.hp : 0);
-      p.load([&](int line) { return mid + (r0 + line) * mp; }, a.n, r0, 2 * a.hp, static_cast<int>(k0));
-      q.load([&](int line) { return (second ? wu : wg) + (k + line) * a.ws; }, a.hidden, k, a.dim, c0);
+      p.load([&](int) { return mid + r0 * mp; }, same, mp, a.n, r0, 2 * a.hp, static_cast<int>(k0));
+      q.load([&](int) { return (second ? wu : wg) + k * a.ws; }, same, a.ws, a.hidden, k, a.dim, c0);
     } else {
-      p.load([&](int line) { return mid + (k0 + line) * mp + (which ? a.hp : 0); }, a.n, k0, a.hp, static_cast<int>(r0));
-      q.load([&](int line) { return x + (k0 + line) * a.xs; }, a.n, k0, a.dim, c0);
+      p.load([&](int) { return mid + k0 * mp + (which ? a.hp : 0); }, same, mp, a.n, k0, a.hp, static_cast<int>(r0));
+      q.load([&](int) { return x + k0 * a.xs; }, same, a.xs, a.n, k0, a.dim, c0);
     }
   };
   auto store = [&](int b, int64_t stage) {
@@ -572,8 +580,8 @@ template <int MODE, bool VEC> __global__ __launch_bounds__(256, 2) void ffn_tile
     f32x4 part[4] = {};
     // fragments are read one sub-step ahead of their products: left alone, the
     // compiler reads them right in front of those and waits (4096 tokens, 512 ->
-    // 2048: the gradient 595 us instead of 586; and 560 with whole runs' loads
-    // free of branches)
+    // 2048: the gradient 595 us instead of 586; 560 with whole runs' loads free of
+    // branches, 536 with their offsets in 32 bits)
     f32x4 fp[2], fq[2][4];
     auto read = [&](int s) {
       fp[s & 1] = decltype(p)::read(lds[b][0], s, wave);
@@ -780,7 +788,8 @@ template <int DT, int MODE> hipError_t run(const FfnArgs& args, hipStream_t stre
     ffn_tile_kernel<MODE><<<dim3(blocks), dim3(kTileThreads), 0, stream>>>(a);
   } else {
     const unsigned blocks = static_cast<unsigned>(grid_of<MODE>(a, kTile32).all) * a.slices;
-    if (a.vec && a.dim % 4 == 0) ffn_tile32_kernel<MODE, true><<<dim3(blocks), dim3(256), 0, stream>>>(a);
+    // a tile's rows lie within 32 bits of offset (the weights' always do)
+    if (a.vec && a.dim % 4 == 0 && a.xs < int64_t{1} << 22) ffn_tile32_kernel<MODE, true><<<dim3(blocks), dim3(256), 0, stream>>>(a);
     else ffn_tile32_kernel<MODE, false><<<dim3(blocks), dim3(256), 0, stream>>>(a);
   }
   if constexpr (MODE == kFfnDx || MODE == kFfnDw) {

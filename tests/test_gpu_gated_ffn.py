@@ -212,3 +212,15 @@ def test_activation_is_zero_or_its_argument_far_out(n, dtype, kind):
     dx, dg, du = nsa.gated_ffn_grad(dh, x, g[:, None], one, kind)
     assert torch.equal(dg[:, 0], (g > 0).to(dtype)) and torch.equal(du[:, 0], want)
     assert torch.isfinite(dx).all()
+
+
+@pytest.mark.parametrize("stride", [(1 << 22) - 4, 1 << 22, (1 << 22) + 4])
+def test_strides_around_the_limit_of_short_offsets(stride):
+    """Aligned fp32 rows up to and beyond 16 MiB apart: the same bits as rows side by side."""
+    n, dim, hidden = 70, 12, 40
+    near, wg, wu, dh = make(n, dim, hidden, F32, 5)
+    x = torch.empty((n - 1) * stride + dim, device="cuda").as_strided((n, dim), (stride, 1))
+    x.copy_(near)
+    assert torch.equal(nsa.gated_ffn(x, wg, wu), nsa.gated_ffn(near, wg, wu))
+    for a, b in zip(nsa.gated_ffn_grad(dh, x, wg, wu), nsa.gated_ffn_grad(dh, near, wg, wu)):
+        assert torch.equal(a, b)
