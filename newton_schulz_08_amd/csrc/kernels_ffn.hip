@@ -31,9 +31,10 @@
 // library product of 8192 on each side reaches 1.38); gradient 4.5 ms, 1.28
 // (projections again 1.67, dx 1.40, weights 1.49); 1 to 4 tokens 43 us, 5.5 TB/s
 // of the weights as they lie in the memory-side cache (fresh ones 48).  512 ->
-// 2048 fp32, gradient of 1001 tokens: 157 us, three products of 50 and a join of
-// 5, where 27 would be the matrix pipe's time: 64 x 64 tiles ask the L2 for 16
-// bytes a cycle and CU, and a stage of two waves a SIMD is too short for its loads.
+// 2048 fp32, gradient of 1001 tokens: 153 to 157 us, three products of 50 and a
+// join of 5, where 27 would be the matrix pipe's time; of 4096 tokens 536, where
+// 328 would be.  Of those, the loads cost 27 and moving them on to LDS 80; the
+// rest is what two waves a SIMD leave open around each stage's barrier.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
