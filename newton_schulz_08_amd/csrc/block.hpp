@@ -95,7 +95,7 @@ struct FfnArgs {
   int dim, kdim;           // kdim: dim, or for bf16 rounded up to whole stages (zeros)
   int hidden, hp;          // hp: hidden rounded up to whole stages
   int act;
-  int vec;                 // operands' and results' runs of 16 bytes are aligned
+  int vec;                 // the runs of 16 bytes of x and the weights are aligned (dh and results may lie anywhere)
   int dx_slices, dw_slices;   // parts of those products' contractions
   int slices;              // set by the launch: its own
   float* part;             // slices x rows x dim rounded up to four: their sums

@@ -525,7 +525,7 @@ int dmuon_gated_ffn_forward(const dmuon_gated_ffn_shape* shape, const void* x, i
     a.wu = w_up;
     a.out = h;
     a.outs = h_stride;
-    a.vec = ffn_vec({&b[0], &b[1], &wg, &wu});
+    a.vec = ffn_vec({&b[0], &wg, &wu});
     const double flops = 4.0 * s.tokens * s.dim * s.hidden;
     const double bytes = static_cast<double>(es) * (s.tokens * (s.dim + s.hidden) + 2 * s.hidden * s.dim);
     hipStream_t stream = static_cast<hipStream_t>(hip_stream);
@@ -570,8 +570,6 @@ int dmuon_gated_ffn_backward(const dmuon_gated_ffn_shape* shape, const void* dh,
     DMUON_TRY(check_bufs(b, 8));
     bool capturing = false;
     DMUON_TRY(check_device(hip_stream, &capturing));
-    const Buf dwg{"dw_gate", dw_gate, s.hidden, s.dim * es, s.dim * es, es, true};
-    const Buf dwu{"dw_up", dw_up, s.hidden, s.dim * es, s.dim * es, es, true};
     FfnArgs a{};
     fill_ffn(s, &a);
     a.x = x;
@@ -587,7 +585,7 @@ int dmuon_gated_ffn_backward(const dmuon_gated_ffn_shape* shape, const void* dh,
     a.mid = workspace;
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.off_part);
     ffn_slices(s.dtype, &a);
-    a.vec = ffn_vec({&b[0], &b[1], &b[2], &wg, &wu, &dwg, &dwu});
+    a.vec = ffn_vec({&b[1], &wg, &wu});
     const double flops = 12.0 * s.tokens * s.dim * s.hidden;
     const double bytes = static_cast<double>(es) * (s.tokens * (2 * s.dim + s.hidden) + 4 * s.hidden * s.dim);
     hipStream_t stream = static_cast<hipStream_t>(hip_stream);

@@ -72,18 +72,18 @@ __device__ __forceinline__ void activate(int kind, float g, float* a, float* da)
   *da = s + gdy2 * s * (e * s);
 }
 
-// Four consecutive elements of a row, as far as it reaches.
-template <typename T> __device__ __forceinline__ void load4(const T* row, int c, int cols, int vec, float* v) {
-  if (vec && c + 4 <= cols) {
-    load_n<4>(row + c, v);
+// Four consecutive elements of a row, as far as it reaches, whatever its alignment.
+template <typename T> __device__ __forceinline__ void load4(const T* row, int c, int cols, float* v) {
+  if (c + 4 <= cols) {
+    load_any<4>(row + c, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = c + i < cols ? static_cast<float>(gmem(row)[c + i]) : 0.0f;
   }
 }
-template <typename T> __device__ __forceinline__ void store4(T* row, int c, int cols, int vec, const float* v) {
-  if (vec && c + 4 <= cols) {
-    store_n<4>(row + c, v);
+template <typename T> __device__ __forceinline__ void store4(T* row, int c, int cols, const float* v) {
+  if (c + 4 <= cols) {
+    store_any<4>(row + c, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -103,12 +103,12 @@ template <int DT, int MODE> __device__ __forceinline__ void finish_gated(const F
     float h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = act[i] * u[i];
-    store4(static_cast<T*>(a.out) + r * a.outs, f, a.hidden, a.vec, h);
+    store4(static_cast<T*>(a.out) + r * a.outs, f, a.hidden, h);
   } else {
     // rows and columns up to whole stages take zeros: they enter sums
     if (r >= a.mid_rows || f >= a.hp) return;
     float dh[4] = {}, dg[4], du[4];
-    if (r < a.n) load4(static_cast<const T*>(a.dh) + r * a.dhs, f, a.hidden, a.vec, dh);
+    if (r < a.n) load4(static_cast<const T*>(a.dh) + r * a.dhs, f, a.hidden, dh);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool in = r < a.n && f + i < a.hidden;
@@ -131,9 +131,9 @@ __device__ __forceinline__ void finish_plain(const FfnArgs& a, int which, int sl
     const int64_t line = MODE == kFfnDx ? slice * rows + r : (2 * static_cast<int64_t>(slice) + which) * rows + r;
     store_n<4>(a.part + line * ((a.dim + 3) / 4 * 4) + c, v);
   } else if constexpr (MODE == kFfnDx) {
-    store4(static_cast<T*>(a.out) + r * a.outs, c, a.dim, a.vec, v);
+    store4(static_cast<T*>(a.out) + r * a.outs, c, a.dim, v);
   } else {
-    store4(static_cast<T*>(which ? a.dwu : a.dwg) + r * a.dim, c, a.dim, a.vec, v);
+    store4(static_cast<T*>(which ? a.dwu : a.dwg) + r * a.dim, c, a.dim, v);
   }
 }
 
