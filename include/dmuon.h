@@ -739,7 +739,9 @@ const char* dmuon_backend_info(void);
 /*
  * Kernel-level timing.  While enabled, every kernel the library enqueues is
  * bracketed by a pair of HIP events on its stream.  dmuon_profile_read waits
- * for those events, returns per-kernel totals and clears the record.
+ * for those events, returns per-kernel totals and clears the record.  Attention
+ * counts the visible pairs of queries and keys of sequences that share the tokens
+ * equally: the offsets are not read on the host.
  */
 typedef struct {
     char name[40];      /* kernel family, e.g. "ns_gemm" */

@@ -156,6 +156,20 @@ void fill_attn(const dmuon_attention_shape& s, AttnArgs* a) {
   a->slots = static_cast<int>(attn_q_slots(s));
 }
 
+// What a call has to compute and move, with all sequences equally long: the offsets
+// are the device's.  A sequence of lq queries and lk keys: the last query sees up to
+// lk keys, each one before it one fewer, and none more than the window.
+struct AttnWork { double pairs, query_elems, key_elems, seen_elems; };   // seen: of the keys that any query sees
+AttnWork attn_work(const dmuon_attention_shape& s) {
+  const double seqs = static_cast<double>(s.sequences), lq = s.q_tokens / seqs, lk = s.k_tokens / seqs;
+  const double most = s.window ? std::min<double>(s.window, lk) : lk;
+  auto sum = [&](double n) { return n <= most ? n * (n + 1.0) / 2.0 : most * (most + 1.0) / 2.0 + (n - most) * most; };   // of min(1..n, most)
+  const double pairs = s.causal ? sum(lk) - sum(std::max(lk - lq, 0.0)) : lq * lk;
+  const double seen = s.window ? std::min(lk, lq + s.window - 1.0) : lk;
+  const double heads = static_cast<double>(s.k_heads) * s.head_dim;
+  return AttnWork{seqs * pairs * s.q_heads, static_cast<double>(s.q_tokens) * s.q_heads * s.head_dim, s.k_tokens * heads, seqs * seen * heads};
+}
+
 // ---------------------------------------------------------------- gated feed-forward
 int check_ffn(const dmuon_gated_ffn_shape* s) {
   if (!s) return invalid("shape is NULL");
@@ -406,11 +420,9 @@ int dmuon_attention_forward(const dmuon_attention_shape* shape, const void* q, i
     a.part = static_cast<float*>(workspace);
     a.slices = attn_slices(s);
     a.vec = attn_vec(s, {&b[0], &b[1], &b[2], &b[3]});
-    const double qe = static_cast<double>(s.q_tokens) * s.q_heads * s.head_dim;
-    const double ke = static_cast<double>(s.k_tokens) * s.k_heads * s.head_dim;
-    // every query of an average sequence with every key
-    return launched("attention", kKAttention, 4.0 * qe * (static_cast<double>(s.k_tokens) / s.sequences),
-                    2.0 * (qe + ke) * size_of(s.dtype), hip_stream, capturing,
+    const AttnWork w = attn_work(s);
+    return launched("attention", kKAttention, 4.0 * w.pairs * s.head_dim, 2.0 * (w.query_elems + w.seen_elems) * size_of(s.dtype),
+                    hip_stream, capturing,
                     [&] { return launch_attention(s.dtype, a, static_cast<hipStream_t>(hip_stream)); });
   });
 }
@@ -478,10 +490,9 @@ int dmuon_attention_backward(const dmuon_attention_shape* shape, const void* dou
     a.slices = 1;
     a.vec = attn_vec(s, {&b[0], &b[1], &b[2], &b[3], &b[4], &b[5], &b[6], &b[7]});
     const int k_slots = static_cast<int>(attn_slots(s.k_tokens, s.sequences));
-    const double qe = static_cast<double>(s.q_tokens) * s.q_heads * s.head_dim;
-    const double ke = static_cast<double>(s.k_tokens) * s.k_heads * s.head_dim;
-    return launched("attention gradient", kKAttentionGrad, 10.0 * qe * (static_cast<double>(s.k_tokens) / s.sequences),
-                    4.0 * (qe + ke) * size_of(s.dtype), hip_stream, capturing,
+    const AttnWork w = attn_work(s);
+    return launched("attention gradient", kKAttentionGrad, 10.0 * w.pairs * s.head_dim,
+                    (4.0 * w.query_elems + 2.0 * (w.seen_elems + w.key_elems)) * size_of(s.dtype), hip_stream, capturing,
                     [&] { return launch_attention_grad(s.dtype, a, k_slots, static_cast<hipStream_t>(hip_stream)); });
   });
 }
