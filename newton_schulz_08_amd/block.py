@@ -12,7 +12,7 @@ import torch
 
 from . import _lib
 from .api import _alloc, dtype_code
-from .ops import _heads, _query, _rows, _run, _tensor, _workspace
+from .ops import _c_int, _heads, _query, _rows, _run, _tensor, _workspace
 
 _ACTIVATIONS = {"silu": _lib.DMUON_ACT_SILU, "gelu": _lib.DMUON_ACT_GELU}
 
@@ -123,7 +123,8 @@ def _attn_args(q, k, v, q_offsets, k_offsets, causal, window, scale):
         if q_offsets.dim() != 1 or q_offsets.shape[0] < 2:
             raise ValueError(f"q_offsets must hold one entry more than there are sequences, got shape {tuple(q_offsets.shape)}")
         sequences = q_offsets.shape[0] - 1
-    s = _lib.AttentionShape(n, nk, sequences, qh, kh, d, 1 if causal else 0, window, d ** -0.5 if scale is None else scale,
+    s = _lib.AttentionShape(n, nk, sequences, _c_int(qh, "q_heads"), _c_int(kh, "k_heads"), _c_int(d, "head_dim"),
+                            1 if causal else 0, _c_int(window, "window"), d ** -0.5 if scale is None else scale,
                             dtype_code(q.dtype))
     return dev, s, head, offs
 
@@ -160,7 +161,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Opti
 def attention_workspace_bytes(q_tokens: int, k_tokens: int, q_heads: int, k_heads: int, head_dim: int,
                               sequences: int = 1) -> int:
     return _query("dmuon_attention_workspace_bytes",
-                  _lib.AttentionShape(q_tokens, k_tokens, sequences, q_heads, k_heads, head_dim, scale=1.0))
+                  _lib.AttentionShape(q_tokens, k_tokens, sequences, _c_int(q_heads, "q_heads"), _c_int(k_heads, "k_heads"),
+                                      _c_int(head_dim, "head_dim"), scale=1.0))
 
 
 def attention_grad(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
@@ -185,7 +187,7 @@ def attention_grad(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
 
 def attention_grad_workspace_bytes(q_tokens: int, q_heads: int) -> int:
     return _query("dmuon_attention_backward_workspace_bytes",
-                  _lib.AttentionShape(q_tokens, 0, 1, q_heads, q_heads, 1, scale=1.0))
+                  _lib.AttentionShape(q_tokens, 0, 1, _c_int(q_heads, "q_heads"), q_heads, 1, scale=1.0))
 
 
 # ---------------------------------------------------------------- gated feed-forward

@@ -41,6 +41,13 @@ def _index_code(t: torch.Tensor, name: str) -> int:
         raise TypeError(f"{name} must be int32 or int64, got {t.dtype}") from None
 
 
+def _c_int(v: int, name: str) -> int:
+    """v, refused where a C int would hold another number in its place."""
+    if not -1 << 31 <= v < 1 << 31:
+        raise ValueError(f"{name} = {v} is too large")
+    return v
+
+
 def _tensor(t, name: str, index: int = -1, dtype: Optional[torch.dtype] = None, shape=None) -> int:
     """Address of a contiguous device tensor, on device `index` and of that
     dtype and shape where given."""
@@ -418,7 +425,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tens
 
 
 def qk_norm_rope_grad_workspace_bytes(tokens: int, q_heads: int, k_heads: int, head_dim: int) -> int:
-    s = _lib.QkShape(tokens=tokens, q_heads=q_heads, k_heads=k_heads, head_dim=head_dim)
+    s = _lib.QkShape(tokens=tokens, q_heads=_c_int(q_heads, "q_heads"), k_heads=_c_int(k_heads, "k_heads"),
+                     head_dim=_c_int(head_dim, "head_dim"))
     return _query("dmuon_qk_norm_rope_backward_workspace_bytes", s)
 
 

@@ -1,0 +1,35 @@
+"""Numbers that a C int cannot hold are refused by attention's binding, not wrapped."""
+import pytest
+import torch
+
+import newton_schulz_08_amd as nsa
+
+WRAPS = 1 << 32   # 0 in an int: no window at all
+
+
+def test_workspace_queries():
+    assert nsa.attention_workspace_bytes(8, 65536, 32, 8, 128, 8) > 0
+    for args in ((8, 65536, WRAPS + 32, 8, 128, 8), (8, 65536, 32, WRAPS + 8, 128, 8), (8, 65536, 32, 8, WRAPS + 128, 8)):
+        with pytest.raises(ValueError, match="too large"):
+            nsa.attention_workspace_bytes(*args)
+    with pytest.raises(ValueError, match="too large"):
+        nsa.attention_grad_workspace_bytes(8, WRAPS + 32)
+    for args in ((8, WRAPS + 4, 2, 64), (8, 4, WRAPS + 2, 64), (8, 4, 2, 64 - WRAPS)):
+        with pytest.raises(ValueError, match="too large"):
+            nsa.qk_norm_rope_grad_workspace_bytes(*args)
+
+
+@pytest.mark.gpu
+def test_windows():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU visible")
+    q, k, v = (torch.randn(300, 4, 64, device="cuda") for _ in range(3))
+    out, lse = nsa.attention(q, k, v)
+    assert torch.equal(nsa.attention(q, k, v, window=1 << 30)[0], out)
+    for window in (WRAPS, WRAPS + 5, 5 - WRAPS):
+        with pytest.raises(ValueError, match="window"):
+            nsa.attention(q, k, v, window=window)
+        with pytest.raises(ValueError, match="window"):
+            nsa.attention_grad(q, q, k, v, out, lse, window=window)
+    with pytest.raises(nsa.DmuonError, match="window"):
+        nsa.attention(q, k, v, window=(1 << 30) + 1)
