@@ -620,7 +620,10 @@ typedef struct {
  * k_offsets[b] .. k_offsets[b + 1] - 1.  Query i of its lq sees key j of its lk
  * when, with causal, j <= i + lk - lq, and, with a window too,
  * j > i + lk - lq - window: the last query stands at the last key, so one call
- * serves whole sequences and single new tokens behind a cache.  A query that
+ * serves whole sequences and single new tokens behind a cache.  Caches that grow
+ * in place have room behind them, which a sequence without queries takes: with
+ * room for C keys each and n0, n1 in use, q_offsets 0, 1, 1, 2, 2 and k_offsets
+ * 0, n0, C, C + n1, 2 C; from token to token only the offsets change.  A query that
  * sees no key has out 0 and lse -infinity.  Query head h reads key head
  * h / (q_heads / k_heads).
  *

@@ -140,7 +140,10 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Opti
     heads have to be contiguous.  q_offsets, k_offsets: int32 (sequences + 1),
     where each sequence begins and the last ends; None for one sequence.  A
     sequence's last query stands at its last key: with more keys than queries
-    the first ones are a cache.  causal, window: which keys a query sees.
+    the first ones are a cache.  The room behind a cache that grows in place is
+    a sequence of its own, without queries: q_offsets [0, 1, 1, 2, 2], k_offsets
+    [0, n0, C, C + n1, 2 C] for two caches of C keys with n0, n1 in use.
+    causal, window: which keys a query sees.
     scale: head_dim ** -0.5 by default.  lse: float32 (q_heads, tokens).
     Rows behind the last sequence are left as they were (unset, where the
     results are allocated here).  Outside autograd: the gradients are

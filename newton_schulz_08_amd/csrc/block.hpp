@@ -54,7 +54,7 @@ struct AttnArgs {
   void* dk;
   void* dv;
   float* stats;            // backward: base-2 lse and dout . out of every row, in the rows' order
-  float* part;             // forward in slices: per slice, tile and row the sum, then maximum and weight
+  float* part;             // forward in slices: per tile, slice and row the sum, then maximum and weight
   int64_t qs, ks, vs, os, dos, dqs, dks, dvs;   // elements between tokens
   int q_tokens, k_tokens, sequences;
   int q_heads, k_heads, group, dim;   // group: query heads of a key head

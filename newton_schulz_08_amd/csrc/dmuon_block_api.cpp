@@ -105,10 +105,15 @@ int check_attn_grid(const dmuon_attention_shape& s) {
 // sequences have keys to share out, at least 512 a part.  In us, in slices and
 // not: a token over 1024 keys 19, 26; 8 over 16384 21, 48; 8 over 65536 48, 177;
 // 31 over 126976 28, 91; 2048 queries on 2048 keys 37, 55; 512 on 512 14 either way.
+// No more sequences than there are queries have any; the others, such as the room
+// behind a growing cache, have places for tiles and leave them at once (a token of
+// 16 sequences over 4096 keys each, as many again as room: 53; counted as sequences
+// with queries 92; without room 48).  Both kinds take workspace, which 2048 parts bound.
 int attn_slices(const dmuon_attention_shape& s) {
-  const int64_t tiles = attn_q_slots(s) * s.k_heads, keys = s.k_tokens / s.sequences;
+  const int64_t active = std::max<int64_t>(1, std::min(s.sequences, s.q_tokens)), all = attn_q_slots(s) * s.k_heads;
+  const int64_t tiles = attn_slots(s.q_tokens * (s.q_heads / s.k_heads), active) * s.k_heads, keys = s.k_tokens / active;
   if (tiles >= 256 || keys < 1024) return 1;
-  return static_cast<int>(std::min<int64_t>({1024 / tiles, keys / 512, 64}));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({1024 / tiles, 2048 / all, keys / 512, 64})));
 }
 int64_t attn_part_bytes(const dmuon_attention_shape& s) {
   const int64_t slices = attn_slices(s);

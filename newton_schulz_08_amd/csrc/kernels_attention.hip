@@ -67,9 +67,12 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<DT, DP>())) void attentio
   const lds_t lds = (lds_t)shared;
 
   // heads vary fastest: the blocks of one XCD share few heads' keys.  The last
-  // tiles of a causal sequence have the most keys: they start first.
+  // tiles of a causal sequence have the most keys: they start first.  A tile's
+  // slices come together: with empty places between the tiles (room behind caches)
+  // the CUs are then filled evenly (8 tokens over 65536 keys, each cache with room
+  // behind it, 50 us; with the places one after another 66).
   const int head = blockIdx.x % a.k_heads, rest = blockIdx.x / a.k_heads;
-  const int slot = a.slots - 1 - rest % a.slots, slice = rest / a.slots;
+  const int slot = a.slots - 1 - rest / a.slices, slice = rest % a.slices;
   const Place p = place(a, slot, false);
   if (!p.any) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -224,8 +227,8 @@ template <int DT, int DP> __global__ __launch_bounds__(64) void attention_join_k
   const Place p = place(a, a.slots - 1 - rest, false);
   const int r = blockIdx.y, lane = threadIdx.x, row = p.row0 + r;
   if (!p.any || row >= p.rows) return;
-  const int64_t step = static_cast<int64_t>(a.k_heads) * a.slots * slice_floats(DP);
-  const float* part = a.part + static_cast<int64_t>(blockIdx.x) * slice_floats(DP);
+  const int64_t step = static_cast<int64_t>(a.k_heads) * slice_floats(DP);
+  const float* part = a.part + (static_cast<int64_t>(rest) * a.slices * a.k_heads + head) * slice_floats(DP);
   const float* ml = part + static_cast<int64_t>(kAttnTile) * DP + 2 * r;
   part += static_cast<int64_t>(r) * DP;
   const bool mine = lane < a.slices;   // at most 64
