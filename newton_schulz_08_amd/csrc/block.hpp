@@ -38,7 +38,6 @@ constexpr int kBnMaxFused = 8192;   // widest row whose column sums stay in regi
 inline int bn_rows_at_once(int64_t dim) { return dim <= 512 ? 4 : 1; }
 
 // ---------------------------------------------------------------- attention over packed sequences
-constexpr int kAttnMaxDim = 256;
 constexpr int kAttnTile = 128;       // rows of a block: queries x the heads that share a key head, or keys
 struct AttnArgs {
   const void* q;
@@ -110,8 +109,7 @@ constexpr int kFfnStage = 64;      // contraction steps of a bf16 stage
 constexpr int kFfnFewTokens = 64;
 hipError_t launch_ffn_few(int dt, const FfnArgs& a, hipStream_t stream);
 hipError_t launch_ffn(int dt, int mode, const FfnArgs& a, hipStream_t stream);
-// Copies rows of `width` elements to rows of `padded`, zeros behind them.
-hipError_t launch_ffn_pad(int dt, const void* src, int64_t stride, void* dst, int64_t rows, int width, int padded,
-                          hipStream_t stream);
+// Copies bf16 rows of `width` elements to rows of `padded`, zeros behind them.
+hipError_t launch_ffn_pad(const void* src, int64_t stride, void* dst, int64_t rows, int width, int padded, hipStream_t stream);
 
 }  // namespace dmuon

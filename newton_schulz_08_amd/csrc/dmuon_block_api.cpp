@@ -248,9 +248,9 @@ hipError_t ffn_operands(const dmuon_gated_ffn_shape& s, const FfnLayout& l, void
   if (!l.copies) return hipSuccess;
   char* ws = static_cast<char*>(workspace);
   const int dim = static_cast<int>(s.dim);
-  hipError_t e = launch_ffn_pad(s.dtype, a->x, a->xs, ws + l.off_x, s.tokens, dim, a->kdim, stream);
-  if (e == hipSuccess) e = launch_ffn_pad(s.dtype, a->wg, s.dim, ws + l.off_g, s.hidden, dim, a->kdim, stream);
-  if (e == hipSuccess) e = launch_ffn_pad(s.dtype, a->wu, s.dim, ws + l.off_u, s.hidden, dim, a->kdim, stream);
+  hipError_t e = launch_ffn_pad(a->x, a->xs, ws + l.off_x, s.tokens, dim, a->kdim, stream);
+  if (e == hipSuccess) e = launch_ffn_pad(a->wg, s.dim, ws + l.off_g, s.hidden, dim, a->kdim, stream);
+  if (e == hipSuccess) e = launch_ffn_pad(a->wu, s.dim, ws + l.off_u, s.hidden, dim, a->kdim, stream);
   a->x = ws + l.off_x;
   a->wg = ws + l.off_g;
   a->wu = ws + l.off_u;

@@ -20,8 +20,9 @@
 // along a row, or (Q of dx, both of dW) with one step a row, and is then read
 // from LDS through transposing reads: no matrix is transposed in memory.
 //
-// fp32: 64 x 64 tiles on v_mfma_f32_16x16x4_f32, loaded through registers with
-// every bound checked.  Products with few tiles cut their contraction into
+// fp32: 64 x 64 tiles on v_mfma_f32_16x16x4_f32, loaded through registers: every
+// thread loads, from the last line or run that exists if it has none of its own,
+// and zeros take their place on the way to LDS.  Products with few tiles cut their contraction into
 // slices, whose sums another launch adds in order.
 //
 // Few tokens: the weights are read once, straight into fragments, by waves
@@ -48,7 +49,6 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) char* lds_t;
 typedef __attribute__((address_space(3))) bf16x4* lds_bf16x4_t;
 
@@ -380,8 +380,7 @@ template <int MODE> __global__ __launch_bounds__(kTileThreads, 2) void ffn_tile_
     // this wave's 32 stage rows: 32 of one weight, for columns 32 (wave / 2) .. of the tile's 128
     const int f0 = tj * 128 + (wave >> 1) * 32;
     const char* w = static_cast<const char*>((wave & 1) ? a.wu : a.wg);
-    // the offsets count from the wave's own rows: rows() below is written for a tile's 256
-    Q.base = uniform_ptr(w);
+    // the offsets count from the wave's own rows; Operand::init's from a tile's 256
     Q.pitch = wp;
     Q.lane = lane;
     Q.wave = wave;
@@ -763,21 +762,19 @@ template <int DT, int G, int U, bool VEC> __global__ __launch_bounds__(64 * kFew
 }
 
 // ---------------------------------------------------------------- padding
-template <int DT> __global__ __launch_bounds__(256) void ffn_pad_kernel(const void* src, int64_t stride, void* dst, int64_t rows,
-                                                                        int width, int padded) {
-  using T = typename OpElem<DT>::T;
+__global__ __launch_bounds__(256) void ffn_pad_kernel(const __bf16* src, int64_t stride, __bf16* dst, int64_t rows, int width, int padded) {
   const int per = padded / 8;
   const int64_t id = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
   const int64_t r = id / per;
   const int c = static_cast<int>(id % per) * 8;
   if (r >= rows) return;
-  const T* s = static_cast<const T*>(src) + r * stride;
+  const __bf16* s = src + r * stride;
   float v[8];
   if (c + 8 <= width) load_any<8>(s + c, v);
   else
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = c + i < width ? static_cast<float>(gmem(s)[c + i]) : 0.0f;
-  store_n<8>(static_cast<T*>(dst) + r * padded + c, v);
+  store_n<8>(dst + r * padded + c, v);
 }
 
 template <int DT, int MODE> hipError_t run(const FfnArgs& args, hipStream_t stream) {
@@ -846,12 +843,10 @@ hipError_t launch_ffn(int dt, int mode, const FfnArgs& a, hipStream_t stream) {
 hipError_t launch_ffn_few(int dt, const FfnArgs& a, hipStream_t stream) {
   return dt == kF32 ? ffn::few<kF32>(a, stream) : ffn::few<kBF16>(a, stream);
 }
-hipError_t launch_ffn_pad(int dt, const void* src, int64_t stride, void* dst, int64_t rows, int width, int padded,
-                          hipStream_t stream) {
+hipError_t launch_ffn_pad(const void* src, int64_t stride, void* dst, int64_t rows, int width, int padded, hipStream_t stream) {
   const int64_t all = (rows * (padded / 8) + 255) / 256, cols = std::min<int64_t>(all, int64_t{1} << 20);
   const dim3 blocks(static_cast<unsigned>(cols), static_cast<unsigned>((all + cols - 1) / cols));
-  if (dt == kF32) ffn::ffn_pad_kernel<kF32><<<blocks, dim3(256), 0, stream>>>(src, stride, dst, rows, width, padded);
-  else ffn::ffn_pad_kernel<kBF16><<<blocks, dim3(256), 0, stream>>>(src, stride, dst, rows, width, padded);
+  ffn::ffn_pad_kernel<<<blocks, dim3(256), 0, stream>>>(static_cast<const __bf16*>(src), stride, static_cast<__bf16*>(dst), rows, width, padded);
   return hipGetLastError();
 }
 
