@@ -18,6 +18,7 @@
 #pragma once
 
 #include "block.hpp"
+#include "lds_fill.hpp"
 
 namespace dmuon {
 namespace attn {
@@ -175,24 +176,6 @@ __device__ __forceinline__ int query_of(const AttnArgs& a, int r) {
   return i;
 }
 
-// 16 bytes from base + voff (per lane) to LDS[dst + 16 lane], with no register
-// between.  Issued through asm so that the compiler's count of outstanding
-// accesses does not make every LDS read wait for it; the reader waits for
-// vmcnt(0) and a barrier.
-__device__ __forceinline__ void dma16(const void* base, uint32_t voff, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(dst) : "memory");
-}
-// The same of four bytes a lane.
-__device__ __forceinline__ void dma4(const void* base, uint32_t voff, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(dst) : "memory");
-}
-__device__ __forceinline__ uint32_t lds_address(lds_t p) { return static_cast<uint32_t>(reinterpret_cast<size_t>(p)); }
-__device__ __forceinline__ const char* uniform_ptr(const void* p) {
-  const uint64_t v = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
-  return reinterpret_cast<const char*>((static_cast<uint64_t>(hi) << 32) | lo);
-}
 // Everything that the block has on its way into LDS is there behind this.
 __device__ __forceinline__ void tiles_landed() {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -224,8 +207,8 @@ template <int DT, int DP, int R, bool VEC> struct Filler {
   }
   __device__ static __forceinline__ void move(const char* base, uint32_t voff, uint32_t lds, int u, bool full) {
     const uint32_t dst = lds + static_cast<uint32_t>(u * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * 1024;
-    if (full) dma16(base, voff, dst);
-    else if (voff != kNone) dma16(base, voff, dst);
+    if (full) lds_dma16(base, voff, dst);
+    else if (voff != kNone) lds_dma16(base, voff, dst);
   }
   // A whole tile whose first row begins at `first`.
   __device__ __forceinline__ void whole(lds_t tile, const void* first, int dim) const {

@@ -271,7 +271,7 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
     const int r0 = begin + tile * 32;
     // 32 rows' pairs; behind the last row, the last one's
     if (wave == 0)
-      dma4(uniform_ptr(sbase + 2 * static_cast<int64_t>(r0)), static_cast<uint32_t>(8 * min(lane >> 1, end - 1 - r0) + 4 * (lane & 1)),
+      lds_dma4(uniform_ptr(sbase + 2 * static_cast<int64_t>(r0)), static_cast<uint32_t>(8 * min(lane >> 1, end - 1 - r0) + 4 * (lane & 1)),
            __builtin_amdgcn_readfirstlane(lds_address(lds + kStats)) + (tile & 1) * 256);
     if constexpr (VEC)
       if (even && r0 + 32 <= end) {

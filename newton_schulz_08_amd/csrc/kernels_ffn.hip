@@ -41,6 +41,7 @@
 #include <algorithm>
 
 #include "block.hpp"
+#include "lds_fill.hpp"
 
 namespace dmuon {
 namespace ffn {
@@ -49,7 +50,6 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) char* lds_t;
 typedef __attribute__((address_space(3))) bf16x4* lds_bf16x4_t;
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -183,22 +183,6 @@ __device__ __forceinline__ void tile_of(const Grid& g, int block, int* ti, int* 
 constexpr int kTileThreads = 512;
 constexpr int kOperandBytes = 32768, kStageBytes = 65536;
 
-__device__ __forceinline__ uint32_t lds_address(const char* p) {
-  return static_cast<uint32_t>(reinterpret_cast<size_t>((lds_t)p));   // address-space cast
-}
-__device__ __forceinline__ const char* uniform_ptr(const void* p) {
-  const uint64_t v = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
-  return reinterpret_cast<const char*>((static_cast<uint64_t>(hi) << 32) | lo);
-}
-// 16 bytes from base + voff (per lane) to LDS[dst + 16 lane].  Through asm, so
-// that the compiler does not make every LDS read wait for it; readers wait for
-// vmcnt(0) and a barrier.
-__device__ __forceinline__ void dma16(const char* base, uint32_t voff, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(dst) : "memory");
-}
-
 // One operand's 256 rows (or columns) of a tile.
 //
 // Steps along a row: stage row r (128 bytes: 64 steps) keeps 16-byte chunk c
@@ -243,7 +227,7 @@ template <bool TR> struct Operand {
       off[u] = static_cast<uint32_t>(min(8 * wave + (lane >> 5) + 2 * u, left - 1)) * pitch + ((u & 1) ? col1 : col);
   }
   __device__ __forceinline__ void load(const char* at, uint32_t lds, int u) const {
-    dma16(at, off[u], lds + static_cast<uint32_t>(wave) * 4096 + u * 1024);
+    lds_dma16(at, off[u], lds + static_cast<uint32_t>(wave) * 4096 + u * 1024);
   }
 };
 
@@ -271,8 +255,8 @@ template <bool TR> struct Reader {
     if constexpr (TR) {
       const int a = threadIdx.x & 3, ch = 2 * block + (a >> 1);
       const char* p = operand + at + ((ch ^ sw) << 4) + 32 * sub * 512;
-      const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(reinterpret_cast<lds_bf16x4_t>((lds_t)p));
-      const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(reinterpret_cast<lds_bf16x4_t>((lds_t)(p + 4 * 512)));
+      const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(reinterpret_cast<lds_bf16x4_t>((lds_ptr_t)p));
+      const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(reinterpret_cast<lds_bf16x4_t>((lds_ptr_t)(p + 4 * 512)));
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
       return *reinterpret_cast<const bf16x8*>(operand + at + (((4 * sub + lk) ^ sw) << 4) + block * 16 * 128);
