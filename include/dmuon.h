@@ -604,7 +604,7 @@ typedef struct {
     int head_dim;         /* D, 1 .. DMUON_MAX_ATTENTION_DIM */
     int causal;           /* 1: a query sees no key behind it */
     int window;           /* with causal: the keys a query sees at most; 0 = no limit */
-    float scale;          /* of q . k; finite, > 0 */
+    float scale;          /* of q . k; > 0, and finite times log2(e), as the scores have to be */
     int dtype;            /* queries, keys, values, outputs and their gradients */
 } dmuon_attention_shape;
 /* A call takes less than 2^24 tiles: of 128 (query, head) rows, and of 128 keys,

@@ -88,7 +88,8 @@ int check_attn(const dmuon_attention_shape* s) {
   DMUON_TRY(check_range(s->head_dim, 1, DMUON_MAX_ATTENTION_DIM, "head_dim"));
   DMUON_TRY(check_range(s->window, 0, int64_t{1} << 30, "window"));
   if (s->window && !s->causal) return invalid("a window needs causal");
-  if (!(std::isfinite(s->scale) && s->scale > 0.0f)) return invalid("scale must be finite and > 0");
+  // the kernels' exponentials are base 2
+  if (!(std::isfinite(s->scale * 1.4426950408889634f) && s->scale > 0.0f)) return invalid("scale times log2(e) must be finite and > 0");
   return check_range(s->q_tokens * (s->q_heads / s->k_heads), 0, int64_t{1} << 30, "q_tokens * q_heads / k_heads");
 }
 

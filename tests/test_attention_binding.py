@@ -3,6 +3,10 @@ import pytest
 import torch
 
 import newton_schulz_08_amd as nsa
+from newton_schulz_08_amd import _lib
+
+from test_block_abi import AT, ATG, at_shape
+from test_ops_abi import BAD, accepted, refused
 
 WRAPS = 1 << 32   # 0 in an int: no window at all
 
@@ -33,3 +37,12 @@ def test_windows():
             nsa.attention_grad(q, q, k, v, out, lse, window=window)
     with pytest.raises(nsa.DmuonError, match="window"):
         nsa.attention(q, k, v, window=(1 << 30) + 1)
+
+
+def test_scales_that_overflow_in_base_2():
+    """Exponentials are base 2: a scale that is infinite times log2(e) would make a score of 0 a NaN."""
+    lib, largest = _lib.load(), 3.4028234e38 / 1.4426952
+    for f, good in ((lib.dmuon_attention_forward, AT), (lib.dmuon_attention_backward, ATG)):
+        good = dict(good, shape=at_shape(k_tokens=6))
+        refused(f, good, [(dict(shape=at_shape(k_tokens=6, scale=s)), BAD) for s in (largest * 1.0001, 3.4e38)])
+        accepted(f, dict(good, shape=at_shape(k_tokens=6, scale=largest * 0.9999)))
