@@ -124,7 +124,7 @@ def _attn_args(q, k, v, q_offsets, k_offsets, causal, window, scale):
             raise ValueError(f"q_offsets must hold one entry more than there are sequences, got shape {tuple(q_offsets.shape)}")
         sequences = q_offsets.shape[0] - 1
     s = _lib.AttentionShape(n, nk, sequences, _c_int(qh, "q_heads"), _c_int(kh, "k_heads"), _c_int(d, "head_dim"),
-                            1 if causal else 0, _c_int(window, "window"), d ** -0.5 if scale is None else scale,
+                            1 if causal else 0, _c_int(window, "window"), max(d, 1) ** -0.5 if scale is None else scale,
                             dtype_code(q.dtype))
     return dev, s, head, offs
 

@@ -46,3 +46,16 @@ def test_scales_that_overflow_in_base_2():
         good = dict(good, shape=at_shape(k_tokens=6))
         refused(f, good, [(dict(shape=at_shape(k_tokens=6, scale=s)), BAD) for s in (largest * 1.0001, 3.4e38)])
         accepted(f, dict(good, shape=at_shape(k_tokens=6, scale=largest * 0.9999)))
+
+
+@pytest.mark.gpu
+def test_heads_of_no_elements_are_refused():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU visible")
+    two, one, lse = torch.empty(5, 2, 0, device="cuda"), torch.empty(5, 1, 0, device="cuda"), torch.zeros(1, 5, device="cuda")
+    with pytest.raises(ValueError, match="next to each other"):   # torch takes a step of 1 between heads of nothing
+        nsa.attention(two, two, two)
+    with pytest.raises(nsa.DmuonError, match="head_dim"):
+        nsa.attention(one, one, one)
+    with pytest.raises(nsa.DmuonError, match="head_dim"):
+        nsa.attention_grad(one, one, one, one, one, lse)
