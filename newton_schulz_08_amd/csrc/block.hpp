@@ -102,11 +102,24 @@ struct FfnArgs {
 // Sets both slices, from the sizes alone.
 void ffn_slices(int dt, FfnArgs* a);
 constexpr int kFfnStage = 64;      // contraction steps of a bf16 stage
-// Most tokens that the forward pass takes without tiles.  64 tokens in us, without
-// and with: 512 -> 2048 bf16 9.5, 14; 2048 -> 8192 26, 40; 4096 -> 14336 89, 73
-// (33 tokens 71, 76); fp32 512 -> 2048 12, 16; 4096 -> 14336 212, 174.  Beyond,
-// a wave's sums would not fit its registers.
+// Most tokens that the forward pass takes without tiles: beyond, a wave's sums
+// would not fit its registers.
 constexpr int kFfnFewTokens = 64;
+// Whether it does.  Without tiles the time grows with the weights and the tokens;
+// tiles of few rows take the same time for 1 to 64 tokens and, up to a tile a CU,
+// for every hidden width.  In us, without and with:
+//   bf16, 4096 -> 8192   32 tokens 33, 76;  48 42, 76;  64 47, 76
+//         4096 -> 14336  32 tokens 62, 76;  48 78, 76;  64 89, 77
+//         4096 -> 28672  16 tokens 108, 118;  24 125, 118;  32 136, 118;  64 189, 119
+//         1024 -> 14336  64 tokens 26, 26;  512 -> 14336  64 tokens 15, 18;  512 -> 28672  64 tokens 24, 20
+//   fp32, 4096 -> 4096   32 tokens 43, 97;  33 66, 97;  64 70, 97
+//         4096 -> 8192   32 tokens 66, 97;  33 100, 97;  64 107, 98
+//         4096 -> 14336  32 tokens 155, 164;  33 194, 164;  64 211, 165
+inline bool ffn_few(int dt, int64_t tokens, int64_t dim, int64_t hidden) {
+  if (tokens > kFfnFewTokens) return false;
+  if (dt == kF32) return tokens <= 32 || hidden < 8192;
+  return dim < 1024 || tokens * hidden <= 3 << 18;
+}
 hipError_t launch_ffn_few(int dt, const FfnArgs& a, hipStream_t stream);
 hipError_t launch_ffn(int dt, int mode, const FfnArgs& a, hipStream_t stream);
 // Copies bf16 rows of `width` elements to rows of `padded`, zeros behind them.

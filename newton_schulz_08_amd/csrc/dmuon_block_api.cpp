@@ -222,7 +222,7 @@ FfnLayout ffn_layout(const dmuon_gated_ffn_shape& s, bool back, bool in_place) {
     const int64_t dx = a.dx_slices > 1 ? a.dx_slices * s.tokens : 0, dw = a.dw_slices > 1 ? a.dw_slices * 2 * s.hidden : 0;
     l.total = l.off_part + align_up(static_cast<size_t>(std::max(dx, dw) * ((s.dim + 3) / 4 * 4) * int64_t{4}));
   }
-  l.copies = s.dtype == DMUON_BF16 && !(in_place && s.dim % kFfnStage == 0) && (back || s.tokens > kFfnFewTokens);
+  l.copies = s.dtype == DMUON_BF16 && !(in_place && s.dim % kFfnStage == 0) && (back || !ffn_few(s.dtype, s.tokens, s.dim, s.hidden));
   if (l.copies) {
     l.off_x = l.total;
     l.off_g = l.off_x + align_up(static_cast<size_t>(s.tokens * a.kdim * es));
@@ -547,7 +547,7 @@ int dmuon_gated_ffn_forward(const dmuon_gated_ffn_shape* shape, const void* x, i
     const double bytes = static_cast<double>(es) * (s.tokens * (s.dim + s.hidden) + 2 * s.hidden * s.dim);
     hipStream_t stream = static_cast<hipStream_t>(hip_stream);
     return launched("gated feed-forward", kKFfn, flops, bytes, hip_stream, capturing, [&] {
-      if (s.tokens <= kFfnFewTokens) return launch_ffn_few(s.dtype, a, stream);
+      if (ffn_few(s.dtype, s.tokens, s.dim, s.hidden)) return launch_ffn_few(s.dtype, a, stream);
       const hipError_t e = ffn_operands(s, l, workspace, &a, stream);
       return e != hipSuccess ? e : launch_ffn(s.dtype, kFfnOut, a, stream);
     });
