@@ -42,8 +42,9 @@ int check_bn(const dmuon_block_norm_shape* s) {
 
 // Blocks of the backward pass, each leaving one row of sums: as many as are at
 // work at once, and, since a row of sums is moved twice, four runs of rows each
-// where that leaves a block a CU (1024 x 4096 27 us, without that 31; 2048 x 1024
-// 27, 29; 777 x 1001 28 either way).  Wide rows: blocks of the pass over columns.
+// where that leaves a block a CU (fp32, in calls from Python: 1024 x 4096 27 us,
+// without that 33; 2048 x 1024 26, 29; 8192 x 512 27, 29; 777 x 1001 26 either way,
+// of which the kernels take 17).  Wide rows: blocks of the pass over columns.
 int bn_grad_blocks(const dmuon_block_norm_shape& s) {
   if (s.dim > kBnMaxFused) {
     const int64_t per = std::max<int64_t>(64, (s.rows + 4095) / 4096);
@@ -104,8 +105,10 @@ int check_attn_grid(const dmuon_attention_shape& s) {
 
 // Parts of a tile's keys: where the tiles alone leave CUs idle and the
 // sequences have keys to share out, at least 512 a part.  In us, in slices and
-// not: a token over 1024 keys 19, 26; 8 over 16384 21, 48; 8 over 65536 48, 177;
-// 31 over 126976 28, 91; 2048 queries on 2048 keys 37, 55; 512 on 512 14 either way.
+// not: a token over 1024 keys 19, 26; 8 over 16384 21, 49; 8 over 65536 49, 179;
+// 31 over 126976 28, 92; 2048 queries on 2048 keys 33, 55; 512 on 512 14 either way.
+// The keys are shared out by their mean: a sequence far longer than the others is
+// cut no finer than they are.
 // No more sequences than there are queries have any; the others, such as the room
 // behind a growing cache, have places for tiles and leave them at once (a token of
 // 16 sequences over 4096 keys each, as many again as room: 53; counted as sequences
@@ -239,7 +242,7 @@ bool ffn_vec(std::initializer_list<const Buf*> bufs) {
 }
 // The bf16 tiles read the operands in place when their rows are whole stages at
 // multiples of 16 bytes, and 256 of them lie within 32 bits of offset.  Copies
-// of all three take 0.2 ms of 8192 tokens' 1.69 ms at 4096 -> 14336.
+// of all three add 0.09 ms to 8192 tokens' 1.50 ms at 4096 -> 14336.
 bool ffn_in_place(const Buf& x, const Buf& wg, const Buf& wu) {
   return ffn_vec({&x, &wg, &wu}) && (x.rows <= 1 || x.pitch <= (int64_t{1} << 23));
 }

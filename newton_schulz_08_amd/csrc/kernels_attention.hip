@@ -21,12 +21,16 @@
 // unnormed sum, maximum and weight; a second launch joins them.
 //
 // Measured, 32 heads over 8 key heads of 128 bf16, causal: two sequences of 8192
-// tokens 1.10 to 1.16 ms, 0.96 to 1.00 PFLOP/s of the visible half (the matrix
-// pipe is busy for 47% of it, the vector pipe for 57%: exponentials, maxima,
-// conversions); one new token of 8 sequences over 65536 keys in all 49 us with
-// the join's 4.8, 5.5 TB/s out of the memory-side cache in part; a fresh cache 63,
-// 4.2 TB/s.  Heads of 64 0.60 ms, of 256 3.3 (one wave a SIMD).
-// fp32, 4096 tokens: 0.62 ms, 0.11 PFLOP/s.
+// tokens 1.10 to 1.23 ms on different cards, 0.90 to 1.00 PFLOP/s of the visible
+// half (the matrix pipe is busy for 47% of it, the vector pipe for 57%:
+// exponentials, maxima, conversions); one new token of 8 sequences over 65536 keys
+// in all 49 us with the join's 4.8, 5.5 TB/s out of the memory-side cache in part,
+// 50 with as many keys again as room behind the caches; a fresh cache 63, 4.2 TB/s.
+// Heads of 64 0.62 to 0.68 ms, of 192 2.9, of 256 3.3 (one wave a SIMD).
+// fp32, 4096 tokens in two sequences: heads of 64 0.34 ms, of 128 0.63 (0.11
+// PFLOP/s), of 192 1.1, of 256 2.3 (86 registers spill).  The 8 tokens over 65536
+// fp32 keys 308 us, 1.7 TB/s: of a block's four waves one has rows, and its chain
+// of fp32 matrix instructions is the time.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -182,6 +186,11 @@ __global__ __launch_bounds__(kThreads, (waves_per_simd<DT, DP>())) void attentio
         for (int b = 0; b < S::kBlocks; ++b) o[b] *= by;
       }
       const float ms = m == kNone ? 0.0f : m;
+      // For bf16 the probabilities are rounded to it as operands of their product;
+      // l, which norms them, adds them as they are.  out of the 16384-token batch is
+      // then 2.2e-3 off (relative, of the whole), of which its own rounding is 1.6e-3.
+      // Two bf16 numbers each would take that product's matrix instructions, half of
+      // all, twice.
       Frag<DT> pf[kKb][2];
 #pragma unroll
       for (int kb = 0; kb < kKb; ++kb)

@@ -6,22 +6,25 @@
 //   ds = p (dout . v - delta) scale
 //   dq = sum over keys of ds k,   dk = sum over rows of ds q,   dv = sum of p dout
 //
-// Three launches.  The first forms delta and puts it beside lse.  dq's blocks keep a tile of rows
-// (queries x the heads that share a key head) and pass over the keys; dk's and
-// dv's keep a tile of keys and pass over the rows, those of all heads that
+// Three launches.  The first forms delta and puts it beside lse.  dq's blocks keep
+// a tile of rows (queries x the heads that share a key head) and pass over the
+// keys; dk's and dv's keep a tile of keys and pass over the rows, those of all heads that
 // share it, so a shared head's gradient is one sum in one block.  Each forms
 // the scores for itself: seven products in all instead of five, but every sum
 // has one owner and one order, with no atomics and no partial results in
 // memory.
 //
 // Measured, 32 heads over 8 key heads of 128 bf16, causal, two sequences of 8192
-// tokens: 4.2 to 4.45 ms (dk and dv 2.35, dq 2.08, statistics 0.055), 0.62 to
-// 0.65 PFLOP/s of five products; with the two that are formed twice and dq's
+// tokens: 4.2 to 4.75 ms on different cards (dk and dv 2.2 to 2.5, dq 2.0 to 2.2,
+// statistics 0.055), 0.58 to 0.65 PFLOP/s of five products; with the two that are formed twice and dq's
 // second operand 1.0.  In dk and dv a wave reads 368 LDS cycles a step of 32
 // rows beside 1024 of matrix instructions, eight waves to one LDS: without
 // barriers, exponentials or later loads it would still take 1.9 ms.  Eight
 // waves on 256 keys with three buffers take 2.45 ms; 64 keys a wave, which would
-// halve the reads, spill (13 ms).  fp32, 4096 tokens: 3.6 ms.
+// halve the reads, spill (13 ms).  Heads of 64 2.85 ms, of 192 13.1, of 256 36.2
+// (151 registers of dk and dv spill: 29.6 of it).  fp32, 4096 tokens in two
+// sequences: heads of 64 1.8 ms, of 128 3.6, of 192 11.8, of 256 21 (both with
+// spills).
 //
 // Rows without visible keys (lse -infinity) take lse = +infinity, which makes
 // their probabilities exp2(-infinity) = 0.
@@ -174,7 +177,7 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
       // not in the errors of rounding ds to bf16: with those alone dq of trained
       // keys is half as far off again as its own rounding.  The product takes ds
       // as two bf16 numbers, from the same fragments of the keys (0.5 ms of the
-      // 16384-token batch; the relative error of dq falls from 2.5e-3 to 1.8e-3).
+      // 16384-token batch; the relative error of dq falls from 2.5e-3 to 1.7e-3, all but its own rounding).
       Frag<DT> ds[2], low[2];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -320,6 +323,11 @@ __global__ __launch_bounds__(kThreads, DT == kBF16 && DP <= 128 ? 2 : 1) void at
         }
       }
       const lptr<const float> stat = reinterpret_cast<lptr<const float>>(lds + kStats + (tile & 1) * 256) + 8 * hf;
+      // P and dS are rounded once, as bf16 operands: what they are summed with, dout
+      // and q, has no common part that would have to cancel as the keys' has in dq.
+      // dk and dv of the 16384-token batch are 2.3e-3 off (relative, of the whole), of
+      // which their own rounding is 1.7e-3; two numbers each would double the matrix
+      // instructions of this phase, and its registers.
       Frag<DT> pf[2], ds[2];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {

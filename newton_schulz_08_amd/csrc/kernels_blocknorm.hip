@@ -27,11 +27,14 @@
 // their column sums are a launch of its own behind one that stores each row's
 // lengths and mean.
 //
-// Measured, fp32 stream and bf16 branch: backward of 32768 x 4096 455 us and of
-// 32768 x 8192 884 us, 5.3 and 5.5 TB/s of the bytes it cannot do without (a
-// copy of 1 GiB moves 5.2); forward of 16 x 4096 4.3 us, which is latency.  Two
-// runs of eight a lane, and half the threads, take 852 us at 4096; loads behind
-// branches 1247.
+// Measured, fp32 stream and bf16 branch: backward of 32768 x 4096 455 to 490 us and
+// of 32768 x 8192 885, 5.0 to 5.5 TB/s of the bytes it cannot do without (a copy
+// of 1 GiB moves 5.2); forward 308 and 615, 5.2.  bf16: backward 311 and 642 us,
+// 5.2 and 5.0 TB/s, forward 211 and 410.  Forward of 16 x 4096 3.8 us, which is
+// latency.  Two runs of eight a lane, and half the threads, take 852 us backward
+// at 4096; loads behind branches 1247.  Rows over 8192 are swept: 8192 x 16384
+// forward 412 us and backward 1255 (statistics 228, columns 285, rows 735) where
+// the bytes would take 311 and 466; bf16 321 and 950.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

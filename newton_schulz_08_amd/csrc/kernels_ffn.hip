@@ -28,14 +28,17 @@
 // Few tokens: the weights are read once, straight into fragments, by waves
 // that split the contraction; at most 64 tokens a wave.
 //
-// Measured, 4096 -> 14336 bf16: 8192 tokens 1.45 to 1.49 ms, 1.30 PFLOP/s (a
-// library product of 8192 on each side reaches 1.38); gradient 4.5 ms, 1.28
-// (projections again 1.67, dx 1.40, weights 1.49); 1 to 4 tokens 43 us, 5.5 TB/s
-// of the weights as they lie in the memory-side cache (fresh ones 48).  512 ->
-// 2048 fp32, gradient of 1001 tokens: 153 to 157 us, three products of 50 and a
-// join of 5, where 27 would be the matrix pipe's time; of 4096 tokens 536, where
-// 328 would be.  Of those, the loads cost 27 and moving them on to LDS 80; the
-// rest is what two waves a SIMD leave open around each stage's barrier.
+// Measured, 4096 -> 14336 bf16: 8192 tokens 1.45 to 1.53 ms, 1.26 to 1.30 PFLOP/s
+// (a library product of 8192 on each side reaches 1.38); gradient 4.5 to 4.6 ms,
+// 1.28 (projections again 1.67, dx 1.40, weights 1.49); 1 to 4 tokens 43 us, 5.5
+// TB/s of the weights as they lie in the memory-side cache (fresh ones 48), 32
+// tokens 61, 64 to 256 tokens 77 to 86 (one row of tiles on 112 CUs), 512 95 to
+// 100.  fp32: 1 to 4 tokens 105 to 135 us, 3.5 to 4.5 TB/s, 64 tokens 165 to 187,
+// 65 twice that (two rows of tiles).  512 -> 2048 fp32, gradient of 1001 tokens:
+// 149 to 167 us on different cards, three products of 48 to 54 and a join of 5,
+// where 27 would be the matrix pipe's time; of 4096 tokens 536 to 610, where 328
+// would be.  Of those, the loads cost 27 and moving them on to LDS 80; the rest is
+// what two waves a SIMD leave open around each stage's barrier.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -115,6 +118,10 @@ template <int DT, int MODE> __device__ __forceinline__ void finish_gated(const F
       dg[i] = in ? dh[i] * u[i] * dact[i] : 0.0f;
       du[i] = in ? dh[i] * act[i] : 0.0f;
     }
+    // rounded to T, once, as operands of the next two products: dx and the weights'
+    // gradients of 8192 bf16 tokens, 4096 -> 14336, are 2.35e-3 off (relative, of the
+    // whole), of which their own rounding is 1.66e-3.  In fp32 those would be fp32
+    // products, at a tenth of the rate.
     T* mid = static_cast<T*>(a.mid) + r * (2 * static_cast<int64_t>(a.hp));
     store_n<4>(mid + f, dg);
     store_n<4>(mid + a.hp + f, du);
@@ -794,8 +801,8 @@ template <int DT> hipError_t run_any(int mode, const FfnArgs& a, hipStream_t str
 }
 // Slices of a product's contraction: where its tiles alone leave CUs idle, at
 // least eight stages each.  Gradients in us, with slices and without:
-//   fp32, 512 -> 2048:  256 tokens 63, 180;  1001 tokens 164, 251
-//   bf16, 1024 -> 4096: 512 tokens 88, 214;  2048 tokens 145, 246;  8192 tokens 420, 464
+//   fp32, 512 -> 2048:  256 tokens 56, 149;  1001 tokens 149, 210
+//   bf16, 1024 -> 4096: 512 tokens 87, 211;  2048 tokens 147, 245;  8192 tokens 426, 465
 template <int DT, int MODE> int slices_of(const FfnArgs& a) {
   const int64_t tiles = grid_of<MODE>(a, DT == kBF16 ? 256 : kTile32).all;
   if (tiles == 0 || tiles > 128) return 1;
